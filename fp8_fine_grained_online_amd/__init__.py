@@ -24,6 +24,16 @@ Backward pass (Dgrad dX = dY W, Wgrad dW = dY^T X):
   fp8q_requant_1x128_to_128x1(q, sa)         -> (qt, st)
   fp8q_transpose_weight_128x128(q, sb)       -> (qt, sbt)
   fp8_gemm_rowscaled(a, sa, b, sb, out_dtype)            -> c
+MoE layer around the experts' products, with gradients:
+  fp8q_moe_route(logits, topk, ...)          -> (topk_ids, weights)   router
+  fp8q_moe_route_bwd(logits, topk_ids, dweights, ...)    -> dlogits
+  fp8q_moe_permute(x, topk_ids, G)           -> (xp, m_offsets, row_of_slot)   rows sorted by expert
+  fp8q_moe_combine(c, row_of_slot, weights)  -> y   the way back (weights None: permute's gradient)
+  fp8q_moe_combine_bwd(dy, c, row_of_slot, weights, m_offsets) -> (dc, dw)
+8-bit integer product, one scale per token and per output channel:
+  fp8q_quant_int8_rows(x)                    -> (q, s)
+  int8_gemm_scaled(a, sa, b, sb, out_dtype)  -> c
+  int8_gemm_grouped(a, sa, b, sb, m_offsets, out_dtype)  -> c
 """
 
 from ._lib import (  # noqa: F401
@@ -46,7 +56,15 @@ from ._lib import (  # noqa: F401
     fp8q_requant_1x128_to_128x1,
     fp8q_transpose_weight_128x128,
     fp8q_quant_weight_128x128,
+    fp8q_moe_combine,
+    fp8q_moe_combine_bwd,
+    fp8q_moe_permute,
+    fp8q_moe_route,
+    fp8q_moe_route_bwd,
+    fp8q_quant_int8_rows,
     fp8q_version,
+    int8_gemm_grouped,
+    int8_gemm_scaled,
     lib,
     lib_path,
 )
@@ -57,4 +75,6 @@ __all__ = [
     "fp8_gemm_blockscaled", "fp8_gemm_blockscaled_bf16a", "fp8_gemm_blockscaled_ws", "fp8_gemm_blockscaled_noalloc", "fp8_gemm_grouped", "fp8q_version", "lib", "lib_path",
     "fp8q_quant_act_128x1", "fp8q_quant_act_1x128_128x1", "fp8q_norm_quant_act_1x128", "fp8q_moe_dispatch_1x128", "fp8q_requant_1x128_to_128x1", "fp8q_transpose_weight_128x128",
     "fp8_gemm_rowscaled",
+    "fp8q_moe_route", "fp8q_moe_route_bwd", "fp8q_moe_permute", "fp8q_moe_combine", "fp8q_moe_combine_bwd",
+    "fp8q_quant_int8_rows", "int8_gemm_scaled", "int8_gemm_grouped",
 ]

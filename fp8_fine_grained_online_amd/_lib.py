@@ -79,6 +79,24 @@ def lib() -> ctypes.CDLL:
         L.fp8q_transpose_weight_128x128.argtypes = [vp, vp, i64, i64, vp, vp, vp]
         L.fp8_gemm_rowscaled.restype = i32
         L.fp8_gemm_rowscaled.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]
+        f32 = ctypes.c_float
+        L.fp8q_moe_route.restype = i32
+        L.fp8q_moe_route.argtypes = [vp, i32, vp, i64, i64, i64, i64, i64, i32, i32, f32, vp, vp, vp]
+        L.fp8q_moe_route_bwd.restype = i32
+        L.fp8q_moe_route_bwd.argtypes = [vp, i32, vp, vp, i64, i64, i64, i32, i32, f32, vp, vp]
+        L.fp8q_moe_permute.restype = i32
+        L.fp8q_moe_permute.argtypes = [vp, i32, vp, i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, vp]
+        L.fp8q_moe_combine.restype = i32
+        L.fp8q_moe_combine.argtypes = [vp, i32, vp, vp, i64, i64, i64, i64, vp, i32, vp]
+        L.fp8q_moe_combine_bwd.restype = i32
+        L.fp8q_moe_combine_bwd.argtypes = [vp, i32, vp, i32, vp, vp, vp, i64, i64, i64, i64, i64, vp,
+                                           vp, vp]
+        L.fp8q_quant_int8_rows.restype = i32
+        L.fp8q_quant_int8_rows.argtypes = [vp, i64, i64, vp, vp, vp]
+        L.int8_gemm_scaled.restype = i32
+        L.int8_gemm_scaled.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]
+        L.int8_gemm_grouped.restype = i32
+        L.int8_gemm_grouped.argtypes = [vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, i64, vp]
         _lib = L
     return _lib
 
@@ -461,4 +479,250 @@ def fp8_gemm_rowscaled(a, sa, b, sb, out_dtype="f32", c=None, stream=None):
     c = _out(c, "c", (M, N), tdt, a.device)
     _check("fp8_gemm_rowscaled",
            lib().fp8_gemm_rowscaled(pa, psa, pb, psb, c.data_ptr(), code, M, N, K, _stream(stream)))
+    return c
+
+
+# ---- MoE layer around the experts' products, and the 8-bit integer product ----
+
+class _Call:
+    """One call's device, stream and argument checks: every tensor on the first
+    one's device, the launch on that device (made current if it is not) and on
+    its current stream unless one is given."""
+
+    def __init__(self, fn, first):
+        self.torch = _torch()
+        self.fn = fn
+        if not isinstance(first, self.torch.Tensor):
+            raise TypeError("arguments must be torch.Tensors")
+        self.device = first.device
+
+    def ptr(self, t, name, dtypes, ndim):
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != self.device or not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor on {self.device}, got {t.device}")
+        if t.dtype is not dtypes and not (isinstance(dtypes, tuple) and t.dtype in dtypes):
+            raise TypeError(f"{name} must be {dtypes}, got {t.dtype}")
+        if t.dim() != ndim:
+            raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def out(self, t, name, shape, dtype):
+        if t is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        self.ptr(t, name, dtype, len(shape))
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        return t
+
+    def __call__(self, *args, stream=None):
+        cuda, index = self.torch.cuda, self.device.index
+        if stream is None:
+            stream = cuda.current_stream(self.device)
+        sp = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        entry = getattr(lib(), self.fn)
+        if cuda.current_device() == index:
+            status = entry(*args, sp)
+        else:
+            with cuda.device(index):
+                status = entry(*args, sp)
+        _check(self.fn, status)
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _element_types(torch):
+    return {torch.float32: FP8Q_OUT_F32, torch.bfloat16: FP8Q_OUT_BF16}
+
+
+def _score(score):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    return SCORES[score]
+
+
+def fp8q_moe_route(logits, topk, bias=None, score="softmax", renormalize=True, scale=1.0, n_groups=1,
+                   topk_groups=1, topk_ids=None, weights=None, stream=None):
+    """Router: logits T x G (float32 or bfloat16) -> (topk_ids int32 T x topk, weights float32
+    T x topk). bias (float32, G) is added to the probabilities for the choice only; with
+    n_groups > 1 experts come from the topk_groups best groups."""
+    call = _Call("fp8q_moe_route", logits)
+    torch = call.torch
+    types = _element_types(torch)
+    px = call.ptr(logits, "logits", tuple(types), 2)
+    T, G = logits.shape
+    pb = None
+    if bias is not None:
+        pb = call.ptr(bias, "bias", torch.float32, 1)
+        if bias.shape[0] != G:
+            raise ValueError("bias must have G entries")
+    topk = int(topk)
+    topk_ids = call.out(topk_ids, "topk_ids", (T, max(topk, 0)), torch.int32)
+    weights = call.out(weights, "weights", (T, max(topk, 0)), torch.float32)
+    call(px, types[logits.dtype], pb, T, G, topk, int(n_groups), int(topk_groups), _score(score),
+         int(bool(renormalize)), float(scale), topk_ids.data_ptr(), weights.data_ptr(), stream=stream)
+    return topk_ids, weights
+
+
+def fp8q_moe_route_bwd(logits, topk_ids, dweights, score="softmax", renormalize=True, scale=1.0,
+                       dlogits=None, stream=None):
+    """Gradient of fp8q_moe_route's weights: dweights (float32 T x topk) -> dlogits (T x G, like logits)."""
+    call = _Call("fp8q_moe_route_bwd", logits)
+    torch = call.torch
+    types = _element_types(torch)
+    px = call.ptr(logits, "logits", tuple(types), 2)
+    pid = call.ptr(topk_ids, "topk_ids", torch.int32, 2)
+    pdw = call.ptr(dweights, "dweights", torch.float32, 2)
+    T, G = logits.shape
+    if topk_ids.shape != dweights.shape or topk_ids.shape[0] != T:
+        raise ValueError("topk_ids and dweights must both be T x topk")
+    dlogits = call.out(dlogits, "dlogits", (T, G), logits.dtype)
+    call(px, types[logits.dtype], pid, pdw, T, G, topk_ids.shape[1], _score(score),
+         int(bool(renormalize)), float(scale), dlogits.data_ptr(), stream=stream)
+    return dlogits
+
+
+def fp8q_moe_permute(x, topk_ids, G, xp=None, m_offsets=None, row_of_slot=None, workspace=None,
+                     stream=None):
+    """Rows sorted by expert: x T x K (bfloat16 or float32), topk_ids int32 T x topk ->
+    (xp M_cap x K, m_offsets int32[G+1], row_of_slot int32 T x topk), the layout of
+    fp8q_moe_dispatch_1x128; rows of xp from m_offsets[G] on are not written."""
+    call = _Call("fp8q_moe_permute", x)
+    torch = call.torch
+    types = _element_types(torch)
+    px = call.ptr(x, "x", tuple(types), 2)
+    pid = call.ptr(topk_ids, "topk_ids", torch.int32, 2)
+    T, K = x.shape
+    if topk_ids.shape[0] != T:
+        raise ValueError("topk_ids must have one row per token")
+    topk = topk_ids.shape[1]
+    L = lib()
+    M_cap = L.fp8q_moe_dispatch_max_rows(T, topk, G)
+    ws_bytes = L.fp8q_moe_dispatch_workspace_bytes(T, topk, G)
+    if M_cap < 0 or ws_bytes < 0:
+        raise ValueError("invalid permute sizes")
+    xp = call.out(xp, "xp", (M_cap, K), x.dtype)
+    m_offsets = call.out(m_offsets, "m_offsets", (G + 1,), torch.int32)
+    row_of_slot = call.out(row_of_slot, "row_of_slot", (T, topk), torch.int32)
+    if workspace is None:
+        workspace = torch.empty(max(ws_bytes, 4), dtype=torch.uint8, device=x.device)
+    pw = call.ptr(workspace, "workspace", torch.uint8, 1)
+    call(px, types[x.dtype], pid, T, K, topk, G, xp.data_ptr(), M_cap, m_offsets.data_ptr(),
+         row_of_slot.data_ptr(), pw, workspace.numel(), stream=stream)
+    return xp, m_offsets, row_of_slot
+
+
+def fp8q_moe_combine(c, row_of_slot, weights=None, out_dtype="bf16", y=None, stream=None):
+    """The way back: y[t] = sum_j weights[t, j] * c[row_of_slot[t, j]] (weights None: ones; rows
+    outside c are skipped). c M x K (bfloat16 or float32) -> y T x K of out_dtype."""
+    call = _Call("fp8q_moe_combine", c)
+    torch = call.torch
+    types = _element_types(torch)
+    code, tdt = _out_dtype(out_dtype)
+    pc = call.ptr(c, "c", tuple(types), 2)
+    pr = call.ptr(row_of_slot, "row_of_slot", torch.int32, 2)
+    pw = None
+    if weights is not None:
+        pw = call.ptr(weights, "weights", torch.float32, 2)
+        if weights.shape != row_of_slot.shape:
+            raise ValueError("weights must have row_of_slot's shape")
+    M, K = c.shape
+    T, topk = row_of_slot.shape
+    y = call.out(y, "y", (T, K), tdt)
+    call(pc, types[c.dtype], pr, pw, T, K, topk, M, y.data_ptr(), code, stream=stream)
+    return y
+
+
+def fp8q_moe_combine_bwd(dy, c, row_of_slot, weights, m_offsets, dc=None, dw=None, with_dw=True,
+                         stream=None):
+    """Gradient of fp8q_moe_combine: dy T x K, c M x K -> (dc M x K like c, dw float32 T x topk);
+    padding rows of dc are zero, rows from m_offsets[G] on are not written. with_dw=False: dw is
+    None and c is only used for its shape and type."""
+    call = _Call("fp8q_moe_combine_bwd", dy)
+    torch = call.torch
+    types = _element_types(torch)
+    pdy = call.ptr(dy, "dy", tuple(types), 2)
+    pc = call.ptr(c, "c", tuple(types), 2)
+    pr = call.ptr(row_of_slot, "row_of_slot", torch.int32, 2)
+    poff = call.ptr(m_offsets, "m_offsets", torch.int32, 1)
+    pw = None
+    if weights is not None:
+        pw = call.ptr(weights, "weights", torch.float32, 2)
+        if weights.shape != row_of_slot.shape:
+            raise ValueError("weights must have row_of_slot's shape")
+    M, K = c.shape
+    T, topk = row_of_slot.shape
+    if tuple(dy.shape) != (T, K):
+        raise ValueError(f"dy must have shape {(T, K)}, got {tuple(dy.shape)}")
+    if m_offsets.shape[0] < 2:
+        raise ValueError("m_offsets must have G+1 entries")
+    dc = call.out(dc, "dc", (M, K), c.dtype)
+    if with_dw or dw is not None:
+        dw = call.out(dw, "dw", (T, topk), torch.float32)
+    call(pdy, types[dy.dtype], pc, types[c.dtype], pr, pw, poff, T, K, topk, m_offsets.shape[0] - 1, M,
+         dc.data_ptr(), dw.data_ptr() if dw is not None else None, stream=stream)
+    return dc, dw
+
+
+def fp8q_quant_int8_rows(x, q=None, s=None, stream=None):
+    """x: bf16 ... x K device tensor (2 or 3 dims: tokens, channels or experts' channels) ->
+    (q int8 like x, s float32 without the last dim): one scale amax / 127 per row."""
+    call = _Call("fp8q_quant_int8_rows", x)
+    torch = call.torch
+    px = call.ptr(x, "x", torch.bfloat16, 3 if x.dim() == 3 else 2)
+    lead, K = tuple(x.shape[:-1]), x.shape[-1]
+    rows = 1
+    for d in lead:
+        rows *= d
+    q = call.out(q, "q", tuple(x.shape), torch.int8)
+    s = call.out(s, "s", lead, torch.float32)
+    call(px, rows, K, q.data_ptr(), s.data_ptr(), stream=stream)
+    return q, s
+
+
+def int8_gemm_scaled(a, sa, b, sb, out_dtype="bf16", c=None, stream=None):
+    """c[m, n] = (sum_k a[m, k] b[n, k]) * sa[m] * sb[n]: a int8 M x K, sa float32 M, b int8 N x K,
+    sb float32 N. Returns c (M x N)."""
+    call = _Call("int8_gemm_scaled", a)
+    torch = call.torch
+    code, tdt = _out_dtype(out_dtype)
+    pa = call.ptr(a, "a", torch.int8, 2)
+    psa = call.ptr(sa, "sa", torch.float32, 1)
+    pb = call.ptr(b, "b", torch.int8, 2)
+    psb = call.ptr(sb, "sb", torch.float32, 1)
+    M, K = a.shape
+    N = b.shape[0]
+    if b.shape[1] != K:
+        raise ValueError("a and b must share K")
+    if sa.shape[0] != M or sb.shape[0] != N:
+        raise ValueError("scale shapes must be (M,) and (N,)")
+    c = call.out(c, "c", (M, N), tdt)
+    call(pa, psa, pb, psb, c.data_ptr(), code, M, N, K, stream=stream)
+    return c
+
+
+def int8_gemm_grouped(a, sa, b, sb, m_offsets, out_dtype="bf16", c=None, M_total=None, stream=None):
+    """Grouped form: a int8 M x K, sa float32 M, b int8 G x N x K, sb float32 G x N, m_offsets
+    int32[G+1] (device, multiples of 128, never read on the host). M_total defaults to a.shape[0]."""
+    call = _Call("int8_gemm_grouped", a)
+    torch = call.torch
+    code, tdt = _out_dtype(out_dtype)
+    pa = call.ptr(a, "a", torch.int8, 2)
+    psa = call.ptr(sa, "sa", torch.float32, 1)
+    pb = call.ptr(b, "b", torch.int8, 3)
+    psb = call.ptr(sb, "sb", torch.float32, 2)
+    poff = call.ptr(m_offsets, "m_offsets", torch.int32, 1)
+    G, N, K = b.shape
+    if m_offsets.shape[0] != G + 1:
+        raise ValueError("m_offsets must have G+1 entries")
+    M = a.shape[0] if M_total is None else int(M_total)
+    if a.shape[1] != K or a.shape[0] < M or sa.shape[0] < M:
+        raise ValueError("a must be at least M_total x K, with a scale per row")
+    if tuple(sb.shape) != (G, N):
+        raise ValueError(f"sb must have shape {(G, N)}, got {tuple(sb.shape)}")
+    c = call.out(c, "c", (M, N), tdt)
+    call(pa, psa, pb, psb, c.data_ptr(), code, poff, G, M, N, K, stream=stream)
     return c

@@ -14,8 +14,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libfp8q.so")
 
-SOURCES = ["quant.hip", "retile.hip", "norm.hip", "moe.hip", "gemm.hip", "gemm_qa.hip", "api.cpp"]
-HEADERS = ["common.hpp", "tiles.hpp"]
+SOURCES = ["quant.hip", "retile.hip", "norm.hip", "moe.hip", "gemm.hip", "gemm_qa.hip", "route.hip",
+           "tokens.hip", "int8.hip", "api.cpp"]
+HEADERS = ["common.hpp", "tiles.hpp", "wave.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

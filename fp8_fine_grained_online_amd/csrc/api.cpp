@@ -50,6 +50,30 @@ hipError_t launch_requant_1x128_to_128x1(const uint8_t* q, const float* sa, int6
                                          uint8_t* qt, float* st, hipStream_t stream);
 hipError_t launch_transpose_weight_128x128(const uint8_t* q, const float* sb, int64_t N, int64_t K,
                                            uint8_t* qt, float* sbt, hipStream_t stream);
+hipError_t launch_route(const void* logits, bool bf16, const float* bias, int64_t T, int64_t G,
+                        int64_t topk, int64_t n_groups, int64_t topk_groups, bool sigmoid,
+                        bool renorm, float scale, int32_t* ids, float* w, hipStream_t stream);
+hipError_t launch_route_bwd(const void* logits, bool bf16, const int32_t* ids, const float* dw,
+                            int64_t T, int64_t G, int64_t topk, bool sigmoid, bool renorm,
+                            float scale, void* dlogits, hipStream_t stream);
+hipError_t launch_moe_permute(const void* x, bool bf16, const int32_t* ids, int64_t T, int64_t K,
+                              int64_t topk, int64_t G, void* xp, int32_t* m_offsets,
+                              int32_t* row_of_slot, void* workspace, hipStream_t stream);
+hipError_t launch_moe_combine(const void* c, bool c_bf16, const int32_t* row_of_slot,
+                              const float* weights, int64_t T, int64_t K, int64_t topk, int64_t M,
+                              void* y, bool y_bf16, hipStream_t stream);
+hipError_t launch_moe_combine_bwd(const void* dy, bool dy_bf16, const void* c, bool c_bf16,
+                                  const int32_t* row_of_slot, const float* weights,
+                                  const int32_t* m_offsets, int64_t T, int64_t K, int64_t topk,
+                                  int64_t G, int64_t M, void* dc, float* dw, hipStream_t stream);
+hipError_t launch_quant_int8_rows(const void* x, int64_t M, int64_t K, int8_t* q, float* s,
+                                  hipStream_t stream);
+hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                            void* c, bool bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+hipError_t launch_int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b,
+                                    const float* sb, void* c, bool bf16, const int32_t* m_offsets,
+                                    int64_t G, int64_t M_total, int64_t N, int64_t K,
+                                    hipStream_t stream);
 }  // namespace fp8q
 
 namespace {
@@ -63,6 +87,10 @@ constexpr int64_t kMaxExperts = 1024;  // dispatch: one scan thread per expert
 // the fused normalization keeps a row in one wavefront's registers
 constexpr int64_t kNormMaxK = 16384;
 constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxTopk = 64;    // router: one lane per choice
+constexpr int64_t kMaxGroups = 64;  // router: one lane per expert group
+// largest K whose int8 sums stay below 2^31 (128 * 128 * K), a multiple of 16
+constexpr int64_t kInt8MaxK = 131056;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -92,6 +120,31 @@ int check_gemm_common(const uint8_t* a, const float* sa, const uint8_t* b, const
   if (out_dtype != FP8Q_OUT_F32 && out_dtype != FP8Q_OUT_BF16) return FP8Q_ERR_DTYPE;
   if (M > kMaxDim || N > kMaxDim || K > kMaxK) return FP8Q_ERR_TOO_LARGE;
   if ((M + 127) / 128 * (N / 128) > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  if (M == 0 || N == 0) return -1;  // valid no-op
+  if (!c) return FP8Q_ERR_NULL;
+  if (K > 0 && (!a || !sa || !b || !sb)) return FP8Q_ERR_NULL;  // K == 0 reads no operand
+  if (!aligned(c, 16)) return FP8Q_ERR_ALIGN;
+  if (K > 0 && (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4)))
+    return FP8Q_ERR_ALIGN;
+  return FP8Q_OK;
+}
+
+bool known_dtype(int d) { return d == FP8Q_OUT_F32 || d == FP8Q_OUT_BF16; }
+
+// Sizes shared by the calls that move rows between tokens and experts.
+int check_rows(int64_t T, int64_t K, int64_t topk, int64_t M) {
+  if (T < 0 || K < 0 || K % 8 || topk < 1 || M < 0) return FP8Q_ERR_SHAPE;
+  if (K > kMaxDim || M > kMaxDim || T > kMaxDim / topk) return FP8Q_ERR_TOO_LARGE;
+  return FP8Q_OK;
+}
+
+int check_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, const void* c,
+               int out_dtype, int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0 || K % 16) return FP8Q_ERR_SHAPE;
+  if (!known_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
+  if (M > kMaxDim || N > kMaxDim || K > kInt8MaxK) return FP8Q_ERR_TOO_LARGE;
+  // tiles, of 16 x 16 outputs at the least, are numbered with 32 bits
+  if ((M + 15) / 16 * ((N + 15) / 16) > kMaxDim) return FP8Q_ERR_TOO_LARGE;
   if (M == 0 || N == 0) return -1;  // valid no-op
   if (!c) return FP8Q_ERR_NULL;
   if (K > 0 && (!a || !sa || !b || !sb)) return FP8Q_ERR_NULL;  // K == 0 reads no operand
@@ -352,6 +405,147 @@ int fp8_gemm_rowscaled(const uint8_t* a, const float* sa, const uint8_t* b, cons
   if ((s = check_device())) return s;
   return launched(fp8q::launch_gemm_rowscaled(a, sa, b, sb, c, out_dtype == FP8Q_OUT_BF16, M, N, K,
                                               (hipStream_t)stream));
+}
+
+int fp8q_moe_route(const void* logits, int dtype, const float* bias, int64_t T, int64_t G,
+                   int64_t topk, int64_t n_groups, int64_t topk_groups, int score, int renormalize,
+                   float scale, int32_t* topk_ids, float* weights, void* stream) {
+  if (T < 0 || G < 1 || topk < 1 || n_groups < 1 || topk_groups < 1 || topk_groups > n_groups)
+    return FP8Q_ERR_SHAPE;
+  if (G > kMaxExperts || topk > kMaxTopk || n_groups > kMaxGroups || T > kMaxDim / topk)
+    return FP8Q_ERR_TOO_LARGE;
+  if (G % n_groups || topk > topk_groups * (G / n_groups)) return FP8Q_ERR_SHAPE;
+  if (score != FP8Q_SCORE_SOFTMAX && score != FP8Q_SCORE_SIGMOID) return FP8Q_ERR_SHAPE;
+  if (renormalize != 0 && renormalize != 1) return FP8Q_ERR_SHAPE;
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return FP8Q_ERR_SHAPE;  // NaN or infinite
+  if (!known_dtype(dtype)) return FP8Q_ERR_DTYPE;
+  if (T == 0) return FP8Q_OK;
+  if (!logits || !topk_ids || !weights) return FP8Q_ERR_NULL;
+  if (!aligned(logits, dtype == FP8Q_OUT_BF16 ? 2 : 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) ||
+      !aligned(weights, 4))
+    return FP8Q_ERR_ALIGN;
+  if (int s = check_device()) return s;
+  return launched(fp8q::launch_route(logits, dtype == FP8Q_OUT_BF16, bias, T, G, topk, n_groups,
+                                     topk_groups, score == FP8Q_SCORE_SIGMOID, renormalize == 1,
+                                     scale, topk_ids, weights, (hipStream_t)stream));
+}
+
+int fp8q_moe_route_bwd(const void* logits, int dtype, const int32_t* topk_ids, const float* dweights,
+                       int64_t T, int64_t G, int64_t topk, int score, int renormalize, float scale,
+                       void* dlogits, void* stream) {
+  if (T < 0 || G < 1 || topk < 1) return FP8Q_ERR_SHAPE;
+  if (G > kMaxExperts || topk > kMaxTopk || T > kMaxDim / topk) return FP8Q_ERR_TOO_LARGE;
+  if (score != FP8Q_SCORE_SOFTMAX && score != FP8Q_SCORE_SIGMOID) return FP8Q_ERR_SHAPE;
+  if (renormalize != 0 && renormalize != 1) return FP8Q_ERR_SHAPE;
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return FP8Q_ERR_SHAPE;
+  if (!known_dtype(dtype)) return FP8Q_ERR_DTYPE;
+  if (T == 0) return FP8Q_OK;
+  if (!logits || !topk_ids || !dweights || !dlogits) return FP8Q_ERR_NULL;
+  const uintptr_t al = dtype == FP8Q_OUT_BF16 ? 2 : 4;
+  if (!aligned(logits, al) || !aligned(dlogits, al) || !aligned(topk_ids, 4) || !aligned(dweights, 4))
+    return FP8Q_ERR_ALIGN;
+  if (int s = check_device()) return s;
+  return launched(fp8q::launch_route_bwd(logits, dtype == FP8Q_OUT_BF16, topk_ids, dweights, T, G, topk,
+                                         score == FP8Q_SCORE_SIGMOID, renormalize == 1, scale,
+                                         dlogits, (hipStream_t)stream));
+}
+
+int fp8q_moe_permute(const void* x, int dtype, const int32_t* topk_ids, int64_t T, int64_t K,
+                     int64_t topk, int64_t G, void* xp, int64_t M_cap, int32_t* m_offsets,
+                     int32_t* row_of_slot, void* workspace, int64_t workspace_bytes, void* stream) {
+  int s = check_rows(T, K, topk, M_cap);
+  if (s) return s;
+  if (G < 1) return FP8Q_ERR_SHAPE;
+  if (!known_dtype(dtype)) return FP8Q_ERR_DTYPE;
+  if (G > kMaxExperts || T > kMaxDim / 4) return FP8Q_ERR_TOO_LARGE;
+  const int64_t need_rows = dispatch_max_rows(T, topk, G);
+  if (need_rows > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  if (M_cap < need_rows) return FP8Q_ERR_SHAPE;  // outputs too small for the worst-case padding
+  if (!m_offsets || !workspace) return FP8Q_ERR_NULL;
+  if (T > 0 && (!topk_ids || !row_of_slot)) return FP8Q_ERR_NULL;
+  if (K > 0 && T > 0 && (!x || !xp)) return FP8Q_ERR_NULL;
+  if (workspace_bytes < fp8q::dispatch_workspace_bytes(T * topk, G)) return FP8Q_ERR_SHAPE;
+  if (!aligned(m_offsets, 4) || !aligned(workspace, 4)) return FP8Q_ERR_ALIGN;
+  if (T > 0 && (!aligned(topk_ids, 4) || !aligned(row_of_slot, 4))) return FP8Q_ERR_ALIGN;
+  if (K > 0 && T > 0 && (!aligned(x, 16) || !aligned(xp, 16))) return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_moe_permute(x, dtype == FP8Q_OUT_BF16, topk_ids, T, K, topk, G, xp,
+                                           m_offsets, row_of_slot, workspace, (hipStream_t)stream));
+}
+
+int fp8q_moe_combine(const void* c, int c_dtype, const int32_t* row_of_slot, const float* weights,
+                     int64_t T, int64_t K, int64_t topk, int64_t M, void* y, int y_dtype,
+                     void* stream) {
+  int s = check_rows(T, K, topk, M);
+  if (s) return s;
+  if (!known_dtype(c_dtype) || !known_dtype(y_dtype)) return FP8Q_ERR_DTYPE;
+  if (T * ((K / 8 + 63) / 64) > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  if (T == 0 || K == 0) return FP8Q_OK;
+  if (!row_of_slot || !y || (M > 0 && !c)) return FP8Q_ERR_NULL;
+  if (!aligned(c, 16) || !aligned(y, 16) || !aligned(row_of_slot, 4) || !aligned(weights, 4))
+    return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_moe_combine(c, c_dtype == FP8Q_OUT_BF16, row_of_slot, weights, T, K,
+                                           topk, M, y, y_dtype == FP8Q_OUT_BF16,
+                                           (hipStream_t)stream));
+}
+
+int fp8q_moe_combine_bwd(const void* dy, int dy_dtype, const void* c, int c_dtype,
+                         const int32_t* row_of_slot, const float* weights,
+                         const int32_t* m_offsets, int64_t T, int64_t K, int64_t topk, int64_t G,
+                         int64_t M, void* dc, float* dw, void* stream) {
+  int s = check_rows(T, K, topk, M);
+  if (s) return s;
+  if (G < 1) return FP8Q_ERR_SHAPE;
+  if (!known_dtype(dy_dtype) || !known_dtype(c_dtype)) return FP8Q_ERR_DTYPE;
+  if (G > kMaxExperts || T > kMaxDim - kMaxExperts) return FP8Q_ERR_TOO_LARGE;
+  if (!m_offsets || (T > 0 && !row_of_slot)) return FP8Q_ERR_NULL;
+  if (K > 0 && ((T > 0 && !dy) || (M > 0 && !dc) || (M > 0 && T > 0 && dw && !c))) return FP8Q_ERR_NULL;
+  if (!aligned(dy, 16) || !aligned(c, 16) || !aligned(dc, 16) || !aligned(row_of_slot, 4) ||
+      !aligned(weights, 4) || !aligned(m_offsets, 4) || !aligned(dw, 4))
+    return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_moe_combine_bwd(dy, dy_dtype == FP8Q_OUT_BF16, c,
+                                               c_dtype == FP8Q_OUT_BF16, row_of_slot, weights,
+                                               m_offsets, T, K, topk, G, M, dc, dw,
+                                               (hipStream_t)stream));
+}
+
+int fp8q_quant_int8_rows(const void* x_bf16, int64_t M, int64_t K, int8_t* q, float* s,
+                         void* stream) {
+  if (M < 0 || K < 0 || K % 16) return FP8Q_ERR_SHAPE;
+  if (M > kMaxDim || K > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  if (M == 0) return FP8Q_OK;
+  if (!s || (K > 0 && (!x_bf16 || !q))) return FP8Q_ERR_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(q, 16) || !aligned(s, 4)) return FP8Q_ERR_ALIGN;
+  if (int st = check_device()) return st;
+  return launched(fp8q::launch_quant_int8_rows(x_bf16, M, K, q, s, (hipStream_t)stream));
+}
+
+int int8_gemm_scaled(const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* c,
+                     int out_dtype, int64_t M, int64_t N, int64_t K, void* stream) {
+  int s = check_int8(a, sa, b, sb, c, out_dtype, M, N, K);
+  if (s == -1) return FP8Q_OK;
+  if (s || (s = check_device())) return s;
+  return launched(fp8q::launch_int8_gemm(a, sa, b, sb, c, out_dtype == FP8Q_OUT_BF16, M, N, K,
+                                         (hipStream_t)stream));
+}
+
+int int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* c,
+                      int out_dtype, const int32_t* m_offsets, int64_t G, int64_t M_total, int64_t N,
+                      int64_t K, void* stream) {
+  if (G < 1 || M_total % kGroup) return FP8Q_ERR_SHAPE;
+  if (G > kMaxDim || N > kMaxDim || G * N > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  int s = check_int8(a, sa, b, sb, c, out_dtype, M_total, N, K);
+  if (s == -1) return FP8Q_OK;
+  if (s) return s;
+  // the grid holds up to one more tile row per expert
+  if ((M_total / kGroup + G + 1) * ((N + 63) / 64) > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  if (!m_offsets) return FP8Q_ERR_NULL;
+  if (!aligned(m_offsets, 4)) return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_int8_gemm_grouped(a, sa, b, sb, c, out_dtype == FP8Q_OUT_BF16,
+                                                 m_offsets, G, M_total, N, K, (hipStream_t)stream));
 }
 
 }  // extern "C"

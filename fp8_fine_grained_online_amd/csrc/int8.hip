@@ -1,0 +1,450 @@
+// 8-bit integer product with one scale per token and per output channel, for
+// gfx950 (CDNA4 MFMA), dense and grouped (MoE), and the row quantization that
+// feeds it.
+//
+//   c[m, n] = (sum_k a[m, k] b[n, k]) sa[m] sb[n]
+//
+// The integer matrix cores (v_mfma_i32_16x16x64_i8, the rate of FP8) add into
+// int32 registers, exactly, over the whole of K: nothing is promoted inside
+// the loop, and any order or split of K gives the same bits. The two scales
+// are applied once, in the epilogue.
+#include "common.hpp"
+#include "tiles.hpp"
+#include "wave.hpp"
+
+namespace fp8q {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kStepK = 128;  // bytes of K per pipeline step
+
+struct I8Args {
+  const uint8_t* a;
+  const float* sa;
+  const uint8_t* b;
+  const float* sb;
+  void* c;
+  const int32_t* m_offsets;  // grouped only
+  int M, N, K, G;
+};
+
+__device__ __forceinline__ float scaled(int v, float sa, float sb) {
+  return ((float)v * sa) * sb;
+}
+
+// ---------------------------------------------------------------------------
+// Row quantization. kWaves wavefronts per row; a lane owns runs of 16 values
+// (32 bytes in, 16 bytes of codes out). A row of up to kHeld runs per lane
+// stays in registers between its maximum and its codes; longer rows are read
+// twice (the second time from the cache).
+// ---------------------------------------------------------------------------
+constexpr int kRowHeld = 8;
+
+__device__ __forceinline__ float absmax16(uint4 a, uint4 b) { return fmaxf(absmax8(a), absmax8(b)); }
+
+__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float s) {
+  const float v[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float q = __builtin_amdgcn_fmed3f(rintf(__fdiv_rn(v[i], s)), -127.0f, 127.0f);
+    out |= ((uint32_t)(int)q & 0xFFu) << (8 * i);
+  }
+  return out;
+}
+
+__device__ __forceinline__ uint4 codes16(uint4 a, uint4 b, float s) {
+  return make_uint4(codes4(a.x, a.y, s), codes4(a.z, a.w, s), codes4(b.x, b.y, s), codes4(b.z, b.w, s));
+}
+
+template <int kWaves>
+__global__ __launch_bounds__(256) void quant_int8_rows_kernel(const uint4* __restrict__ x, int M,
+                                                              int K, uint4* __restrict__ q,
+                                                              float* __restrict__ s_out) {
+  constexpr int kThreads = 64 * kWaves;  // per row
+  __shared__ float wave_amax[4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m = (int64_t)blockIdx.x * (4 / kWaves) + wave / kWaves;
+  if (m >= M) return;
+  const int tid = threadIdx.x % kThreads;
+  const int n_runs = K / 16;
+  const uint4* xr = x + m * (2 * (int64_t)n_runs);
+  uint4* qr = q + m * n_runs;
+  const bool held = n_runs <= kRowHeld * kThreads;
+  uint4 v[kRowHeld][2];
+  float amax = 0.0f;
+  if (held) {
+#pragma unroll
+    for (int u = 0; u < kRowHeld; ++u) {
+      const int r = tid + u * kThreads;
+      v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+      if (r < n_runs) v[u][0] = load_nt(xr + 2 * r), v[u][1] = load_nt(xr + 2 * r + 1);
+    }
+#pragma unroll
+    for (int u = 0; u < kRowHeld; ++u) amax = fmaxf(amax, absmax16(v[u][0], v[u][1]));
+  } else {
+    for (int r = tid; r < n_runs; r += kThreads) amax = fmaxf(amax, absmax16(xr[2 * r], xr[2 * r + 1]));
+  }
+  // magnitudes of finite values order like their bits
+  amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
+  if constexpr (kWaves > 1) {
+    if ((threadIdx.x & 63) == 0) wave_amax[wave] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) amax = fmaxf(amax, wave_amax[w]);
+  }
+  const float s = __fdiv_rn(amax, 127.0f);
+  const float d = amax > 0.0f ? s : 1.0f;
+  if (tid == 0) s_out[m] = s;
+  if (held) {
+#pragma unroll
+    for (int u = 0; u < kRowHeld; ++u) {
+      const int r = tid + u * kThreads;
+      if (r < n_runs) qr[r] = codes16(v[u][0], v[u][1], d);
+    }
+  } else {
+    for (int r = tid; r < n_runs; r += kThreads) qr[r] = codes16(xr[2 * r], xr[2 * r + 1], d);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiled product. A workgroup computes a BM x BN tile with WAVES_M x WAVES_N
+// waves, each a WM x WN part. Per step of 128 bytes of K the slabs of A and B
+// go straight from global memory to LDS in one of two stages; 16-byte chunk c
+// of row r sits at position c ^ (r % 8), so the 16 rows of one operand load
+// fall in distinct banks.
+//
+// Operand lanes: lane l supplies row l % 16 of a 16-row block and the 16 bytes
+// of K at chunk l / 16 (or 4 + l / 16 for the step's second half). B is the
+// first operand, so a lane holds C[m = l % 16][n = 4 (l / 16) + r], four
+// consecutive columns of one row.
+//
+// Edges: the buffer descriptors cover the tile's valid rows, and in the last
+// step the chunks past K get an offset outside them; both read as zeros.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WAVES_M, int WAVES_N>
+struct I8Tile {
+  static constexpr int kThreads = 64 * WAVES_M * WAVES_N;
+  static constexpr int kWM = BM / WAVES_M, kWN = BN / WAVES_N;
+  static constexpr int kLdsA = BM * kStepK, kLdsB = BN * kStepK;
+  static constexpr int kStage = kLdsA + kLdsB;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kLoadsA = BM * 8 / kThreads, kLoadsB = BN * 8 / kThreads;
+  static_assert(kWN == 64 && kWM % 16 == 0, "the epilogue's rows are 64 columns");
+  static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0 && kThreads % 64 == 0, "whole copies");
+  static_assert(kLds <= 160 * 1024, "LDS");
+};
+
+constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor: reads as zero
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, bool kBf16, bool kGrouped>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(I8Args p) {
+  using Cfg = I8Tile<BM, BN, WAVES_M, WAVES_N>;
+  constexpr int WM = Cfg::kWM, WN = Cfg::kWN;
+  constexpr int SUBM = WM / 16, SUBN = WN / 16;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Cfg::kLds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+  const int lr = lane & 15, lk = lane >> 4;
+  const int n_tiles_n = (p.N + BN - 1) / BN;
+  const int tile = xcd_tile(blockIdx.x, gridDim.x);
+
+  int m0, m_end, tm, tn;
+  const uint8_t* bmat = p.b;
+  const float* sbv = p.sb;
+  if constexpr (kGrouped) {
+    // one expert per lane, 64 a round: the first whose running tile count passes the tile
+    int e = -1, before = 0, lo = 0, hi = 0, te = 0;
+    for (int e0 = 0; e0 < p.G; e0 += 64) {
+      const int ee = e0 + lane;
+      int l_lo = 0, l_hi = 0, l_te = 0;
+      if (ee < p.G) {
+        l_lo = min(max(p.m_offsets[ee], 0), p.M);
+        l_hi = min(max(p.m_offsets[ee + 1], l_lo), p.M);
+        l_te = (l_hi - l_lo + BM - 1) / BM;
+      }
+      const int cnt = l_te * n_tiles_n;
+      int incl = cnt;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(incl, d);
+        if (lane >= d) incl += v;
+      }
+      const uint64_t hit = __ballot(ee < p.G && tile < before + incl);
+      if (hit) {
+        const int L = __builtin_ctzll(hit);
+        e = e0 + L;
+        lo = __builtin_amdgcn_readlane(l_lo, L);
+        hi = __builtin_amdgcn_readlane(l_hi, L);
+        te = __builtin_amdgcn_readlane(l_te, L);
+        before += __builtin_amdgcn_readlane(incl - cnt, L);
+        break;
+      }
+      before += __builtin_amdgcn_readlane(incl, 63);
+    }
+    if (e < 0) return;  // the grid is an upper bound
+    band_tile<kBandGrouped>(tile - before, te, n_tiles_n, tm, tn);
+    m0 = lo + tm * BM;
+    m_end = min(m0 + BM, hi);
+    bmat += (int64_t)e * p.N * p.K;
+    sbv += (int64_t)e * p.N;
+  } else {
+    band_tile(tile, (p.M + BM - 1) / BM, n_tiles_n, tm, tn);
+    m0 = tm * BM;
+    m_end = min(m0 + BM, p.M);
+  }
+  const int n0 = tn * BN;
+  const int rows_a = m_end - m0, rows_b = min(BN, p.N - n0);
+  const __amdgpu_buffer_rsrc_t rsrc_a = make_rsrc(p.a + (int64_t)m0 * p.K, (uint32_t)rows_a * (uint32_t)p.K);
+  const __amdgpu_buffer_rsrc_t rsrc_b = make_rsrc(bmat + (int64_t)n0 * p.K, (uint32_t)rows_b * (uint32_t)p.K);
+  const int steps = (p.K + kStepK - 1) / kStepK;
+  const int row0 = tid >> 3, lc0 = (tid & 7) ^ (row0 & 7);
+  const uint32_t off = (uint32_t)row0 * (uint32_t)p.K + lc0 * 16;
+  const uint32_t row_step = (uint32_t)(Cfg::kThreads / 8) * (uint32_t)p.K;
+  const uint32_t off_last = (steps - 1) * kStepK + lc0 * 16 < p.K ? off : kOutside;
+  constexpr int kCopies = Cfg::kLoadsA + Cfg::kLoadsB;
+  auto issue = [&](int q, int g, uint8_t* __restrict__ st) {
+    const uint32_t o = g == steps - 1 ? off_last : off;
+    if (q < Cfg::kLoadsA)
+      load_lds(rsrc_a, st + (q * Cfg::kThreads + wave * 64) * 16, 16, o + q * row_step, g * kStepK);
+    else
+      load_lds(rsrc_b, st + Cfg::kLdsA + ((q - Cfg::kLoadsA) * Cfg::kThreads + wave * 64) * 16, 16,
+               o + (q - Cfg::kLoadsA) * row_step, g * kStepK);
+  };
+
+  v4i acc[SUBM][SUBN];
+#pragma unroll
+  for (int i = 0; i < SUBM; ++i)
+#pragma unroll
+    for (int j = 0; j < SUBN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  const int lane_off[2] = {lr * kStepK + ((lk ^ (lr & 7)) << 4), lr * kStepK + (((4 + lk) ^ (lr & 7)) << 4)};
+  auto step = [&](const uint8_t* __restrict__ cur, uint8_t* __restrict__ nxt, int g) {
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) issue(q, g, nxt);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v4i bf[SUBN];
+#pragma unroll
+      for (int j = 0; j < SUBN; ++j)
+        bf[j] = *(const v4i*)(cur + Cfg::kLdsA + (wn * WN + j * 16) * kStepK + lane_off[h]);
+#pragma unroll
+      for (int i = 0; i < SUBM; ++i) {
+        const v4i af = *(const v4i*)(cur + (wm * WM + i * 16) * kStepK + lane_off[h]);
+#pragma unroll
+        for (int j = 0; j < SUBN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af, acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < kCopies; ++q) issue(q, 0, lds);
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __syncthreads();
+  for (int g = 0; g < steps; ++g) {
+    // past the last step the copies repeat it into a stage that is not read again
+    step(lds + (g & 1) * Cfg::kStage, lds + ((g + 1) & 1) * Cfg::kStage, min(g + 1, steps - 1));
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+  }
+
+  // ---- epilogue: scale, stage the wave's part in its own LDS, store rows ----
+  const int nw = n0 + wn * WN;
+  float sbc[SUBN][4];
+#pragma unroll
+  for (int j = 0; j < SUBN; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = nw + j * 16 + 4 * lk + r;
+      sbc[j][r] = n < p.N && p.K > 0 ? sbv[n] : 0.0f;  // K == 0: no operand is read
+    }
+  constexpr int kEl = kBf16 ? 2 : 4;        // bytes per output
+  constexpr int kRowBytes = WN * kEl;       // 128 or 256
+  constexpr int kChunks = kRowBytes / 16;   // 8 or 16
+  static_assert(Cfg::kThreads / 64 * 16 * kRowBytes <= Cfg::kLds, "staging fits in the stages");
+  uint8_t* st = lds + wave * (16 * kRowBytes);
+  const bool whole = p.N % (16 / kEl) == 0;  // every 16-byte store is aligned and inside its row
+#pragma unroll
+  for (int i = 0; i < SUBM; ++i) {
+    const int gm = m0 + wm * WM + i * 16 + lr;
+    const float sav = gm < m_end && p.K > 0 ? p.sa[gm] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < SUBN; ++j) {
+      float v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = scaled(acc[i][j][r], sav, sbc[j][r]);
+      const int byte = (j * 16 + 4 * lk) * kEl;
+      uint8_t* to = st + lr * kRowBytes + (((byte >> 4) ^ (lr & (kChunks - 1))) << 4) + (byte & 15);
+      if constexpr (kBf16) *(bf16x4*)to = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+      else *(v4f*)to = v4f{v[0], v[1], v[2], v[3]};
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): a wave reads back only its own part
+    __builtin_amdgcn_wave_barrier();
+    constexpr int kRowsAtOnce = 64 / kChunks;
+    const int ch = lane % kChunks;
+#pragma unroll
+    for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
+      const int m = k * kRowsAtOnce + lane / kChunks;
+      const int om = m0 + wm * WM + i * 16 + m;
+      const uint4 v = *(const uint4*)(st + m * kRowBytes + ((ch ^ (m & (kChunks - 1))) << 4));
+      const int n = nw + ch * (16 / kEl);
+      if (om < m_end && n < p.N) {
+        uint8_t* to = (uint8_t*)p.c + ((int64_t)om * p.N + n) * kEl;
+        if (whole) {
+          *(uint4*)to = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int u = 0; u < 16 / kEl; ++u) {
+            if (n + u >= p.N) break;
+            if constexpr (kBf16) ((uint16_t*)to)[u] = (uint16_t)(w[u / 2] >> (16 * (u & 1)));
+            else ((uint32_t*)to)[u] = w[u];
+          }
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: a workgroup owns 16 MB x 16 NB outputs and its W waves split the
+// steps of K between them, each streaming its fragments straight from global
+// memory to registers; the int32 partial blocks are added through LDS. B is
+// read once per 16 MB rows.
+// ---------------------------------------------------------------------------
+template <int MB, int NB, int W, bool kBf16>
+__global__ __launch_bounds__(64 * W) void gemm_i8_few_kernel(I8Args p) {
+  __shared__ __attribute__((aligned(16))) v4i part[W][MB * NB][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lk = lane >> 4;
+  const int n_blocks = (p.N + 16 * NB - 1) / (16 * NB);
+  const int n0 = (blockIdx.x % n_blocks) * 16 * NB;
+  const int m0 = (blockIdx.x / n_blocks) * 16 * MB;
+  const int steps = (p.K + kStepK - 1) / kStepK;
+  const int g_begin = (int)((int64_t)steps * wave / W);
+  const int g_end = (int)((int64_t)steps * (wave + 1) / W);
+  const int rows_a = min(16 * MB, p.M - m0), rows_b = min(16 * NB, p.N - n0);
+  const __amdgpu_buffer_rsrc_t rsrc_a = make_rsrc(p.a + (int64_t)m0 * p.K, (uint32_t)rows_a * (uint32_t)p.K);
+  const __amdgpu_buffer_rsrc_t rsrc_b = make_rsrc(p.b + (int64_t)n0 * p.K, (uint32_t)rows_b * (uint32_t)p.K);
+  const uint32_t off = (uint32_t)lr * (uint32_t)p.K + lk * 16;
+  const uint32_t blk = 16u * (uint32_t)p.K;
+
+  struct Frags {
+    v4i a[MB][2], b[NB][2];
+  };
+  auto load = [&](int g, Frags& f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t o = g * kStepK + h * 64 + lk * 16 < p.K ? off : kOutside;
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        f.b[j][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc_b, o + j * blk, g * kStepK + h * 64, 0));
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+        f.a[i][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc_a, o + i * blk, g * kStepK + h * 64, 0));
+    }
+  };
+  v4i acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  auto compute = [&](const Frags& f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[j][h], f.a[i][h], acc[i][j], 0, 0, 0);
+  };
+  Frags f0, f1;
+  int g = g_begin;
+  if (g < g_end) load(g, f0);
+  for (; g + 1 < g_end; g += 2) {
+    load(g + 1, f1);
+    compute(f0);
+    if (g + 2 < g_end) load(g + 2, f0);
+    compute(f1);
+  }
+  if (g < g_end) compute(f0);
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) part[wave][i * NB + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int u = tid; u < MB * NB * 64; u += 64 * W) {
+    const int b = u >> 6;
+    v4i sum = part[0][b][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum += part[w][b][lane];
+    const int gm = m0 + (b / NB) * 16 + lr;
+    const int gn = n0 + (b % NB) * 16 + 4 * lk;
+    if (gm >= p.M) continue;
+    const float sav = p.K > 0 ? p.sa[gm] : 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (gn + r >= p.N) break;
+      const float v = scaled(sum[r], sav, p.K > 0 ? p.sb[gn + r] : 0.0f);
+      if constexpr (kBf16) ((__bf16*)p.c)[(int64_t)gm * p.N + gn + r] = (__bf16)v;
+      else ((float*)p.c)[(int64_t)gm * p.N + gn + r] = v;
+    }
+  }
+}
+
+hipError_t launch_quant_int8_rows(const void* x, int64_t M, int64_t K, int8_t* q, float* s,
+                                  hipStream_t stream) {
+  // few rows: a whole workgroup each; many: a wavefront each
+  if (M < 4096)
+    hipLaunchKernelGGL(quant_int8_rows_kernel<4>, dim3((unsigned)M), dim3(256), 0, stream,
+                       (const uint4*)x, (int)M, (int)K, (uint4*)q, s);
+  else
+    hipLaunchKernelGGL(quant_int8_rows_kernel<1>, dim3((unsigned)((M + 3) / 4)), dim3(256), 0, stream,
+                       (const uint4*)x, (int)M, (int)K, (uint4*)q, s);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, bool kGrouped>
+static hipError_t launch_tiles(const I8Args& a, bool bf16, int64_t m_tiles, hipStream_t stream) {
+  const dim3 grid((unsigned)(m_tiles * ((a.N + BN - 1) / BN))), block(64 * WAVES_M * WAVES_N);
+  if (bf16)
+    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, WAVES_M, WAVES_N, true, kGrouped>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, WAVES_M, WAVES_N, false, kGrouped>), grid, block, 0, stream, a);
+  return hipGetLastError();
+}
+
+template <int MB, int NB, int W>
+static hipError_t launch_few(const I8Args& a, bool bf16, hipStream_t stream) {
+  const int64_t wgs = (int64_t)((a.M + 16 * MB - 1) / (16 * MB)) * ((a.N + 16 * NB - 1) / (16 * NB));
+  if (bf16)
+    hipLaunchKernelGGL((gemm_i8_few_kernel<MB, NB, W, true>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
+  else
+    hipLaunchKernelGGL((gemm_i8_few_kernel<MB, NB, W, false>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                            void* c, bool bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  const I8Args p{(const uint8_t*)a, sa, (const uint8_t*)b, sb, c, nullptr, (int)M, (int)N, (int)K, 1};
+  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
+  if (big < kCus / 2) {
+    if (M <= 16) return launch_few<1, 1, 8>(p, bf16, stream);
+    return launch_few<4, 2, 8>(p, bf16, stream);
+  }
+  return launch_tiles<256, 256, 2, 4, false>(p, bf16, (M + 255) / 256, stream);
+}
+
+hipError_t launch_int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b,
+                                    const float* sb, void* c, bool bf16, const int32_t* m_offsets,
+                                    int64_t G, int64_t M_total, int64_t N, int64_t K,
+                                    hipStream_t stream) {
+  const I8Args p{(const uint8_t*)a, sa, (const uint8_t*)b, sb, c, m_offsets, (int)M_total, (int)N, (int)K, (int)G};
+  // upper bound on sum_e ceil(rows_e / 256) for rows_e multiples of 128
+  return launch_tiles<256, 256, 2, 4, true>(p, bf16, (M_total / 128 + G + 1) / 2, stream);
+}
+
+}  // namespace fp8q

@@ -1,0 +1,346 @@
+// Rows sorted by expert and back, for gfx950: the copy of the tokens' rows
+// into the padded per-expert layout (permute), the weighted sum back to tokens
+// (combine) and that sum's gradient (combine_bwd).
+//
+//   xp[row_of_slot[t, j], :] = x[t, :]
+//   y[t, :] = sum_j w[t, j] c[row_of_slot[t, j], :]
+//   dc[row_of_slot[t, j], :] = w[t, j] dy[t, :],  dw[t, j] = <dy[t, :], c[row_of_slot[t, j], :]>
+//
+// All three move rows and do almost no arithmetic: they are bound by HBM.
+// Rows are handled in chunks of 8 values, one chunk per lane (16 bytes of
+// bfloat16, 32 of float32).
+#include "common.hpp"
+#include "wave.hpp"
+
+namespace fp8q {
+
+constexpr int kTokWaves = 4;  // wavefronts per workgroup
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// 8 values of a row: kept as loaded (Raw), and as floats
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {  // bfloat16
+  struct Raw { u32x4 v; };
+  static constexpr int kBytes = 16;
+  static __device__ __forceinline__ Raw load(const void* p) { return {*(const u32x4*)p}; }
+  static __device__ __forceinline__ Raw load_nt(const void* p) {
+    return {__builtin_nontemporal_load((const u32x4*)p)};
+  }
+  static __device__ __forceinline__ Raw zero() { return {u32x4{0, 0, 0, 0}}; }
+  template <bool kNt>
+  static __device__ __forceinline__ void store(void* p, Raw r) {
+    if constexpr (kNt) __builtin_nontemporal_store(r.v, (u32x4*)p);
+    else *(u32x4*)p = r.v;
+  }
+  static __device__ __forceinline__ void floats(Raw r, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(r.v[i]), f[2 * i + 1] = bf16_hi(r.v[i]);
+  }
+  static __device__ __forceinline__ Raw round(const float (&f)[8]) {
+    bf16x8 b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = (__bf16)f[i];
+    return {__builtin_bit_cast(u32x4, b)};
+  }
+};
+template <>
+struct Chunk<float> {
+  struct Raw { u32x4 v, w; };
+  static constexpr int kBytes = 32;
+  static __device__ __forceinline__ Raw load(const void* p) {
+    return {((const u32x4*)p)[0], ((const u32x4*)p)[1]};
+  }
+  static __device__ __forceinline__ Raw load_nt(const void* p) {
+    return {__builtin_nontemporal_load((const u32x4*)p), __builtin_nontemporal_load((const u32x4*)p + 1)};
+  }
+  static __device__ __forceinline__ Raw zero() { return {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}}; }
+  template <bool kNt>
+  static __device__ __forceinline__ void store(void* p, Raw r) {
+    if constexpr (kNt) {
+      __builtin_nontemporal_store(r.v, (u32x4*)p);
+      __builtin_nontemporal_store(r.w, (u32x4*)p + 1);
+    } else {
+      ((u32x4*)p)[0] = r.v;
+      ((u32x4*)p)[1] = r.w;
+    }
+  }
+  static __device__ __forceinline__ void floats(Raw r, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r.v[i]), f[4 + i] = __uint_as_float(r.w[i]);
+  }
+  static __device__ __forceinline__ Raw round(const float (&f)[8]) {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = __float_as_uint(f[i]), r.w[i] = __float_as_uint(f[4 + i]);
+    return r;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// permute: one wavefront per token copies its row to the rows of its valid
+// slots; further wavefronts, one per possible padding row (127 per expert),
+// zero the padding rows.
+// ---------------------------------------------------------------------------
+template <typename T, bool kNt>
+__global__ __launch_bounds__(64 * kTokWaves) void permute_copy_kernel(
+    const uint8_t* __restrict__ x, const int32_t* __restrict__ row_of_slot,
+    const int32_t* __restrict__ m_offsets, const int32_t* __restrict__ counts, int n_tok, int K,
+    int topk, int G, uint8_t* __restrict__ xp) {
+  using C = Chunk<T>;
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * kTokWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n_chunks = K / 8;
+  const int64_t row_bytes = (int64_t)n_chunks * C::kBytes;
+  if (t >= n_tok) {
+    const int64_t pi = t - n_tok;
+    const int e = (int)(pi / (kGroup - 1));
+    if (e >= G) return;
+    const int64_t row = (int64_t)m_offsets[e] + counts[e] + pi % (kGroup - 1);
+    if (row >= m_offsets[e + 1]) return;
+    for (int c = lane; c < n_chunks; c += 64) C::template store<kNt>(xp + row * row_bytes + c * C::kBytes, C::zero());
+    return;
+  }
+  const uint8_t* xr = x + t * row_bytes;
+  constexpr int kHeld = 4;  // chunks of the row a lane holds at a time
+  for (int c0 = lane; c0 < n_chunks; c0 += 64 * kHeld) {
+    typename C::Raw v[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (c0 + 64 * u < n_chunks) v[u] = C::load_nt(xr + (int64_t)(c0 + 64 * u) * C::kBytes);
+    for (int j = 0; j < topk; ++j) {
+      const int row = row_of_slot[t * topk + j];
+      if (row < 0) continue;
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (c0 + 64 * u < n_chunks)
+          C::template store<kNt>(xp + row * row_bytes + (int64_t)(c0 + 64 * u) * C::kBytes, v[u]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// combine: one wavefront per token and run of 64 chunks. All rows of a batch
+// of 8 choices are in flight together.
+// ---------------------------------------------------------------------------
+template <typename Tin, typename Tout>
+__global__ __launch_bounds__(64 * kTokWaves) void combine_kernel(
+    const uint8_t* __restrict__ c, const int32_t* __restrict__ row_of_slot,
+    const float* __restrict__ weights, int n_tok, int K, int topk, int M, int n_runs,
+    uint8_t* __restrict__ y) {
+  using CI = Chunk<Tin>;
+  using CO = Chunk<Tout>;
+  const int lane = threadIdx.x & 63;
+  const int64_t task = (int64_t)blockIdx.x * kTokWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = task / n_runs;
+  if (t >= n_tok) return;
+  const int n_chunks = K / 8;
+  const int chunk = (int)(task - t * n_runs) * 64 + lane;
+  const bool have = chunk < n_chunks;
+  const uint8_t* col = c + (int64_t)chunk * CI::kBytes;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  constexpr int kBatch = 8;
+  for (int j0 = 0; j0 < topk; j0 += kBatch) {
+    int row[kBatch];
+    float w[kBatch];
+    typename CI::Raw v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      row[u] = -1;
+      w[u] = 1.0f;
+      if (j0 + u < topk) {
+        const int64_t slot = t * topk + j0 + u;
+        row[u] = row_of_slot[slot];
+        if (weights) w[u] = weights[slot];
+        if (row[u] >= M) row[u] = -1;
+      }
+      if (row[u] >= 0 && have) v[u] = CI::load_nt(col + (int64_t)row[u] * n_chunks * CI::kBytes);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (row[u] < 0) continue;  // wave-uniform
+      float f[8];
+      CI::floats(v[u], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[u], f[i], acc[i]);
+    }
+  }
+  if (have) CO::template store<false>(y + (t * n_chunks + chunk) * CO::kBytes, CO::round(acc));
+}
+
+// ---------------------------------------------------------------------------
+// combine_bwd: one workgroup per token. dy's row is read once per batch of 8
+// choices; each choice's row of c is read once, its dot product summed over
+// the workgroup in a fixed order, and its row of dc written. Workgroups past
+// the tokens', one per expert, zero the padding rows of their block: those
+// past the last row that any slot maps into it.
+// ---------------------------------------------------------------------------
+template <typename Ty, typename Tc, bool kDw>
+__global__ __launch_bounds__(64 * kTokWaves) void combine_bwd_kernel(
+    const uint8_t* __restrict__ dy, const uint8_t* __restrict__ c,
+    const int32_t* __restrict__ row_of_slot, const float* __restrict__ weights,
+    const int32_t* __restrict__ m_offsets, int n_tok, int K, int topk, int M,
+    uint8_t* __restrict__ dc, float* __restrict__ dw) {
+  using CY = Chunk<Ty>;
+  using CC = Chunk<Tc>;
+  constexpr int kThreads = 64 * kTokWaves;
+  constexpr int kBatch = 8;
+  __shared__ float part[kTokWaves][kBatch];
+  __shared__ int last_of_wave[kTokWaves];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n_chunks = K / 8;
+  const int64_t rb = (int64_t)n_chunks * CC::kBytes;
+  if ((int)blockIdx.x >= n_tok) {
+    const int e = blockIdx.x - n_tok;
+    const int lo = min(max(m_offsets[e], 0), M);
+    const int hi = min(max(m_offsets[e + 1], lo), M);
+    if (hi == lo) return;
+    int last = lo - 1;
+    for (int64_t s = tid; s < (int64_t)n_tok * topk; s += kThreads) {
+      const int r = row_of_slot[s];
+      if (r >= lo && r < hi) last = max(last, r);
+    }
+    last = (int)wave_max_u32((uint32_t)(last + 1)) - 1;
+    if (lane == 0) last_of_wave[wave] = last;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTokWaves; ++w) last = max(last, last_of_wave[w]);
+    for (int64_t i = (int64_t)(last + 1) * n_chunks + tid; i < (int64_t)hi * n_chunks; i += kThreads)
+      CC::template store<false>(dc + i * CC::kBytes, CC::zero());
+    return;
+  }
+  const int64_t t = blockIdx.x;
+  for (int j0 = 0; j0 < topk; j0 += kBatch) {
+    int row[kBatch];
+    float w[kBatch], dot[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      row[u] = -1;
+      w[u] = 1.0f;
+      dot[u] = 0.0f;
+      if (j0 + u < topk) {
+        const int64_t slot = t * topk + j0 + u;
+        row[u] = row_of_slot[slot];
+        if (weights) w[u] = weights[slot];
+        if (row[u] >= M) row[u] = -1;
+      }
+    }
+    for (int ch = tid; ch < n_chunks; ch += kThreads) {
+      typename CC::Raw v[kBatch];
+      if constexpr (kDw) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (row[u] >= 0) v[u] = CC::load_nt(c + (int64_t)row[u] * rb + (int64_t)ch * CC::kBytes);
+      }
+      float g[8];
+      CY::floats(CY::load(dy + (t * n_chunks + ch) * CY::kBytes), g);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (row[u] < 0) continue;  // wave-uniform
+        float f[8];
+        if constexpr (kDw) {
+          CC::floats(v[u], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[u] = __builtin_fmaf(g[i], f[i], dot[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = w[u] * g[i];
+        CC::template store<true>(dc + (int64_t)row[u] * rb + (int64_t)ch * CC::kBytes, CC::round(f));
+      }
+    }
+    if constexpr (kDw) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float s = wave_sum_f32(dot[u]);
+        if (lane == 0) part[wave][u] = s;
+      }
+      __syncthreads();
+      if (tid < kBatch && j0 + tid < topk) {
+        float s = part[0][tid];
+#pragma unroll
+        for (int v = 1; v < kTokWaves; ++v) s += part[v][tid];
+        dw[t * topk + j0 + tid] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+hipError_t launch_moe_dispatch(const void* x, const int32_t* ids, int64_t T, int64_t K, int64_t k,
+                               int64_t G, uint8_t* q, float* sa, int32_t* m_offsets,
+                               int32_t* row_of_slot, void* workspace, hipStream_t stream);
+int64_t dispatch_blocks(int64_t slots);
+
+hipError_t launch_moe_permute(const void* x, bool bf16, const int32_t* ids, int64_t T, int64_t K,
+                              int64_t topk, int64_t G, void* xp, int32_t* m_offsets,
+                              int32_t* row_of_slot, void* workspace, hipStream_t stream) {
+  hipError_t err = launch_moe_dispatch(nullptr, ids, T, 0, topk, G, nullptr, nullptr, m_offsets,
+                                       row_of_slot, workspace, stream);
+  if (err != hipSuccess || T == 0 || K == 0) return err;
+  // the dispatch leaves every expert's count behind its histogram and bases
+  const int32_t* counts = (const int32_t*)workspace + 2 * dispatch_blocks(T * topk) * G;
+  const int64_t waves = T + (kGroup - 1) * G;
+  const dim3 grid((unsigned)((waves + kTokWaves - 1) / kTokWaves)), block(64 * kTokWaves);
+  // rows larger than the 256 MB Infinity Cache cannot stay there for their reader
+  const bool nt = T * topk * K * (bf16 ? 2 : 4) > (int64_t(256) << 20);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, row_of_slot, m_offsets,
+                       counts, (int)T, (int)K, (int)topk, (int)G, (uint8_t*)xp);
+  };
+  if (bf16)
+    nt ? go(permute_copy_kernel<uint16_t, true>) : go(permute_copy_kernel<uint16_t, false>);
+  else
+    nt ? go(permute_copy_kernel<float, true>) : go(permute_copy_kernel<float, false>);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const void* c, bool c_bf16, const int32_t* row_of_slot,
+                              const float* weights, int64_t T, int64_t K, int64_t topk, int64_t M,
+                              void* y, bool y_bf16, hipStream_t stream) {
+  const int64_t n_runs = (K / 8 + 63) / 64;
+  const dim3 grid((unsigned)((T * n_runs + kTokWaves - 1) / kTokWaves)), block(64 * kTokWaves);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)c, row_of_slot, weights,
+                       (int)T, (int)K, (int)topk, (int)M, (int)n_runs, (uint8_t*)y);
+  };
+  if (c_bf16)
+    y_bf16 ? go(combine_kernel<uint16_t, uint16_t>) : go(combine_kernel<uint16_t, float>);
+  else
+    y_bf16 ? go(combine_kernel<float, uint16_t>) : go(combine_kernel<float, float>);
+  return hipGetLastError();
+}
+
+template <typename Ty, typename Tc>
+static void go_combine_bwd(dim3 grid, hipStream_t stream, const void* dy, const void* c,
+                           const int32_t* rows, const float* weights, const int32_t* m_offsets,
+                           int64_t T, int64_t K, int64_t topk, int64_t M, void* dc, float* dw) {
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * kTokWaves), 0, stream, (const uint8_t*)dy,
+                       (const uint8_t*)c, rows, weights, m_offsets, (int)T, (int)K, (int)topk,
+                       (int)M, (uint8_t*)dc, dw);
+  };
+  dw ? go(combine_bwd_kernel<Ty, Tc, true>) : go(combine_bwd_kernel<Ty, Tc, false>);
+}
+
+hipError_t launch_moe_combine_bwd(const void* dy, bool dy_bf16, const void* c, bool c_bf16,
+                                  const int32_t* row_of_slot, const float* weights,
+                                  const int32_t* m_offsets, int64_t T, int64_t K, int64_t topk,
+                                  int64_t G, int64_t M, void* dc, float* dw, hipStream_t stream) {
+  const dim3 grid((unsigned)(T + G));
+  if (dy_bf16)
+    c_bf16 ? go_combine_bwd<uint16_t, uint16_t>(grid, stream, dy, c, row_of_slot, weights, m_offsets, T, K, topk, M, dc, dw)
+           : go_combine_bwd<uint16_t, float>(grid, stream, dy, c, row_of_slot, weights, m_offsets, T, K, topk, M, dc, dw);
+  else
+    c_bf16 ? go_combine_bwd<float, uint16_t>(grid, stream, dy, c, row_of_slot, weights, m_offsets, T, K, topk, M, dc, dw)
+           : go_combine_bwd<float, float>(grid, stream, dy, c, row_of_slot, weights, m_offsets, T, K, topk, M, dc, dw);
+  return hipGetLastError();
+}
+
+}  // namespace fp8q

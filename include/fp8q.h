@@ -447,6 +447,177 @@ FP8Q_API int fp8q_transpose_weight_128x128(const uint8_t* q, const float* sb, in
 FP8Q_API int fp8_gemm_rowscaled(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
                                 void* c, int out_dtype, int64_t M, int64_t N, int64_t K, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * MoE layer around the experts' products: the router, rows sorted by expert
+ * in the grouped GEMM's padded layout, and the way back, each with its
+ * gradient. Same source as the dispatch: the paragraph on the combine and
+ * dispatch components of "Six Reasons Deepseek Ai Is A Waste Of Time".
+ *
+ * Element types are named by fp8q_out_dtype (FP8Q_OUT_F32, FP8Q_OUT_BF16).
+ * Sums are formed in binary32 or wider and rounded once. Every entry point is
+ * deterministic (no floating-point atomics) and allocates nothing.
+ * ---------------------------------------------------------------------------
+ */
+
+typedef enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 } fp8q_score;
+
+/*
+ * Router: expert ids and weights of every token from its logits.
+ *   p[t, e] = softmax over e of logits[t, :], or 1 / (1 + exp(-logits[t, e]));
+ *   z[t, e] = p[t, e] + bias[e]       (bias steers the choice, not the weight)
+ *   n_groups > 1: the experts form n_groups runs of G / n_groups; a group's
+ *     score is the sum of its two largest z, and only experts of the
+ *     topk_groups best groups may be chosen;
+ *   topk_ids[t, :] = the topk experts with the largest z, largest first;
+ *   weights[t, j] = scale * p[t, id_j], divided by sum_j p[t, id_j] when
+ *     renormalize is 1 (0 when that sum is 0).
+ * Ties go to the lowest index, for groups as for experts. All of it is
+ * computed in float64, so that the choice between nearly equal experts does
+ * not depend on rounding; weights are rounded once to binary32.
+ *
+ * An expert whose logit is -infinity or NaN (or whose bias is) has p = 0 and
+ * is never chosen. When fewer than topk experts can be chosen, the remaining
+ * choices are -1 with weight 0 (fp8q_moe_dispatch_1x128, fp8q_moe_permute
+ * drop those, and the other calls skip them). Logits of +infinity are outside
+ * the contract (ids stay in range).
+ *
+ *   logits   : in,  T x G, float32 (4-byte aligned) or bfloat16 (2-byte)
+ *   bias     : in,  G float32, or NULL for none
+ *   topk_ids : out, T x topk int32;   weights : out, T x topk float32
+ * 1 <= G <= 1024, 1 <= topk <= 64, 1 <= topk_groups <= n_groups <= 64,
+ * G % n_groups == 0, topk <= topk_groups * (G / n_groups), scale finite.
+ * T == 0 is a no-op. One kernel.
+ */
+FP8Q_API int fp8q_moe_route(const void* logits, int dtype, const float* bias, int64_t T, int64_t G,
+                            int64_t topk, int64_t n_groups, int64_t topk_groups, int score,
+                            int renormalize, float scale, int32_t* topk_ids, float* weights,
+                            void* stream);
+
+/*
+ * Gradient of fp8q_moe_route's weights with respect to the logits, the ids
+ * held fixed (the choice itself has no gradient, nor has the bias):
+ *   dlogits[t, e] = sum_j dweights[t, j] * d weights[t, j] / d logits[t, e].
+ * Choices outside [0, G) are skipped; an expert listed twice counts twice.
+ * Masked logits (-infinity, NaN) get 0. Computed in float64, rounded once.
+ *
+ *   logits, dtype, T, G, topk, score, renormalize, scale: as in the forward call
+ *   topk_ids : in, T x topk int32;  dweights : in, T x topk float32
+ *   dlogits  : out, T x G, of the logits' type; every element is written.
+ *              It may not overlap logits.
+ */
+FP8Q_API int fp8q_moe_route_bwd(const void* logits, int dtype, const int32_t* topk_ids,
+                                const float* dweights, int64_t T, int64_t G, int64_t topk,
+                                int score, int renormalize, float scale, void* dlogits,
+                                void* stream);
+
+/*
+ * Rows sorted by expert: fp8q_moe_dispatch_1x128 without the quantization.
+ * Same slots, counts, m_offsets, row_of_slot and padding; row r of xp is x's
+ * row of the token it belongs to, bit for bit; padding rows are zero; rows
+ * from m_offsets[G] to M_cap are not written. The gradient of x is
+ * fp8q_moe_combine of xp's gradient with weights == NULL.
+ *
+ *   x    : in,  T x K of `dtype`, 16-byte aligned
+ *   xp   : out, M_cap x K of `dtype`, 16-byte aligned; M_cap as for the dispatch
+ *   topk_ids, m_offsets, row_of_slot, workspace: as for the dispatch
+ *          (fp8q_moe_dispatch_workspace_bytes, fp8q_moe_dispatch_max_rows)
+ * Requires K % 8 == 0, topk >= 1, 1 <= G <= 1024. T == 0 writes m_offsets
+ * (all zero); K == 0 writes m_offsets and row_of_slot only.
+ */
+FP8Q_API int fp8q_moe_permute(const void* x, int dtype, const int32_t* topk_ids, int64_t T,
+                              int64_t K, int64_t topk, int64_t G, void* xp, int64_t M_cap,
+                              int32_t* m_offsets, int32_t* row_of_slot, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/*
+ * The way back: y[t, :] = sum over j of weights[t, j] * c[row_of_slot[t, j], :],
+ * in binary32 with one fused multiply-add per term, j ascending, rounded once
+ * to y's type. A slot whose row is not in [0, M) contributes nothing (a token
+ * without valid slots gets zeros); the values of other rows (padding, rows of
+ * dropped slots) are never read. weights == NULL means all ones.
+ *
+ *   c           : in,  M x K of c_dtype, 16-byte aligned
+ *   row_of_slot : in,  DEVICE int32 T x topk;  weights : in, T x topk float32 or NULL
+ *   y           : out, T x K of y_dtype, 16-byte aligned; may not overlap c
+ * Requires K % 8 == 0, topk >= 1. T == 0 or K == 0 is a no-op. One kernel.
+ */
+FP8Q_API int fp8q_moe_combine(const void* c, int c_dtype, const int32_t* row_of_slot,
+                              const float* weights, int64_t T, int64_t K, int64_t topk, int64_t M,
+                              void* y, int y_dtype, void* stream);
+
+/*
+ * Gradient of fp8q_moe_combine, in one pass over the rows:
+ *   dc[row_of_slot[t, j], :] = weights[t, j] * dy[t, :]   (rounded once to c's type)
+ *   dw[t, j] = sum over k of dy[t, k] * c[row_of_slot[t, j], k]   (binary32)
+ * A slot whose row is not in [0, M) writes no row and gets dw = 0. In every
+ * expert's block [m_offsets[e], m_offsets[e+1]) the rows past the block's
+ * last mapped row are padding and are set to zero, so that a weight-gradient
+ * product may read whole blocks; rows from m_offsets[G] on are not written.
+ * The map must be the one of fp8q_moe_permute or fp8q_moe_dispatch_1x128
+ * (rows distinct); m_offsets are clamped to [0, M].
+ *
+ *   dy : in, T x K of dy_dtype;  c : in, M x K of c_dtype;  both 16-byte aligned
+ *   weights : in, T x topk float32, or NULL for ones
+ *   dc : out, M x K of c_dtype, 16-byte aligned; may not overlap c or dy
+ *   dw : out, T x topk float32, or NULL when it is not wanted (c is then not
+ *        read and may be NULL)
+ * Requires K % 8 == 0, topk >= 1, 1 <= G <= 1024. T == 0 still zeroes the
+ * blocks. K == 0 writes dw = 0 only. One kernel.
+ */
+FP8Q_API int fp8q_moe_combine_bwd(const void* dy, int dy_dtype, const void* c, int c_dtype,
+                                  const int32_t* row_of_slot, const float* weights,
+                                  const int32_t* m_offsets, int64_t T, int64_t K, int64_t topk,
+                                  int64_t G, int64_t M, void* dc, float* dw, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit integer product with one scale per token and one per output channel:
+ * the coarser-grained counterpart of the block-scaled FP8 GEMM, for layers
+ * served with INT8 weights. The scale rule is the standard-practice paragraph
+ * of "Six Reasons Deepseek Ai Is A Waste Of Time" (the largest magnitude maps
+ * to the largest representable value) applied to whole rows.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Symmetric 8-bit quantization of whole rows (tokens of an activation, output
+ * channels of an N x K weight; G experts' weights are G * N rows).
+ *   amax = max |x[m, :]|, s[m] = fl32(amax / 127),
+ *   q[m, k] = clamp(RNE(fl32(x[m, k] / s[m])), -127, 127);
+ * a zero row has scale 0 and zero codes.
+ *   x_bf16 : in,  M x K bfloat16, 16-byte aligned
+ *   q      : out, M x K int8, 16-byte aligned;   s : out, M float32
+ * Requires K % 16 == 0. M == 0 is a no-op; K == 0 writes zero scales.
+ */
+FP8Q_API int fp8q_quant_int8_rows(const void* x_bf16, int64_t M, int64_t K, int8_t* q, float* s,
+                                  void* stream);
+
+/*
+ * c[m, n] = fl(fl32(fl32(sum_k a[m, k] b[n, k]) * sa[m]) * sb[n]): the sum is
+ * exact (int32), each product is rounded to binary32 and the result, for
+ * bfloat16 outputs, once more.
+ *   a  : in, M x K int8 (any value), 16-byte aligned;  sa : in, M float32
+ *   b  : in, N x K int8, 16-byte aligned;              sb : in, N float32
+ *   c  : out, M x N, float32 or bfloat16 per out_dtype, 16-byte aligned
+ * Requires K % 16 == 0 and K <= 131056 (sums stay below 2^31); M and N are
+ * arbitrary. M == 0 or N == 0 is a no-op; K == 0 writes zeros (no operand is
+ * read, a, sa, b, sb may then be NULL).
+ */
+FP8Q_API int int8_gemm_scaled(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                              void* c, int out_dtype, int64_t M, int64_t N, int64_t K,
+                              void* stream);
+
+/*
+ * Grouped (MoE) form: expert e owns rows [m_offsets[e], m_offsets[e+1]) of a,
+ * sa and c, with its own weights b[e] (N x K) and channel scales sb[e] (N).
+ * m_offsets, M_total and the rows that are neither read nor written: as for
+ * fp8_gemm_grouped (entries multiples of 128, M_total % 128 == 0).
+ */
+FP8Q_API int int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                               void* c, int out_dtype, const int32_t* m_offsets, int64_t G,
+                               int64_t M_total, int64_t N, int64_t K, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

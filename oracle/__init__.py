@@ -39,6 +39,9 @@ Modules:
   accsim   limited-precision accumulator model for the K = 4096 demonstration.
   norm     RMS / layer normalization whose binary32 output feeds the 1x128 cast.
   moe      FP8 dispatch: quantize tokens, permute into the padded per-expert layout.
+  route    MoE router (scores, groups, top-k, weights) and its gradient.
+  tokens   rows sorted by expert, the weighted way back and its gradient.
+  int8     8-bit row quantization and the 8-bit integer product.
 """
 
 from . import e4m3, bf16, quant, gemm, accsim  # noqa: F401

@@ -1,0 +1,183 @@
+"""GPU row quantization and 8-bit integer products against the oracle, bit for bit
+(every step is a defined binary32 rounding; bfloat16 outputs are those, rounded once)."""
+
+import numpy as np
+import pytest
+
+from conftest import gpu_available
+from fp8_fine_grained_online_amd import synthetic as S
+from oracle import int8
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+
+def codes(shape, seed):
+    """All 256 values, -128 among them."""
+    return S.rng_for(seed, 0).integers(-128, 128, shape).astype(np.int8)
+
+
+def scales(shape, seed):
+    return (0.001 + S.rng_for(seed, 1).random(shape)).astype(np.float32)
+
+
+def dev(a):
+    import torch
+    return torch.from_numpy(a).cuda()
+
+
+def rounded(f32, out):
+    import torch
+    t = torch.from_numpy(f32)
+    return t if out == "f32" else t.to(torch.bfloat16)
+
+
+def same(got, want):
+    import torch
+    got = got.cpu()
+    assert got.dtype == want.dtype and got.shape == want.shape
+    bad = (got.double() != want.double()) & ~(torch.isnan(got) & torch.isnan(want))
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 7168), (3, 48), (33, 2064), (5, 32768), (2, 65552), (4100, 112),
+                                 (4097, 8208), (4096, 16), (7, 131072)])
+def test_quant_rows(M, K):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    rng = S.rng_for(2700 + M, K)
+    x = torch.from_numpy(rng.standard_normal((M, K), dtype=np.float32)).to(torch.bfloat16)
+    x[:, 3] *= 100
+    x[M // 2] = 0                                  # a row of nothing
+    x[0] *= 2.0 ** -120                            # a subnormal scale
+    if M > 2:
+        x[1] = torch.where(torch.arange(K) % 2 == 0, 1.0, 0.5)  # 63.5: ties
+        x[2] *= 2.0 ** 118
+    q = torch.full((M, K), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((M,), float("nan"), device="cuda")
+    F.fp8q_quant_int8_rows(x.cuda(), q=q, s=s)
+    want_q, want_s = int8.quant_rows(x.float().numpy())
+    assert np.array_equal(s.cpu().numpy(), want_s)
+    assert np.array_equal(q.cpu().numpy(), want_q)
+
+
+def test_quant_every_value_under_every_maximum():
+    """One binade of maxima (128 significands) by all smaller bfloat16 values down to codes of zero."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    for field in (127, 1, 0, 254):
+        rows = S.exhaustive_tiles(field, depth=10)
+        x = torch.from_numpy(rows.view(np.int16)).view(torch.bfloat16)
+        q, s = F.fp8q_quant_int8_rows(x.cuda())
+        want_q, want_s = int8.quant_rows(x.float().numpy())
+        assert np.array_equal(s.cpu().numpy(), want_s)
+        assert np.array_equal(q.cpu().numpy(), want_q)
+
+
+def test_quant_weights_of_experts():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = torch.from_numpy(S.rng_for(2710, 0).standard_normal((3, 40, 64), dtype=np.float32)).to(torch.bfloat16).cuda()
+    q, s = F.fp8q_quant_int8_rows(x)
+    assert q.shape == (3, 40, 64) and s.shape == (3, 40)
+    q2, s2 = F.fp8q_quant_int8_rows(x.reshape(120, 64))
+    assert torch.equal(q.reshape(120, 64), q2) and torch.equal(s.reshape(-1), s2)
+
+
+DENSE = [(1, 1, 16), (1, 7168, 1024), (2, 33, 48), (16, 100, 4112), (17, 129, 128), (64, 65, 256), (100, 2050, 272),
+         (129, 257, 144), (333, 514, 2064), (1000, 31, 640), (1, 64, 131056), (520, 520, 144), (260, 4100, 96),
+         (1500, 3000, 400), (2049, 4097, 128), (4100, 2056, 272)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_dense(M, N, K, out):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    a, b = codes((M, K), 2720 + M), codes((N, K), 2721 + N)
+    sa, sb = scales(M, 2722), scales(N, 2723)
+    sa[M // 2] = 0  # a zero row's scale
+    c = torch.full((M, N), float("nan"), dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    F.int8_gemm_scaled(dev(a), dev(sa), dev(b), dev(sb), out, c=c)
+    same(c, rounded(int8.gemm(a, sa, b, sb), out))
+
+
+def test_largest_sums():
+    """-128 by -128 over the largest K: 2^14 * 131056 < 2^31."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    K = 131056
+    for M, N in ((3, 5), (2100, 4100)):
+        a = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+        b = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+        c = F.int8_gemm_scaled(a, torch.ones(M, device="cuda"), b, torch.ones(N, device="cuda"), "f32")
+        assert (c == float(np.float32(16384 * K))).all()
+
+
+def test_empty_sizes():
+    import torch
+    import fp8_fine_grained_online_amd as F
+
+    def z(*shape, dtype=torch.int8):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+    f = torch.float32
+    assert F.int8_gemm_scaled(z(0, 64), z(0, dtype=f), z(5, 64), z(5, dtype=f)).shape == (0, 5)
+    assert F.int8_gemm_scaled(z(4, 64), z(4, dtype=f), z(0, 64), z(0, dtype=f)).shape == (4, 0)
+    for M, N in ((4, 5), (3000, 3000)):
+        c = torch.full((M, N), float("nan"), device="cuda")
+        F.int8_gemm_scaled(z(M, 0), torch.ones(M, device="cuda"), z(N, 0), torch.ones(N, device="cuda"), "f32", c=c)
+        assert not c.any()
+    q, s = F.fp8q_quant_int8_rows(z(4, 0, dtype=torch.bfloat16))
+    assert q.shape == (4, 0) and not s.any()
+
+
+GROUPED = [([128], 64, 64), ([0, 128, 0], 100, 48), ([128, 384, 256, 0], 257, 272), ([256] * 5, 514, 1040),
+           ([128] * 40, 128, 144), ([1024, 128, 2048], 300, 128), ([0, 0], 64, 64), ([128] * 70 + [256], 96, 64)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,N,K", GROUPED, ids=[f"{len(r)}x{sum(r)}_{n}_{k}" for r, n, k in GROUPED])
+def test_grouped(rows, N, K, out):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    G, M = len(rows), sum(rows) + 256  # rows behind the last block
+    off = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    a, b = codes((M, K), 2730 + G), codes((G, N, K), 2731 + G)
+    sa, sb = scales(M, 2732), scales((G, N), 2733)
+    c = torch.full((M, N), float("nan"), dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    F.int8_gemm_grouped(dev(a), dev(sa), dev(b), dev(sb), dev(off), out, c=c)
+    same(c, rounded(int8.gemm_grouped(a, sa, b, sb, off), out))  # NaN where nothing is written
+
+
+def test_grouped_without_k():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    off = torch.tensor([0, 128, 256], dtype=torch.int32, device="cuda")
+    c = torch.full((384, 70), 5.0, device="cuda")
+    F.int8_gemm_grouped(torch.zeros((384, 0), dtype=torch.int8, device="cuda"), torch.ones(384, device="cuda"),
+                        torch.zeros((2, 70, 0), dtype=torch.int8, device="cuda"), torch.ones((2, 70), device="cuda"),
+                        off, "f32", c=c)
+    assert not c[:256].any() and (c[256:] == 5).all()
+
+
+def test_refusals():
+    import torch
+    import fp8_fine_grained_online_amd as F
+
+    def z(*shape, dtype=torch.int8):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+    f = torch.float32
+    with pytest.raises(F.Fp8qError):
+        F.int8_gemm_scaled(z(4, 40), z(4, dtype=f), z(5, 40), z(5, dtype=f))  # K % 16
+    with pytest.raises(ValueError):
+        F.int8_gemm_scaled(z(4, 64), z(3, dtype=f), z(5, 64), z(5, dtype=f))
+    with pytest.raises(ValueError):
+        F.int8_gemm_scaled(z(4, 64), z(4, dtype=f), z(5, 32), z(5, dtype=f))
+    with pytest.raises(TypeError):
+        F.int8_gemm_scaled(z(4, 64, dtype=torch.uint8), z(4, dtype=f), z(5, 64), z(5, dtype=f))
+    with pytest.raises(ValueError):
+        F.int8_gemm_scaled(z(4, 64), z(4, dtype=f), z(5, 64), z(5, dtype=f), out_dtype="f16")
+    with pytest.raises(TypeError):
+        F.fp8q_quant_int8_rows(z(4, 64))
+    with pytest.raises(ValueError):
+        F.int8_gemm_grouped(z(128, 64), z(128, dtype=f), z(2, 5, 64), z(2, 4, dtype=f),
+                            torch.zeros(3, dtype=torch.int32, device="cuda"))

@@ -1,0 +1,149 @@
+"""GPU router and its gradient against the float64 oracle: ids equal, weights and
+gradients within the one rounding to the output type."""
+
+import numpy as np
+import pytest
+
+from conftest import gpu_available
+from fp8_fine_grained_online_amd import synthetic as S
+from oracle import route
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}  # half a step, relative
+TINY = 2.0 ** -149                              # and of a subnormal, absolute (binary32)
+
+
+def logits_of(T, G, dtype, seed, ties=False, masked=0.0):
+    import torch
+    rng = S.rng_for(seed, 0)
+    x = 1.5 * rng.standard_normal((T, G))
+    if ties:
+        x = np.round(x)  # many equal scores
+    if masked:
+        x[rng.random((T, G)) < masked] = -np.inf
+    t = torch.from_numpy(x).to(torch.float32 if dtype == "f32" else torch.bfloat16).cuda()
+    return t, t.double().cpu().numpy()
+
+
+def check(x_dev, x, topk, bias=None, **kw):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    b = None if bias is None else torch.from_numpy(bias).float().cuda()
+    T = x.shape[0]
+    ids = torch.full((T, topk), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, topk), float("nan"), device="cuda")
+    F.fp8q_moe_route(x_dev, topk, bias=b, topk_ids=ids, weights=w, **kw)
+    want_ids, want_w = route.route(x, topk, None if b is None else b.double().cpu().numpy(), **kw)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    got = w.double().cpu().numpy()
+    # float64 arithmetic (a few hundred roundings of 2^-53 at most), then one rounding to binary32
+    assert np.all(np.abs(got - want_w) <= np.abs(want_w) * (HALF["f32"] + 2.0 ** -44) + TINY)
+    return ids, want_ids
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("T,G,topk,dtype", [(1, 1, 1, "f32"), (1, 256, 8, "f32"), (7, 63, 6, "bf16"),
+                                            (33, 65, 10, "f32"), (130, 128, 64, "bf16"), (5, 1024, 8, "f32"),
+                                            (65, 257, 3, "bf16"), (9, 520, 9, "f32")])
+def test_route(T, G, topk, dtype, score, renormalize):
+    xd, x = logits_of(T, G, dtype, 2200 + T)
+    bias = 0.1 * S.rng_for(2200, G).standard_normal(G) if T % 2 else None
+    check(xd, x, topk, bias, score=score, renormalize=renormalize, scale=2.5)
+
+
+@pytest.mark.parametrize("G,groups,kept,topk", [(256, 8, 4, 8), (256, 8, 1, 8), (60, 6, 2, 7), (64, 64, 5, 5),
+                                                (24, 2, 2, 10), (1024, 2, 1, 8), (128, 16, 3, 1)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_groups(G, groups, kept, topk, ties):
+    xd, x = logits_of(37, G, "f32", 2300 + G, ties=ties)
+    check(xd, x, topk, score="sigmoid", n_groups=groups, topk_groups=kept)
+    check(xd, x, topk, score="softmax", renormalize=False, n_groups=groups, topk_groups=kept)
+
+
+def test_ties_go_to_the_lowest_index():
+    xd, x = logits_of(200, 100, "bf16", 2400, ties=True)
+    check(xd, x, 9, score="softmax")
+    check(xd, x, 9, score="sigmoid", bias=np.round(S.rng_for(2401, 0).standard_normal(100)))
+
+
+def test_masked_logits_and_empty_rows():
+    import torch
+    xd, x = logits_of(64, 40, "f32", 2402, masked=0.9)
+    xd[3], x[3] = -float("inf"), -np.inf   # nothing left
+    xd[5], x[5] = float("nan"), np.nan
+    xd[6, 7], x[6, 7] = float("nan"), np.nan
+    for kw in ({"score": "softmax"}, {"score": "sigmoid", "renormalize": False},
+               {"score": "sigmoid", "n_groups": 8, "topk_groups": 3}):
+        ids, want = check(xd, x, 6, **kw)
+        assert (want[3] == -1).all() and (want[5] == -1).all() and (want == -1).sum() > 40
+        g = torch.ones(64, 6, device="cuda")
+        kw = {k: v for k, v in kw.items() if k in ("score", "renormalize")}
+        import fp8_fine_grained_online_amd as F
+        d = F.fp8q_moe_route_bwd(xd, ids, g, **kw).cpu().numpy()
+        assert np.isfinite(d).all() and not d[3].any() and not d[5].any()
+
+
+def test_extreme_logits():
+    """Scores that underflow, saturate, or differ in the last bit of binary32."""
+    import torch
+    x = torch.tensor([[100.0, -100.0, 3e38, -3e38, 0.0, 1e-38, 88.0, 800.0],
+                      [1.0, 1.0 + 2 ** -23, 1.0, 1.0 - 2 ** -24, 0, 0, 0, 0]], device="cuda")
+    for score in ("softmax", "sigmoid"):
+        check(x, x.double().cpu().numpy(), 5, score=score)
+        check(x, x.double().cpu().numpy(), 8, score=score, renormalize=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("T,G,topk,dtype", [(1, 1, 1, "f32"), (3, 256, 8, "f32"), (70, 64, 6, "bf16"),
+                                            (17, 100, 10, "f32"), (6, 1024, 64, "bf16"), (9, 300, 2, "f32")])
+def test_gradient(T, G, topk, dtype, score, renormalize):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    xd, x = logits_of(T, G, dtype, 2500 + T)
+    rng = S.rng_for(2501, T)
+    ids = np.argsort(rng.random((T, G)), axis=1)[:, :topk].astype(np.int32)
+    if T > 2 and topk > 1:
+        ids[1, 0] = -1
+        ids[2, 1] = G        # not an expert
+        ids[0, 1] = ids[0, 0]  # listed twice
+    g = rng.standard_normal((T, topk)).astype(np.float32)
+    d = torch.full((T, G), float("nan"), dtype=xd.dtype, device="cuda")
+    F.fp8q_moe_route_bwd(xd, torch.from_numpy(ids).cuda(), torch.from_numpy(g).cuda(), score=score,
+                         renormalize=renormalize, scale=2.5, dlogits=d)
+    want = route.route_bwd(x, ids, g, score, renormalize, 2.5)
+    # float64 with cancellation against the row's sum of |g| (a few hundred roundings), then one
+    # rounding to binary32 and one to the output type
+    slack = 2.0 ** -44 * 2.5 * np.abs(g).sum(1, keepdims=True)
+    half = HALF["f32"] + (HALF["bf16"] if dtype == "bf16" else 0.0)
+    assert np.all(np.abs(d.double().cpu().numpy() - want) <= half * (1 + 2.0 ** -8) * np.abs(want) + slack + TINY)
+
+
+def test_no_tokens():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = torch.empty((0, 16), device="cuda")
+    ids, w = F.fp8q_moe_route(x, 4)
+    assert ids.shape == (0, 4) and w.shape == (0, 4)
+    assert F.fp8q_moe_route_bwd(x, ids, w).shape == (0, 16)
+
+
+def test_refusals():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = torch.zeros(4, 16, device="cuda")
+    for bad in (lambda: F.fp8q_moe_route(x, 0), lambda: F.fp8q_moe_route(x, 17),
+                lambda: F.fp8q_moe_route(x, 5, n_groups=4, topk_groups=1),
+                lambda: F.fp8q_moe_route(x, 2, n_groups=3), lambda: F.fp8q_moe_route(x, 2, scale=float("nan"))):
+        with pytest.raises(F.Fp8qError):
+            bad()
+    with pytest.raises(ValueError):
+        F.fp8q_moe_route(x, 2, score="tanh")
+    with pytest.raises(TypeError):
+        F.fp8q_moe_route(x.double(), 2)
+    with pytest.raises(ValueError):
+        F.fp8q_moe_route(x.t(), 2)
+    with pytest.raises(ValueError):
+        F.fp8q_moe_route(x, 2, bias=torch.zeros(15, device="cuda"))

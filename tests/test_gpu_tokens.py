@@ -1,0 +1,204 @@
+"""GPU permute, combine and combine's gradient against the float64 oracle: rows bit
+for bit, sums within the roundings of their terms, unwritten rows untouched."""
+
+import numpy as np
+import pytest
+
+from conftest import gpu_available
+from fp8_fine_grained_online_amd import synthetic as S
+from oracle import tokens
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+EPS32 = 2.0 ** -24   # half a step of binary32, relative
+BF16 = 2.0 ** -8     # and of bfloat16
+
+
+def dtype(name):
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16}[name]
+
+
+def rounding(name):
+    return BF16 if name == "bf16" else 0.0
+
+
+def routing(T, topk, G, seed, drop=0):
+    rng = S.rng_for(seed, 1)
+    ids = np.stack([rng.permutation(G)[:topk] if topk <= G else rng.integers(0, G, topk) for _ in range(T)])
+    ids = ids.astype(np.int32).reshape(T, topk)
+    if drop and T:
+        ids[::drop, 0] = -1
+        ids[1::drop, topk - 1] = G + 2
+    return ids
+
+
+def randn(shape, name, seed):
+    import torch
+    return torch.from_numpy(S.rng_for(seed, 2).standard_normal(shape)).to(dtype(name)).cuda()
+
+
+CASES = [(1, 1, 1, 8), (1, 8, 32, 7168), (3, 2, 4, 16), (33, 6, 64, 2056), (300, 2, 7, 512), (129, 1, 1, 128),
+         (50, 8, 256, 1032), (700, 4, 5, 520), (9, 70, 128, 64), (2, 300, 1024, 72), (1500, 8, 600, 8)]
+
+
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+@pytest.mark.parametrize("T,topk,G,K", CASES)
+def test_permute(T, topk, G, K, name):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    ids = routing(T, topk, G, 2600 + T, drop=5)
+    x = randn((T, K), name, 2601)
+    cap = F.lib().fp8q_moe_dispatch_max_rows(T, topk, G)
+    xp = torch.full((cap, K), float("nan"), dtype=dtype(name), device="cuda")
+    _, off, rows = F.fp8q_moe_permute(x, torch.from_numpy(ids).cuda(), G, xp=xp)
+    want, want_off, want_rows = tokens.permute(x.float().cpu().numpy(), ids, G)
+    assert np.array_equal(off.cpu().numpy(), want_off)
+    assert np.array_equal(rows.cpu().numpy(), want_rows)
+    got = xp.float().cpu().numpy()
+    assert np.array_equal(got[:len(want)], want)
+    assert np.isnan(got[len(want):]).all()  # not written
+
+
+def test_permute_is_the_dispatch_layout():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    for T, topk, G in ((64, 8, 32), (3000, 6, 100)):
+        ids = torch.from_numpy(routing(T, topk, G, 2610, drop=7)).cuda()
+        x = randn((T, 256), "bf16", 2611)
+        _, _, off, rows = F.fp8q_moe_dispatch_1x128(x, ids, G)
+        _, off2, rows2 = F.fp8q_moe_permute(x, ids, G)
+        assert torch.equal(off, off2) and torch.equal(rows, rows2)
+
+
+def test_permute_without_tokens_or_columns():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    off = torch.full((9,), -7, dtype=torch.int32, device="cuda")
+    F.fp8q_moe_permute(torch.empty((0, 64), device="cuda"), torch.empty((0, 2), dtype=torch.int32, device="cuda"), 8,
+                       m_offsets=off)
+    assert not off.any()
+    ids = routing(40, 2, 8, 2612)
+    _, off, rows = F.fp8q_moe_permute(torch.empty((40, 0), device="cuda"), torch.from_numpy(ids).cuda(), 8)
+    want_rows, want_off, _ = tokens.layout(ids, 8)
+    assert np.array_equal(off.cpu().numpy(), want_off) and np.array_equal(rows.cpu().numpy(), want_rows)
+
+
+@pytest.mark.parametrize("src", ["bf16", "f32"])
+@pytest.mark.parametrize("dst", ["bf16", "f32"])
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("T,topk,G,K", CASES)
+def test_combine(T, topk, G, K, src, dst, weighted):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    ids = routing(T, topk, G, 2620 + T, drop=4)
+    if T > 2:
+        ids[2] = -1  # a token without experts
+    rows, off, _ = tokens.layout(ids, G)
+    M = int(off[-1])
+    c = torch.full((max(M, 1), K), float("nan"), dtype=dtype(src), device="cuda")  # rows that nothing maps: NaN
+    used = np.unique(rows[rows >= 0])
+    c[torch.from_numpy(used).cuda().long()] = randn((used.size, K), src, 2621)
+    w = S.rng_for(2622, T).random((T, topk)).astype(np.float32) if weighted else None
+    if weighted:
+        w[rows < 0] = np.nan  # nor is a dropped choice's weight used
+    y = torch.full((T, K), float("nan"), dtype=dtype(dst), device="cuda")
+    F.fp8q_moe_combine(c, torch.from_numpy(rows).cuda(), None if w is None else torch.from_numpy(w).cuda(),
+                       out_dtype=dst, y=y)
+    want, mag = tokens.combine(c.double().cpu().numpy(), rows, w)
+    # one rounding per term of at most the running sum of magnitudes, then the output's
+    tol = topk * EPS32 * mag + rounding(dst) * (np.abs(want) + topk * EPS32 * mag)
+    assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol)
+
+
+def test_combine_skips_rows_outside():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    c = randn((128, 64), "bf16", 2630)
+    rows = torch.tensor([[0, 128], [-5, 127], [2 ** 31 - 1, -2 ** 31]], dtype=torch.int32, device="cuda")
+    y = F.fp8q_moe_combine(c, rows, out_dtype="f32")
+    assert torch.equal(y, torch.stack([c[0], c[127], torch.zeros_like(c[0])]).float())
+
+
+@pytest.mark.parametrize("gy", ["bf16", "f32"])
+@pytest.mark.parametrize("src", ["bf16", "f32"])
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("T,topk,G,K", CASES)
+def test_combine_gradient(T, topk, G, K, gy, src, weighted):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    ids = routing(T, topk, G, 2640 + T, drop=3)
+    rows, off, _ = tokens.layout(ids, G)
+    M = int(off[-1]) + 128  # rows behind the last block
+    c = randn((M, K), src, 2641)
+    dy = randn((T, K), gy, 2642)
+    w = S.rng_for(2643, T).random((T, topk)).astype(np.float32) if weighted else None
+    wd = None if w is None else torch.from_numpy(w).cuda()
+    dc = torch.full((M, K), float("nan"), dtype=dtype(src), device="cuda")
+    rd, od = torch.from_numpy(rows).cuda(), torch.from_numpy(off).cuda()
+    _, dw = F.fp8q_moe_combine_bwd(dy, c, rd, wd, od, dc=dc)
+    want, want_dw, mag = tokens.combine_bwd(dy.double().cpu().numpy(), c.double().cpu().numpy(), rows, w, off)
+    got = dc.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want))  # padding written, rows behind not
+    ok = ~np.isnan(want)
+    # one product rounded to binary32 and to c's type
+    assert np.all(np.abs(got - want)[ok] <= (EPS32 + rounding(src) * (1 + EPS32)) * np.abs(want[ok]))
+    # a lane's chain is at most K / 64 terms long here; the tree over lanes and waves adds under 16
+    assert np.all(np.abs(dw.double().cpu().numpy() - want_dw) <= (K / 64 + 24) * EPS32 * mag)
+    dc2 = torch.full_like(dc, float("nan"))
+    _, none = F.fp8q_moe_combine_bwd(dy, c, rd, wd, od, dc=dc2, with_dw=False)
+    assert none is None and torch.equal(torch.nan_to_num(dc2), torch.nan_to_num(dc))
+
+
+def test_gradient_without_tokens_zeroes_the_blocks():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    off = torch.tensor([0, 128, 128, 256], dtype=torch.int32, device="cuda")
+    c = torch.ones(384, 16, device="cuda")
+    dc = torch.full_like(c, 3.0)
+    dw = F.fp8q_moe_combine_bwd(torch.empty((0, 16), device="cuda"), c,
+                                torch.empty((0, 2), dtype=torch.int32, device="cuda"), None, off, dc=dc)[1]
+    assert dw.shape == (0, 2) and not dc[:256].any() and (dc[256:] == 3).all()
+
+
+def test_offsets_past_32_bits():
+    """Rows whose byte offset does not fit 32 bits: 9000 x 131072 float32 is 4.7 GB."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    K, M = 131072, 8960
+    c = torch.zeros(M, K, device="cuda")
+    c[M - 1] = torch.arange(K, device="cuda")
+    rows = torch.tensor([[M - 1, 0]], dtype=torch.int32, device="cuda")
+    y = F.fp8q_moe_combine(c, rows, out_dtype="f32")
+    assert torch.equal(y[0], c[M - 1])
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    dc = torch.zeros_like(c)
+    F.fp8q_moe_combine_bwd(y, c, rows, None, off, dc=dc)
+    assert torch.equal(dc[M - 1], y[0]) and torch.equal(dc[0], y[0])
+    assert not dc[1:M - 1:997].any()
+
+
+def test_refusals():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = torch.zeros(4, 64, device="cuda")
+    rows = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(F.Fp8qError):
+        F.fp8q_moe_permute(torch.zeros(4, 60, device="cuda"), rows, 4)
+    with pytest.raises(ValueError):
+        F.fp8q_moe_permute(x, rows, 0)
+    with pytest.raises(TypeError):
+        F.fp8q_moe_permute(x.half(), rows, 4)
+    with pytest.raises(ValueError):
+        F.fp8q_moe_permute(x, rows[:3], 4)
+    with pytest.raises(ValueError):
+        F.fp8q_moe_combine(x, rows.cpu())
+    with pytest.raises(ValueError):
+        F.fp8q_moe_combine(x, rows, torch.ones(4, 3, device="cuda"))
+    with pytest.raises(ValueError):
+        F.fp8q_moe_combine(x[:, ::2], rows)
+    with pytest.raises(ValueError):
+        F.fp8q_moe_combine_bwd(x[:3], x, rows, None, off)
+    with pytest.raises(TypeError):
+        F.fp8q_moe_combine_bwd(x, x, rows.long(), None, off)
