@@ -109,44 +109,62 @@ __global__ __launch_bounds__(256) void quant_int8_rows_kernel(const uint4* __res
 }
 
 // ---------------------------------------------------------------------------
-// Tiled product. A workgroup computes a BM x BN tile with WAVES_M x WAVES_N
-// waves, each a WM x WN part. Per step of 128 bytes of K the slabs of A and B
-// go straight from global memory to LDS in one of two stages; 16-byte chunk c
-// of row r sits at position c ^ (r % 8), so the 16 rows of one operand load
-// fall in distinct banks.
+// Tiled product. A workgroup of four wavefronts, one per SIMD, computes a
+// BM x BN tile, each wave a WM x WN quarter of it. Because nothing but MFMAs
+// touches the accumulators they can live in AGPRs, so a wave may hold a
+// 128 x 128 part (256 registers) and still has 256 VGPRs: a large part needs
+// the fewest operand bytes from LDS per MFMA.
+//
+// Per step of 128 bytes of K the slabs of A and B go straight from global
+// memory to LDS; 16-byte chunk c of row r sits at position c ^ (r % 8), so the
+// rows of one operand load fall in distinct banks. A step is multiplied in two
+// halves of 64 bytes (one MFMA deep), each from its own set of operand
+// registers: while half h multiplies, the other half's operands are read from
+// LDS, so an MFMA never waits for a read issued just before it.
+//
+//   first half of step g   multiplies (g, 0), reads (g, 1), copies A of g + 2
+//   barrier: every wave has read all of step g's slabs, and step g + 1's have landed
+//   second half            multiplies (g, 1), reads (g + 1, 0), copies B of g + 2
+//
+// A's slabs rotate through three buffers, B's through two (160 KB in all for
+// 256 x 256): an A copy has a whole step to land, a B copy most of one.
 //
 // Operand lanes: lane l supplies row l % 16 of a 16-row block and the 16 bytes
-// of K at chunk l / 16 (or 4 + l / 16 for the step's second half). B is the
-// first operand, so a lane holds C[m = l % 16][n = 4 (l / 16) + r], four
-// consecutive columns of one row.
+// of K at chunk l / 16 (or 4 + l / 16 for the second half). B is the first
+// operand, so a lane holds C[m = l % 16][n = 4 (l / 16) + r], four consecutive
+// columns of one row.
 //
 // Edges: the buffer descriptors cover the tile's valid rows, and in the last
 // step the chunks past K get an offset outside them; both read as zeros.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WAVES_M, int WAVES_N>
+template <int BM, int BN>
 struct I8Tile {
-  static constexpr int kThreads = 64 * WAVES_M * WAVES_N;
-  static constexpr int kWM = BM / WAVES_M, kWN = BN / WAVES_N;
-  static constexpr int kLdsA = BM * kStepK, kLdsB = BN * kStepK;
-  static constexpr int kStage = kLdsA + kLdsB;
-  static constexpr int kLds = 2 * kStage;
+  static constexpr int kThreads = 256;
+  static constexpr int kWM = BM / 2, kWN = BN / 2;
+  static constexpr int kSlabA = BM * kStepK, kSlabB = BN * kStepK;
+  static constexpr int kLds = 3 * kSlabA + 2 * kSlabB;
   static constexpr int kLoadsA = BM * 8 / kThreads, kLoadsB = BN * 8 / kThreads;
-  static_assert(kWN == 64 && kWM % 16 == 0, "the epilogue's rows are 64 columns");
-  static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0 && kThreads % 64 == 0, "whole copies");
+  static_assert(kWM % 16 == 0 && kWN % 16 == 0, "whole MFMA blocks");
+  static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0, "whole copies");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
 constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor: reads as zero
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, bool kBf16, bool kGrouped>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(I8Args p) {
-  using Cfg = I8Tile<BM, BN, WAVES_M, WAVES_N>;
+// s_waitcnt immediates: vector-memory count <= n alone; LDS count 0 alone
+constexpr int wait_vm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int kWaitLds = 0xC07F;
+
+template <int BM, int BN, bool kBf16, bool kGrouped>
+__global__ __launch_bounds__(256, 1) void gemm_i8_kernel(I8Args p) {
+  using Cfg = I8Tile<BM, BN>;
   constexpr int WM = Cfg::kWM, WN = Cfg::kWN;
   constexpr int SUBM = WM / 16, SUBN = WN / 16;
+  constexpr int kMfmas = SUBM * SUBN;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Cfg::kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+  const int wm = wave >> 1, wn = wave & 1;
   const int lr = lane & 15, lk = lane >> 4;
   const int n_tiles_n = (p.N + BN - 1) / BN;
   const int tile = xcd_tile(blockIdx.x, gridDim.x);
@@ -200,18 +218,25 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(I8Args 
   const __amdgpu_buffer_rsrc_t rsrc_a = make_rsrc(p.a + (int64_t)m0 * p.K, (uint32_t)rows_a * (uint32_t)p.K);
   const __amdgpu_buffer_rsrc_t rsrc_b = make_rsrc(bmat + (int64_t)n0 * p.K, (uint32_t)rows_b * (uint32_t)p.K);
   const int steps = (p.K + kStepK - 1) / kStepK;
+  // copy q of thread tid brings row q * 32 + tid / 8, stored chunk tid % 8
   const int row0 = tid >> 3, lc0 = (tid & 7) ^ (row0 & 7);
-  const uint32_t off = (uint32_t)row0 * (uint32_t)p.K + lc0 * 16;
-  const uint32_t row_step = (uint32_t)(Cfg::kThreads / 8) * (uint32_t)p.K;
-  const uint32_t off_last = (steps - 1) * kStepK + lc0 * 16 < p.K ? off : kOutside;
-  constexpr int kCopies = Cfg::kLoadsA + Cfg::kLoadsB;
-  auto issue = [&](int q, int g, uint8_t* __restrict__ st) {
-    const uint32_t o = g == steps - 1 ? off_last : off;
-    if (q < Cfg::kLoadsA)
-      load_lds(rsrc_a, st + (q * Cfg::kThreads + wave * 64) * 16, 16, o + q * row_step, g * kStepK);
-    else
-      load_lds(rsrc_b, st + Cfg::kLdsA + ((q - Cfg::kLoadsA) * Cfg::kThreads + wave * 64) * 16, 16,
-               o + (q - Cfg::kLoadsA) * row_step, g * kStepK);
+  constexpr int kRows = Cfg::kLoadsA > Cfg::kLoadsB ? Cfg::kLoadsA : Cfg::kLoadsB;
+  uint32_t off[kRows];
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) off[q] = (uint32_t)(row0 + q * 32) * (uint32_t)p.K + lc0 * 16;
+  // from the last step's copies on, a thread whose chunk is past K reads zeros
+  const bool past = (steps - 1) * kStepK + lc0 * 16 >= p.K;
+  auto enter_step = [&](int g) {
+    if (g == steps - 1) {
+#pragma unroll
+      for (int q = 0; q < kRows; ++q) off[q] = past ? kOutside : off[q];
+    }
+  };
+  auto copy_a = [&](int q, int g, uint8_t* __restrict__ to) {
+    load_lds(rsrc_a, to + (q * 256 + wave * 64) * 16, 16, off[q], g * kStepK);
+  };
+  auto copy_b = [&](int q, int g, uint8_t* __restrict__ to) {
+    load_lds(rsrc_b, to + (q * 256 + wave * 64) * 16, 16, off[q], g * kStepK);
   };
 
   v4i acc[SUBM][SUBN];
@@ -219,38 +244,99 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(I8Args 
   for (int i = 0; i < SUBM; ++i)
 #pragma unroll
     for (int j = 0; j < SUBN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-  const int lane_off[2] = {lr * kStepK + ((lk ^ (lr & 7)) << 4), lr * kStepK + (((4 + lk) ^ (lr & 7)) << 4)};
-  auto step = [&](const uint8_t* __restrict__ cur, uint8_t* __restrict__ nxt, int g) {
+  v4i ra[2][SUBM], rb[2][SUBN];  // operands of the two halves
+  const int a_off[2] = {(wm * WM + lr) * kStepK + ((lk ^ (lr & 7)) << 4),
+                        (wm * WM + lr) * kStepK + (((4 + lk) ^ (lr & 7)) << 4)};
+  const int b_off[2] = {a_off[0] + (wn * WN - wm * WM) * kStepK, a_off[1] + (wn * WN - wm * WM) * kStepK};
+  // operand number u of half h: B's blocks first, the order the MFMAs want them in
+  auto read_operand = [&](int u, int h, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ sb) {
+    if (u < SUBN) rb[h][u] = *(const v4i*)(sb + b_off[h] + u * 16 * kStepK);
+    else ra[h][u - SUBN] = *(const v4i*)(sa + a_off[h] + (u - SUBN) * 16 * kStepK);
+  };
+  // Half h of a step: its MFMAs, with the other half's operands read from
+  // (sa, sb) and one operand's copies (`issue`) spread between them. Scheduling
+  // barriers keep that order.
+  auto half = [&](int h, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ sb, int g,
+                  uint8_t* __restrict__ to, bool copy_is_a) {
 #pragma unroll
-    for (int q = 0; q < kCopies; ++q) issue(q, g, nxt);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v4i bf[SUBN];
-#pragma unroll
-      for (int j = 0; j < SUBN; ++j)
-        bf[j] = *(const v4i*)(cur + Cfg::kLdsA + (wn * WN + j * 16) * kStepK + lane_off[h]);
-#pragma unroll
-      for (int i = 0; i < SUBM; ++i) {
-        const v4i af = *(const v4i*)(cur + (wm * WM + i * 16) * kStepK + lane_off[h]);
-#pragma unroll
-        for (int j = 0; j < SUBN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af, acc[i][j], 0, 0, 0);
+    for (int t = 0; t < kMfmas; ++t) {
+      const int i = t / SUBN, j = t % SUBN;
+      if (t % 2 == 0 && t / 2 < SUBM + SUBN) read_operand(t / 2, 1 - h, sa, sb);
+      if (t % 2 == 1) {
+        const int q = t / 2;
+        if (copy_is_a) { if (q < Cfg::kLoadsA) copy_a(q, g, to); }
+        else { if (q < Cfg::kLoadsB) copy_b(q, g, to); }
       }
+      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(rb[h][j], ra[h][i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-#pragma unroll
-  for (int q = 0; q < kCopies; ++q) issue(q, 0, lds);
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-  __syncthreads();
-  for (int g = 0; g < steps; ++g) {
-    // past the last step the copies repeat it into a stage that is not read again
-    step(lds + (g & 1) * Cfg::kStage, lds + ((g + 1) & 1) * Cfg::kStage, min(g + 1, steps - 1));
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
-  }
+  static_assert(kMfmas / 2 >= SUBM + SUBN && kMfmas / 2 >= Cfg::kLoadsA && kMfmas / 2 >= Cfg::kLoadsB,
+                "reads and copies fit between the MFMAs");
 
-  // ---- epilogue: scale, stage the wave's part in its own LDS, store rows ----
+  // a wave whose rows all lie past the tile's valid ones only copies
+  const bool idle = wm * WM >= rows_a;
+  uint8_t* const lds_b = lds + 3 * Cfg::kSlabA;
+  if (steps > 0) {
+    const int g1 = min(1, steps - 1);
+    enter_step(0);
+#pragma unroll
+    for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, 0, lds);
+#pragma unroll
+    for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, 0, lds_b);
+    enter_step(g1);
+#pragma unroll
+    for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, g1, lds + Cfg::kSlabA);
+#pragma unroll
+    for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, g1, lds_b + Cfg::kSlabB);
+    __builtin_amdgcn_s_waitcnt(wait_vm(Cfg::kLoadsA + Cfg::kLoadsB));
+    __builtin_amdgcn_s_barrier();
+    if (!idle) {
+#pragma unroll
+      for (int u = 0; u < SUBM + SUBN; ++u) read_operand(u, 0, lds, lds_b);
+    }
+  }
+  // buffers of A's slabs: of this step, the next and the one after
+  uint8_t *a0 = lds, *a1 = lds + Cfg::kSlabA, *a2 = lds + 2 * Cfg::kSlabA;
+  uint8_t *b0 = lds_b, *b1 = lds_b + Cfg::kSlabB;
+  for (int g = 0; g < steps; ++g) {
+    const int gn = min(g + 2, steps - 1);  // past the end the last step is copied again, unread
+    enter_step(gn);
+    if (idle) {
+#pragma unroll
+      for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, gn, a2);
+    } else {
+      half(0, a0, b0, gn, a2, true);
+    }
+    // this wave has read all of step g, and its copies of step g + 1 have landed
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    __builtin_amdgcn_s_waitcnt(wait_vm(Cfg::kLoadsA));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (idle) {
+#pragma unroll
+      for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, gn, b0);
+    } else {
+      half(1, a1, b1, gn, b0, false);
+    }
+    uint8_t* const ta = a0;
+    a0 = a1, a1 = a2, a2 = ta;
+    uint8_t* const tb = b0;
+    b0 = b1, b1 = tb;
+  }
+  // the last copies may still be writing the buffers that the epilogue stages in
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  __syncthreads();
+
+  // ---- epilogue: scale, stage 16 rows of the wave's part in its own LDS, store rows ----
   const int nw = n0 + wn * WN;
+  constexpr int kEl = kBf16 ? 2 : 4;        // bytes per output
+  constexpr int kRowBytes = WN * kEl;
+  constexpr int kChunks = kRowBytes / 16;
+  constexpr int kRowsAtOnce = 64 / kChunks;
+  static_assert(4 * 16 * kRowBytes <= Cfg::kLds && kRowsAtOnce >= 1, "staging");
+  uint8_t* st = lds + wave * (16 * kRowBytes);
+  const bool whole = p.N % (16 / kEl) == 0;  // every 16-byte store is aligned and inside its row
   float sbc[SUBN][4];
 #pragma unroll
   for (int j = 0; j < SUBN; ++j)
@@ -259,12 +345,6 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(I8Args 
       const int n = nw + j * 16 + 4 * lk + r;
       sbc[j][r] = n < p.N && p.K > 0 ? sbv[n] : 0.0f;  // K == 0: no operand is read
     }
-  constexpr int kEl = kBf16 ? 2 : 4;        // bytes per output
-  constexpr int kRowBytes = WN * kEl;       // 128 or 256
-  constexpr int kChunks = kRowBytes / 16;   // 8 or 16
-  static_assert(Cfg::kThreads / 64 * 16 * kRowBytes <= Cfg::kLds, "staging fits in the stages");
-  uint8_t* st = lds + wave * (16 * kRowBytes);
-  const bool whole = p.N % (16 / kEl) == 0;  // every 16-byte store is aligned and inside its row
 #pragma unroll
   for (int i = 0; i < SUBM; ++i) {
     const int gm = m0 + wm * WM + i * 16 + lr;
@@ -279,9 +359,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(I8Args 
       if constexpr (kBf16) *(bf16x4*)to = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
       else *(v4f*)to = v4f{v[0], v[1], v[2], v[3]};
     }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): a wave reads back only its own part
+    __builtin_amdgcn_s_waitcnt(kWaitLds);  // a wave reads back only its own part
     __builtin_amdgcn_wave_barrier();
-    constexpr int kRowsAtOnce = 64 / kChunks;
     const int ch = lane % kChunks;
 #pragma unroll
     for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
@@ -407,13 +486,13 @@ hipError_t launch_quant_int8_rows(const void* x, int64_t M, int64_t K, int8_t* q
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, bool kGrouped>
+template <int BM, int BN, bool kGrouped>
 static hipError_t launch_tiles(const I8Args& a, bool bf16, int64_t m_tiles, hipStream_t stream) {
-  const dim3 grid((unsigned)(m_tiles * ((a.N + BN - 1) / BN))), block(64 * WAVES_M * WAVES_N);
+  const dim3 grid((unsigned)(m_tiles * ((a.N + BN - 1) / BN))), block(256);
   if (bf16)
-    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, WAVES_M, WAVES_N, true, kGrouped>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, true, kGrouped>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, WAVES_M, WAVES_N, false, kGrouped>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, false, kGrouped>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
@@ -435,7 +514,7 @@ hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, c
     if (M <= 16) return launch_few<1, 1, 8>(p, bf16, stream);
     return launch_few<4, 2, 8>(p, bf16, stream);
   }
-  return launch_tiles<256, 256, 2, 4, false>(p, bf16, (M + 255) / 256, stream);
+  return launch_tiles<256, 256, false>(p, bf16, (M + 255) / 256, stream);
 }
 
 hipError_t launch_int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b,
@@ -444,7 +523,7 @@ hipError_t launch_int8_gemm_grouped(const int8_t* a, const float* sa, const int8
                                     hipStream_t stream) {
   const I8Args p{(const uint8_t*)a, sa, (const uint8_t*)b, sb, c, m_offsets, (int)M_total, (int)N, (int)K, (int)G};
   // upper bound on sum_e ceil(rows_e / 256) for rows_e multiples of 128
-  return launch_tiles<256, 256, 2, 4, true>(p, bf16, (M_total / 128 + G + 1) / 2, stream);
+  return launch_tiles<256, 256, true>(p, bf16, (M_total / 128 + G + 1) / 2, stream);
 }
 
 }  // namespace fp8q
