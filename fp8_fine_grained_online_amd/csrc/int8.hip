@@ -122,12 +122,13 @@ __global__ __launch_bounds__(256) void quant_int8_rows_kernel(const uint4* __res
 // registers: while half h multiplies, the other half's operands are read from
 // LDS, so an MFMA never waits for a read issued just before it.
 //
-//   first half of step g   multiplies (g, 0), reads (g, 1), copies A of g + 2
+//   first half of step g   multiplies (g, 0), reads (g, 1), copies A of g + D
 //   barrier: every wave has read all of step g's slabs, and step g + 1's have landed
-//   second half            multiplies (g, 1), reads (g + 1, 0), copies B of g + 2
+//   second half            multiplies (g, 1), reads (g + 1, 0), copies B of g + D
 //
-// A's slabs rotate through three buffers, B's through two (160 KB in all for
-// 256 x 256): an A copy has a whole step to land, a B copy most of one.
+// A's slabs rotate through D + 1 buffers, B's through D (D = 2 and 160 KB in all
+// for 256 x 256): a copy has D - 1 steps to land, A's half a step more. Smaller
+// tiles multiply a step in less time than a copy takes, and look further ahead.
 //
 // Operand lanes: lane l supplies row l % 16 of a 16-row block and the 16 bytes
 // of K at chunk l / 16 (or 4 + l / 16 for the second half). B is the first
@@ -137,16 +138,18 @@ __global__ __launch_bounds__(256) void quant_int8_rows_kernel(const uint4* __res
 // Edges: the buffer descriptors cover the tile's valid rows, and in the last
 // step the chunks past K get an offset outside them; both read as zeros.
 // ---------------------------------------------------------------------------
-template <int BM, int BN>
+template <int BM, int BN, int D, int S>
 struct I8Tile {
-  static constexpr int kThreads = 256;
+  static constexpr int kThreads = 256;  // of one K group
   static constexpr int kWM = BM / 2, kWN = BN / 2;
   static constexpr int kSlabA = BM * kStepK, kSlabB = BN * kStepK;
-  static constexpr int kLds = 3 * kSlabA + 2 * kSlabB;
+  static constexpr int kRing = (D + 1) * kSlabA + D * kSlabB;
+  static constexpr int kLds = S * kRing;
   static constexpr int kLoadsA = BM * 8 / kThreads, kLoadsB = BN * 8 / kThreads;
   static_assert(kWM % 16 == 0 && kWN % 16 == 0, "whole MFMA blocks");
   static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0, "whole copies");
-  static_assert(kLds <= 160 * 1024, "LDS");
+  static_assert(kLds <= 160 * 1024 && D >= 2, "LDS");
+  static_assert((D - 1) * (kLoadsA + kLoadsB) <= 63, "the wait counter holds the copies in flight");
 };
 
 constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor: reads as zero
@@ -155,61 +158,72 @@ constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor: reads as z
 constexpr int wait_vm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 constexpr int kWaitLds = 0xC07F;
 
-template <int BM, int BN, bool kBf16, bool kGrouped>
-__global__ __launch_bounds__(256, 1) void gemm_i8_kernel(I8Args p) {
-  using Cfg = I8Tile<BM, BN>;
+template <int BM, int BN, int D, int S, bool kBf16, bool kGrouped>
+__global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
+  using Cfg = I8Tile<BM, BN, D, S>;
   constexpr int WM = Cfg::kWM, WN = Cfg::kWN;
   constexpr int SUBM = WM / 16, SUBN = WN / 16;
   constexpr int kMfmas = SUBM * SUBN;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[Cfg::kLds];
-  const int tid = threadIdx.x, lane = tid & 63;
+  __shared__ __attribute__((aligned(16))) uint8_t lds_all[Cfg::kLds];
+  const int tid = threadIdx.x & 255, lane = tid & 63;
+  const int group = S > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  uint8_t* const lds = lds_all + group * Cfg::kRing;
   const int wm = wave >> 1, wn = wave & 1;
   const int lr = lane & 15, lk = lane >> 4;
   const int n_tiles_n = (p.N + BN - 1) / BN;
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
 
   int m0, m_end, tm, tn;
   const uint8_t* bmat = p.b;
   const float* sbv = p.sb;
   if constexpr (kGrouped) {
-    // one expert per lane, 64 a round: the first whose running tile count passes the tile
-    int e = -1, before = 0, lo = 0, hi = 0, te = 0;
-    for (int e0 = 0; e0 < p.G; e0 += 64) {
-      const int ee = e0 + lane;
-      int l_lo = 0, l_hi = 0, l_te = 0;
-      if (ee < p.G) {
-        l_lo = min(max(p.m_offsets[ee], 0), p.M);
-        l_hi = min(max(p.m_offsets[ee + 1], l_lo), p.M);
+    // The grid is an upper bound: the host does not know the offsets. Count the
+    // real tiles (one expert per lane, 64 a round) and give every XCD its share
+    // of those, then find the expert that holds this workgroup's tile.
+    // Values found by a lane are read back with readlane into variables of
+    // their own: a buffer descriptor built from a vector value becomes a loop.
+    int l_lo = 0, l_hi = 0, l_te = 0;
+    auto expert = [&](int e) {  // this lane's expert's rows and tiles; tiles up to and with this lane
+      l_lo = l_hi = l_te = 0;
+      if (e < p.G) {
+        l_lo = min(max(p.m_offsets[e], 0), p.M);
+        l_hi = min(max(p.m_offsets[e + 1], l_lo), p.M);
         l_te = (l_hi - l_lo + BM - 1) / BM;
       }
-      const int cnt = l_te * n_tiles_n;
-      int incl = cnt;
+      int incl = l_te * n_tiles_n;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const int v = __shfl_up(incl, d);
         if (lane >= d) incl += v;
       }
-      const uint64_t hit = __ballot(ee < p.G && tile < before + incl);
+      return incl;
+    };
+    int total = 0;
+    for (int e0 = 0; e0 < p.G; e0 += 64) total += __builtin_amdgcn_readlane(expert(e0 + lane), 63);
+    if ((int)blockIdx.x >= total) return;
+    const int tile = xcd_tile(blockIdx.x, total);
+    int e = 0, before = 0, lo = 0, hi = 0, te = 0;
+    for (int e0 = 0; e0 < p.G; e0 += 64) {
+      const int incl = expert(e0 + lane);
+      const uint64_t hit = __ballot(tile < before + incl);
       if (hit) {
         const int L = __builtin_ctzll(hit);
         e = e0 + L;
         lo = __builtin_amdgcn_readlane(l_lo, L);
         hi = __builtin_amdgcn_readlane(l_hi, L);
         te = __builtin_amdgcn_readlane(l_te, L);
-        before += __builtin_amdgcn_readlane(incl - cnt, L);
+        before += __builtin_amdgcn_readlane(incl - l_te * n_tiles_n, L);
         break;
       }
       before += __builtin_amdgcn_readlane(incl, 63);
     }
-    if (e < 0) return;  // the grid is an upper bound
     band_tile<kBandGrouped>(tile - before, te, n_tiles_n, tm, tn);
     m0 = lo + tm * BM;
     m_end = min(m0 + BM, hi);
     bmat += (int64_t)e * p.N * p.K;
     sbv += (int64_t)e * p.N;
   } else {
-    band_tile(tile, (p.M + BM - 1) / BM, n_tiles_n, tm, tn);
+    band_tile(xcd_tile(blockIdx.x, gridDim.x), (p.M + BM - 1) / BM, n_tiles_n, tm, tn);
     m0 = tm * BM;
     m_end = min(m0 + BM, p.M);
   }
@@ -217,26 +231,31 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(I8Args p) {
   const int rows_a = m_end - m0, rows_b = min(BN, p.N - n0);
   const __amdgpu_buffer_rsrc_t rsrc_a = make_rsrc(p.a + (int64_t)m0 * p.K, (uint32_t)rows_a * (uint32_t)p.K);
   const __amdgpu_buffer_rsrc_t rsrc_b = make_rsrc(bmat + (int64_t)n0 * p.K, (uint32_t)rows_b * (uint32_t)p.K);
-  const int steps = (p.K + kStepK - 1) / kStepK;
+  // this group's steps of K: first .. first + steps - 1, those past the last reading zeros
+  const int all_steps = (p.K + kStepK - 1) / kStepK;
+  const int steps = (all_steps + S - 1) / S;
+  const int first = group * steps;
   // copy q of thread tid brings row q * 32 + tid / 8, stored chunk tid % 8
   const int row0 = tid >> 3, lc0 = (tid & 7) ^ (row0 & 7);
   constexpr int kRows = Cfg::kLoadsA > Cfg::kLoadsB ? Cfg::kLoadsA : Cfg::kLoadsB;
   uint32_t off[kRows];
 #pragma unroll
   for (int q = 0; q < kRows; ++q) off[q] = (uint32_t)(row0 + q * 32) * (uint32_t)p.K + lc0 * 16;
-  // from the last step's copies on, a thread whose chunk is past K reads zeros
-  const bool past = (steps - 1) * kStepK + lc0 * 16 >= p.K;
+  // From the last step's copies on, a thread whose chunk is past K reads zeros
+  // (and every thread, past that step)
+  const bool past = (all_steps - 1) * kStepK + lc0 * 16 >= p.K;
   auto enter_step = [&](int g) {
-    if (g == steps - 1) {
+    if (first + g >= all_steps - 1) {
+      const bool out = past || first + g >= all_steps;
 #pragma unroll
-      for (int q = 0; q < kRows; ++q) off[q] = past ? kOutside : off[q];
+      for (int q = 0; q < kRows; ++q) off[q] = out ? kOutside : off[q];
     }
   };
   auto copy_a = [&](int q, int g, uint8_t* __restrict__ to) {
-    load_lds(rsrc_a, to + (q * 256 + wave * 64) * 16, 16, off[q], g * kStepK);
+    load_lds(rsrc_a, to + (q * 256 + wave * 64) * 16, 16, off[q], (first + g) * kStepK);
   };
   auto copy_b = [&](int q, int g, uint8_t* __restrict__ to) {
-    load_lds(rsrc_b, to + (q * 256 + wave * 64) * 16, 16, off[q], g * kStepK);
+    load_lds(rsrc_b, to + (q * 256 + wave * 64) * 16, 16, off[q], (first + g) * kStepK);
   };
 
   v4i acc[SUBM][SUBN];
@@ -253,6 +272,8 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(I8Args p) {
     if (u < SUBN) rb[h][u] = *(const v4i*)(sb + b_off[h] + u * 16 * kStepK);
     else ra[h][u - SUBN] = *(const v4i*)(sa + a_off[h] + (u - SUBN) * 16 * kStepK);
   };
+  // MFMAs from one operand read (and from one copy) to the next
+  constexpr int kEvery = kMfmas >= 2 * (SUBM + SUBN) ? 2 : 1;
   // Half h of a step: its MFMAs, with the other half's operands read from
   // (sa, sb) and one operand's copies (`issue`) spread between them. Scheduling
   // barriers keep that order.
@@ -261,9 +282,9 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(I8Args p) {
 #pragma unroll
     for (int t = 0; t < kMfmas; ++t) {
       const int i = t / SUBN, j = t % SUBN;
-      if (t % 2 == 0 && t / 2 < SUBM + SUBN) read_operand(t / 2, 1 - h, sa, sb);
-      if (t % 2 == 1) {
-        const int q = t / 2;
+      if (t % kEvery == 0 && t / kEvery < SUBM + SUBN) read_operand(t / kEvery, 1 - h, sa, sb);
+      if (t % kEvery == kEvery - 1) {
+        const int q = t / kEvery;
         if (copy_is_a) { if (q < Cfg::kLoadsA) copy_a(q, g, to); }
         else { if (q < Cfg::kLoadsB) copy_b(q, g, to); }
       }
@@ -271,72 +292,84 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(I8Args p) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  static_assert(kMfmas / 2 >= SUBM + SUBN && kMfmas / 2 >= Cfg::kLoadsA && kMfmas / 2 >= Cfg::kLoadsB,
-                "reads and copies fit between the MFMAs");
+  static_assert(kMfmas / kEvery >= SUBM + SUBN && kMfmas / kEvery >= kRows, "reads and copies fit between the MFMAs");
 
   // a wave whose rows all lie past the tile's valid ones only copies
   const bool idle = wm * WM >= rows_a;
-  uint8_t* const lds_b = lds + 3 * Cfg::kSlabA;
+  uint8_t* const lds_b = lds + (D + 1) * Cfg::kSlabA;
   if (steps > 0) {
-    const int g1 = min(1, steps - 1);
     enter_step(0);
 #pragma unroll
-    for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, 0, lds);
+    for (int d = 0; d < D; ++d) {
+      const int g = min(d, steps - 1);
+      if (d > 0) enter_step(g);
 #pragma unroll
-    for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, 0, lds_b);
-    enter_step(g1);
+      for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, g, lds + d * Cfg::kSlabA);
 #pragma unroll
-    for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, g1, lds + Cfg::kSlabA);
-#pragma unroll
-    for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, g1, lds_b + Cfg::kSlabB);
-    __builtin_amdgcn_s_waitcnt(wait_vm(Cfg::kLoadsA + Cfg::kLoadsB));
+      for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, g, lds_b + d * Cfg::kSlabB);
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm((D - 1) * (Cfg::kLoadsA + Cfg::kLoadsB)));
     __builtin_amdgcn_s_barrier();
     if (!idle) {
 #pragma unroll
       for (int u = 0; u < SUBM + SUBN; ++u) read_operand(u, 0, lds, lds_b);
     }
   }
-  // buffers of A's slabs: of this step, the next and the one after
-  uint8_t *a0 = lds, *a1 = lds + Cfg::kSlabA, *a2 = lds + 2 * Cfg::kSlabA;
-  uint8_t *b0 = lds_b, *b1 = lds_b + Cfg::kSlabB;
+  // offsets of the buffers of this step's and the next step's slabs, and of the one A is copied to
+  int a0 = 0, a1 = Cfg::kSlabA, a2 = D * Cfg::kSlabA;
+  int b0 = 0, b1 = D > 1 ? Cfg::kSlabB : 0;
   for (int g = 0; g < steps; ++g) {
-    const int gn = min(g + 2, steps - 1);  // past the end the last step is copied again, unread
+    const int gn = min(g + D, steps - 1);  // past the end the last step is copied again, unread
     enter_step(gn);
     if (idle) {
 #pragma unroll
-      for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, gn, a2);
+      for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, gn, lds + a2);
     } else {
-      half(0, a0, b0, gn, a2, true);
+      half(0, lds + a0, lds_b + b0, gn, lds + a2, true);
     }
     // this wave has read all of step g, and its copies of step g + 1 have landed
     __builtin_amdgcn_s_waitcnt(kWaitLds);
-    __builtin_amdgcn_s_waitcnt(wait_vm(Cfg::kLoadsA));
+    __builtin_amdgcn_s_waitcnt(wait_vm((D - 1) * Cfg::kLoadsA + (D - 2) * Cfg::kLoadsB));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     if (idle) {
 #pragma unroll
-      for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, gn, b0);
+      for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, gn, lds_b + b0);
     } else {
-      half(1, a1, b1, gn, b0, false);
+      half(1, lds + a1, lds_b + b1, gn, lds_b + b0, false);
     }
-    uint8_t* const ta = a0;
-    a0 = a1, a1 = a2, a2 = ta;
-    uint8_t* const tb = b0;
-    b0 = b1, b1 = tb;
+    a2 = a0, a0 = a1, b0 = b1;
+    a1 = a1 == D * Cfg::kSlabA ? 0 : a1 + Cfg::kSlabA;
+    b1 = b1 == (D - 1) * Cfg::kSlabB ? 0 : b1 + Cfg::kSlabB;
   }
-  // the last copies may still be writing the buffers that the epilogue stages in
+  // the last copies may still be writing the buffers that are used again below
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
   __syncthreads();
+  if constexpr (S > 1) {
+    // add the groups' sums: integers, so any order gives the same bits
+    static_assert((S - 1) * BM * BN * 4 <= Cfg::kLds, "the other groups' sums fit");
+    v4i* const part = (v4i*)lds_all + wave * (kMfmas * 64) + lane;
+    if (group > 0) {
+#pragma unroll
+      for (int t = 0; t < kMfmas; ++t) part[(group - 1) * (4 * kMfmas * 64) + t * 64] = acc[t / SUBN][t % SUBN];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+#pragma unroll
+      for (int t = 0; t < kMfmas; ++t) acc[t / SUBN][t % SUBN] += part[s * (4 * kMfmas * 64) + t * 64];
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+  }
 
   // ---- epilogue: scale, stage 16 rows of the wave's part in its own LDS, store rows ----
   const int nw = n0 + wn * WN;
   constexpr int kEl = kBf16 ? 2 : 4;        // bytes per output
   constexpr int kRowBytes = WN * kEl;
   constexpr int kChunks = kRowBytes / 16;
-  constexpr int kRowsAtOnce = 64 / kChunks;
-  static_assert(4 * 16 * kRowBytes <= Cfg::kLds && kRowsAtOnce >= 1, "staging");
-  uint8_t* st = lds + wave * (16 * kRowBytes);
-  const bool whole = p.N % (16 / kEl) == 0;  // every 16-byte store is aligned and inside its row
+  static_assert((S > 1 ? kMfmas * 64 * 16 : Cfg::kLds / 4) >= 16 * kRowBytes, "staging");
+  // (with S > 1 a wave stages where its own part of the other groups' sums was)
+  uint8_t* st = lds + wave * (S > 1 ? kMfmas * 64 * 16 : 16 * kRowBytes);
   float sbc[SUBN][4];
 #pragma unroll
   for (int j = 0; j < SUBN; ++j)
@@ -361,40 +394,46 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_kernel(I8Args p) {
     }
     __builtin_amdgcn_s_waitcnt(kWaitLds);  // a wave reads back only its own part
     __builtin_amdgcn_wave_barrier();
-    const int ch = lane % kChunks;
+    // stores of `Unit`s, neighbouring lanes in a row: 16 bytes where every row
+    // of c starts at a multiple of 16, else 4, or a single bfloat16
+    auto store_rows = [&](auto unit) {
+      using Unit = decltype(unit);
+      constexpr int kUnits = kRowBytes / (int)sizeof(Unit);  // of a row
+      static_assert(kUnits % 64 == 0 || 64 % kUnits == 0, "whole wave stores");
+      // (the narrow forms stay loops: unrolled, the three outgrow the instruction cache)
+      auto piece = [&](int k) {
+        const int m = (k * 64 + lane) / kUnits, byte = (k * 64 + lane) % kUnits * (int)sizeof(Unit);
+        const int om = m0 + wm * WM + i * 16 + m;
+        const Unit v = *(const Unit*)(st + m * kRowBytes + (((byte >> 4) ^ (m & (kChunks - 1))) << 4) + (byte & 15));
+        const int n = nw + byte / kEl;
+        if (om < m_end && n < p.N) *(Unit*)((uint8_t*)p.c + ((int64_t)om * p.N + n) * kEl) = v;
+      };
+      if constexpr (sizeof(Unit) == 16) {
 #pragma unroll
-    for (int k = 0; k < 16 / kRowsAtOnce; ++k) {
-      const int m = k * kRowsAtOnce + lane / kChunks;
-      const int om = m0 + wm * WM + i * 16 + m;
-      const uint4 v = *(const uint4*)(st + m * kRowBytes + ((ch ^ (m & (kChunks - 1))) << 4));
-      const int n = nw + ch * (16 / kEl);
-      if (om < m_end && n < p.N) {
-        uint8_t* to = (uint8_t*)p.c + ((int64_t)om * p.N + n) * kEl;
-        if (whole) {
-          *(uint4*)to = v;
-        } else {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int u = 0; u < 16 / kEl; ++u) {
-            if (n + u >= p.N) break;
-            if constexpr (kBf16) ((uint16_t*)to)[u] = (uint16_t)(w[u / 2] >> (16 * (u & 1)));
-            else ((uint32_t*)to)[u] = w[u];
-          }
-        }
+        for (int k = 0; k < kUnits / 4; ++k) piece(k);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < kUnits / 4; ++k) piece(k);
       }
-    }
+    };
+    if (p.N % (16 / kEl) == 0) store_rows(uint4{});
+    else if (!kBf16 || p.N % 2 == 0) store_rows(uint32_t{});
+    else store_rows(uint16_t{});
     __builtin_amdgcn_wave_barrier();
   }
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: a workgroup owns 16 MB x 16 NB outputs and its W waves split the
-// steps of K between them, each streaming its fragments straight from global
-// memory to registers; the int32 partial blocks are added through LDS. B is
-// read once per 16 MB rows.
+// Small products: a workgroup owns 16 MB x 16 NB outputs and its W waves split
+// K between them in pieces of 64 bytes (one MFMA deep), each streaming its
+// fragments straight from global memory to registers, kAhead pieces ahead; the
+// int32 partial blocks are added through LDS. For products too small to give
+// every CU a large tile, and for few rows, where B is read once.
 // ---------------------------------------------------------------------------
-template <int MB, int NB, int W, bool kBf16>
-__global__ __launch_bounds__(64 * W) void gemm_i8_few_kernel(I8Args p) {
+constexpr int kPiece = 64;
+
+template <int MB, int NB, int W, int kAhead, bool kBf16>
+__global__ __launch_bounds__(64 * W) void gemm_i8_small_kernel(I8Args p) {
   __shared__ __attribute__((aligned(16))) v4i part[W][MB * NB][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -402,9 +441,9 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_few_kernel(I8Args p) {
   const int n_blocks = (p.N + 16 * NB - 1) / (16 * NB);
   const int n0 = (blockIdx.x % n_blocks) * 16 * NB;
   const int m0 = (blockIdx.x / n_blocks) * 16 * MB;
-  const int steps = (p.K + kStepK - 1) / kStepK;
-  const int g_begin = (int)((int64_t)steps * wave / W);
-  const int g_end = (int)((int64_t)steps * (wave + 1) / W);
+  const int pieces = (p.K + kPiece - 1) / kPiece;
+  const int g_begin = (int)((int64_t)pieces * wave / W);
+  const int g_end = (int)((int64_t)pieces * (wave + 1) / W);
   const int rows_a = min(16 * MB, p.M - m0), rows_b = min(16 * NB, p.N - n0);
   const __amdgpu_buffer_rsrc_t rsrc_a = make_rsrc(p.a + (int64_t)m0 * p.K, (uint32_t)rows_a * (uint32_t)p.K);
   const __amdgpu_buffer_rsrc_t rsrc_b = make_rsrc(p.b + (int64_t)n0 * p.K, (uint32_t)rows_b * (uint32_t)p.K);
@@ -412,19 +451,16 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_few_kernel(I8Args p) {
   const uint32_t blk = 16u * (uint32_t)p.K;
 
   struct Frags {
-    v4i a[MB][2], b[NB][2];
+    v4i a[MB], b[NB];
   };
   auto load = [&](int g, Frags& f) {
+    const uint32_t o = g * kPiece + lk * 16 < p.K ? off : kOutside;  // chunks past K read as zeros
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t o = g * kStepK + h * 64 + lk * 16 < p.K ? off : kOutside;
+    for (int j = 0; j < NB; ++j)
+      f.b[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc_b, o + j * blk, g * kPiece, 0));
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        f.b[j][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc_b, o + j * blk, g * kStepK + h * 64, 0));
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-        f.a[i][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc_a, o + i * blk, g * kStepK + h * 64, 0));
-    }
+    for (int i = 0; i < MB; ++i)
+      f.a[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc_a, o + i * blk, g * kPiece, 0));
   };
   v4i acc[MB][NB];
 #pragma unroll
@@ -433,30 +469,28 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_few_kernel(I8Args p) {
     for (int j = 0; j < NB; ++j) acc[i][j] = v4i{0, 0, 0, 0};
   auto compute = [&](const Frags& f) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[j][h], f.a[i][h], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < NB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
   };
-  Frags f0, f1;
-  int g = g_begin;
-  if (g < g_end) load(g, f0);
-  for (; g + 1 < g_end; g += 2) {
-    load(g + 1, f1);
-    compute(f0);
-    if (g + 2 < g_end) load(g + 2, f0);
-    compute(f1);
+  Frags f[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (g_begin + u < g_end) load(g_begin + u, f[u]);
+  for (int g = g_begin; g < g_end; g += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (g + u < g_end) compute(f[u]);
+      if (g + u + kAhead < g_end) load(g + u + kAhead, f[u]);
+    }
   }
-  if (g < g_end) compute(f0);
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) part[wave][i * NB + j][lane] = acc[i][j];
   __syncthreads();
-  for (int u = tid; u < MB * NB * 64; u += 64 * W) {
-    const int b = u >> 6;
+  for (int b = wave; b < MB * NB; b += W) {
     v4i sum = part[0][b][lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) sum += part[w][b][lane];
@@ -464,12 +498,21 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_few_kernel(I8Args p) {
     const int gn = n0 + (b % NB) * 16 + 4 * lk;
     if (gm >= p.M) continue;
     const float sav = p.K > 0 ? p.sa[gm] : 0.0f;
+    float v[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (gn + r >= p.N) break;
-      const float v = scaled(sum[r], sav, p.K > 0 ? p.sb[gn + r] : 0.0f);
-      if constexpr (kBf16) ((__bf16*)p.c)[(int64_t)gm * p.N + gn + r] = (__bf16)v;
-      else ((float*)p.c)[(int64_t)gm * p.N + gn + r] = v;
+    for (int r = 0; r < 4; ++r) v[r] = scaled(sum[r], sav, gn + r < p.N && p.K > 0 ? p.sb[gn + r] : 0.0f);
+    const int64_t at = (int64_t)gm * p.N + gn;
+    if (p.N % 4 == 0) {  // all four in or all out, and aligned
+      if (gn >= p.N) continue;
+      if constexpr (kBf16) *(bf16x4*)((__bf16*)p.c + at) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+      else *(v4f*)((float*)p.c + at) = v4f{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (gn + r >= p.N) break;
+        if constexpr (kBf16) ((__bf16*)p.c)[at + r] = (__bf16)v[r];
+        else ((float*)p.c)[at + r] = v[r];
+      }
     }
   }
 }
@@ -486,35 +529,58 @@ hipError_t launch_quant_int8_rows(const void* x, int64_t M, int64_t K, int8_t* q
   return hipGetLastError();
 }
 
-template <int BM, int BN, bool kGrouped>
+template <int BM, int BN, int D, int S, bool kGrouped>
 static hipError_t launch_tiles(const I8Args& a, bool bf16, int64_t m_tiles, hipStream_t stream) {
-  const dim3 grid((unsigned)(m_tiles * ((a.N + BN - 1) / BN))), block(256);
+  const dim3 grid((unsigned)(m_tiles * ((a.N + BN - 1) / BN))), block(256 * S);
   if (bf16)
-    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, true, kGrouped>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, D, S, true, kGrouped>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, false, kGrouped>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, D, S, false, kGrouped>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
-template <int MB, int NB, int W>
-static hipError_t launch_few(const I8Args& a, bool bf16, hipStream_t stream) {
+template <int MB, int NB, int W, int kAhead>
+static hipError_t launch_small(const I8Args& a, bool bf16, hipStream_t stream) {
   const int64_t wgs = (int64_t)((a.M + 16 * MB - 1) / (16 * MB)) * ((a.N + 16 * NB - 1) / (16 * NB));
   if (bf16)
-    hipLaunchKernelGGL((gemm_i8_few_kernel<MB, NB, W, true>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_small_kernel<MB, NB, W, kAhead, true>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
   else
-    hipLaunchKernelGGL((gemm_i8_few_kernel<MB, NB, W, false>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_small_kernel<MB, NB, W, kAhead, false>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
   return hipGetLastError();
 }
 
 hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
                             void* c, bool bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const I8Args p{(const uint8_t*)a, sa, (const uint8_t*)b, sb, c, nullptr, (int)M, (int)N, (int)K, 1};
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-  if (big < kCus / 2) {
-    if (M <= 16) return launch_few<1, 1, 8>(p, bf16, stream);
-    return launch_few<4, 2, 8>(p, bf16, stream);
-  }
-  return launch_tiles<256, 256, false>(p, bf16, (M + 255) / 256, stream);
+  // Workgroups of bm x bn outputs
+  auto wgs = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
+  // The smallest tile that still gives every CU at most one workgroup: below
+  // that, CUs idle while others load twice the operand bytes (a CU loads about
+  // 90 GB/s whatever its tile); above it, some CUs work twice. Measured on
+  // MI355X, us for the chosen tile against its neighbours in size:
+  //   64 x 512 x 512         16x16 2.70   32x16 2.98   32x32 3.24
+  //   256 x 512 x 2048       32x16 5.10   32x32 5.92   64x64 6.33
+  //   256 x 1024 x 512       32x32 3.40   32x16 3.90   64x64 4.64
+  //   333 x 2050 x 2064      64x64 8.76   64x128 11.8  32x32 15.4
+  //   1024 x 2048 x 2048     64x128 9.36  64x64 12.3   128x128 11.7
+  //   1024 x 4096 x 4096     128x128 20.1 64x128 26.7  256x256 45.7
+  // Long K is better shared through LDS: 32 x 7168 x 7168 takes 12.4 us in
+  // 64x64 tiles and 15.4 in 32x32; at K = 2048 6.4 and 6.9.
+  if (M <= 16 && wgs(16, 16) > kCus) return launch_small<1, 2, 8, 7>(p, bf16, stream);
+  if (wgs(16, 16) <= kCus) return launch_small<1, 1, 8, 4>(p, bf16, stream);
+  if (wgs(32, 16) <= kCus) return launch_small<2, 1, 8, 6>(p, bf16, stream);
+  if (wgs(32, 32) <= kCus && K < 2048) return launch_small<2, 2, 8, 4>(p, bf16, stream);
+  if (wgs(64, 64) <= kCus) return launch_tiles<64, 64, 3, 2, false>(p, bf16, (M + 63) / 64, stream);
+  if (wgs(64, 128) <= kCus) return launch_tiles<64, 128, 4, 1, false>(p, bf16, (M + 63) / 64, stream);
+  if (wgs(128, 128) <= kCus) return launch_tiles<128, 128, 3, 1, false>(p, bf16, (M + 127) / 128, stream);
+  // Large products: 256 x 256 tiles, one per CU, against 128 x 128, two at a
+  // time per CU, whose round takes 0.56 of the time of the other's (4096^3:
+  // 58.3 us in one round of 256, 65.6 in two of 128; 2048 x 4096 x 2048: 31.1
+  // in half a round of 256, 21.3 in one of 128)
+  const int64_t rounds256 = (wgs(256, 256) + kCus - 1) / kCus;
+  const int64_t rounds128 = (wgs(128, 128) + 2 * kCus - 1) / (2 * kCus);
+  if (rounds128 * 56 < rounds256 * 100) return launch_tiles<128, 128, 2, 1, false>(p, bf16, (M + 127) / 128, stream);
+  return launch_tiles<256, 256, 2, 1, false>(p, bf16, (M + 255) / 256, stream);
 }
 
 hipError_t launch_int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b,
@@ -522,8 +588,18 @@ hipError_t launch_int8_gemm_grouped(const int8_t* a, const float* sa, const int8
                                     int64_t G, int64_t M_total, int64_t N, int64_t K,
                                     hipStream_t stream) {
   const I8Args p{(const uint8_t*)a, sa, (const uint8_t*)b, sb, c, m_offsets, (int)M_total, (int)N, (int)K, (int)G};
+  // Rows per expert decide (M_total bounds them: the offsets stay on the GPU).
+  // us with 256 x 256 / 128 x 128 tiles, MI355X: 32 experts x 384 rows x 4096 x
+  // 2048 140 / 146, 8 x 512 x 4096 x 4096 59 / 81, 8 x 2048 x 4096 x 2048 139 /
+  // 186; but with one block of 128 rows each, half of a 256-row tile, 32 x 128 x
+  // 4096 x 7168 206 / 200 and 256 x 128 x 2048 x 2048 300 / 272. Where even 64 x
+  // 128 tiles leave CUs free they are used: 8 x 128 x 2048 x 2048 11.5 (128 x
+  // 128: 14.5).
+  const int64_t m128 = M_total / 128;
+  if (2 * m128 * ((N + 127) / 128) <= kCus) return launch_tiles<64, 128, 4, 1, true>(p, bf16, 2 * m128, stream);
+  if (M_total < 256 * G) return launch_tiles<128, 128, 2, 1, true>(p, bf16, m128, stream);
   // upper bound on sum_e ceil(rows_e / 256) for rows_e multiples of 128
-  return launch_tiles<256, 256, true>(p, bf16, (M_total / 128 + G + 1) / 2, stream);
+  return launch_tiles<256, 256, 2, 1, true>(p, bf16, (m128 + G + 1) / 2, stream);
 }
 
 }  // namespace fp8q
