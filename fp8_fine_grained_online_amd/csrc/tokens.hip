@@ -9,6 +9,8 @@
 // All three move rows and do almost no arithmetic: they are bound by HBM.
 // Rows are handled in chunks of 8 values, one chunk per lane (16 bytes of
 // bfloat16, 32 of float32).
+#include <type_traits>
+
 #include "common.hpp"
 #include "wave.hpp"
 
@@ -81,43 +83,151 @@ struct Chunk<float> {
 };
 
 // ---------------------------------------------------------------------------
-// permute: one wavefront per token copies its row to the rows of its valid
-// slots; further wavefronts, one per possible padding row (127 per expert),
-// zero the padding rows.
+// permute: one workgroup per token copies its row to the rows of its valid
+// slots; further workgroups, kPadParts per expert, zero the padding rows.
+//
+// Where a slot's row is comes from the dispatch's counting and scanning kernels
+// (row_of_slot holds ranks inside 256-slot blocks, `base` the blocks' first
+// rows; the rows replace the ranks here). With few slots (kSort) that is one
+// launch too many twice over: every workgroup then sorts the ids by itself, in
+// LDS, which takes it about 2 us, and the whole call is this kernel.
+//
+// Rows are written with ordinary stores even where they cannot stay in the
+// Infinity Cache: 8192 tokens x top-8 x 7168 took 197 us with them and 210 with
+// non-temporal ones (a wavefront per token, its row held in registers: 205 and
+// 227).
 // ---------------------------------------------------------------------------
-template <typename T, bool kNt>
-__global__ __launch_bounds__(64 * kTokWaves) void permute_copy_kernel(
-    const uint8_t* __restrict__ x, const int32_t* __restrict__ row_of_slot,
-    const int32_t* __restrict__ m_offsets, const int32_t* __restrict__ counts, int n_tok, int K,
-    int topk, int G, uint8_t* __restrict__ xp) {
+constexpr int kPadParts = 16;
+constexpr int kSortSlots = 4096;   // most slots a workgroup sorts by itself
+constexpr int kDispBlock = 256;    // slots per block of the counting kernel
+constexpr int kMaxExperts = 1024;
+
+struct PermuteArgs {
+  const uint8_t* x;
+  const int32_t* ids;
+  const int32_t* base;    // !kSort: first row of each (block, expert)
+  const int32_t* counts;  // !kSort: slots of each expert
+  int32_t* row_of_slot;
+  int32_t* m_offsets;
+  uint8_t* xp;
+  int n_tok, K, topk, G;
+};
+
+struct SortLds {
+  int32_t ids[kSortSlots];           // -1: dropped
+  int32_t counts[kMaxExperts];
+  int32_t offsets[kMaxExperts + 1];  // first row of each expert's block
+  int32_t wave_sum[kTokWaves];
+};
+
+struct NoSort {};
+
+// Counts and padded offsets of all experts, by the whole workgroup.
+__device__ __forceinline__ void sort_experts(SortLds& s, const int32_t* __restrict__ ids, int slots, int G) {
+  constexpr int kThreads = 64 * kTokWaves;
+  constexpr int kEach = kMaxExperts / kThreads;  // consecutive experts per thread
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < G; e += kThreads) s.counts[e] = 0;
+  __syncthreads();
+  for (int i = tid; i < slots; i += kThreads) {
+    const int e = ids[i];
+    const bool on = e >= 0 && e < G;
+    s.ids[i] = on ? e : -1;
+    if (on) atomicAdd(&s.counts[e], 1);  // integers: any order, the same counts
+  }
+  __syncthreads();
+  int padded[kEach], sum = 0;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int e = tid * kEach + u;
+    padded[u] = e < G ? (s.counts[e] + kGroup - 1) / kGroup * kGroup : 0;
+    sum += padded[u];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 63) s.wave_sum[wave] = incl;
+  __syncthreads();
+  int at = incl - sum;
+  for (int w = 0; w < wave; ++w) at += s.wave_sum[w];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int e = tid * kEach + u;
+    if (e < G) s.offsets[e] = at;
+    at += padded[u];
+    if (e == G - 1) s.offsets[G] = at;
+  }
+  __syncthreads();
+}
+
+template <typename T, bool kSort>
+__global__ __launch_bounds__(64 * kTokWaves) void permute_kernel(PermuteArgs a) {
   using C = Chunk<T>;
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * kTokWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n_chunks = K / 8;
+  constexpr int kThreads = 64 * kTokWaves;
+  constexpr int kHeld = 4;  // chunks of the row a lane holds at a time
+  __shared__ std::conditional_t<kSort, SortLds, NoSort> sort;
+  __shared__ int32_t rows[64];  // of the current 64 choices
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n_chunks = a.K / 8;
   const int64_t row_bytes = (int64_t)n_chunks * C::kBytes;
-  if (t >= n_tok) {
-    const int64_t pi = t - n_tok;
-    const int e = (int)(pi / (kGroup - 1));
-    if (e >= G) return;
-    const int64_t row = (int64_t)m_offsets[e] + counts[e] + pi % (kGroup - 1);
-    if (row >= m_offsets[e + 1]) return;
-    for (int c = lane; c < n_chunks; c += 64) C::template store<kNt>(xp + row * row_bytes + c * C::kBytes, C::zero());
+  const int64_t first_slot = (int64_t)blockIdx.x * a.topk;
+  if constexpr (kSort) {
+    sort_experts(sort, a.ids, a.n_tok * a.topk, a.G);
+    if (blockIdx.x == 0)
+      for (int e = tid; e <= a.G; e += kThreads) a.m_offsets[e] = sort.offsets[e];
+  }
+  if ((int)blockIdx.x >= a.n_tok) {
+    const int pad = blockIdx.x - a.n_tok;
+    const int e = pad / kPadParts;
+    int row, end;
+    if constexpr (kSort) row = sort.offsets[e] + sort.counts[e], end = sort.offsets[e + 1];
+    else row = a.m_offsets[e] + a.counts[e], end = a.m_offsets[e + 1];
+    for (row += pad % kPadParts; row < end; row += kPadParts)
+      for (int c = tid; c < n_chunks; c += kThreads)
+        C::template store<false>(a.xp + row * row_bytes + (int64_t)c * C::kBytes, C::zero());
     return;
   }
-  const uint8_t* xr = x + t * row_bytes;
-  constexpr int kHeld = 4;  // chunks of the row a lane holds at a time
-  for (int c0 = lane; c0 < n_chunks; c0 += 64 * kHeld) {
-    typename C::Raw v[kHeld];
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (c0 + 64 * u < n_chunks) v[u] = C::load_nt(xr + (int64_t)(c0 + 64 * u) * C::kBytes);
-    for (int j = 0; j < topk; ++j) {
-      const int row = row_of_slot[t * topk + j];
-      if (row < 0) continue;
+  const uint8_t* xr = a.x + blockIdx.x * row_bytes;
+  for (int j0 = 0; j0 < a.topk; j0 += 64) {
+    const int n = min(64, a.topk - j0);
+    // ---- rows of choices j0 .. j0 + n - 1 ----
+    if (j0 > 0) __syncthreads();
+    if constexpr (kSort) {
+      // a slot's rank: the earlier slots with its expert
+      for (int j = wave; j < n; j += kTokWaves) {
+        const int slot = (int)first_slot + j0 + j;
+        const int e = sort.ids[slot];
+        int rank = 0;
+        for (int i0 = 0; i0 < slot; i0 += 64)
+          rank += __popcll(__ballot(i0 + lane < slot && sort.ids[i0 + lane] == e));
+        if (lane == 0) rows[j] = e < 0 ? -1 : sort.offsets[e] + rank;
+      }
+    } else if (wave == 0 && lane < n) {
+      const int64_t slot = first_slot + j0 + lane;
+      const int rank = a.row_of_slot[slot];
+      rows[lane] = rank < 0 ? -1 : a.base[(slot / kDispBlock) * a.G + a.ids[slot]] + rank;
+    }
+    __syncthreads();
+    if (wave == 0 && lane < n) a.row_of_slot[first_slot + j0 + lane] = rows[lane];
+    const int lane_row = lane < n ? rows[lane] : -1;
+    // ---- copies ----
+    for (int c0 = tid; c0 < n_chunks; c0 += kThreads * kHeld) {
+      typename C::Raw v[kHeld];
 #pragma unroll
       for (int u = 0; u < kHeld; ++u)
-        if (c0 + 64 * u < n_chunks)
-          C::template store<kNt>(xp + row * row_bytes + (int64_t)(c0 + 64 * u) * C::kBytes, v[u]);
+        if (c0 + kThreads * u < n_chunks) v[u] = C::load_nt(xr + (int64_t)(c0 + kThreads * u) * C::kBytes);
+      for (int j = 0; j < n; ++j) {
+        const int row = __builtin_amdgcn_readlane(lane_row, j);
+        if (row < 0) continue;
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u)
+          if (c0 + kThreads * u < n_chunks)
+            C::template store<false>(a.xp + row * row_bytes + (int64_t)(c0 + kThreads * u) * C::kBytes, v[u]);
+      }
     }
   }
 }
@@ -273,31 +383,37 @@ __global__ __launch_bounds__(64 * kTokWaves) void combine_bwd_kernel(
   }
 }
 
-hipError_t launch_moe_dispatch(const void* x, const int32_t* ids, int64_t T, int64_t K, int64_t k,
-                               int64_t G, uint8_t* q, float* sa, int32_t* m_offsets,
-                               int32_t* row_of_slot, void* workspace, hipStream_t stream);
+// the dispatch's counting and scanning kernels, and its workspace: histogram,
+// first rows, counts
+__global__ void dispatch_count_kernel(const int32_t* __restrict__ ids, int S, int G,
+                                      int32_t* __restrict__ hist, int32_t* __restrict__ in_block);
+__global__ void dispatch_scan_kernel(const int32_t* __restrict__ hist, int n_blk, int G,
+                                     int32_t* __restrict__ base, int32_t* __restrict__ counts,
+                                     int32_t* __restrict__ m_offsets);
 int64_t dispatch_blocks(int64_t slots);
 
 hipError_t launch_moe_permute(const void* x, bool bf16, const int32_t* ids, int64_t T, int64_t K,
                               int64_t topk, int64_t G, void* xp, int32_t* m_offsets,
                               int32_t* row_of_slot, void* workspace, hipStream_t stream) {
-  hipError_t err = launch_moe_dispatch(nullptr, ids, T, 0, topk, G, nullptr, nullptr, m_offsets,
-                                       row_of_slot, workspace, stream);
-  if (err != hipSuccess || T == 0 || K == 0) return err;
-  // the dispatch leaves every expert's count behind its histogram and bases
-  const int32_t* counts = (const int32_t*)workspace + 2 * dispatch_blocks(T * topk) * G;
-  const int64_t waves = T + (kGroup - 1) * G;
-  const dim3 grid((unsigned)((waves + kTokWaves - 1) / kTokWaves)), block(64 * kTokWaves);
-  // rows larger than the 256 MB Infinity Cache cannot stay there for their reader
-  const bool nt = T * topk * K * (bf16 ? 2 : 4) > (int64_t(256) << 20);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, row_of_slot, m_offsets,
-                       counts, (int)T, (int)K, (int)topk, (int)G, (uint8_t*)xp);
-  };
+  const int64_t slots = T * topk, n_blk = dispatch_blocks(slots);
+  int32_t* hist = (int32_t*)workspace;
+  int32_t* base = hist + n_blk * G;
+  int32_t* counts = base + n_blk * G;
+  const bool sort = T > 0 && slots <= kSortSlots;
+  if (!sort) {
+    if (T > 0)
+      dispatch_count_kernel<<<dim3((unsigned)n_blk), dim3(kDispBlock), 0, stream>>>(ids, (int)slots, (int)G, hist, row_of_slot);
+    dispatch_scan_kernel<<<dim3(1), dim3(kMaxExperts), 0, stream>>>(hist, (int)n_blk, (int)G, base, counts, m_offsets);
+    if (T == 0) return hipGetLastError();
+  }
+  const PermuteArgs a{(const uint8_t*)x, ids, base, counts, row_of_slot, m_offsets, (uint8_t*)xp,
+                      (int)T, (int)K, (int)topk, (int)G};
+  const dim3 grid((unsigned)(T + (K > 0 ? kPadParts * G : 0))), block(64 * kTokWaves);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
   if (bf16)
-    nt ? go(permute_copy_kernel<uint16_t, true>) : go(permute_copy_kernel<uint16_t, false>);
+    sort ? go(permute_kernel<uint16_t, true>) : go(permute_kernel<uint16_t, false>);
   else
-    nt ? go(permute_copy_kernel<float, true>) : go(permute_copy_kernel<float, false>);
+    sort ? go(permute_kernel<float, true>) : go(permute_kernel<float, false>);
   return hipGetLastError();
 }
 
