@@ -498,7 +498,7 @@ int fp8q_moe_combine_bwd(const void* dy, int dy_dtype, const void* c, int c_dtyp
   if (s) return s;
   if (G < 1) return FP8Q_ERR_SHAPE;
   if (!known_dtype(dy_dtype) || !known_dtype(c_dtype)) return FP8Q_ERR_DTYPE;
-  if (G > kMaxExperts || T > kMaxDim - kMaxExperts) return FP8Q_ERR_TOO_LARGE;
+  if (G > kMaxExperts || T > kMaxDim - 16 * kMaxExperts) return FP8Q_ERR_TOO_LARGE;
   if (!m_offsets || (T > 0 && !row_of_slot)) return FP8Q_ERR_NULL;
   if (K > 0 && ((T > 0 && !dy) || (M > 0 && !dc) || (M > 0 && T > 0 && dw && !c))) return FP8Q_ERR_NULL;
   if (!aligned(dy, 16) || !aligned(c, 16) || !aligned(dc, 16) || !aligned(row_of_slot, 4) ||
