@@ -443,7 +443,7 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
       using Unit = decltype(unit);
       constexpr int kUnits = kRowBytes / (int)sizeof(Unit);  // of a row
       static_assert(kUnits % 64 == 0 || 64 % kUnits == 0, "whole wave stores");
-      // (the narrow forms stay loops: unrolled, the three outgrow the instruction cache)
+      // (the narrow forms stay loops: fully unrolled, the three outgrow the instruction cache)
       auto piece = [&](int k) {
         const int m = (k * 64 + lane) / kUnits, byte = (k * 64 + lane) % kUnits * (int)sizeof(Unit);
         const int om = m0 + wm * WM + i * 16 + m;
@@ -455,7 +455,7 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
 #pragma unroll
         for (int k = 0; k < kUnits / 4; ++k) piece(k);
       } else {
-#pragma unroll 1
+#pragma unroll 4
         for (int k = 0; k < kUnits / 4; ++k) piece(k);
       }
     };

@@ -8,7 +8,8 @@
 //
 // One wavefront per token, lane l holding the E consecutive experts from l E
 // on (E = 1, 2, 4, 8, 16: up to 1024 experts), so that the lowest lane of a
-// tie has the lowest index. Scores are float64: whether an expert is chosen is
+// tie has the lowest index. A lane sorts its keys once; each choice is then one
+// maximum over the wavefront, and the winner's next key moves up. Scores are float64: whether an expert is chosen is
 // a comparison of two nearly equal numbers, and its answer should be that of
 // the formula, not of the rounding.
 #include "common.hpp"
@@ -25,13 +26,62 @@ struct RouteArgs {
   const float* bias;
   int T, G, topk, n_groups, topk_groups;
   int sigmoid, renorm;
+  int whole;  // a lane's experts are all in the row or all past it, and aligned
   float scale;
   int32_t* ids;
   float* w;
 };
 
-__device__ __forceinline__ float load_logit(const float* p) { return *p; }
-__device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ float as_logit(float v) { return v; }
+__device__ __forceinline__ float as_logit(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// The E consecutive logits from `at` on; masked (-inf) past the row's G. With
+// `whole` (uniform) every lane's E are inside or outside the row, and aligned.
+template <int E, typename Tin>
+__device__ __forceinline__ void load_logits(const Tin* row, int at, int G, bool whole, float (&x)[E]) {
+  typedef Tin vec __attribute__((ext_vector_type(E > 1 ? E : 2), aligned(E * sizeof(Tin) < 16 ? E * sizeof(Tin) : 16)));
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = -__builtin_huge_valf();
+  if (E > 1 && whole) {
+    if (at < G) {
+      const vec v = *(const vec*)(row + at);
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = as_logit((Tin)v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (at + i < G) x[i] = as_logit(row[at + i]);
+  }
+}
+
+// e^x for x <= 710 to about one unit in the last place: x = k ln 2 + r with ln 2
+// in two parts, the Taylor series of e^r to r^13 (|r| <= 0.347: the next term is
+// below 5e-18), and the power of two put back.
+__device__ __forceinline__ double exp64(double x) {
+  x = __builtin_fmax(x, -746.0);  // e^-746 rounds to 0
+  const double k = __builtin_rint(x * 0x1.71547652b82fep+0);
+  double r = __builtin_fma(k, -0x1.62e42fefa3p-1, x);  // the first 41 bits of ln 2: exact
+  r = __builtin_fma(k, -0x1.3de6af278ece6p-42, r);     // and the next 53
+  constexpr double c[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
+                            1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600, 1.0 / 6227020800};
+  double s = c[13];
+#pragma unroll
+  for (int i = 12; i >= 0; --i) s = __builtin_fma(s, r, c[i]);
+  return __builtin_ldexp(s, (int)k);
+}
+
+// 1 / d for 1 <= d < 2^1023: two Newton steps from the hardware's estimate
+__device__ __forceinline__ double recip64(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+
+__device__ __forceinline__ double sigmoid64(float x) {
+  // e^709 + 1 still has a reciprocal; past it the formula's value is below 2^-1022
+  return x < -709.0f ? 0.0 : recip64(1.0 + exp64(-(double)x));
+}
 
 // 64-bit key ordered like the double; 0 (below every finite value's key) marks
 // an expert that may not be chosen.
@@ -59,15 +109,55 @@ __device__ __forceinline__ uint64_t wave_best(uint64_t k, int& lane) {
   return ((uint64_t)mhi << 32) | lane_u32(lo, lane);
 }
 
-// Probability of expert l E + i for a lane's E logits; masked ones have 0.
+// A lane's E keys, largest first, with their places in the lane; equal keys by
+// place (Batcher's odd-even merging network).
 template <int E>
-__device__ __forceinline__ void route_scores(const float (&x)[E], bool sigmoid, double (&p)[E]) {
-  constexpr float kNegInf = -__builtin_huge_valf();
-  if (sigmoid) {
+__device__ __forceinline__ void sort_lane(uint64_t (&k)[E], int (&at)[E]) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) p[i] = x[i] > kNegInf ? 1.0 / (1.0 + exp(-(double)x[i])) : 0.0;
-    return;
+  for (int p = 1; p < E; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < E; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          const int u = i + j, v = i + j + q;
+          if (v < E && u / (2 * p) == v / (2 * p)) {
+            const bool swap = k[v] > k[u] || (k[v] == k[u] && at[v] < at[u]);
+            const uint64_t ku = k[u];
+            const int au = at[u];
+            k[u] = swap ? k[v] : ku, at[u] = swap ? at[v] : au;
+            k[v] = swap ? ku : k[v], at[v] = swap ? au : at[v];
+          }
+        }
+}
+
+// The two largest of the pairs (k0 >= k1) of neighbouring lanes, folded over
+// runs of `lanes` (a power of two); every lane of a run gets the result.
+__device__ __forceinline__ void merge_two(uint64_t& k0, uint64_t& k1, uint64_t o0, uint64_t o1) {
+  const uint64_t low = min(k0, o0);
+  k0 = max(k0, o0);
+  k1 = max(low, max(k1, o1));
+}
+template <int kCtrl>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
+  return ((uint64_t)dpp_u32<kCtrl>((uint32_t)(v >> 32)) << 32) | dpp_u32<kCtrl>((uint32_t)v);
+}
+__device__ __forceinline__ void fold_two(uint64_t& k0, uint64_t& k1, int lanes) {
+  if (lanes >= 2) merge_two(k0, k1, dpp_u64<0xB1>(k0), dpp_u64<0xB1>(k1));
+  if (lanes >= 4) merge_two(k0, k1, dpp_u64<0x4E>(k0), dpp_u64<0x4E>(k1));
+  if (lanes >= 8) merge_two(k0, k1, dpp_u64<0x141>(k0), dpp_u64<0x141>(k1));
+  if (lanes >= 16) merge_two(k0, k1, dpp_u64<0x140>(k0), dpp_u64<0x140>(k1));
+  for (int d = 16; d < lanes; d *= 2) {
+    const uint64_t o0 = __shfl_xor((unsigned long long)k0, d), o1 = __shfl_xor((unsigned long long)k1, d);
+    merge_two(k0, k1, o0, o1);
   }
+}
+
+// Numerators of the softmax (all over `sum`), or sigmoids; masked logits have 0.
+template <int E>
+__device__ __forceinline__ double softmax_terms(const float (&x)[E], double (&p)[E]) {
+  constexpr float kNegInf = -__builtin_huge_valf();
   // order the floats as integers: the maximum over the wavefront is exact
   uint32_t m = 0;
 #pragma unroll
@@ -80,57 +170,62 @@ __device__ __forceinline__ void route_scores(const float (&x)[E], bool sigmoid, 
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    p[i] = x[i] > kNegInf ? exp((double)x[i] - top) : 0.0;
+    p[i] = x[i] > kNegInf ? exp64((double)x[i] - top) : 0.0;
     sum += p[i];
   }
-  sum = wave_sum_f64(sum);
-#pragma unroll
-  for (int i = 0; i < E; ++i) p[i] = sum > 0.0 ? p[i] / sum : 0.0;
+  return wave_sum_f64(sum);
 }
 
 template <int E, typename Tin>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
-  __shared__ uint64_t group_keys[kRouteWaves][64 * E];
+  // scores by expert: the probabilities of the chosen are looked up at the end,
+  // and group scores that do not fall on whole lanes are formed here
+  __shared__ uint64_t table[kRouteWaves][64 * E];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x * kRouteWaves + wave;
   if (t >= a.T) return;
-  const Tin* row = (const Tin*)a.logits + (int64_t)t * a.G;
+  uint64_t* const tab = table[wave];
   float x[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int e = lane * E + i;
-    x[i] = e < a.G ? load_logit(row + e) : -__builtin_huge_valf();
-  }
+  load_logits<E>((const Tin*)a.logits + (int64_t)t * a.G, lane * E, a.G, a.whole, x);
   double p[E];
-  route_scores<E>(x, a.sigmoid, p);
+  if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) p[i] = x[i] > -__builtin_huge_valf() ? sigmoid64(x[i]) : 0.0;
+  } else {
+    const double sum = softmax_terms<E>(x, p);
+    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;  // (no logit but masked ones: 0)
+#pragma unroll
+    for (int i = 0; i < E; ++i) p[i] *= inv;
+  }
   uint64_t key[E];
+  int place[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const int e = lane * E + i;
     const double z = (a.bias && e < a.G) ? p[i] + (double)a.bias[e] : p[i];
     key[i] = x[i] > -__builtin_huge_valf() ? order_key(z) : 0;
+    place[i] = i;
   }
 
-  if (a.n_groups > 1) {
-    // a group's two largest keys, found by the lane of its number
-    uint64_t* k = group_keys[wave];
+  const int gs = a.G / a.n_groups;
+  const int lanes = gs / E;  // of a group, if groups fall on whole lanes
+  const bool by_lanes = gs % E == 0 && (lanes & (lanes - 1)) == 0;
+  if (a.n_groups > 1 && !by_lanes) {
+    // the two largest keys of group g, by lane g; experts of closed groups lose theirs
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (lane * E + i < a.G) k[lane * E + i] = key[i];
+    for (int i = 0; i < E; ++i) tab[lane * E + i] = key[i];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int gs = a.G / a.n_groups;
     uint64_t g1 = 0, g2 = 0;
     if (lane < a.n_groups) {
       for (int i = 0; i < gs; ++i) {
-        const uint64_t v = k[lane * gs + i];
+        const uint64_t v = tab[lane * gs + i];
         g2 = max(g2, min(g1, v));
         g1 = max(g1, v);
       }
     }
-    const double gz = g1 ? key_value(g1) + (g2 ? key_value(g2) : 0.0) : -__builtin_huge_val();
-    uint64_t gk = order_key(gz);
+    uint64_t gk = g1 ? order_key(key_value(g1) + (g2 ? key_value(g2) : 0.0)) : 0;
     uint64_t open = 0;  // bit g: group g may be used (wave-uniform)
     for (int j = 0; j < a.topk_groups; ++j) {
       int at;
@@ -143,30 +238,43 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
       const int e = lane * E + i;
       if (e < a.G && !((open >> (e / gs)) & 1)) key[i] = 0;
     }
+    __builtin_amdgcn_wave_barrier();
+  }
+  sort_lane<E>(key, place);
+  if (a.n_groups > 1 && by_lanes) {
+    uint64_t g1 = key[0], g2 = E > 1 ? key[E > 1 ? 1 : 0] : 0;
+    fold_two(g1, g2, lanes);
+    uint64_t gk = g1 ? order_key(key_value(g1) + (g2 ? key_value(g2) : 0.0)) : 0;
+    bool open = false;
+    for (int j = 0; j < a.topk_groups; ++j) {
+      int at;
+      if (!wave_best(gk, at)) break;
+      if ((lane & -lanes) == (at & -lanes)) open = true, gk = 0;  // the winner's run of lanes
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) key[i] = open ? key[i] : 0;
   }
 
-  int my_id = -1;     // lane j: choice j
-  double my_p = 0.0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) tab[lane * E + i] = (uint64_t)__double_as_longlong(p[i]);
+  int my_id = -1;  // lane j: choice j
   for (int j = 0; j < a.topk; ++j) {
-    uint64_t bk = key[0];
-    int bi = 0;
-    double bp = p[0];
-#pragma unroll
-    for (int i = 1; i < E; ++i)
-      if (key[i] > bk) bk = key[i], bi = i, bp = p[i];
     int at;
-    if (!wave_best(bk, at)) break;  // nothing left to choose
-    const int id = at * E + __builtin_amdgcn_readlane(bi, at);
-    const double pj = lane_f64(bp, at);
-    if (lane == j) my_id = id, my_p = pj;
+    if (!wave_best(key[0], at)) break;  // nothing left to choose
+    const int id = at * E + __builtin_amdgcn_readlane(place[0], at);
+    if (lane == j) my_id = id;
+    // the winner's next key moves up
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (lane == at && i == bi) key[i] = 0;
+    for (int i = 0; i + 1 < E; ++i)
+      if (lane == at) key[i] = key[i + 1], place[i] = place[i + 1];
+    if (lane == at) key[E - 1] = 0;
   }
-  double w = my_p;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  double w = my_id >= 0 ? __longlong_as_double((long long)tab[my_id]) : 0.0;
   if (a.renorm) {
-    const double sum = wave_sum_f64(my_p);
-    w = sum > 0.0 ? my_p / sum : 0.0;
+    const double sum = wave_sum_f64(w);
+    w = sum > 0.0 ? w / sum : 0.0;
   }
   if (lane < a.topk) {
     a.ids[(int64_t)t * a.topk + lane] = my_id;
@@ -198,14 +306,32 @@ __device__ __forceinline__ void store_logit(uint16_t* p, double v) {
   *p = __builtin_bit_cast(uint16_t, b);
 }
 
+//
+// The row is put together in LDS: zeros, then the choices' shares at their
+// experts. Should an expert be listed twice, which shows when a lane does not
+// read back the number it wrote there, the shares are added one by one.
 template <int E, typename Tin>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteBwdArgs a) {
   constexpr float kNegInf = -__builtin_huge_valf();
+  __shared__ double shares[kRouteWaves][64 * E];
+  __shared__ int owners[kRouteWaves][64 * E];
   const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * kRouteWaves + wave;
   if (t >= a.T) return;
+  double* const share = shares[wave];
+  int* const owner = owners[wave];
   const Tin* row = (const Tin*)a.logits + (int64_t)t * a.G;
   Tin* drow = (Tin*)a.dlogits + (int64_t)t * a.G;
+  const bool dense = !a.sigmoid && !a.renorm;
+  float x[E];  // lane l holds the experts l + 64 i: dlogits are stored in runs of 64
+  if (dense) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int e = i * 64 + lane;
+      x[i] = e < a.G ? as_logit(row[e]) : kNegInf;
+    }
+  }
   int id = -1;
   double g = 0.0;
   if (lane < a.topk) {
@@ -214,54 +340,58 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteBwdArg
   }
   const bool on = id >= 0 && id < a.G;
   if (!on) id = -1, g = 0.0;
-  const float xj = on ? load_logit(row + id) : kNegInf;
-  const bool dense = !a.sigmoid && !a.renorm;
-
-  double v;  // this choice's share of dl[id]
-  double p[E];
-  double mean = 0.0;
-  if (dense) {
-    // lane l holds the experts l + 64 i here: dlogits are stored in rows of 64
-    float x[E];
+  const float xj = on ? as_logit(row[id]) : kNegInf;
+  if (on) owner[id] = lane;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int e = i * 64 + lane;
-      x[i] = e < a.G ? load_logit(row + e) : kNegInf;
-    }
-    route_scores<E>(x, false, p);
-    v = g;
-  } else if (a.sigmoid) {
+  for (int i = 0; i < E; ++i) share[i * 64 + lane] = 0.0;
+
+  double v = g;  // this choice's share of dl[id]; of the dense form, of dp[id]
+  if (a.sigmoid) {
     const bool live = xj > kNegInf;
-    const double pj = live ? 1.0 / (1.0 + exp(-(double)xj)) : 0.0;
-    const double rest = live ? 1.0 / (1.0 + exp((double)xj)) : 0.0;  // 1 - pj, without cancellation
-    double dp = g;
+    // p and 1 - p, the smaller one without cancellation
+    const double ex = live ? exp64(-__builtin_fabs((double)xj)) : 0.0;
+    const double big = recip64(1.0 + ex), small = ex * big;
+    const double pj = !live ? 0.0 : xj >= 0.0f ? big : small;
+    const double rest = !live ? 0.0 : xj >= 0.0f ? small : big;
     if (a.renorm) {
       const double sum = wave_sum_f64(pj);
       const double gp = wave_sum_f64(g * pj);
-      dp = (on && sum > 0.0) ? (g - gp / sum) / sum : 0.0;
+      v = (on && sum > 0.0) ? (g - gp / sum) / sum : 0.0;
     }
-    v = dp * pj * rest;
-  } else {
+    v *= pj * rest;
+  } else if (!dense) {
     const float one[1] = {xj};
     double q[1];
-    route_scores<1>(one, false, q);
+    const double sum = softmax_terms<1>(one, q);
+    q[0] = sum > 0.0 ? q[0] / sum : 0.0;
     const double gq = wave_sum_f64(g * q[0]);
     v = on ? q[0] * (g - gq) : 0.0;
   }
 
+  // (the wave's LDS accesses are in order; the fence keeps the compiler to it)
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const bool alone = !on || owner[id] == lane;
+  if (__ballot(!alone) == 0) {
+    if (on) share[id] = v;
+  } else {
+    for (int j = 0; j < a.topk; ++j) {  // wave-uniform; in order
+      if (lane == j && on) share[id] += v;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
   double d[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i) d[i] = 0.0;
-  for (int j = 0; j < a.topk; ++j) {
-    const int ej = __builtin_amdgcn_readlane(id, j);
-    const double vj = lane_f64(v, j);
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (ej == i * 64 + lane) d[i] += vj;
-  }
+  for (int i = 0; i < E; ++i) d[i] = share[i * 64 + lane];
   if (dense) {
+    double p[E], mean = 0.0;
+    const double sum = softmax_terms<E>(x, p);
+    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) mean += d[i] * p[i];
+    for (int i = 0; i < E; ++i) p[i] *= inv, mean += d[i] * p[i];
     mean = wave_sum_f64(mean);
 #pragma unroll
     for (int i = 0; i < E; ++i) d[i] = p[i] * (d[i] - mean);
@@ -283,11 +413,13 @@ static void by_experts(const Args& a, Launch&& launch) {
 hipError_t launch_route(const void* logits, bool bf16, const float* bias, int64_t T, int64_t G,
                         int64_t topk, int64_t n_groups, int64_t topk_groups, bool sigmoid,
                         bool renorm, float scale, int32_t* ids, float* w, hipStream_t stream) {
-  const RouteArgs a{logits, bias, (int)T, (int)G, (int)topk, (int)n_groups, (int)topk_groups,
-                    sigmoid, renorm, scale, ids, w};
+  RouteArgs a{logits, bias, (int)T, (int)G, (int)topk, (int)n_groups, (int)topk_groups,
+              sigmoid, renorm, 0, scale, ids, w};
   const dim3 grid((unsigned)((T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
   by_experts(a, [&](auto e) {
     constexpr int E = decltype(e)::value;
+    const int bytes = E * (bf16 ? 2 : 4);
+    a.whole = G % E == 0 && (uintptr_t)logits % (bytes < 16 ? bytes : 16) == 0 && G % (bytes < 16 ? E : 16 / (bf16 ? 2 : 4)) == 0;
     if (bf16)
       hipLaunchKernelGGL((route_kernel<E, uint16_t>), grid, block, 0, stream, a);
     else
