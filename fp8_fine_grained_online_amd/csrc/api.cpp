@@ -129,6 +129,9 @@ int check_gemm_common(const uint8_t* a, const float* sa, const uint8_t* b, const
   return FP8Q_OK;
 }
 
+// One launch holds less than 2^32 threads.
+bool launchable(int64_t workgroups, int64_t threads) { return workgroups * threads < (int64_t(1) << 32); }
+
 bool known_dtype(int d) { return d == FP8Q_OUT_F32 || d == FP8Q_OUT_BF16; }
 
 // Sizes shared by the calls that move rows between tokens and experts.
@@ -143,8 +146,10 @@ int check_int8(const int8_t* a, const float* sa, const int8_t* b, const float* s
   if (M < 0 || N < 0 || K < 0 || K % 16) return FP8Q_ERR_SHAPE;
   if (!known_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
   if (M > kMaxDim || N > kMaxDim || K > kInt8MaxK) return FP8Q_ERR_TOO_LARGE;
-  // tiles, of 16 x 16 outputs at the least, are numbered with 32 bits
-  if ((M + 15) / 16 * ((N + 15) / 16) > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  // tiles are numbered with 32 bits; where there are many they are 128 x 128 or
+  // larger (16 x 32 for up to 16 rows, by workgroups of 512 threads)
+  const int64_t tm = M <= 16 ? 1 : (M + 127) / 128, tn = M <= 16 ? (N + 31) / 32 : (N + 127) / 128;
+  if (tm * tn > kMaxDim || !launchable(tm * tn, M <= 16 ? 512 : 256)) return FP8Q_ERR_TOO_LARGE;
   if (M == 0 || N == 0) return -1;  // valid no-op
   if (!c) return FP8Q_ERR_NULL;
   if (K > 0 && (!a || !sa || !b || !sb)) return FP8Q_ERR_NULL;  // K == 0 reads no operand
@@ -414,6 +419,7 @@ int fp8q_moe_route(const void* logits, int dtype, const float* bias, int64_t T, 
     return FP8Q_ERR_SHAPE;
   if (G > kMaxExperts || topk > kMaxTopk || n_groups > kMaxGroups || T > kMaxDim / topk)
     return FP8Q_ERR_TOO_LARGE;
+  if (!launchable((T + 3) / 4, 256)) return FP8Q_ERR_TOO_LARGE;
   if (G % n_groups || topk > topk_groups * (G / n_groups)) return FP8Q_ERR_SHAPE;
   if (score != FP8Q_SCORE_SOFTMAX && score != FP8Q_SCORE_SIGMOID) return FP8Q_ERR_SHAPE;
   if (renormalize != 0 && renormalize != 1) return FP8Q_ERR_SHAPE;
@@ -435,6 +441,7 @@ int fp8q_moe_route_bwd(const void* logits, int dtype, const int32_t* topk_ids, c
                        void* dlogits, void* stream) {
   if (T < 0 || G < 1 || topk < 1) return FP8Q_ERR_SHAPE;
   if (G > kMaxExperts || topk > kMaxTopk || T > kMaxDim / topk) return FP8Q_ERR_TOO_LARGE;
+  if (!launchable((T + 3) / 4, 256)) return FP8Q_ERR_TOO_LARGE;
   if (score != FP8Q_SCORE_SOFTMAX && score != FP8Q_SCORE_SIGMOID) return FP8Q_ERR_SHAPE;
   if (renormalize != 0 && renormalize != 1) return FP8Q_ERR_SHAPE;
   if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return FP8Q_ERR_SHAPE;
@@ -457,7 +464,7 @@ int fp8q_moe_permute(const void* x, int dtype, const int32_t* topk_ids, int64_t 
   if (s) return s;
   if (G < 1) return FP8Q_ERR_SHAPE;
   if (!known_dtype(dtype)) return FP8Q_ERR_DTYPE;
-  if (G > kMaxExperts || T > kMaxDim / 4) return FP8Q_ERR_TOO_LARGE;
+  if (G > kMaxExperts || !launchable(T + 16 * G, 256)) return FP8Q_ERR_TOO_LARGE;
   const int64_t need_rows = dispatch_max_rows(T, topk, G);
   if (need_rows > kMaxDim) return FP8Q_ERR_TOO_LARGE;
   if (M_cap < need_rows) return FP8Q_ERR_SHAPE;  // outputs too small for the worst-case padding
@@ -479,7 +486,7 @@ int fp8q_moe_combine(const void* c, int c_dtype, const int32_t* row_of_slot, con
   int s = check_rows(T, K, topk, M);
   if (s) return s;
   if (!known_dtype(c_dtype) || !known_dtype(y_dtype)) return FP8Q_ERR_DTYPE;
-  if (T * ((K / 8 + 63) / 64) > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  if (T > 0 && !launchable((T * ((K / 8 + 63) / 64) + 3) / 4, 256)) return FP8Q_ERR_TOO_LARGE;
   if (T == 0 || K == 0) return FP8Q_OK;
   if (!row_of_slot || !y || (M > 0 && !c)) return FP8Q_ERR_NULL;
   if (!aligned(c, 16) || !aligned(y, 16) || !aligned(row_of_slot, 4) || !aligned(weights, 4))
@@ -498,7 +505,7 @@ int fp8q_moe_combine_bwd(const void* dy, int dy_dtype, const void* c, int c_dtyp
   if (s) return s;
   if (G < 1) return FP8Q_ERR_SHAPE;
   if (!known_dtype(dy_dtype) || !known_dtype(c_dtype)) return FP8Q_ERR_DTYPE;
-  if (G > kMaxExperts || T > kMaxDim - 16 * kMaxExperts) return FP8Q_ERR_TOO_LARGE;
+  if (G > kMaxExperts || !launchable(T + 16 * G, 256)) return FP8Q_ERR_TOO_LARGE;
   if (!m_offsets || (T > 0 && !row_of_slot)) return FP8Q_ERR_NULL;
   if (K > 0 && ((T > 0 && !dy) || (M > 0 && !dc) || (M > 0 && T > 0 && dw && !c))) return FP8Q_ERR_NULL;
   if (!aligned(dy, 16) || !aligned(c, 16) || !aligned(dc, 16) || !aligned(row_of_slot, 4) ||
@@ -514,7 +521,7 @@ int fp8q_moe_combine_bwd(const void* dy, int dy_dtype, const void* c, int c_dtyp
 int fp8q_quant_int8_rows(const void* x_bf16, int64_t M, int64_t K, int8_t* q, float* s,
                          void* stream) {
   if (M < 0 || K < 0 || K % 16) return FP8Q_ERR_SHAPE;
-  if (M > kMaxDim || K > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  if (M > kMaxDim || K > kMaxDim || !launchable(K <= 2048 ? (M + 3) / 4 : M, 256)) return FP8Q_ERR_TOO_LARGE;
   if (M == 0) return FP8Q_OK;
   if (!s || (K > 0 && (!x_bf16 || !q))) return FP8Q_ERR_NULL;
   if (!aligned(x_bf16, 16) || !aligned(q, 16) || !aligned(s, 4)) return FP8Q_ERR_ALIGN;
@@ -540,7 +547,7 @@ int int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b, const f
   if (s == -1) return FP8Q_OK;
   if (s) return s;
   // the grid holds up to one more tile row per expert
-  if ((M_total / kGroup + G + 1) * ((N + 63) / 64) > kMaxDim) return FP8Q_ERR_TOO_LARGE;
+  if (!launchable((M_total / kGroup + G + 1) * ((N + 127) / 128), 256)) return FP8Q_ERR_TOO_LARGE;
   if (!m_offsets) return FP8Q_ERR_NULL;
   if (!aligned(m_offsets, 4)) return FP8Q_ERR_ALIGN;
   if ((s = check_device())) return s;
