@@ -1,7 +1,7 @@
-"""ctypes binding of libfp8q.so: argument marshalling only."""
+"""Binding of libfp8q.so: argument marshalling only (ctypes; the calls that a layer
+makes for single tokens through a native extension, csrc/binding.cpp)."""
 
 import ctypes
-import functools
 import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -197,7 +197,7 @@ def fp8q_quant_weight_128x128(w, q=None, sb=None, stream=None):
 
 
 def _out_dtype(out_dtype):
-    torch = _t or _torch()
+    torch = _torch()
     if out_dtype in (torch.bfloat16, "bf16", FP8Q_OUT_BF16):
         return FP8Q_OUT_BF16, torch.bfloat16
     if out_dtype in (torch.float32, "f32", FP8Q_OUT_F32):
@@ -484,88 +484,44 @@ def fp8_gemm_rowscaled(a, sa, b, sb, out_dtype="f32", c=None, stream=None):
 
 
 # ---- MoE layer around the experts' products, and the 8-bit integer product ----
+#
+# These calls are short enough for a binding's own time to count, so their
+# argument checks and allocations are native (csrc/binding.cpp).
 
-# These calls are short enough for the binding's own time to count (a serving
-# step's router takes a few microseconds on the GPU), so each tensor is checked
-# in one expression and only a failing one is looked at again for its message.
-_t = None            # the torch module, once a call has needed it
-_types = None        # element type -> fp8q_out_dtype code
-_raw_stream = None   # device index -> its current stream's hipStream_t
-_current_device = None
+_native = None  # the extension module, once a call has needed it
 
 
-def _bind(first):
-    """The torch module, and the device index of a call's first tensor."""
-    global _t, _types, _raw_stream, _current_device
-    if _t is None:
-        torch = _torch()
-        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        _types = {torch.float32: FP8Q_OUT_F32, torch.bfloat16: FP8Q_OUT_BF16}
-        _t = torch
-    try:
-        return _t, first.get_device()
-    except AttributeError:
-        raise TypeError("arguments must be torch.Tensors") from None
+def _binding():
+    global _native
+    if _native is None:
+        _torch()  # the extension links to its libraries
+        path = os.path.join(PKG_DIR, "_binding.so")
+        if not os.path.exists(path):
+            raise ImportError(
+                f"{path} is missing: build it with `python -m fp8_fine_grained_online_amd.build`"
+                " (there is no fallback path)")
+        lib()
+        from . import _binding as module
+        _native = module
+    return _native
 
 
-def _ptr(t, name, dtype, ndim, index):
-    """Address of a contiguous tensor of `dtype` (None: float32 or bfloat16) with ndim dims on device `index`."""
-    try:
-        if ((t.dtype is dtype or dtype is None and t.dtype in _types) and t.dim() == ndim
-                and t.get_device() == index >= 0 and t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch.Tensor") from None
-    if not t.is_cuda or t.get_device() != index:
-        raise ValueError(f"{name} must be a device tensor on the call's device (index {index}), got {t.device}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise TypeError(f"{name} must be {dtype or sorted(map(str, _types))}, got {t.dtype}")
-
-
-def _result(t, name, shape, dtype, first, stream):
-    """An output the caller passed (checked), or a new one on `first`'s device,
-    taken from the memory pool of the stream the call runs on: memory freed on
-    another stream may still be in use there."""
-    if t is None:
-        if stream is None:
-            # (with its strides given, an allocation takes a quarter less time)
-            if len(shape) == 2:
-                return _t.empty_strided(shape, (shape[1] or 1, 1), dtype=dtype, device=first.device)
-            return _t.empty(shape, dtype=dtype, device=first.device)
-        cuda = _t.cuda
+def _run(fn, stream, first, *args):
+    """A native call on the current stream of the tensors' device, or with
+    `stream` current: new outputs then come from that stream's memory too
+    (memory freed on another stream may still be in use there)."""
+    call = getattr(_native or _binding(), fn)
+    if stream is None:
+        result = call(first, *args)
+    else:
+        cuda = _torch().cuda
         if not hasattr(stream, "cuda_stream"):
             stream = cuda.ExternalStream(int(stream), device=first.device)
         with cuda.stream(stream):
-            return first.new_empty(shape, dtype=dtype)
-    _ptr(t, name, dtype, len(shape), first.get_device())
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
-
-
-_entries = {}  # name -> entry point, once the library is there
-
-
-def _launch(fn, index, stream, *args):
-    """The entry point on device `index` (made current if it is not), on its
-    current stream unless one is given."""
-    entry = _entries.get(fn)
-    if entry is None:
-        entry = _entries[fn] = getattr(lib(), fn)
-    if stream is None:
-        sp = _raw_stream(index)
-    else:
-        sp = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if _current_device() == index:
-        status = entry(*args, sp)
-    else:
-        with _torch().cuda.device(index):
-            status = entry(*args, sp)
-    if status:
-        _check(fn, status)
+            result = call(first, *args)
+    if type(result) is int:
+        _check(fn, result)
+    return result
 
 
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -582,45 +538,15 @@ def fp8q_moe_route(logits, topk, bias=None, score="softmax", renormalize=True, s
     """Router: logits T x G (float32 or bfloat16) -> (topk_ids int32 T x topk, weights float32
     T x topk). bias (float32, G) is added to the probabilities for the choice only; with
     n_groups > 1 experts come from the topk_groups best groups."""
-    torch, index = _bind(logits)
-    px = _ptr(logits, "logits", None, 2, index)
-    T, G = logits.shape
-    pb = None
-    if bias is not None:
-        pb = _ptr(bias, "bias", torch.float32, 1, index)
-        if bias.shape[0] != G:
-            raise ValueError("bias must have G entries")
-    topk = int(topk)
-    topk_ids = _result(topk_ids, "topk_ids", (T, max(topk, 0)), torch.int32, logits, stream)
-    weights = _result(weights, "weights", (T, max(topk, 0)), torch.float32, logits, stream)
-    _launch("fp8q_moe_route", index, stream, px, _types[logits.dtype], pb, T, G, topk,
-            int(n_groups), int(topk_groups), _score(score), int(bool(renormalize)), float(scale),
-            topk_ids.data_ptr(), weights.data_ptr())
-    return topk_ids, weights
+    return _run("fp8q_moe_route", stream, logits, bias, topk, _score(score), bool(renormalize), scale,
+                n_groups, topk_groups, topk_ids, weights)
 
 
 def fp8q_moe_route_bwd(logits, topk_ids, dweights, score="softmax", renormalize=True, scale=1.0,
                        dlogits=None, stream=None):
     """Gradient of fp8q_moe_route's weights: dweights (float32 T x topk) -> dlogits (T x G, like logits)."""
-    torch, index = _bind(logits)
-    px = _ptr(logits, "logits", None, 2, index)
-    pid = _ptr(topk_ids, "topk_ids", torch.int32, 2, index)
-    pdw = _ptr(dweights, "dweights", torch.float32, 2, index)
-    T, G = logits.shape
-    if topk_ids.shape != dweights.shape or topk_ids.shape[0] != T:
-        raise ValueError("topk_ids and dweights must both be T x topk")
-    dlogits = _result(dlogits, "dlogits", (T, G), logits.dtype, logits, stream)
-    _launch("fp8q_moe_route_bwd", index, stream, px, _types[logits.dtype], pid, pdw, T, G,
-            topk_ids.shape[1], _score(score), int(bool(renormalize)), float(scale),
-            dlogits.data_ptr())
-    return dlogits
-
-
-@functools.lru_cache(maxsize=1024)
-def _dispatch_sizes(T, topk, G):
-    """(rows of the outputs, bytes of workspace); -1 for invalid sizes."""
-    return (lib().fp8q_moe_dispatch_max_rows(T, topk, G),
-            lib().fp8q_moe_dispatch_workspace_bytes(T, topk, G))
+    return _run("fp8q_moe_route_bwd", stream, logits, topk_ids, dweights, _score(score),
+                bool(renormalize), scale, dlogits)
 
 
 def fp8q_moe_permute(x, topk_ids, G, xp=None, m_offsets=None, row_of_slot=None, workspace=None,
@@ -628,132 +554,38 @@ def fp8q_moe_permute(x, topk_ids, G, xp=None, m_offsets=None, row_of_slot=None, 
     """Rows sorted by expert: x T x K (bfloat16 or float32), topk_ids int32 T x topk ->
     (xp M_cap x K, m_offsets int32[G+1], row_of_slot int32 T x topk), the layout of
     fp8q_moe_dispatch_1x128; rows of xp from m_offsets[G] on are not written."""
-    torch, index = _bind(x)
-    px = _ptr(x, "x", None, 2, index)
-    pid = _ptr(topk_ids, "topk_ids", torch.int32, 2, index)
-    T, K = x.shape
-    if topk_ids.shape[0] != T:
-        raise ValueError("topk_ids must have one row per token")
-    topk = topk_ids.shape[1]
-    M_cap, ws_bytes = _dispatch_sizes(T, topk, G)
-    if M_cap < 0 or ws_bytes < 0:
-        raise ValueError("invalid permute sizes")
-    xp = _result(xp, "xp", (M_cap, K), x.dtype, x, stream)
-    m_offsets = _result(m_offsets, "m_offsets", (G + 1,), torch.int32, x, stream)
-    row_of_slot = _result(row_of_slot, "row_of_slot", (T, topk), torch.int32, x, stream)
-    if workspace is None:
-        workspace = _result(None, "workspace", (max(ws_bytes, 4),), torch.uint8, x, stream)
-    pw = _ptr(workspace, "workspace", torch.uint8, 1, index)
-    _launch("fp8q_moe_permute", index, stream, px, _types[x.dtype], pid, T, K, topk, G,
-            xp.data_ptr(), M_cap, m_offsets.data_ptr(), row_of_slot.data_ptr(), pw,
-            workspace.numel())
-    return xp, m_offsets, row_of_slot
+    return _run("fp8q_moe_permute", stream, x, topk_ids, G, xp, m_offsets, row_of_slot, workspace)
 
 
 def fp8q_moe_combine(c, row_of_slot, weights=None, out_dtype="bf16", y=None, stream=None):
     """The way back: y[t] = sum_j weights[t, j] * c[row_of_slot[t, j]] (weights None: ones; rows
     outside c are skipped). c M x K (bfloat16 or float32) -> y T x K of out_dtype."""
-    torch, index = _bind(c)
-    code, tdt = _out_dtype(out_dtype)
-    pc = _ptr(c, "c", None, 2, index)
-    pr = _ptr(row_of_slot, "row_of_slot", torch.int32, 2, index)
-    pw = None
-    if weights is not None:
-        pw = _ptr(weights, "weights", torch.float32, 2, index)
-        if weights.shape != row_of_slot.shape:
-            raise ValueError("weights must have row_of_slot's shape")
-    M, K = c.shape
-    T, topk = row_of_slot.shape
-    y = _result(y, "y", (T, K), tdt, c, stream)
-    _launch("fp8q_moe_combine", index, stream, pc, _types[c.dtype], pr, pw, T, K, topk, M,
-            y.data_ptr(), code)
-    return y
+    return _run("fp8q_moe_combine", stream, c, row_of_slot, weights, _out_dtype(out_dtype)[0], y)
 
 
 def fp8q_moe_combine_bwd(dy, c, row_of_slot, weights, m_offsets, dc=None, dw=None, with_dw=True,
                          stream=None):
     """Gradient of fp8q_moe_combine: dy T x K, c M x K -> (dc M x K like c, dw float32 T x topk);
     padding rows of dc are zero, rows from m_offsets[G] on are not written. with_dw=False: dw is
-    None and c is only used for its shape and type."""
-    torch, index = _bind(dy)
-    pdy = _ptr(dy, "dy", None, 2, index)
-    pc = _ptr(c, "c", None, 2, index)
-    pr = _ptr(row_of_slot, "row_of_slot", torch.int32, 2, index)
-    poff = _ptr(m_offsets, "m_offsets", torch.int32, 1, index)
-    pw = None
-    if weights is not None:
-        pw = _ptr(weights, "weights", torch.float32, 2, index)
-        if weights.shape != row_of_slot.shape:
-            raise ValueError("weights must have row_of_slot's shape")
-    M, K = c.shape
-    T, topk = row_of_slot.shape
-    if tuple(dy.shape) != (T, K):
-        raise ValueError(f"dy must have shape {(T, K)}, got {tuple(dy.shape)}")
-    if m_offsets.shape[0] < 2:
-        raise ValueError("m_offsets must have G+1 entries")
-    dc = _result(dc, "dc", (M, K), c.dtype, dy, stream)
-    if with_dw or dw is not None:
-        dw = _result(dw, "dw", (T, topk), torch.float32, dy, stream)
-    _launch("fp8q_moe_combine_bwd", index, stream, pdy, _types[dy.dtype], pc, _types[c.dtype], pr,
-            pw, poff, T, K, topk, m_offsets.shape[0] - 1, M, dc.data_ptr(), dw.data_ptr() if dw is
-            not None else None)
-    return dc, dw
+    None (unless given) and c is only used for its shape and type."""
+    return _run("fp8q_moe_combine_bwd", stream, dy, c, row_of_slot, weights, m_offsets, dc, dw,
+                bool(with_dw))
 
 
 def fp8q_quant_int8_rows(x, q=None, s=None, stream=None):
     """x: bf16 ... x K device tensor (2 or 3 dims: tokens, channels or experts' channels) ->
     (q int8 like x, s float32 without the last dim): one scale amax / 127 per row."""
-    torch, index = _bind(x)
-    px = _ptr(x, "x", torch.bfloat16, 3 if x.dim() == 3 else 2, index)
-    lead, K = tuple(x.shape[:-1]), x.shape[-1]
-    rows = 1
-    for d in lead:
-        rows *= d
-    q = _result(q, "q", tuple(x.shape), torch.int8, x, stream)
-    s = _result(s, "s", lead, torch.float32, x, stream)
-    _launch("fp8q_quant_int8_rows", index, stream, px, rows, K, q.data_ptr(), s.data_ptr())
-    return q, s
+    return _run("fp8q_quant_int8_rows", stream, x, q, s)
 
 
 def int8_gemm_scaled(a, sa, b, sb, out_dtype="bf16", c=None, stream=None):
     """c[m, n] = (sum_k a[m, k] b[n, k]) * sa[m] * sb[n]: a int8 M x K, sa float32 M, b int8 N x K,
     sb float32 N. Returns c (M x N)."""
-    torch, index = _bind(a)
-    code, tdt = _out_dtype(out_dtype)
-    pa = _ptr(a, "a", torch.int8, 2, index)
-    psa = _ptr(sa, "sa", torch.float32, 1, index)
-    pb = _ptr(b, "b", torch.int8, 2, index)
-    psb = _ptr(sb, "sb", torch.float32, 1, index)
-    M, K = a.shape
-    N = b.shape[0]
-    if b.shape[1] != K:
-        raise ValueError("a and b must share K")
-    if sa.shape[0] != M or sb.shape[0] != N:
-        raise ValueError("scale shapes must be (M,) and (N,)")
-    c = _result(c, "c", (M, N), tdt, a, stream)
-    _launch("int8_gemm_scaled", index, stream, pa, psa, pb, psb, c.data_ptr(), code, M, N, K)
-    return c
+    return _run("int8_gemm_scaled", stream, a, sa, b, sb, _out_dtype(out_dtype)[0], c)
 
 
 def int8_gemm_grouped(a, sa, b, sb, m_offsets, out_dtype="bf16", c=None, M_total=None, stream=None):
     """Grouped form: a int8 M x K, sa float32 M, b int8 G x N x K, sb float32 G x N, m_offsets
     int32[G+1] (device, multiples of 128, never read on the host). M_total defaults to a.shape[0]."""
-    torch, index = _bind(a)
-    code, tdt = _out_dtype(out_dtype)
-    pa = _ptr(a, "a", torch.int8, 2, index)
-    psa = _ptr(sa, "sa", torch.float32, 1, index)
-    pb = _ptr(b, "b", torch.int8, 3, index)
-    psb = _ptr(sb, "sb", torch.float32, 2, index)
-    poff = _ptr(m_offsets, "m_offsets", torch.int32, 1, index)
-    G, N, K = b.shape
-    if m_offsets.shape[0] != G + 1:
-        raise ValueError("m_offsets must have G+1 entries")
-    M = a.shape[0] if M_total is None else int(M_total)
-    if a.shape[1] != K or a.shape[0] < M or sa.shape[0] < M:
-        raise ValueError("a must be at least M_total x K, with a scale per row")
-    if tuple(sb.shape) != (G, N):
-        raise ValueError(f"sb must have shape {(G, N)}, got {tuple(sb.shape)}")
-    c = _result(c, "c", (M, N), tdt, a, stream)
-    _launch("int8_gemm_grouped", index, stream, pa, psa, pb, psb, c.data_ptr(), code, poff, G, M, N,
-            K)
-    return c
+    return _run("int8_gemm_grouped", stream, a, sa, b, sb, m_offsets, _out_dtype(out_dtype)[0], c,
+                M_total)

@@ -1,11 +1,14 @@
-"""Build libfp8q.so (HIP, gfx950) in-tree with hipcc.
+"""Build libfp8q.so (HIP, gfx950) in-tree with hipcc, and the Python binding beside
+it (host code, against the installed torch) with g++.
 
 Usage: python -m fp8_fine_grained_online_amd.build [--verbose]
 """
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -57,8 +60,27 @@ def build(verbose: bool = False) -> str:
     tmp = LIB_PATH + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
+    build_binding(verbose)
     build_probes(verbose)
     return LIB_PATH
+
+
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
+
+
+def build_binding(verbose: bool = False) -> str:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    libs = os.path.join(torch_dir, "lib")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM", "-I", sysconfig.get_paths()["include"],
+          "-I", os.path.join(torch_dir, "include"), "-I", os.path.join(rocm, "include"),
+          os.path.join(CSRC, "binding.cpp"), "-o", BINDING_PATH + ".tmp",
+          "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+          "-L", os.path.join(rocm, "lib"), "-lamdhip64", "-L", PKG_DIR, "-l:" + os.path.basename(LIB_PATH),
+          "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    return BINDING_PATH
 
 
 # Test-only GPU probes (tests/probes/*.hip), each built into its own shared
