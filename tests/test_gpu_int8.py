@@ -73,6 +73,21 @@ def test_quant_every_value_under_every_maximum():
         assert np.array_equal(q.cpu().numpy(), want_q)
 
 
+def test_quant_codes_beyond_the_cache():
+    """Over 256 MiB of codes (stored another way), against the same formula in torch: the division of two
+    tensors and the rounding are IEEE there too."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    M, K = 40000, 7168
+    x = torch.randn(M, K, device="cuda", generator=torch.Generator("cuda").manual_seed(5)).to(torch.bfloat16)
+    q, s = F.fp8q_quant_int8_rows(x)
+    for m in range(0, M, 8000):
+        xf = x[m:m + 8000].float()
+        want_s = xf.abs().amax(1) / torch.full((), 127.0, device="cuda")
+        assert torch.equal(s[m:m + 8000], want_s)
+        assert torch.equal(q[m:m + 8000], torch.round(xf / want_s.unsqueeze(1)).to(torch.int8))
+
+
 def test_quant_weights_of_experts():
     import torch
     import fp8_fine_grained_online_amd as F
@@ -85,7 +100,8 @@ def test_quant_weights_of_experts():
 
 DENSE = [(1, 1, 16), (1, 7168, 1024), (2, 33, 48), (16, 100, 4112), (17, 129, 128), (64, 65, 256), (100, 2050, 272),
          (129, 257, 144), (333, 514, 2064), (1000, 31, 640), (1, 64, 131056), (520, 520, 144), (260, 4100, 96),
-         (1500, 3000, 400), (2049, 4097, 128), (4100, 2056, 272)]
+         (1500, 3000, 400), (2049, 4097, 128), (4100, 2056, 272), (300, 300, 208), (500, 500, 528),
+         (1000, 1900, 272), (1500, 2000, 400), (1000, 1901, 2064)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -131,7 +147,8 @@ def test_empty_sizes():
 
 
 GROUPED = [([128], 64, 64), ([0, 128, 0], 100, 48), ([128, 384, 256, 0], 257, 272), ([256] * 5, 514, 1040),
-           ([128] * 40, 128, 144), ([1024, 128, 2048], 300, 128), ([0, 0], 64, 64), ([128] * 70 + [256], 96, 64)]
+           ([128] * 40, 128, 144), ([1024, 128, 2048], 300, 128), ([0, 0], 64, 64), ([128] * 70 + [256], 96, 64),
+           ([128] * 40, 514, 144), ([1024, 128, 2048, 384], 1030, 272), ([512, 0, 256] * 30, 300, 1040)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])

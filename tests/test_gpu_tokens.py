@@ -111,6 +111,32 @@ def test_combine(T, topk, G, K, src, dst, weighted):
     assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol)
 
 
+def test_rows_beyond_the_cache():
+    """More than 256 MiB of rows (read and stored another way), against float64 sums in torch."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    T, topk, G, K = 2600, 8, 16, 7168
+    ids = torch.from_numpy(routing(T, topk, G, 2635, drop=9)).cuda()
+    x = randn((T, K), "bf16", 2636)
+    xp, off, rows = F.fp8q_moe_permute(x, ids, G)
+    want_rows, want_off, _ = tokens.layout(ids.cpu().numpy(), G)
+    assert np.array_equal(rows.cpu().numpy(), want_rows) and np.array_equal(off.cpu().numpy(), want_off)
+    on = rows >= 0
+    assert torch.equal(xp[rows[on].long()], x.unsqueeze(1).expand(T, topk, K)[on])
+    w = torch.rand(T, topk, device="cuda", generator=torch.Generator("cuda").manual_seed(6))
+    y = F.fp8q_moe_combine(xp, rows, w, out_dtype="f32")
+    for t in range(0, T, 650):
+        s = slice(t, t + 650)
+        terms = torch.where(on[s].unsqueeze(2), xp[rows[s].clamp(min=0).long()].double() * w[s].double().unsqueeze(2), 0.0)
+        assert torch.all((y[s].double() - terms.sum(1)).abs() <= topk * EPS32 * terms.abs().sum(1))
+    dc, dw = F.fp8q_moe_combine_bwd(x, xp, rows, w, off)
+    # dc = w x: one product rounded to binary32, then to bfloat16; c's rows are x's, so dw is |x|^2
+    want = (w.unsqueeze(2) * x.float().unsqueeze(1))[on].to(torch.bfloat16)
+    assert torch.equal(dc[rows[on].long()], want)
+    norm = x.double().square().sum(1, keepdim=True)
+    assert torch.all((dw.double() - torch.where(on, norm, 0.0)).abs() <= (K / 64 + 24) * EPS32 * norm)
+
+
 def test_combine_skips_rows_outside():
     import torch
     import fp8_fine_grained_online_amd as F
