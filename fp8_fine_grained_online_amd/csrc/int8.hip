@@ -278,6 +278,26 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
   const int all_steps = (p.K + kStepK - 1) / kStepK;
   const int steps = (all_steps + S - 1) / S;
   const int first = group * steps;
+  // The epilogue's scales. Loaded before the loop, they are not one more wait for
+  // memory at the end (the largest wave tile has no registers to hold them).
+  const int nw = n0 + wn * WN;
+  constexpr bool kScalesFirst = SUBM * SUBN < 64;
+  float sav[SUBM], sbc[SUBN][4];
+  auto load_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < SUBM; ++i) {
+      const int m = m0 + wm * WM + i * 16 + lr;
+      sav[i] = m < m_end && p.K > 0 ? p.sa[m] : 0.0f;  // K == 0: no operand is read
+    }
+#pragma unroll
+    for (int j = 0; j < SUBN; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = nw + j * 16 + 4 * lk + r;
+        sbc[j][r] = n < p.N && p.K > 0 ? sbv[n] : 0.0f;
+      }
+  };
+  if constexpr (kScalesFirst) load_scales();
   // copy q of thread tid brings row q * 32 + tid / 8, stored chunk tid % 8
   const int row0 = tid >> 3, lc0 = (tid & 7) ^ (row0 & 7);
   constexpr int kRows = Cfg::kLoadsA > Cfg::kLoadsB ? Cfg::kLoadsA : Cfg::kLoadsB;
@@ -406,30 +426,20 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
   }
 
   // ---- epilogue: scale, stage 16 rows of the wave's part in its own LDS, store rows ----
-  const int nw = n0 + wn * WN;
   constexpr int kEl = kBf16 ? 2 : 4;        // bytes per output
   constexpr int kRowBytes = WN * kEl;
   constexpr int kChunks = kRowBytes / 16;
   static_assert((S > 1 ? kMfmas * 64 * 16 : Cfg::kLds / 4) >= 16 * kRowBytes, "staging");
   // (with S > 1 a wave stages where its own part of the other groups' sums was)
   uint8_t* st = lds + wave * (S > 1 ? kMfmas * 64 * 16 : 16 * kRowBytes);
-  float sbc[SUBN][4];
-#pragma unroll
-  for (int j = 0; j < SUBN; ++j)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int n = nw + j * 16 + 4 * lk + r;
-      sbc[j][r] = n < p.N && p.K > 0 ? sbv[n] : 0.0f;  // K == 0: no operand is read
-    }
+  if constexpr (!kScalesFirst) load_scales();
 #pragma unroll
   for (int i = 0; i < SUBM; ++i) {
-    const int gm = m0 + wm * WM + i * 16 + lr;
-    const float sav = gm < m_end && p.K > 0 ? p.sa[gm] : 0.0f;
 #pragma unroll
     for (int j = 0; j < SUBN; ++j) {
       float v[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = scaled(acc[i][j][r], sav, sbc[j][r]);
+      for (int r = 0; r < 4; ++r) v[r] = scaled(acc[i][j][r], sav[i], sbc[j][r]);
       const int byte = (j * 16 + 4 * lk) * kEl;
       uint8_t* to = st + lr * kRowBytes + (((byte >> 4) ^ (lr & (kChunks - 1))) << 4) + (byte & 15);
       if constexpr (kBf16) *(bf16x4*)to = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
@@ -493,6 +503,18 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_small_kernel(I8Args p) {
   const uint32_t off = (uint32_t)lr * (uint32_t)p.K + lk * 16;
   const uint32_t blk = 16u * (uint32_t)p.K;
 
+  // Wave b finishes block b of the workgroup's outputs; its scales are loaded
+  // before the loop, not to be one more wait for memory at the end.
+  static_assert(MB * NB <= W, "a wave per block");
+  float sa0 = 0.0f, sb0[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (wave < MB * NB && p.K > 0) {  // K == 0: no operand is read
+    const int gm = m0 + (wave / NB) * 16 + lr, gn = n0 + (wave % NB) * 16 + 4 * lk;
+    if (gm < p.M) sa0 = p.sa[gm];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (gn + r < p.N) sb0[r] = p.sb[gn + r];
+  }
+
   struct Frags {
     v4i a[MB], b[NB];
   };
@@ -533,20 +555,20 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_small_kernel(I8Args p) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) part[wave][i * NB + j][lane] = acc[i][j];
   __syncthreads();
-  for (int b = wave; b < MB * NB; b += W) {
+  if (wave < MB * NB) {
+    const int b = wave;
     v4i sum = part[0][b][lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) sum += part[w][b][lane];
     const int gm = m0 + (b / NB) * 16 + lr;
     const int gn = n0 + (b % NB) * 16 + 4 * lk;
-    if (gm >= p.M) continue;
-    const float sav = p.K > 0 ? p.sa[gm] : 0.0f;
+    if (gm >= p.M) return;
     float v[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = scaled(sum[r], sav, gn + r < p.N && p.K > 0 ? p.sb[gn + r] : 0.0f);
+    for (int r = 0; r < 4; ++r) v[r] = scaled(sum[r], sa0, sb0[r]);
     const int64_t at = (int64_t)gm * p.N + gn;
     if (p.N % 4 == 0) {  // all four in or all out, and aligned
-      if (gn >= p.N) continue;
+      if (gn >= p.N) return;
       if constexpr (kBf16) *(bf16x4*)((__bf16*)p.c + at) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
       else *(v4f*)((float*)p.c + at) = v4f{v[0], v[1], v[2], v[3]};
     } else {
