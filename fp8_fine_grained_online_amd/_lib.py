@@ -516,7 +516,7 @@ def _run(fn, stream, first, *args):
     else:
         cuda = _torch().cuda
         if not hasattr(stream, "cuda_stream"):
-            stream = cuda.ExternalStream(int(stream), device=first.device)
+            stream = cuda.ExternalStream(int(stream), device=getattr(first, "device", None))
         with cuda.stream(stream):
             result = call(first, *args)
     if type(result) is int:

@@ -25,6 +25,7 @@ struct RouteArgs {
   const void* logits;
   const float* bias;
   int T, G, topk, n_groups, topk_groups;
+  int gs;  // experts of a group
   int sigmoid, renorm;
   int whole;  // a lane's experts are all in the row or all past it, and aligned
   float scale;
@@ -188,13 +189,16 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   uint64_t* const tab = table[wave];
   float x[E];
   load_logits<E>((const Tin*)a.logits + (int64_t)t * a.G, lane * E, a.G, a.whole, x);
+  float bias[E];  // loaded with the logits: later it would be a second wait for memory
+#pragma unroll
+  for (int i = 0; i < E; ++i) bias[i] = a.bias && lane * E + i < a.G ? a.bias[lane * E + i] : 0.0f;
   double p[E];
   if (a.sigmoid) {
 #pragma unroll
     for (int i = 0; i < E; ++i) p[i] = x[i] > -__builtin_huge_valf() ? sigmoid64(x[i]) : 0.0;
   } else {
     const double sum = softmax_terms<E>(x, p);
-    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;  // (no logit but masked ones: 0)
+    const double inv = sum > 0.0 ? recip64(sum) : 0.0;  // 1 <= sum <= G; no logit but masked ones: 0
 #pragma unroll
     for (int i = 0; i < E; ++i) p[i] *= inv;
   }
@@ -202,13 +206,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   int place[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    const int e = lane * E + i;
-    const double z = (a.bias && e < a.G) ? p[i] + (double)a.bias[e] : p[i];
+    const double z = p[i] + (double)bias[i];
     key[i] = x[i] > -__builtin_huge_valf() ? order_key(z) : 0;
     place[i] = i;
   }
 
-  const int gs = a.G / a.n_groups;
+  const int gs = a.gs;
   const int lanes = gs / E;  // of a group, if groups fall on whole lanes
   const bool by_lanes = gs % E == 0 && (lanes & (lanes - 1)) == 0;
   if (a.n_groups > 1 && !by_lanes) {
@@ -389,7 +392,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteBwdArg
   if (dense) {
     double p[E], mean = 0.0;
     const double sum = softmax_terms<E>(x, p);
-    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+    const double inv = sum > 0.0 ? recip64(sum) : 0.0;
 #pragma unroll
     for (int i = 0; i < E; ++i) p[i] *= inv, mean += d[i] * p[i];
     mean = wave_sum_f64(mean);
@@ -414,7 +417,7 @@ hipError_t launch_route(const void* logits, bool bf16, const float* bias, int64_
                         int64_t topk, int64_t n_groups, int64_t topk_groups, bool sigmoid,
                         bool renorm, float scale, int32_t* ids, float* w, hipStream_t stream) {
   RouteArgs a{logits, bias, (int)T, (int)G, (int)topk, (int)n_groups, (int)topk_groups,
-              sigmoid, renorm, 0, scale, ids, w};
+              (int)(G / n_groups), sigmoid, renorm, 0, scale, ids, w};
   const dim3 grid((unsigned)((T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
   by_experts(a, [&](auto e) {
     constexpr int E = decltype(e)::value;

@@ -191,6 +191,40 @@ def test_layer_in_a_captured_graph():
             assert torch.equal(g[k], want_g[k]), (seed, k)
 
 
+def test_many_tokens_in_a_captured_graph():
+    """The permutation's counting and scanning kernels and their workspace, captured: enough slots for
+    them to run, and other choices on every replay."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    tok, experts, k = 3000, 40, 3
+    x = torch.randn(tok, 64, device="cuda")
+    logits = torch.randn(tok, experts, device="cuda")
+
+    def step():
+        ids, w = F.fp8q_moe_route(logits, k)
+        xp, off, rows = F.fp8q_moe_permute(x, ids, experts, xp=torch.zeros(cap, 64, device="cuda"))
+        y = F.fp8q_moe_combine(xp, rows, w, out_dtype="f32")
+        dc, dw = F.fp8q_moe_combine_bwd(x, xp, rows, w, off, dc=torch.zeros_like(xp))
+        return ids, w, xp, off, rows, y, dc, dw
+
+    cap = F.lib().fp8q_moe_dispatch_max_rows(tok, k, experts)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = step()
+    for _ in range(4):
+        logits.normal_()
+        x.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
 def test_two_streams_at_once():
     import torch
     fs = [inputs(6), inputs(7)]
