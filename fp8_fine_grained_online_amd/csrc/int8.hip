@@ -644,13 +644,23 @@ hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, c
   if (wgs(64, 64) <= kCus) return launch_tiles<64, 64, 3, 2, false>(p, bf16, (M + 63) / 64, stream);
   if (wgs(64, 128) <= kCus) return launch_tiles<64, 128, 4, 1, false>(p, bf16, (M + 63) / 64, stream);
   if (wgs(128, 128) <= kCus) return launch_tiles<128, 128, 3, 1, false>(p, bf16, (M + 127) / 128, stream);
-  // Large products: 256 x 256 tiles, one per CU, against 128 x 128, two at a
-  // time per CU, whose round takes 0.56 of the time of the other's (4096^3:
-  // 58.3 us in one round of 256, 65.6 in two of 128; 2048 x 4096 x 2048: 31.1
-  // in half a round of 256, 21.3 in one of 128)
-  const int64_t rounds256 = (wgs(256, 256) + kCus - 1) / kCus;
-  const int64_t rounds128 = (wgs(128, 128) + 2 * kCus - 1) / (2 * kCus);
-  if (rounds128 * 56 < rounds256 * 100) return launch_tiles<128, 128, 2, 1, false>(p, bf16, (M + 127) / 128, stream);
+  // Large products: 256 x 256 tiles, one per CU, against 128 x 128, two at a time
+  // per CU. In rounds of 256 tiles of the large kind: its last, partly filled
+  // round costs about 0.8 of a full one. A round of 512 small tiles costs 0.51 at
+  // K = 1024 and more with K (the large tile's loads and LDS reads per MFMA are
+  // half as many), its last one at least half. us, 256 x 256 / 128 x 128, MI355X:
+  //   4096 x 4096 x 4096 55.8 / 61.1    8192 x 8192 x 8192 378 / 472
+  //   8192 x 7168 x 2048  125 / 116     2500 x 7168 x 7168 152 / 118
+  //   6000 x 4096 x 4096  102 / 88.7    4500 x 4096 x 4096 95.5 / 73.6
+  // (Workgroups that stay and take tile after tile, the next tile's copies begun
+  // under the last one's output, were 2-15% slower: the CUs write their outputs
+  // at the same time either way, and the loop with the next tile's lookup in it
+  // spills registers.)
+  const double r256 = (double)wgs(256, 256) / kCus, r128 = (double)wgs(128, 128) / (2 * kCus);
+  const double part256 = r256 - (int64_t)r256, part128 = r128 - (int64_t)r128;
+  const double cost256 = (int64_t)r256 + (part256 > 0 ? 0.8 : 0);
+  const double cost128 = ((int64_t)r128 + (part128 > 0.5 ? part128 : part128 > 0 ? 0.5 : 0)) * (0.5 + 0.011 * K / 1024);
+  if (cost128 < cost256) return launch_tiles<128, 128, 2, 1, false>(p, bf16, (M + 127) / 128, stream);
   return launch_tiles<256, 256, 2, 1, false>(p, bf16, (M + 255) / 256, stream);
 }
 
