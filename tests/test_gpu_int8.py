@@ -101,7 +101,8 @@ def test_quant_weights_of_experts():
 DENSE = [(1, 1, 16), (1, 7168, 1024), (2, 33, 48), (16, 100, 4112), (17, 129, 128), (64, 65, 256), (100, 2050, 272),
          (129, 257, 144), (333, 514, 2064), (1000, 31, 640), (1, 64, 131056), (520, 520, 144), (260, 4100, 96),
          (1500, 3000, 400), (2049, 4097, 128), (4100, 2056, 272), (300, 300, 208), (500, 500, 528),
-         (1000, 1900, 272), (1500, 2000, 400), (1000, 1901, 2064)]
+         (1000, 1900, 272), (1500, 2000, 400), (1000, 1901, 2064),
+         (4090, 4080, 272), (4000, 4081, 400)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
