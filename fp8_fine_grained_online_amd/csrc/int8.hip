@@ -260,8 +260,10 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
       }
       before += __builtin_amdgcn_readlane(incl, 63);
     }
-    if (te == 0) return;  // (offsets outside the contract: counts that overflow)
-    band_tile<kBandGrouped>(tile - before, te, n_tiles_n, tm, tn);
+    const int local = tile - before;
+    // (fails only for offsets outside the contract, where the counts overflow)
+    if ((uint32_t)local >= (uint32_t)(te * n_tiles_n)) return;
+    band_tile<kBandGrouped>(local, te, n_tiles_n, tm, tn);
     m0 = lo + tm * BM;
     m_end = min(m0 + BM, hi);
     bmat += (int64_t)e * p.N * p.K;

@@ -9,12 +9,19 @@
 // One wavefront per token, lane l holding the E consecutive experts from l E
 // on (E = 1, 2, 4, 8, 16: up to 1024 experts), so that the lowest lane of a
 // tie has the lowest index. A lane sorts its keys once; each choice is then one
-// maximum over the wavefront, and the winner's next key moves up. Scores are float64: whether an expert is chosen is
-// a comparison of two nearly equal numbers, and its answer should be that of
-// the formula, not of the rounding.
-#include "common.hpp"
+// maximum over the wavefront, and the winner's next key moves up. Scores are
+// float64: whether an expert is chosen is a comparison of two nearly equal
+// numbers, and its answer should be that of the formula, not of the rounding.
+//
+// Few bytes move (at most 17 MB below, 3.5 us), so the time is mostly that of one
+// launch (1.8 us for an empty kernel) and of one wavefront's chain: a load, the
+// softmax, its choices. MI355X, us: 16 tokens of 256 experts in 8 groups, top-8, sigmoid 6.0;
+// 8192 of 64, top-6 5.6; gradient, 8192 of 256 5.3. (With every choice searched
+// through all keys, the library's exponential, and gradient shares passed from
+// lane to lane the first took 8.8 and the gradient 8.3.)
 #include <type_traits>
 
+#include "common.hpp"
 #include "wave.hpp"
 
 namespace fp8q {
@@ -293,6 +300,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
 //   sigmoid           dl_e = sum_{j: id_j = e} dp_j p_j (1 - p_j), dp_j = g_j or
 //                     (g_j - sum_i g_i q_i) / sum_i p_i
 // so only the plain softmax needs every probability of the row.
+//
+// The row is put together in LDS: zeros, then the choices' shares at their
+// experts. Should an expert be listed twice, which shows when a lane does not
+// read back the number it wrote there, the shares are added one by one.
 struct RouteBwdArgs {
   const void* logits;
   const int32_t* ids;
@@ -309,10 +320,6 @@ __device__ __forceinline__ void store_logit(uint16_t* p, double v) {
   *p = __builtin_bit_cast(uint16_t, b);
 }
 
-//
-// The row is put together in LDS: zeros, then the choices' shares at their
-// experts. Should an expert be listed twice, which shows when a lane does not
-// read back the number it wrote there, the shares are added one by one.
 template <int E, typename Tin>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteBwdArgs a) {
   constexpr float kNegInf = -__builtin_huge_valf();

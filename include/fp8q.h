@@ -456,9 +456,11 @@ FP8Q_API int fp8_gemm_rowscaled(const uint8_t* a, const float* sa, const uint8_t
  *
  * Element types are named by fp8q_out_dtype (FP8Q_OUT_F32, FP8Q_OUT_BF16).
  * Sums are formed in binary32 or wider and rounded once. Every entry point is
- * deterministic (no floating-point atomics) and allocates nothing. A call
- * whose kernel would need 2^32 threads or more returns FP8Q_ERR_TOO_LARGE
- * (2^26 tokens for the router, 2^24 for the permutation).
+ * deterministic (no floating-point atomics) and allocates nothing. No output
+ * or workspace may overlap an input or another output, and calls that may run
+ * at the same time need workspaces of their own. A call whose kernel would
+ * need 2^32 threads or more returns FP8Q_ERR_TOO_LARGE (2^26 tokens for the
+ * router, 2^24 for the permutation).
  * ---------------------------------------------------------------------------
  */
 
