@@ -9,6 +9,7 @@
 // All three move rows and do almost no arithmetic: they are bound by HBM.
 // Rows are handled in chunks of 8 values, one chunk per lane (16 bytes of
 // bfloat16, 32 of float32).
+#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
@@ -98,7 +99,7 @@ struct Chunk<float> {
 // 227).
 // ---------------------------------------------------------------------------
 constexpr int kPadParts = 16;
-constexpr int kSortSlots = 4096;   // most slots a workgroup sorts by itself
+constexpr int kSortSlots = 2048;   // most slots a workgroup sorts by itself
 constexpr int kDispBlock = 256;    // slots per block of the counting kernel
 constexpr int kMaxExperts = 1024;
 
@@ -110,11 +111,11 @@ struct PermuteArgs {
   int32_t* row_of_slot;
   int32_t* m_offsets;
   uint8_t* xp;
-  int n_tok, K, topk, G;
+  int n_tok, K, topk, G, pad_parts;
 };
 
 struct SortLds {
-  int32_t ids[kSortSlots];           // -1: dropped
+  int16_t ids[kSortSlots];           // -1: dropped
   int32_t counts[kMaxExperts];
   int32_t offsets[kMaxExperts + 1];  // first row of each expert's block
   int32_t wave_sum[kTokWaves];
@@ -132,7 +133,7 @@ __device__ __forceinline__ void sort_experts(SortLds& s, const int32_t* __restri
   for (int i = tid; i < slots; i += kThreads) {
     const int e = ids[i];
     const bool on = e >= 0 && e < G;
-    s.ids[i] = on ? e : -1;
+    s.ids[i] = on ? (int16_t)e : (int16_t)-1;
     if (on) atomicAdd(&s.counts[e], 1);  // integers: any order, the same counts
   }
   __syncthreads();
@@ -182,13 +183,13 @@ __global__ __launch_bounds__(64 * kTokWaves) void permute_kernel(PermuteArgs a) 
   }
   if ((int)blockIdx.x >= a.n_tok) {
     const int pad = blockIdx.x - a.n_tok;
-    const int e = pad / kPadParts;
+    const int e = pad / a.pad_parts;
     int row, end;
     if constexpr (kSort) row = sort.offsets[e] + sort.counts[e], end = sort.offsets[e + 1];
     else row = a.m_offsets[e] + a.counts[e], end = a.m_offsets[e + 1];
-    for (row += pad % kPadParts; row < end; row += kPadParts)
-      for (int c = tid; c < n_chunks; c += kThreads)
-        C::template store<false>(a.xp + row * row_bytes + (int64_t)c * C::kBytes, C::zero());
+    const int64_t n = (int64_t)(end - row) * n_chunks;  // contiguous
+    for (int64_t i = pad % a.pad_parts * kThreads + tid; i < n; i += a.pad_parts * kThreads)
+      C::template store<false>(a.xp + row * row_bytes + i * C::kBytes, C::zero());
     return;
   }
   const uint8_t* xr = a.x + blockIdx.x * row_bytes;
@@ -343,9 +344,9 @@ __global__ __launch_bounds__(64 * kTokWaves) void combine_bwd_kernel(
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kTokWaves; ++w) last = max(last, last_of_wave[w]);
-    for (int64_t row = last + 1 + blockIdx.x % pad_parts; row < hi; row += pad_parts)
-      for (int ch = tid; ch < n_chunks; ch += kThreads)
-        CC::template store<kNt>(dc + row * rb + (int64_t)ch * CC::kBytes, CC::zero());
+    const int64_t n = (int64_t)(hi - 1 - last) * n_chunks;  // contiguous
+    for (int64_t i = blockIdx.x % pad_parts * kThreads + tid; i < n; i += pad_parts * kThreads)
+      CC::template store<kNt>(dc + (last + 1) * rb + i * CC::kBytes, CC::zero());
     return;
   }
   const int64_t t = blockIdx.x - n_pad;
@@ -428,9 +429,10 @@ hipError_t launch_moe_permute(const void* x, bool bf16, const int32_t* ids, int6
     dispatch_scan_kernel<<<dim3(1), dim3(kMaxExperts), 0, stream>>>(hist, (int)n_blk, (int)G, base, counts, m_offsets);
     if (T == 0) return hipGetLastError();
   }
+  const int64_t parts = std::min<int64_t>(std::max<int64_t>(K * (bf16 ? 2 : 4) / 256, 1), kPadParts);
   const PermuteArgs a{(const uint8_t*)x, ids, base, counts, row_of_slot, m_offsets, (uint8_t*)xp,
-                      (int)T, (int)K, (int)topk, (int)G};
-  const dim3 grid((unsigned)(T + (K > 0 ? kPadParts * G : 0))), block(64 * kTokWaves);
+                      (int)T, (int)K, (int)topk, (int)G, (int)parts};
+  const dim3 grid((unsigned)(T + (K > 0 ? parts * G : 0))), block(64 * kTokWaves);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
   if (bf16)
     sort ? go(permute_kernel<uint16_t, true>) : go(permute_kernel<uint16_t, false>);
