@@ -76,7 +76,7 @@ def build_binding(verbose: bool = False) -> str:
           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM", "-I", sysconfig.get_paths()["include"],
           "-I", os.path.join(torch_dir, "include"), "-I", os.path.join(rocm, "include"),
           os.path.join(CSRC, "binding.cpp"), "-o", BINDING_PATH + ".tmp",
-          "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+          "-L", libs, "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip",
           "-L", os.path.join(rocm, "lib"), "-lamdhip64", "-L", PKG_DIR, "-l:" + os.path.basename(LIB_PATH),
           "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(BINDING_PATH + ".tmp", BINDING_PATH)

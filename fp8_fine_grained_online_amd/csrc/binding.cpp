@@ -3,7 +3,7 @@
 // stream, and the call. A serving step's kernels take a few microseconds each,
 // so the binding's own time is part of the latency: the same checks and
 // allocations in Python around a ctypes call took 8.4 us for the router; these
-// take 5.5, of which the launch itself is 2.9.
+// take 4.9, of which the launch itself is 2.9.
 //
 // Every function returns its outputs, or the library's status as an int when
 // that is not FP8Q_OK; wrong types and shapes raise TypeError and ValueError.
@@ -11,7 +11,8 @@
 // is current.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPStream.h>
 #include <hip/hip_runtime.h>
 #include <torch/csrc/Exceptions.h>
@@ -70,12 +71,13 @@ struct Call {
   }
 
   // Argument i as an output of this type and shape: the caller's, or a new one
-  // (from the memory of the device's current stream) for None
+  // (from the memory of the device's current stream) for None: straight from the
+  // allocator (the router's call 4.9 us, 5.4 through the dispatcher)
   at::Tensor out(int i, const char* name, at::IntArrayRef shape, ScalarType type) {
     if (none(i)) {
       for (int64_t d : shape)
         if (d < 0) refuse(PyExc_ValueError, "%s would have a negative size", name);
-      return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (at::DeviceIndex)device));
+      return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (at::DeviceIndex)device), std::nullopt));
     }
     const at::Tensor& t = tensor(i, name, {type}, (int64_t)shape.size());
     if (t.sizes() != shape) {
