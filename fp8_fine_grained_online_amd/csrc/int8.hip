@@ -8,6 +8,8 @@
 // int32 registers, exactly, over the whole of K: nothing is promoted inside
 // the loop, and any order or split of K gives the same bits. The two scales
 // are applied once, in the epilogue.
+#include <type_traits>
+
 #include "common.hpp"
 #include "tiles.hpp"
 #include "wave.hpp"
@@ -16,6 +18,10 @@ namespace fp8q {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes at an address aligned to an element only
+typedef uint32_t u32x4_by2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_by4 __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kStepK = 128;  // bytes of K per pipeline step
 
@@ -450,31 +456,30 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
     }
     __builtin_amdgcn_s_waitcnt(kWaitLds);  // a wave reads back only its own part
     __builtin_amdgcn_wave_barrier();
-    // stores of `Unit`s, neighbouring lanes in a row: 16 bytes where every row
-    // of c starts at a multiple of 16, else 4, or a single bfloat16
-    auto store_rows = [&](auto unit) {
-      using Unit = decltype(unit);
-      constexpr int kUnits = kRowBytes / (int)sizeof(Unit);  // of a row
-      static_assert(kUnits % 64 == 0 || 64 % kUnits == 0, "whole wave stores");
-      // (the narrow forms stay loops: fully unrolled, the three outgrow the instruction cache)
-      auto piece = [&](int k) {
-        const int m = (k * 64 + lane) / kUnits, byte = (k * 64 + lane) % kUnits * (int)sizeof(Unit);
-        const int om = m0 + wm * WM + i * 16 + m;
-        const Unit v = *(const Unit*)(st + m * kRowBytes + (((byte >> 4) ^ (m & (kChunks - 1))) << 4) + (byte & 15));
-        const int n = nw + byte / kEl;
-        if (om < m_end && n < p.N) *(Unit*)((uint8_t*)p.c + ((int64_t)om * p.N + n) * kEl) = v;
-      };
-      if constexpr (sizeof(Unit) == 16) {
+    // 16 bytes per lane, neighbouring lanes in a row. Rows of c start at any
+    // element, so the stores are not aligned to more than that (narrower, aligned
+    // ones where N is odd: 1024 x 4097 x 2048 17.7 -> 21.5 us, bfloat16).
+    using Out = std::conditional_t<kBf16, u32x4_by2, u32x4_by4>;
+    constexpr int kPer = 16 / kEl;
+    static_assert(kChunks % 64 == 0 || 64 % kChunks == 0, "whole wave stores");
 #pragma unroll
-        for (int k = 0; k < kUnits / 4; ++k) piece(k);
-      } else {
-#pragma unroll 4
-        for (int k = 0; k < kUnits / 4; ++k) piece(k);
+    for (int k = 0; k < kChunks / 4; ++k) {
+      const int m = (k * 64 + lane) / kChunks, ch = (k * 64 + lane) % kChunks;
+      const int om = m0 + wm * WM + i * 16 + m, n = nw + ch * kPer;
+      const v4i v = *(const v4i*)(st + m * kRowBytes + ((ch ^ (m & (kChunks - 1))) << 4));
+      if (om >= m_end) continue;
+      uint8_t* const to = (uint8_t*)p.c + ((int64_t)om * p.N + n) * kEl;
+      if (n + kPer <= p.N) {
+        *(Out*)to = __builtin_bit_cast(Out, v);
+      } else {  // the row's end
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) {
+          if (n + r >= p.N) break;
+          if constexpr (kBf16) ((uint16_t*)to)[r] = (uint16_t)(v[r / 2] >> (r % 2 * 16));
+          else ((int*)to)[r] = v[r];
+        }
       }
-    };
-    if (p.N % (16 / kEl) == 0) store_rows(uint4{});
-    else if (!kBf16 || p.N % 2 == 0) store_rows(uint32_t{});
-    else store_rows(uint16_t{});
+    }
     __builtin_amdgcn_wave_barrier();
   }
 }
@@ -570,10 +575,11 @@ __global__ __launch_bounds__(64 * W) void gemm_i8_small_kernel(I8Args p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] = scaled(sum[r], sa0, sb0[r]);
     const int64_t at = (int64_t)gm * p.N + gn;
-    if (p.N % 4 == 0) {  // all four in or all out, and aligned
-      if (gn >= p.N) return;
-      if constexpr (kBf16) *(bf16x4*)((__bf16*)p.c + at) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-      else *(v4f*)((float*)p.c + at) = v4f{v[0], v[1], v[2], v[3]};
+    if (gn + 4 <= p.N) {  // (rows of c start at any element)
+      typedef __bf16 Out16 __attribute__((ext_vector_type(4), aligned(2)));
+      typedef float Out32 __attribute__((ext_vector_type(4), aligned(4)));
+      if constexpr (kBf16) *(Out16*)((__bf16*)p.c + at) = Out16{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+      else *(Out32*)((float*)p.c + at) = Out32{v[0], v[1], v[2], v[3]};
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
