@@ -130,6 +130,44 @@ def test_largest_sums():
         assert (c == float(np.float32(16384 * K))).all()
 
 
+def test_operands_past_32_bits():
+    """Rows whose byte offset does not fit 32 bits: a 40000 x 131056, b 40 x 1024 x 131056 (5.2 and 5.4 GB)."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    K, N = 131056, 17
+    ones = torch.ones(40960, device="cuda")
+    k = torch.arange(K, device="cuda")
+    row, col = (k % 251 - 125).to(torch.int8), (k % 127 - 63).to(torch.int8)
+    sums = float(np.float32(int((row.long() * col.long()).sum())))
+    a = torch.zeros((40000, K), dtype=torch.int8, device="cuda")
+    a[-1] = row
+    b = torch.zeros((N, K), dtype=torch.int8, device="cuda")
+    b[-1] = col
+    c = F.int8_gemm_scaled(a, ones[:40000], b, ones[:N], "f32")
+    assert c[-1, -1] == sums and torch.count_nonzero(c) == 1
+    del a
+    b = torch.zeros((40, 1024, K), dtype=torch.int8, device="cuda")
+    b[-1, -1] = col
+    a = torch.zeros((128, K), dtype=torch.int8, device="cuda")
+    a[5] = row
+    off = torch.zeros(41, dtype=torch.int32, device="cuda")
+    off[40] = 128
+    c = F.int8_gemm_grouped(a, ones[:128], b, ones.view(40, 1024), off, "f32")
+    assert c[5, -1] == sums and torch.count_nonzero(c) == 1
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_outputs_past_32_bits(out):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    M, N, K = 65537, 40001, 16
+    sa, sb = scales(M, 2750), scales(N, 2751)
+    a, b = codes((M, K), 2752), codes((N, K), 2753)
+    c = F.int8_gemm_scaled(dev(a), dev(sa), dev(b), dev(sb), out)
+    for rows in (slice(0, 3), slice(M - 3, M)):
+        same(c[rows], rounded(int8.gemm(a[rows], sa[rows], b, sb), out))
+
+
 def test_empty_sizes():
     import torch
     import fp8_fine_grained_online_amd as F

@@ -85,6 +85,32 @@ def test_masked_logits_and_empty_rows():
         assert np.isfinite(d).all() and not d[3].any() and not d[5].any()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logits_at_any_element(dtype):
+    """Contiguous logits that start one element past an aligned address."""
+    import torch
+    xd, x = logits_of(33, 256, dtype, 2404)
+    shifted = torch.empty(33 * 256 + 1, dtype=xd.dtype, device="cuda")[1:].view(33, 256)
+    shifted.copy_(xd)
+    check(shifted, x, 8, score="sigmoid", n_groups=8, topk_groups=4)
+    check(shifted, x, 8, score="softmax", renormalize=False)
+
+
+def test_logits_past_32_bits():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    T, G = 4200000, 1024  # 8.6 GB
+    xd, x = logits_of(5, G, "bf16", 2405)
+    big = torch.zeros((T, G), dtype=torch.bfloat16, device="cuda")
+    big[-5:] = xd
+    ids, w = F.fp8q_moe_route(big, 6, score="softmax")
+    few, wf = F.fp8q_moe_route(xd, 6, score="softmax")
+    assert torch.equal(ids[-5:], few) and torch.equal(w[-5:], wf)
+    assert torch.equal(ids[0], torch.arange(6, dtype=torch.int32, device="cuda"))
+    d = F.fp8q_moe_route_bwd(big, ids, w)
+    assert torch.equal(d[-5:], F.fp8q_moe_route_bwd(xd, few, wf))
+
+
 def test_extreme_logits():
     """Scores that underflow, saturate, or differ in the last bit of binary32."""
     import torch

@@ -60,6 +60,20 @@ def test_permute(T, topk, G, K, name):
     assert np.isnan(got[len(want):]).all()  # not written
 
 
+@pytest.mark.parametrize("T,topk,G", [(2048, 1, 8), (2049, 1, 8), (256, 8, 1024), (257, 8, 1024), (32, 64, 100)])
+def test_permute_where_the_sort_changes_hands(T, topk, G):
+    """2048 slots are sorted inside the copy, more are not: the same rows."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    ids = routing(T, topk, G, 2650 + T, drop=9)
+    x = randn((T, 24), "bf16", 2651)
+    xp, off, rows = F.fp8q_moe_permute(x, torch.from_numpy(ids).cuda(), G)
+    want, want_off, want_rows = tokens.permute(x.float().cpu().numpy(), ids, G)
+    assert np.array_equal(off.cpu().numpy(), want_off)
+    assert np.array_equal(rows.cpu().numpy(), want_rows)
+    assert np.array_equal(xp[:len(want)].float().cpu().numpy(), want)
+
+
 def test_permute_is_the_dispatch_layout():
     import torch
     import fp8_fine_grained_online_amd as F
@@ -202,6 +216,20 @@ def test_offsets_past_32_bits():
     F.fp8q_moe_combine_bwd(y, c, rows, None, off, dc=dc)
     assert torch.equal(dc[M - 1], y[0]) and torch.equal(dc[0], y[0])
     assert not dc[1:M - 1:997].any()
+
+
+def test_permuted_rows_past_32_bits():
+    """70 experts' blocks of 128 rows of 262144 bfloat16: 4.7 GB, the last token's row and its padding at its end."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    K, G = 262144, 70
+    x = torch.arange(1, G + 1, device="cuda").to(torch.bfloat16).unsqueeze(1).expand(G, K).contiguous()
+    ids = torch.arange(G, dtype=torch.int32, device="cuda").unsqueeze(1)
+    xp, off, rows = F.fp8q_moe_permute(x, ids, G, xp=torch.full((F.lib().fp8q_moe_dispatch_max_rows(G, 1, G), K), 3.0,
+                                                                dtype=torch.bfloat16, device="cuda"))
+    assert off[G] == 128 * G and torch.equal(rows[:, 0], 128 * torch.arange(G, dtype=torch.int32, device="cuda"))
+    for e in (0, G - 1):
+        assert (xp[128 * e] == e + 1).all() and not xp[128 * e + 1:128 * e + 128].any()
 
 
 def test_refusals():
