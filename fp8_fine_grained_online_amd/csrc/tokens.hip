@@ -89,15 +89,22 @@ struct Chunk<float> {
 // (at most 127, 32 KB each at least: 512 slots of 1024 experts, K = 256, took
 // 29.5 us with 16 parts, a row per part, and 9.3 with 2).
 //
-// Where a slot's row is comes from the dispatch's counting and scanning kernels
-// (row_of_slot holds ranks inside 256-slot blocks, `base` the blocks' first
-// rows; the rows replace the ranks here). With few slots (kSort) that is one
-// launch too many twice over: every workgroup then sorts the ids by itself, in
-// LDS, and the whole call is this kernel. us, by itself / in three launches, K =
-// 2048: 128 slots of 8 experts 4.9 / 10.7, 2048 of 8 11.6 / 11.4, 2048 of 64 14.4
-// / 19.6, but 4096 of 8 20.8 / 12.7 and of 64 25.1 / 20.4. (The ids held in
-// registers, ranks counted by ballots: 8.8 for 10.5 at 2048 of 8, K = 256, but 5.0
-// for 4.5 at 128.)
+// A slot's row is its expert's first row plus the number of earlier slots with
+// that expert. Where that comes from (Way):
+//   kSort   every workgroup sorts the ids by itself, in LDS: the call is this
+//           kernel alone. Up to kSortSlots slots.
+//   kCount  a kernel counts blocks of kCountBlock slots and leaves every slot's
+//           rank in its block; the workgroups here add the blocks up. Up to
+//           kCountBlocks blocks and kCountTokens tokens (each pays for it).
+//   kScan   the dispatch's counting and scanning kernels.
+// us on MI355X, kSort / kCount / kScan:
+//   16 tokens, top-8 of 8, K = 256      4.5 /   - / 10.3
+//   1024, top-1 of 64, K = 256          6.2 /   - / 13.6
+//   256, top-8 of 8, K = 256           10.4 / 7.7 / 10.7
+//   512, top-8 of 32, K = 7168            - / 20.9 / 25.7
+//   2048, top-8 of 32, K = 7168           - / 54.1 / 59.9
+//   4096, top-1 of 8, K = 256             - / 12.5 / 11.8; K = 7168 29.3 / 31.8
+//   8192, top-8 of 32, K = 7168           - / 226 / 215
 //
 // Rows are written with ordinary stores even where they cannot stay in the
 // Infinity Cache: 8192 tokens x top-8 x 7168 took 197 us with them and 210 with
@@ -105,43 +112,132 @@ struct Chunk<float> {
 // 227).
 // ---------------------------------------------------------------------------
 constexpr int kPadParts = 16;
-constexpr int kSortSlots = 2048;   // most slots a workgroup sorts by itself
-constexpr int kDispBlock = 256;    // slots per block of the counting kernel
+constexpr int kSortSlots = 1024;   // most slots a workgroup sorts by itself
+constexpr int kCountBlock = 4096;  // slots per block of the counting kernel below
+constexpr int kCountBlocks = 16;
+constexpr int kCountTokens = 4096;
+constexpr int kDispBlock = 256;    // and of the dispatch's
 constexpr int kMaxExperts = 1024;
 
 struct PermuteArgs {
   const uint8_t* x;
   const int32_t* ids;
-  const int32_t* base;    // !kSort: first row of each (block, expert)
-  const int32_t* counts;  // !kSort: slots of each expert
+  const int32_t* hist;    // kCount: slots of each (block, expert)
+  const int32_t* base;    // kScan: first row of each (block, expert)
+  const int32_t* counts;  // kScan: slots of each expert
   int32_t* row_of_slot;
   int32_t* m_offsets;
   uint8_t* xp;
   int n_tok, K, topk, G, pad_parts;
 };
 
-struct SortLds {
-  int16_t ids[kSortSlots];           // -1: dropped
+enum Way { kSort, kCount, kScan };
+
+// Ranks of the slots of a block among its slots with the same expert (-1: no
+// expert), and the block's histogram. 16 wavefronts, each with a histogram of
+// its 256 slots so far: lanes with the same expert find each other bit by bit
+// of its number.
+constexpr int kCountWaves = kCountBlock / 256;
+
+__global__ __launch_bounds__(64 * kCountWaves) void token_count_kernel(const int32_t* __restrict__ ids, int slots,
+                                                                      int G, int32_t* __restrict__ hist,
+                                                                      int32_t* __restrict__ in_block) {
+  __shared__ int32_t of_wave[kCountWaves][kMaxExperts];
+  constexpr int kSets = 4;  // of 64 slots per wavefront
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t slot0 = (int64_t)blockIdx.x * kCountBlock + wave * 256 + lane;
+  int e[kSets], rank[kSets];
+#pragma unroll
+  for (int u = 0; u < kSets; ++u) e[u] = slot0 + u * 64 < slots ? ids[slot0 + u * 64] : -1;
+  for (int i = lane; i < G; i += 64) of_wave[wave][i] = 0;
+  const int bits = G > 1 ? 32 - __builtin_clz(G - 1) : 0;
+#pragma unroll
+  for (int u = 0; u < kSets; ++u) {
+    const bool on = e[u] >= 0 && e[u] < G;
+    uint64_t same = __ballot(on);
+    for (int b = 0; b < bits; ++b) {
+      const bool one = (e[u] >> b) & 1;
+      const uint64_t ones = __ballot(one);
+      same &= one ? ones : ~ones;
+    }
+    if (!on) e[u] = -1;
+    // (the wave's LDS accesses are in order; the fences keep the compiler to it)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int before = on ? of_wave[wave][e[u]] : 0;
+    rank[u] = before + __popcll(same & ((1ull << lane) - 1));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (on && (same >> lane) == 1) of_wave[wave][e[u]] = rank[u] + 1;  // the last of them
+  }
+  __syncthreads();
+  for (int x = tid; x < G; x += 64 * kCountWaves) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kCountWaves; ++w) {
+      const int c = of_wave[w][x];
+      of_wave[w][x] = sum;
+      sum += c;
+    }
+    hist[(int64_t)blockIdx.x * G + x] = sum;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kSets; ++u)
+    if (slot0 + u * 64 < slots) in_block[slot0 + u * 64] = e[u] < 0 ? -1 : rank[u] + of_wave[wave][e[u]];
+}
+
+struct ExpertLds {
   int32_t counts[kMaxExperts];
   int32_t offsets[kMaxExperts + 1];  // first row of each expert's block
   int32_t wave_sum[kTokWaves];
 };
+struct SortLds : ExpertLds {
+  int16_t ids[kSortSlots];  // -1: dropped
+};
+struct CountLds : ExpertLds {
+  int32_t before[kMaxExperts];  // slots of each expert in the blocks before the token's
+};
+struct ScanLds {};
 
-struct NoSort {};
+template <Way kWay>
+using WayLds = std::conditional_t<kWay == kSort, SortLds, std::conditional_t<kWay == kCount, CountLds, ScanLds>>;
 
-// Counts and padded offsets of all experts, by the whole workgroup.
-__device__ __forceinline__ void sort_experts(SortLds& s, const int32_t* __restrict__ ids, int slots, int G) {
+// The ids and every expert's count, by the whole workgroup.
+__device__ __forceinline__ void count_experts(SortLds& s, const PermuteArgs& a) {
   constexpr int kThreads = 64 * kTokWaves;
-  constexpr int kEach = kMaxExperts / kThreads;  // consecutive experts per thread
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e < G; e += kThreads) s.counts[e] = 0;
+  const int tid = threadIdx.x, slots = a.n_tok * a.topk;
+  for (int e = tid; e < a.G; e += kThreads) s.counts[e] = 0;
   __syncthreads();
   for (int i = tid; i < slots; i += kThreads) {
-    const int e = ids[i];
-    const bool on = e >= 0 && e < G;
+    const int e = a.ids[i];
+    const bool on = e >= 0 && e < a.G;
     s.ids[i] = on ? (int16_t)e : (int16_t)-1;
     if (on) atomicAdd(&s.counts[e], 1);  // integers: any order, the same counts
   }
+}
+
+// Every expert's count, and that of the blocks before block `own`.
+__device__ __forceinline__ void count_experts(CountLds& s, const PermuteArgs& a, int n_blk, int own) {
+  for (int e = threadIdx.x; e < a.G; e += 64 * kTokWaves) {
+    int h[kCountBlocks], before = 0, sum = 0;
+#pragma unroll
+    for (int b = 0; b < kCountBlocks; ++b) h[b] = b < n_blk ? a.hist[b * a.G + e] : 0;
+#pragma unroll
+    for (int b = 0; b < kCountBlocks; ++b) {
+      if (b == own) before = sum;
+      sum += h[b];
+    }
+    s.counts[e] = sum;
+    s.before[e] = before;
+  }
+}
+
+// Padded offsets from the counts, by the whole workgroup.
+__device__ __forceinline__ void offset_experts(ExpertLds& s, int G) {
+  constexpr int kThreads = 64 * kTokWaves;
+  constexpr int kEach = kMaxExperts / kThreads;  // consecutive experts per thread
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   __syncthreads();
   int padded[kEach], sum = 0;
 #pragma unroll
@@ -170,28 +266,40 @@ __device__ __forceinline__ void sort_experts(SortLds& s, const int32_t* __restri
   __syncthreads();
 }
 
-template <typename T, bool kSort>
+template <typename T, Way kWay>
 __global__ __launch_bounds__(64 * kTokWaves) void permute_kernel(PermuteArgs a) {
   using C = Chunk<T>;
   constexpr int kThreads = 64 * kTokWaves;
   constexpr int kHeld = 4;  // chunks of the row a lane holds at a time
-  __shared__ std::conditional_t<kSort, SortLds, NoSort> sort;
+  __shared__ WayLds<kWay> experts;
   __shared__ int32_t rows[64];  // of the current 64 choices
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n_chunks = a.K / 8;
   const int64_t row_bytes = (int64_t)n_chunks * C::kBytes;
   const int64_t first_slot = (int64_t)blockIdx.x * a.topk;
-  if constexpr (kSort) {
-    sort_experts(sort, a.ids, a.n_tok * a.topk, a.G);
+  const int own = (int)(first_slot / kCountBlock);  // kCount: the block of the token's first slot
+  int rank = -1, mine = -1;                         // choice j0 + lane: rank in its block, and expert
+  auto load_choice = [&](int j) {
+    rank = mine = -1;
+    if (j < a.topk) rank = a.row_of_slot[first_slot + j], mine = a.ids[first_slot + j];
+  };
+  if constexpr (kWay != kScan) {
+    if constexpr (kWay == kSort) {
+      count_experts(experts, a);
+    } else {
+      if ((int)blockIdx.x < a.n_tok && wave == 0) load_choice(lane);
+      count_experts(experts, a, (int)(((int64_t)a.n_tok * a.topk + kCountBlock - 1) / kCountBlock), own);
+    }
+    offset_experts(experts, a.G);
     if (blockIdx.x == 0)
-      for (int e = tid; e <= a.G; e += kThreads) a.m_offsets[e] = sort.offsets[e];
+      for (int e = tid; e <= a.G; e += kThreads) a.m_offsets[e] = experts.offsets[e];
   }
   if ((int)blockIdx.x >= a.n_tok) {
     const int pad = blockIdx.x - a.n_tok;
     const int e = pad / a.pad_parts;
     int row, end;
-    if constexpr (kSort) row = sort.offsets[e] + sort.counts[e], end = sort.offsets[e + 1];
+    if constexpr (kWay != kScan) row = experts.offsets[e] + experts.counts[e], end = experts.offsets[e + 1];
     else row = a.m_offsets[e] + a.counts[e], end = a.m_offsets[e + 1];
     const int64_t n = (int64_t)(end - row) * n_chunks;  // contiguous
     for (int64_t i = pad % a.pad_parts * kThreads + tid; i < n; i += a.pad_parts * kThreads)
@@ -203,20 +311,29 @@ __global__ __launch_bounds__(64 * kTokWaves) void permute_kernel(PermuteArgs a) 
     const int n = min(64, a.topk - j0);
     // ---- rows of choices j0 .. j0 + n - 1 ----
     if (j0 > 0) __syncthreads();
-    if constexpr (kSort) {
+    if constexpr (kWay == kSort) {
       // a slot's rank: the earlier slots with its expert
       for (int j = wave; j < n; j += kTokWaves) {
         const int slot = (int)first_slot + j0 + j;
-        const int e = sort.ids[slot];
+        const int e = experts.ids[slot];
         int rank = 0;
         for (int i0 = 0; i0 < slot; i0 += 64)
-          rank += __popcll(__ballot(i0 + lane < slot && sort.ids[i0 + lane] == e));
-        if (lane == 0) rows[j] = e < 0 ? -1 : sort.offsets[e] + rank;
+          rank += __popcll(__ballot(i0 + lane < slot && experts.ids[i0 + lane] == e));
+        if (lane == 0) rows[j] = e < 0 ? -1 : experts.offsets[e] + rank;
       }
     } else if (wave == 0 && lane < n) {
       const int64_t slot = first_slot + j0 + lane;
-      const int rank = a.row_of_slot[slot];
-      rows[lane] = rank < 0 ? -1 : a.base[(slot / kDispBlock) * a.G + a.ids[slot]] + rank;
+      if (kWay == kScan || j0 > 0) load_choice(j0 + lane);
+      int row = rank;
+      if constexpr (kWay == kCount) {
+        if (rank >= 0) {
+          row += experts.offsets[mine] + experts.before[mine];
+          for (int b = own; b < (int)(slot / kCountBlock); ++b) row += a.hist[b * a.G + mine];
+        }
+      } else {
+        if (rank >= 0) row += a.base[(slot / kDispBlock) * a.G + mine];
+      }
+      rows[lane] = row;
     }
     __syncthreads();
     if (wave == 0 && lane < n) a.row_of_slot[first_slot + j0 + lane] = rows[lane];
@@ -428,22 +545,30 @@ hipError_t launch_moe_permute(const void* x, bool bf16, const int32_t* ids, int6
   int32_t* hist = (int32_t*)workspace;
   int32_t* base = hist + n_blk * G;
   int32_t* counts = base + n_blk * G;
-  const bool sort = T > 0 && slots <= kSortSlots;
-  if (!sort) {
+  const Way way = T == 0               ? kScan
+                  : slots <= kSortSlots ? kSort
+                  : slots <= kCountBlock * kCountBlocks && T <= kCountTokens ? kCount : kScan;
+  if (way == kCount) {
+    token_count_kernel<<<dim3((unsigned)((slots + kCountBlock - 1) / kCountBlock)), dim3(64 * kCountWaves), 0, stream>>>(
+        ids, (int)slots, (int)G, hist, row_of_slot);
+  } else if (way == kScan) {
     if (T > 0)
       dispatch_count_kernel<<<dim3((unsigned)n_blk), dim3(kDispBlock), 0, stream>>>(ids, (int)slots, (int)G, hist, row_of_slot);
     dispatch_scan_kernel<<<dim3(1), dim3(kMaxExperts), 0, stream>>>(hist, (int)n_blk, (int)G, base, counts, m_offsets);
     if (T == 0) return hipGetLastError();
   }
   const int64_t parts = std::min<int64_t>(std::max<int64_t>(K * (bf16 ? 2 : 4) / 256, 1), kPadParts);
-  const PermuteArgs a{(const uint8_t*)x, ids, base, counts, row_of_slot, m_offsets, (uint8_t*)xp,
+  const PermuteArgs a{(const uint8_t*)x, ids, hist, base, counts, row_of_slot, m_offsets, (uint8_t*)xp,
                       (int)T, (int)K, (int)topk, (int)G, (int)parts};
   const dim3 grid((unsigned)(T + (K > 0 ? parts * G : 0))), block(64 * kTokWaves);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
-  if (bf16)
-    sort ? go(permute_kernel<uint16_t, true>) : go(permute_kernel<uint16_t, false>);
-  else
-    sort ? go(permute_kernel<float, true>) : go(permute_kernel<float, false>);
+  auto by_way = [&](auto t) {
+    using E = decltype(t);
+    way == kSort    ? go(permute_kernel<E, kSort>)
+    : way == kCount ? go(permute_kernel<E, kCount>)
+                    : go(permute_kernel<E, kScan>);
+  };
+  bf16 ? by_way(uint16_t{}) : by_way(float{});
   return hipGetLastError();
 }
 

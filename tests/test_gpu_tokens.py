@@ -60,9 +60,13 @@ def test_permute(T, topk, G, K, name):
     assert np.isnan(got[len(want):]).all()  # not written
 
 
-@pytest.mark.parametrize("T,topk,G", [(2048, 1, 8), (2049, 1, 8), (256, 8, 1024), (257, 8, 1024), (32, 64, 100)])
+@pytest.mark.parametrize("T,topk,G", [(2048, 1, 8), (2049, 1, 8), (256, 8, 1024), (257, 8, 1024), (32, 64, 100),
+                                      (1024, 1, 8), (1025, 1, 8), (128, 8, 1024), (129, 8, 1024), (16, 64, 100),
+                                      (1000, 6, 1024), (1366, 3, 1), (3, 5000, 100), (4096, 16, 40), (4097, 2, 3),
+                                      (5, 13200, 64), (65537, 1, 3), (9000, 8, 64)])
 def test_permute_where_the_sort_changes_hands(T, topk, G):
-    """2048 slots are sorted inside the copy, more are not: the same rows."""
+    """1024 slots are sorted inside the copy, 65536 of at most 4096 tokens are counted in blocks of 4096 (a token's
+    slots may lie in several), more in blocks of 256: the same rows."""
     import torch
     import fp8_fine_grained_online_amd as F
     ids = routing(T, topk, G, 2650 + T, drop=9)
