@@ -323,17 +323,18 @@ __global__ __launch_bounds__(64 * kTokWaves) void permute_kernel(PermuteArgs a) 
       }
     } else if (wave == 0 && lane < n) {
       const int64_t slot = first_slot + j0 + lane;
-      if (kWay == kScan || j0 > 0) load_choice(j0 + lane);
-      int row = rank;
       if constexpr (kWay == kCount) {
+        if (j0 > 0) load_choice(j0 + lane);
+        int row = rank;
         if (rank >= 0) {
           row += experts.offsets[mine] + experts.before[mine];
           for (int b = own; b < (int)(slot / kCountBlock); ++b) row += a.hist[b * a.G + mine];
         }
+        rows[lane] = row;
       } else {
-        if (rank >= 0) row += a.base[(slot / kDispBlock) * a.G + mine];
+        const int in_block = a.row_of_slot[slot];
+        rows[lane] = in_block < 0 ? -1 : a.base[(slot / kDispBlock) * a.G + a.ids[slot]] + in_block;
       }
-      rows[lane] = row;
     }
     __syncthreads();
     if (wave == 0 && lane < n) a.row_of_slot[first_slot + j0 + lane] = rows[lane];
