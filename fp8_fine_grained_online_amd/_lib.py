@@ -516,7 +516,10 @@ def _run(fn, stream, first, *args):
     else:
         cuda = _torch().cuda
         if not hasattr(stream, "cuda_stream"):
-            stream = cuda.ExternalStream(int(stream), device=getattr(first, "device", None))
+            device = getattr(first, "device", None)  # (ExternalStream takes 0 as a wish for a new stream)
+            stream = cuda.ExternalStream(int(stream), device=device) if int(stream) else cuda.default_stream(device)
+        if getattr(first, "is_cuda", False) and stream.device != first.device:
+            raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {first.device}")
         with cuda.stream(stream):
             result = call(first, *args)
     if type(result) is int:

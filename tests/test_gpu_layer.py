@@ -260,3 +260,20 @@ def test_stream_argument():
         M = int(off[-1])
         assert torch.equal(ids, ids2) and torch.equal(w, w2) and torch.equal(off, off2) and torch.equal(rows, rows2)
         assert torch.equal(xp[:M], xp2[:M]) and torch.equal(y2, F.fp8q_moe_combine(xp, rows, w))
+
+
+def test_null_stream_by_handle():
+    """Handle 0 is the default stream, whatever stream is current: its earlier work is waited for."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = torch.zeros(64, 512, dtype=torch.bfloat16, device="cuda")
+    late = torch.randn(64, 512, device="cuda").to(torch.bfloat16)
+    want_q, want_s = F.fp8q_quant_int8_rows(late)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)  # about 10 ms on the default stream, then the values
+    x.copy_(late)
+    with torch.cuda.stream(side):
+        q, s = F.fp8q_quant_int8_rows(x, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(q, want_q) and torch.equal(s, want_s)

@@ -137,3 +137,17 @@ def test_binding_refuses_before_any_device_call():
         F.fp8q_moe_permute(None, x, 4)
     with pytest.raises(ValueError, match="device tensor"):
         F.fp8q_moe_combine(x, torch.zeros(4, 2, dtype=torch.int32))
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    import torch
+    from fp8_fine_grained_online_amd import _lib
+
+    class Stream:
+        cuda_stream, device = 64, torch.device("cuda", 1)
+
+    class Tensor:
+        is_cuda, device = True, torch.device("cuda", 0)
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        _lib._run("fp8q_quant_int8_rows", Stream(), Tensor(), None, None)
