@@ -15,10 +15,12 @@
 //
 // Few bytes move (at most 17 MB below, 3.5 us), so the time is mostly that of one
 // launch (1.8 us for an empty kernel) and of one wavefront's chain: a load, the
-// softmax, its choices. MI355X, us: 16 tokens of 256 experts in 8 groups, top-8, sigmoid 6.0;
-// 8192 of 64, top-6 5.6; gradient, 8192 of 256 5.3. (With every choice searched
-// through all keys, the library's exponential, and gradient shares passed from
-// lane to lane the first took 8.8 and the gradient 8.3.)
+// softmax, its choices (0.2 us each). MI355X, us: 16 tokens of 256 experts in 8
+// groups, top-8, sigmoid 6.0; 8192 of 64, top-6 5.6; 100 of 1024, top-64 26.9 (41.6
+// with the places of a lane's experts moved up one by one); gradient, 8192 of 256
+// 5.3. (With every choice searched through all keys, the library's exponential,
+// and gradient shares passed from lane to lane the first took 8.8 and the gradient
+// 8.3.)
 #include <type_traits>
 
 #include "common.hpp"
@@ -102,19 +104,20 @@ __device__ __forceinline__ double key_value(uint64_t k) {
   return __longlong_as_double((long long)((k >> 63) ? k & ~(1ull << 63) : ~k));
 }
 
-// Largest key of the wavefront and its lowest lane; 0 when there is none. The
+// The lane of the wavefront's largest key, the lowest if several have it. The
 // upper halves are compared first; only if several lanes share the largest
-// (wave-uniform, rare) are the lower halves.
-__device__ __forceinline__ uint64_t wave_best(uint64_t k, int& lane) {
+// (wave-uniform, rare) are the lower halves. Returns the upper half: 0 when every
+// key is 0 (a finite value's is not).
+__device__ __forceinline__ uint32_t wave_best(uint64_t k, int& lane) {
   const uint32_t hi = (uint32_t)(k >> 32), lo = (uint32_t)k;
   const uint32_t mhi = wave_max_u32(hi);
   uint64_t at = __ballot(hi == mhi);
-  if (__popcll(at) > 1) {
+  if (at & (at - 1)) {
     const uint32_t mlo = wave_max_u32(hi == mhi ? lo : 0u);
     at = __ballot(hi == mhi && lo == mlo);
   }
   lane = __builtin_ctzll(at);
-  return ((uint64_t)mhi << 32) | lane_u32(lo, lane);
+  return mhi;
 }
 
 // A lane's E keys, largest first, with their places in the lane; equal keys by
@@ -267,17 +270,24 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
 
 #pragma unroll
   for (int i = 0; i < E; ++i) tab[lane * E + i] = (uint64_t)__double_as_longlong(p[i]);
+  typedef std::conditional_t<(E > 8), uint64_t, uint32_t> Places;  // 4 bits each, the first lowest
+  Places places = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) places |= (Places)place[i] << (4 * i);
   int my_id = -1;  // lane j: choice j
   for (int j = 0; j < a.topk; ++j) {
+    // (no branch where nothing is left to choose: the keys stay 0)
     int at;
-    if (!wave_best(key[0], at)) break;  // nothing left to choose
-    const int id = at * E + __builtin_amdgcn_readlane(place[0], at);
-    if (lane == j) my_id = id;
+    const uint32_t best = wave_best(key[0], at);
+    const int id = best ? at * E + (__builtin_amdgcn_readlane((int)places, at) & 15) : -1;
+    my_id = lane == j ? id : my_id;
     // the winner's next key moves up
+    if (lane == at) {
 #pragma unroll
-    for (int i = 0; i + 1 < E; ++i)
-      if (lane == at) key[i] = key[i + 1], place[i] = place[i + 1];
-    if (lane == at) key[E - 1] = 0;
+      for (int i = 0; i + 1 < E; ++i) key[i] = key[i + 1];
+      key[E - 1] = 0;
+      places >>= 4;
+    }
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();

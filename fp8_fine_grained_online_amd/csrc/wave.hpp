@@ -41,10 +41,7 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   v = max(v, dpp_u32<0x4E>(v));
   v = max(v, dpp_u32<0x141>(v));
   v = max(v, dpp_u32<0x140>(v));
-  // row_bcast:15 into rows 1 and 3, row_bcast:31 into rows 2 and 3: lane 63 has seen all four
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x142, 0xA, 0xF, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x143, 0xC, 0xF, false));
-  return lane_u32(v, 63);
+  return max(max(lane_u32(v, 0), lane_u32(v, 16)), max(lane_u32(v, 32), lane_u32(v, 48)));
 }
 
 __device__ __forceinline__ float wave_sum_f32(float v) {
