@@ -15,8 +15,8 @@
 //
 // Few bytes move (at most 17 MB below, 3.5 us), so the time is mostly that of one
 // launch (1.8 us for an empty kernel) and of one wavefront's chain: a load, the
-// softmax, its choices (0.2 us each). MI355X, us: 16 tokens of 256 experts in 8
-// groups, top-8, sigmoid 6.0; 8192 of 64, top-6 5.6; 100 of 1024, top-64 26.9 (41.6
+// softmax, its choices (0.15 us each). MI355X, us: 16 tokens of 256 experts in 8
+// groups, top-8, sigmoid 5.6; 8192 of 64, top-6 5.6; 100 of 1024, top-64 23.2 (41.6
 // with the places of a lane's experts moved up one by one); gradient, 8192 of 256
 // 5.3. (With every choice searched through all keys, the library's exponential,
 // and gradient shares passed from lane to lane the first took 8.8 and the gradient
@@ -192,6 +192,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   // scores by expert: the probabilities of the chosen are looked up at the end,
   // and group scores that do not fall on whole lanes are formed here
   __shared__ uint64_t table[kRouteWaves][64 * E];
+  __shared__ int chosen[kRouteWaves][64];  // ids of the choices
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x * kRouteWaves + wave;
@@ -274,15 +275,14 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   Places places = 0;
 #pragma unroll
   for (int i = 0; i < E; ++i) places |= (Places)place[i] << (4 * i);
-  int my_id = -1;  // lane j: choice j
+  int* const ids = chosen[wave];
+  ids[lane] = -1;
   for (int j = 0; j < a.topk; ++j) {
-    // (no branch where nothing is left to choose: the keys stay 0)
     int at;
-    const uint32_t best = wave_best(key[0], at);
-    const int id = best ? at * E + (__builtin_amdgcn_readlane((int)places, at) & 15) : -1;
-    my_id = lane == j ? id : my_id;
-    // the winner's next key moves up
+    if (!wave_best(key[0], at)) break;  // nothing left to choose
     if (lane == at) {
+      // the winner notes its expert, and its next key moves up
+      ids[j] = lane * E + (int)(places & 15);
 #pragma unroll
       for (int i = 0; i + 1 < E; ++i) key[i] = key[i + 1];
       key[E - 1] = 0;
@@ -291,6 +291,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
+  const int my_id = ids[lane];  // lane j: choice j
   double w = my_id >= 0 ? __longlong_as_double((long long)tab[my_id]) : 0.0;
   if (a.renorm) {
     const double sum = wave_sum_f64(w);
