@@ -640,8 +640,8 @@ hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, c
   //   64 x 512 x 512         16x16 2.70   32x16 2.98   32x32 3.24
   //   256 x 512 x 2048       32x16 5.10   32x32 5.92   64x64 6.33
   //   256 x 1024 x 512       32x32 3.40   32x16 3.90   64x64 4.64
-  //   333 x 2050 x 2064      64x64 8.76   64x128 11.8  32x32 15.4
-  //   1024 x 2048 x 2048     64x128 9.36  64x64 12.3   128x128 11.7
+  //   333 x 2050 x 2064      64x64 8.3    64x128 10.6  32x32 15.4
+  //   1024 x 2048 x 2048     64x128 9.0   64x64 12.6   128x128 11.3
   //   1024 x 4096 x 4096     128x128 20.1 64x128 26.7  256x256 45.7
   // Long K is better shared through LDS: 32 x 7168 x 7168 takes 12.4 us in
   // 64x64 tiles and 15.4 in 32x32; at K = 2048 6.4 and 6.9.
@@ -649,8 +649,15 @@ hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, c
   if (wgs(16, 16) <= kCus) return launch_small<1, 1, 8, 4>(p, bf16, stream);
   if (wgs(32, 16) <= kCus) return launch_small<2, 1, 8, 6>(p, bf16, stream);
   if (wgs(32, 32) <= kCus && K < 2048) return launch_small<2, 2, 8, 4>(p, bf16, stream);
-  if (wgs(64, 64) <= kCus) return launch_tiles<64, 64, 3, 2, false>(p, bf16, (M + 63) / 64, stream);
-  if (wgs(64, 128) <= kCus) return launch_tiles<64, 128, 4, 1, false>(p, bf16, (M + 63) / 64, stream);
+  if (wgs(64, 64) <= kCus) {
+    // Two groups of waves that share K start with half the steps but have their
+    // sums to add. 200 x 4096, us at K = 256, 992, 2048, 4096, 8192: one group, 5
+    // buffers 3.7, 5.4, 7.1, 10.7, 17.7; two groups, 3 buffers 4.2, 6.0, 7.1, 9.7,
+    // 17.2 (4 buffers: the same). 17 steps do not halve: 333 x 2050 x 2064 7.8, 8.1.
+    if (K <= 17 * kStepK) return launch_tiles<64, 64, 5, 1, false>(p, bf16, (M + 63) / 64, stream);
+    return launch_tiles<64, 64, 3, 2, false>(p, bf16, (M + 63) / 64, stream);
+  }
+  if (wgs(64, 128) <= kCus) return launch_tiles<64, 128, 3, 1, false>(p, bf16, (M + 63) / 64, stream);
   if (wgs(128, 128) <= kCus) return launch_tiles<128, 128, 3, 1, false>(p, bf16, (M + 127) / 128, stream);
   // Large products: 256 x 256 tiles, one per CU, against 128 x 128, two at a time
   // per CU. In rounds of 256 tiles of the large kind: its last, partly filled
@@ -685,7 +692,7 @@ hipError_t launch_int8_gemm_grouped(const int8_t* a, const float* sa, const int8
   // 128 tiles leave CUs free they are used: 8 x 128 x 2048 x 2048 11.5 (128 x
   // 128: 14.5).
   const int64_t m128 = M_total / 128;
-  if (2 * m128 * ((N + 127) / 128) <= kCus) return launch_tiles<64, 128, 4, 1, true>(p, bf16, 2 * m128, stream);
+  if (2 * m128 * ((N + 127) / 128) <= kCus) return launch_tiles<64, 128, 3, 1, true>(p, bf16, 2 * m128, stream);
   if (M_total < 256 * G) return launch_tiles<128, 128, 2, 1, true>(p, bf16, m128, stream);
   // upper bound on sum_e ceil(rows_e / 256) for rows_e multiples of 128
   return launch_tiles<256, 256, 2, 1, true>(p, bf16, (m128 + G + 1) / 2, stream);
