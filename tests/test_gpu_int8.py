@@ -102,7 +102,8 @@ DENSE = [(1, 1, 16), (1, 7168, 1024), (2, 33, 48), (16, 100, 4112), (17, 129, 12
          (129, 257, 144), (333, 514, 2064), (1000, 31, 640), (1, 64, 131056), (520, 520, 144), (260, 4100, 96),
          (1500, 3000, 400), (2049, 4097, 128), (4100, 2056, 272), (300, 300, 208), (500, 500, 528),
          (1000, 1900, 272), (1500, 2000, 400), (1000, 1901, 2064),
-         (4090, 4080, 272), (4000, 4081, 400)]
+         (4090, 4080, 272), (4000, 4081, 400), (333, 514, 2192), (200, 1030, 2320), (100, 4097, 4112),
+         (500, 1000, 2176)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
