@@ -502,32 +502,32 @@ def _binding():
                 " (there is no fallback path)")
         lib()
         from . import _binding as module
+        module.on_status(_check)
         _native = module
     return _native
 
 
-def _run(fn, stream, first, *args):
-    """A native call on the current stream of the tensors' device, or with
-    `stream` current: new outputs then come from that stream's memory too
-    (memory freed on another stream may still be in use there)."""
-    call = getattr(_native or _binding(), fn)
-    if stream is None:
-        result = call(first, *args)
-    else:
-        cuda = _torch().cuda
-        if not hasattr(stream, "cuda_stream"):
-            device = getattr(first, "device", None)  # (ExternalStream takes 0 as a wish for a new stream)
-            stream = cuda.ExternalStream(int(stream), device=device) if int(stream) else cuda.default_stream(device)
-        if getattr(first, "is_cuda", False) and stream.device != first.device:
-            raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {first.device}")
-        with cuda.stream(stream):
-            result = call(first, *args)
-    if type(result) is int:
-        _check(fn, result)
-    return result
+def _on_stream(stream, fn, first, *args):
+    """A call with `stream` current: new outputs then come from that stream's memory too
+    (memory freed on another stream may still be in use there). Without a stream the
+    calls below run on the current stream of the tensors' device."""
+    cuda = _torch().cuda
+    device = getattr(first, "device", None)
+    if not hasattr(stream, "cuda_stream"):
+        # (ExternalStream takes 0 as a wish for a new stream)
+        stream = cuda.ExternalStream(int(stream), device=device) if int(stream) else cuda.default_stream(device)
+    if getattr(first, "is_cuda", False) and stream.device != device:
+        raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {device}")
+    with cuda.stream(stream):
+        return fn(first, *args)
 
 
 SCORES = {"softmax": 0, "sigmoid": 1}
+_OUT_CODES = {"bf16": FP8Q_OUT_BF16, "f32": FP8Q_OUT_F32}
+
+
+def _out_code(out_dtype):
+    return _OUT_CODES[out_dtype] if out_dtype in _OUT_CODES else _out_dtype(out_dtype)[0]
 
 
 def _score(score):
@@ -541,15 +541,20 @@ def fp8q_moe_route(logits, topk, bias=None, score="softmax", renormalize=True, s
     """Router: logits T x G (float32 or bfloat16) -> (topk_ids int32 T x topk, weights float32
     T x topk). bias (float32, G) is added to the probabilities for the choice only; with
     n_groups > 1 experts come from the topk_groups best groups."""
-    return _run("fp8q_moe_route", stream, logits, bias, topk, _score(score), bool(renormalize), scale,
-                n_groups, topk_groups, topk_ids, weights)
+    if stream is not None:
+        return _on_stream(stream, fp8q_moe_route, logits, topk, bias, score, renormalize, scale, n_groups, topk_groups,
+                          topk_ids, weights)
+    return (_native or _binding()).fp8q_moe_route(logits, bias, topk, _score(score), renormalize, scale, n_groups,
+                                                   topk_groups, topk_ids, weights)
 
 
 def fp8q_moe_route_bwd(logits, topk_ids, dweights, score="softmax", renormalize=True, scale=1.0,
                        dlogits=None, stream=None):
     """Gradient of fp8q_moe_route's weights: dweights (float32 T x topk) -> dlogits (T x G, like logits)."""
-    return _run("fp8q_moe_route_bwd", stream, logits, topk_ids, dweights, _score(score),
-                bool(renormalize), scale, dlogits)
+    if stream is not None:
+        return _on_stream(stream, fp8q_moe_route_bwd, logits, topk_ids, dweights, score, renormalize, scale, dlogits)
+    return (_native or _binding()).fp8q_moe_route_bwd(logits, topk_ids, dweights, _score(score), renormalize,
+                                                       scale, dlogits)
 
 
 def fp8q_moe_permute(x, topk_ids, G, xp=None, m_offsets=None, row_of_slot=None, workspace=None,
@@ -557,13 +562,17 @@ def fp8q_moe_permute(x, topk_ids, G, xp=None, m_offsets=None, row_of_slot=None, 
     """Rows sorted by expert: x T x K (bfloat16 or float32), topk_ids int32 T x topk ->
     (xp M_cap x K, m_offsets int32[G+1], row_of_slot int32 T x topk), the layout of
     fp8q_moe_dispatch_1x128; rows of xp from m_offsets[G] on are not written."""
-    return _run("fp8q_moe_permute", stream, x, topk_ids, G, xp, m_offsets, row_of_slot, workspace)
+    if stream is not None:
+        return _on_stream(stream, fp8q_moe_permute, x, topk_ids, G, xp, m_offsets, row_of_slot, workspace)
+    return (_native or _binding()).fp8q_moe_permute(x, topk_ids, G, xp, m_offsets, row_of_slot, workspace)
 
 
 def fp8q_moe_combine(c, row_of_slot, weights=None, out_dtype="bf16", y=None, stream=None):
     """The way back: y[t] = sum_j weights[t, j] * c[row_of_slot[t, j]] (weights None: ones; rows
     outside c are skipped). c M x K (bfloat16 or float32) -> y T x K of out_dtype."""
-    return _run("fp8q_moe_combine", stream, c, row_of_slot, weights, _out_dtype(out_dtype)[0], y)
+    if stream is not None:
+        return _on_stream(stream, fp8q_moe_combine, c, row_of_slot, weights, out_dtype, y)
+    return (_native or _binding()).fp8q_moe_combine(c, row_of_slot, weights, _out_code(out_dtype), y)
 
 
 def fp8q_moe_combine_bwd(dy, c, row_of_slot, weights, m_offsets, dc=None, dw=None, with_dw=True,
@@ -571,24 +580,31 @@ def fp8q_moe_combine_bwd(dy, c, row_of_slot, weights, m_offsets, dc=None, dw=Non
     """Gradient of fp8q_moe_combine: dy T x K, c M x K -> (dc M x K like c, dw float32 T x topk);
     padding rows of dc are zero, rows from m_offsets[G] on are not written. with_dw=False: dw is
     None (unless given) and c is only used for its shape and type."""
-    return _run("fp8q_moe_combine_bwd", stream, dy, c, row_of_slot, weights, m_offsets, dc, dw,
-                bool(with_dw))
+    if stream is not None:
+        return _on_stream(stream, fp8q_moe_combine_bwd, dy, c, row_of_slot, weights, m_offsets, dc, dw, with_dw)
+    return (_native or _binding()).fp8q_moe_combine_bwd(dy, c, row_of_slot, weights, m_offsets, dc, dw, with_dw)
 
 
 def fp8q_quant_int8_rows(x, q=None, s=None, stream=None):
     """x: bf16 ... x K device tensor (2 or 3 dims: tokens, channels or experts' channels) ->
     (q int8 like x, s float32 without the last dim): one scale amax / 127 per row."""
-    return _run("fp8q_quant_int8_rows", stream, x, q, s)
+    if stream is not None:
+        return _on_stream(stream, fp8q_quant_int8_rows, x, q, s)
+    return (_native or _binding()).fp8q_quant_int8_rows(x, q, s)
 
 
 def int8_gemm_scaled(a, sa, b, sb, out_dtype="bf16", c=None, stream=None):
     """c[m, n] = (sum_k a[m, k] b[n, k]) * sa[m] * sb[n]: a int8 M x K, sa float32 M, b int8 N x K,
     sb float32 N. Returns c (M x N)."""
-    return _run("int8_gemm_scaled", stream, a, sa, b, sb, _out_dtype(out_dtype)[0], c)
+    if stream is not None:
+        return _on_stream(stream, int8_gemm_scaled, a, sa, b, sb, out_dtype, c)
+    return (_native or _binding()).int8_gemm_scaled(a, sa, b, sb, _out_code(out_dtype), c)
 
 
 def int8_gemm_grouped(a, sa, b, sb, m_offsets, out_dtype="bf16", c=None, M_total=None, stream=None):
     """Grouped form: a int8 M x K, sa float32 M, b int8 G x N x K, sb float32 G x N, m_offsets
     int32[G+1] (device, multiples of 128, never read on the host). M_total defaults to a.shape[0]."""
-    return _run("int8_gemm_grouped", stream, a, sa, b, sb, m_offsets, _out_dtype(out_dtype)[0], c,
-                M_total)
+    if stream is not None:
+        return _on_stream(stream, int8_gemm_grouped, a, sa, b, sb, m_offsets, out_dtype, c, M_total)
+    return (_native or _binding()).int8_gemm_grouped(a, sa, b, sb, m_offsets, _out_code(out_dtype), c,
+                                                      M_total)

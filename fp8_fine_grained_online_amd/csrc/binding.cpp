@@ -5,8 +5,9 @@
 // allocations in Python around a ctypes call took 8.4 us for the router; these
 // take 4.9, of which the launch itself is 2.9.
 //
-// Every function returns its outputs, or the library's status as an int when
-// that is not FP8Q_OK; wrong types and shapes raise TypeError and ValueError.
+// Every function returns its outputs. Wrong types and shapes raise TypeError and
+// ValueError; for a status other than FP8Q_OK the function given to on_status is
+// called, which raises the binding's own error.
 // The work goes to the current stream of the tensors' device, whatever device
 // is current.
 #include <Python.h>
@@ -36,14 +37,17 @@ using at::ScalarType;
   throw python_error();
 }
 
+PyObject* status_handler = nullptr;  // (name, status) -> raises
+
 // One call's tensors: all on the device of the first.
 struct Call {
   int device = -1;
   int previous = -1;
+  const char* name;
   PyObject* const* args;
 
-  Call(PyObject* const* a, Py_ssize_t given, Py_ssize_t wanted) : args(a) {
-    if (given != wanted) refuse(PyExc_TypeError, "expected %d arguments", (int)wanted);
+  Call(const char* f, PyObject* const* a, Py_ssize_t given, Py_ssize_t wanted) : name(f), args(a) {
+    if (given != wanted) refuse(PyExc_TypeError, "%s: expected %d arguments", f, (int)wanted);
   }
   ~Call() {
     if (previous >= 0) (void)hipSetDevice(previous);
@@ -93,6 +97,11 @@ struct Call {
     if (v == -1 && PyErr_Occurred()) throw python_error();
     return v;
   }
+  int truth(int i) const {
+    const int v = PyObject_IsTrue(args[i]);
+    if (v < 0) throw python_error();
+    return v;
+  }
   double number(int i) const {
     const double v = PyFloat_AsDouble(args[i]);
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -118,10 +127,14 @@ PyObject* wrap(const Call& c, int i, const at::Tensor& t) {
   return c.args[i];
 }
 
-// The outputs (arguments `at`), or the status
+// The outputs (arguments `at`), or the status as an error
 template <size_t n>
 PyObject* result(int status, const Call& c, const int (&at)[n], const at::Tensor* const (&outs)[n]) {
-  if (status) return PyLong_FromLong(status);
+  if (status) {
+    PyObject* none = PyObject_CallFunction(status_handler, "si", c.name, status);
+    if (none) Py_DECREF(none), refuse(PyExc_RuntimeError, "%s: status %d", c.name, status);
+    throw python_error();
+  }
   if (n == 1) return wrap(c, at[0], *outs[0]);
   PyObject* tuple = PyTuple_New(n);
   if (!tuple) throw python_error();
@@ -147,7 +160,7 @@ int launch(F&& f) {
 // logits, bias, topk, score, renormalize, scale, n_groups, topk_groups, topk_ids, weights
 PyObject* moe_route(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c(args, n, 10);
+  Call c("fp8q_moe_route", args, n, 10);
   const at::Tensor& x = c.tensor(0, "logits", kFloats, 2);
   const int64_t T = x.size(0), G = x.size(1), topk = c.integer(2);
   at::Tensor bias;
@@ -155,7 +168,7 @@ PyObject* moe_route(PyObject*, PyObject* const* args, Py_ssize_t n) {
     bias = c.tensor(1, "bias", {ScalarType::Float}, 1);
     if (bias.size(0) != G) refuse(PyExc_ValueError, "bias must have G entries");
   }
-  const int64_t score = c.integer(3), renorm = c.integer(4), groups = c.integer(6), kept = c.integer(7);
+  const int64_t score = c.integer(3), renorm = c.truth(4), groups = c.integer(6), kept = c.integer(7);
   const float scale = (float)c.number(5);
   const at::Tensor ids = c.out(8, "topk_ids", {T, topk < 0 ? 0 : topk}, ScalarType::Int);
   const at::Tensor w = c.out(9, "weights", {T, topk < 0 ? 0 : topk}, ScalarType::Float);
@@ -171,13 +184,13 @@ PyObject* moe_route(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // logits, topk_ids, dweights, score, renormalize, scale, dlogits
 PyObject* moe_route_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c(args, n, 7);
+  Call c("fp8q_moe_route_bwd", args, n, 7);
   const at::Tensor& x = c.tensor(0, "logits", kFloats, 2);
   const at::Tensor& ids = c.tensor(1, "topk_ids", {ScalarType::Int}, 2);
   const at::Tensor& dw = c.tensor(2, "dweights", {ScalarType::Float}, 2);
   const int64_t T = x.size(0), G = x.size(1);
   if (ids.sizes() != dw.sizes() || ids.size(0) != T) refuse(PyExc_ValueError, "topk_ids and dweights must both be T x topk");
-  const int64_t score = c.integer(3), renorm = c.integer(4);
+  const int64_t score = c.integer(3), renorm = c.truth(4);
   const float scale = (float)c.number(5);
   const at::Tensor d = c.out(6, "dlogits", {T, G}, x.scalar_type());
   void* s = c.stream();
@@ -192,7 +205,7 @@ PyObject* moe_route_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // x, topk_ids, G, xp, m_offsets, row_of_slot, workspace
 PyObject* moe_permute(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c(args, n, 7);
+  Call c("fp8q_moe_permute", args, n, 7);
   const at::Tensor& x = c.tensor(0, "x", kFloats, 2);
   const at::Tensor& ids = c.tensor(1, "topk_ids", {ScalarType::Int}, 2);
   const int64_t T = x.size(0), K = x.size(1), topk = ids.size(1), G = c.integer(2);
@@ -223,7 +236,7 @@ at::Tensor slot_weights(Call& c, int i, const at::Tensor& rows) {
 // c, row_of_slot, weights, out_dtype, y
 PyObject* moe_combine(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c(args, n, 5);
+  Call c("fp8q_moe_combine", args, n, 5);
   const at::Tensor& x = c.tensor(0, "c", kFloats, 2);
   const at::Tensor& rows = c.tensor(1, "row_of_slot", {ScalarType::Int}, 2);
   const at::Tensor w = slot_weights(c, 2, rows);
@@ -241,7 +254,7 @@ PyObject* moe_combine(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // dy, c, row_of_slot, weights, m_offsets, dc, dw, with_dw
 PyObject* moe_combine_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c(args, n, 8);
+  Call c("fp8q_moe_combine_bwd", args, n, 8);
   const at::Tensor& dy = c.tensor(0, "dy", kFloats, 2);
   const at::Tensor& x = c.tensor(1, "c", kFloats, 2);
   const at::Tensor& rows = c.tensor(2, "row_of_slot", {ScalarType::Int}, 2);
@@ -252,7 +265,7 @@ PyObject* moe_combine_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (off.size(0) < 2) refuse(PyExc_ValueError, "m_offsets must have G+1 entries");
   const at::Tensor dc = c.out(5, "dc", {M, K}, x.scalar_type());
   at::Tensor dw;
-  if (c.integer(7) || !c.none(6)) dw = c.out(6, "dw", {T, topk}, ScalarType::Float);
+  if (c.truth(7) || !c.none(6)) dw = c.out(6, "dw", {T, topk}, ScalarType::Float);
   void* s = c.stream();
   const int status = launch([&] {
     return fp8q_moe_combine_bwd(ptr(dy), code(dy), ptr(x), code(x), (const int32_t*)ptr(rows), (const float*)ptr(w),
@@ -265,7 +278,7 @@ PyObject* moe_combine_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // x, q, s
 PyObject* quant_int8_rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c(args, n, 3);
+  Call c("fp8q_quant_int8_rows", args, n, 3);
   const bool experts = THPVariable_Check(args[0]) && THPVariable_Unpack(args[0]).dim() == 3;
   const at::Tensor& x = c.tensor(0, "x", {ScalarType::BFloat16}, experts ? 3 : 2);
   const int64_t K = x.size(-1), rows = experts ? x.size(0) * x.size(1) : x.size(0);
@@ -280,7 +293,7 @@ PyObject* quant_int8_rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // a, sa, b, sb, out_dtype, c
 PyObject* int8_gemm_dense(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c(args, n, 6);
+  Call c("int8_gemm_scaled", args, n, 6);
   const at::Tensor& a = c.tensor(0, "a", {ScalarType::Char}, 2);
   const at::Tensor& sa = c.tensor(1, "sa", {ScalarType::Float}, 1);
   const at::Tensor& b = c.tensor(2, "b", {ScalarType::Char}, 2);
@@ -301,7 +314,7 @@ PyObject* int8_gemm_dense(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // a, sa, b, sb, m_offsets, out_dtype, c, M_total
 PyObject* int8_gemm_experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c(args, n, 8);
+  Call c("int8_gemm_grouped", args, n, 8);
   const at::Tensor& a = c.tensor(0, "a", {ScalarType::Char}, 2);
   const at::Tensor& sa = c.tensor(1, "sa", {ScalarType::Float}, 1);
   const at::Tensor& b = c.tensor(2, "b", {ScalarType::Char}, 3);
@@ -323,6 +336,13 @@ PyObject* int8_gemm_experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+PyObject* on_status(PyObject*, PyObject* handler) {
+  Py_INCREF(handler);
+  Py_XDECREF(status_handler);
+  status_handler = handler;
+  Py_RETURN_NONE;
+}
+
 #define FP8Q_METHOD(name, f) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     FP8Q_METHOD("fp8q_moe_route", moe_route),
@@ -333,6 +353,7 @@ PyMethodDef methods[] = {
     FP8Q_METHOD("fp8q_quant_int8_rows", quant_int8_rows),
     FP8Q_METHOD("int8_gemm_scaled", int8_gemm_dense),
     FP8Q_METHOD("int8_gemm_grouped", int8_gemm_experts),
+    {"on_status", on_status, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -141,7 +141,7 @@ def test_binding_refuses_before_any_device_call():
 
 def test_binding_refuses_a_stream_of_another_device():
     import torch
-    from fp8_fine_grained_online_amd import _lib
+    import fp8_fine_grained_online_amd as F
 
     class Stream:
         cuda_stream, device = 64, torch.device("cuda", 1)
@@ -150,4 +150,4 @@ def test_binding_refuses_a_stream_of_another_device():
         is_cuda, device = True, torch.device("cuda", 0)
 
     with pytest.raises(ValueError, match="cuda:1"):
-        _lib._run("fp8q_quant_int8_rows", Stream(), Tensor(), None, None)
+        F.fp8q_quant_int8_rows(Tensor(), stream=Stream())
