@@ -323,11 +323,16 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
       for (int q = 0; q < kRows; ++q) off[q] = out ? kOutside : off[q];
     }
   };
-  auto copy_a = [&](int q, int g, uint8_t* __restrict__ to) {
-    load_lds(rsrc_a, to + (q * 256 + wave * 64) * 16, 16, off[q], (first + g) * kStepK);
+  // Byte of K where step g of this group starts. The second group may have one step
+  // more than K: its offset stays that of the last step, because a load's range check
+  // may subtract the scalar offset from the descriptor's size, and past a tile of one
+  // row the difference would wrap around and let the load through.
+  auto step_k = [&](int g) { return (S > 1 ? min(first + g, all_steps - 1) : first + g) * kStepK; };
+  auto copy_a = [&](int q, int k, uint8_t* __restrict__ to) {
+    load_lds(rsrc_a, to + (q * 256 + wave * 64) * 16, 16, off[q], k);
   };
-  auto copy_b = [&](int q, int g, uint8_t* __restrict__ to) {
-    load_lds(rsrc_b, to + (q * 256 + wave * 64) * 16, 16, off[q], (first + g) * kStepK);
+  auto copy_b = [&](int q, int k, uint8_t* __restrict__ to) {
+    load_lds(rsrc_b, to + (q * 256 + wave * 64) * 16, 16, off[q], k);
   };
 
   v4i acc[SUBM][SUBN];
@@ -349,7 +354,7 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
   // Half h of a step: its MFMAs, with the other half's operands read from
   // (sa, sb) and one operand's copies (`issue`) spread between them. Scheduling
   // barriers keep that order.
-  auto half = [&](int h, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ sb, int g,
+  auto half = [&](int h, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ sb, int k,
                   uint8_t* __restrict__ to, bool copy_is_a) {
 #pragma unroll
     for (int t = 0; t < kMfmas; ++t) {
@@ -357,8 +362,8 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
       if (t % kEvery == 0 && t / kEvery < SUBM + SUBN) read_operand(t / kEvery, 1 - h, sa, sb);
       if (t % kEvery == kEvery - 1) {
         const int q = t / kEvery;
-        if (copy_is_a) { if (q < Cfg::kLoadsA) copy_a(q, g, to); }
-        else { if (q < Cfg::kLoadsB) copy_b(q, g, to); }
+        if (copy_is_a) { if (q < Cfg::kLoadsA) copy_a(q, k, to); }
+        else { if (q < Cfg::kLoadsB) copy_b(q, k, to); }
       }
       acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(rb[h][j], ra[h][i], acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
@@ -375,10 +380,11 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
     for (int d = 0; d < D; ++d) {
       const int g = min(d, steps - 1);
       if (d > 0) enter_step(g);
+      const int k = step_k(g);
 #pragma unroll
-      for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, g, lds + d * Cfg::kSlabA);
+      for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, k, lds + d * Cfg::kSlabA);
 #pragma unroll
-      for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, g, lds_b + d * Cfg::kSlabB);
+      for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, k, lds_b + d * Cfg::kSlabB);
     }
     __builtin_amdgcn_s_waitcnt(wait_vm((D - 1) * (Cfg::kLoadsA + Cfg::kLoadsB)));
     __builtin_amdgcn_s_barrier();
@@ -393,11 +399,12 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
   for (int g = 0; g < steps; ++g) {
     const int gn = min(g + D, steps - 1);  // past the end the last step is copied again, unread
     enter_step(gn);
+    const int kn = step_k(gn);
     if (idle) {
 #pragma unroll
-      for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, gn, lds + a2);
+      for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, kn, lds + a2);
     } else {
-      half(0, lds + a0, lds_b + b0, gn, lds + a2, true);
+      half(0, lds + a0, lds_b + b0, kn, lds + a2, true);
     }
     // this wave has read all of step g, and its copies of step g + 1 have landed
     __builtin_amdgcn_s_waitcnt(kWaitLds);
@@ -406,9 +413,9 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
     __builtin_amdgcn_sched_barrier(0);
     if (idle) {
 #pragma unroll
-      for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, gn, lds_b + b0);
+      for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, kn, lds_b + b0);
     } else {
-      half(1, lds + a1, lds_b + b1, gn, lds_b + b0, false);
+      half(1, lds + a1, lds_b + b1, kn, lds_b + b0, false);
     }
     a2 = a0, a0 = a1, b0 = b1;
     a1 = a1 == D * Cfg::kSlabA ? 0 : a1 + Cfg::kSlabA;

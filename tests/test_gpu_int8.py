@@ -119,6 +119,19 @@ def test_dense(M, N, K, out):
     same(c, rounded(int8.gemm(a, sa, b, sb), out))
 
 
+@pytest.mark.parametrize("M,N,K", [(129, 1025, 2320), (1025, 129, 4112), (64, 4097, 6160), (65, 4033, 2576)])
+def test_last_rows_alone_in_their_tiles(M, N, K):
+    """One row of a, of b or of both in a 64 x 64 tile, and a K that two groups of waves do not halve: the second
+    group's last step lies past K, where its copies must read zeros."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    a, b = codes((M, K), 2760 + M), codes((N, K), 2761 + N)
+    sa, sb = scales(M, 2762), scales(N, 2763)
+    c = torch.full((M, N), float("nan"), device="cuda")
+    F.int8_gemm_scaled(dev(a), dev(sa), dev(b), dev(sb), "f32", c=c)
+    same(c, rounded(int8.gemm(a, sa, b, sb), "f32"))
+
+
 def test_largest_sums():
     """-128 by -128 over the largest K: 2^14 * 131056 < 2^31."""
     import torch
