@@ -165,19 +165,39 @@ __device__ __forceinline__ void fold_two(uint64_t& k0, uint64_t& k1, int lanes) 
   }
 }
 
-// Numerators of the softmax (all over `sum`), or sigmoids; masked logits have 0.
+// The wavefront's largest logit (0 when all are masked): the floats are ordered
+// as integers, so the maximum is exact.
 template <int E>
-__device__ __forceinline__ double softmax_terms(const float (&x)[E], double (&p)[E]) {
-  constexpr float kNegInf = -__builtin_huge_valf();
-  // order the floats as integers: the maximum over the wavefront is exact
+__device__ __forceinline__ double wave_top(const float (&x)[E]) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const uint32_t u = __float_as_uint(x[i]);
-    if (x[i] > kNegInf) m = max(m, (u >> 31) ? ~u : u | 0x80000000u);
+    if (x[i] > -__builtin_huge_valf()) m = max(m, (u >> 31) ? ~u : u | 0x80000000u);
   }
   m = wave_max_u32(m);
-  const double top = m ? (double)__uint_as_float((m >> 31) ? m & 0x7FFFFFFFu : ~m) : 0.0;
+  return m ? (double)__uint_as_float((m >> 31) ? m & 0x7FFFFFFFu : ~m) : 0.0;
+}
+
+// Renormalized weights are ratios p_j / sum_i p_i of the chosen. Probabilities below
+// this have lost bits to underflow, or are about to; their ratios are formed from
+// shifted_sigmoid instead.
+constexpr double kSmallScore = 0x1p-960;
+
+// The chosen logits' sigmoids, one per lane (masked: 0), without the factor e^top
+// that all share where the largest chosen logit, top, is negative.
+__device__ __forceinline__ double shifted_sigmoid(float x) {
+  const float one[1] = {x};
+  const double top = __builtin_fmin(wave_top<1>(one), 0.0);
+  const double v = (double)x;
+  return x > -__builtin_huge_valf() ? exp64(__builtin_fmin(v, 0.0) - top) * recip64(1.0 + exp64(-__builtin_fabs(v))) : 0.0;
+}
+
+// Numerators of the softmax (all over `sum`), or sigmoids; masked logits have 0.
+template <int E>
+__device__ __forceinline__ double softmax_terms(const float (&x)[E], double (&p)[E]) {
+  constexpr float kNegInf = -__builtin_huge_valf();
+  const double top = wave_top<E>(x);
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
@@ -308,8 +328,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
 //   softmax, renorm   dl_e = sum_{j: id_j = e} q_j (g_j - sum_i g_i q_i), since
 //                     the weights are the softmax over the chosen logits alone
 //   softmax           dl_e = p_e (sum_{j: id_j = e} g_j - sum_j g_j p_j)
-//   sigmoid           dl_e = sum_{j: id_j = e} dp_j p_j (1 - p_j), dp_j = g_j or
-//                     (g_j - sum_i g_i q_i) / sum_i p_i
+//   sigmoid, renorm   dl_e = sum_{j: id_j = e} q_j (g_j - sum_i g_i q_i) (1 - p_j)
+//   sigmoid           dl_e = sum_{j: id_j = e} g_j p_j (1 - p_j)
 // so only the plain softmax needs every probability of the row.
 //
 // The row is put together in LDS: zeros, then the choices' shares at their
@@ -375,11 +395,15 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteBwdArg
     const double pj = !live ? 0.0 : xj >= 0.0f ? big : small;
     const double rest = !live ? 0.0 : xj >= 0.0f ? small : big;
     if (a.renorm) {
-      const double sum = wave_sum_f64(pj);
-      const double gp = wave_sum_f64(g * pj);
-      v = (on && sum > 0.0) ? (g - gp / sum) / sum : 0.0;
+      // q and q (g - sum g q) are ordinary numbers; 1 / sum may not be one
+      const double part = __ballot(live && pj < kSmallScore) ? shifted_sigmoid(xj) : pj;
+      const double sum = wave_sum_f64(part);
+      const double q = sum > 0.0 ? part / sum : 0.0;
+      const double gq = wave_sum_f64(g * q);
+      v = q * (g - gq) * rest;
+    } else {
+      v *= pj * rest;
     }
-    v *= pj * rest;
   } else if (!dense) {
     const float one[1] = {xj};
     double q[1];

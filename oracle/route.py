@@ -28,6 +28,24 @@ def scores(logits, score):
         return p
 
 
+def ratios(x, score):
+    """p_j / sum_i p_i over the logits x, with the factor e^top that all p share taken out: it holds however small
+    the probabilities are. Masked logits count as 0; all masked: all 0."""
+    x = np.asarray(x, np.float64)
+    live = x > -np.inf
+    if not live.any():
+        return np.zeros_like(x)
+    v = np.where(live, x, 0.0)
+    top = v[live].max()
+    with np.errstate(under="ignore"):
+        if score == "sigmoid":
+            n = np.exp(np.minimum(v, 0.0) - min(top, 0.0)) / (1.0 + np.exp(-np.abs(v)))
+        else:
+            n = np.exp(v - top)
+    n = np.where(live, n, 0.0)
+    return n / n.sum()
+
+
 def route(logits, topk, bias=None, score="softmax", renormalize=True, scale=1.0, n_groups=1, topk_groups=1):
     x = np.asarray(logits, np.float64)
     T, G = x.shape
@@ -71,20 +89,22 @@ def weights_of(logits, ids, score, renormalize, scale):
 
 def route_bwd(logits, ids, dweights, score="softmax", renormalize=True, scale=1.0):
     """dlogits[t, e] = sum_j dweights[t, j] d weights[t, j] / d logits[t, e], by the product rule."""
+    logits = np.asarray(logits, np.float64)
     p = scores(logits, score)
     ids, g = np.asarray(ids), np.asarray(dweights, np.float64) * scale
     T, G = p.shape
     d = np.zeros((T, G))
     for t in range(T):
         on = [(int(e), g[t, j]) for j, e in enumerate(ids[t]) if 0 <= e < G]
+        if renormalize:  # dw_j / dl_e = q_j (delta_je - q_e), times 1 - p_e for sigmoids
+            q = ratios([logits[t, e] for e, _ in on], score)
+            mean = sum(gj * qj for (_, gj), qj in zip(on, q))
+            for (e, gj), qj in zip(on, q):
+                d[t, e] += qj * (gj - mean) * (1 - p[t, e] if score == "sigmoid" else 1.0)
+            continue
         dp = np.zeros(G)
-        total = sum(p[t, e] for e, _ in on)
-        mean = sum(gj * p[t, e] for e, gj in on)
         for e, gj in on:
-            if not renormalize:
-                dp[e] += gj
-            elif total > 0:
-                dp[e] += (gj - mean / total) / total
+            dp[e] += gj
         if score == "sigmoid":
             d[t] = dp * p[t] * (1 - p[t])
         else:

@@ -147,6 +147,30 @@ def test_gradient(T, G, topk, dtype, score, renormalize):
     assert np.all(np.abs(d.double().cpu().numpy() - want) <= half * (1 + 2.0 ** -8) * np.abs(want) + slack + TINY)
 
 
+# rows of two chosen logits whose probabilities underflow, or nearly, and of ordinary ones beside them
+FAR = [(-707, -706), (-720, -721), (-745.5, -744), (-800, -801), (-3e38, -2e38), (-720, 3), (0, -750), (40, -40),
+       (-709.5, -709.25), (-1, 0.5)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_renormalized_gradient_of_far_logits(score, dtype):
+    """The renormalized weights are ratios: their gradient is ordinary however small the probabilities are."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = np.array([(1.0, a, 0.25, b, -2.0) for a, b in FAR])
+    xd = torch.from_numpy(x).to(torch.float32 if dtype == "f32" else torch.bfloat16).cuda()
+    ids = np.tile(np.array([[3, 1]], np.int32), (len(FAR), 1))
+    g = np.array([(200.0, -200.0), (1.0, -2.0)] * (len(FAR) // 2), np.float32)
+    d = F.fp8q_moe_route_bwd(xd, torch.from_numpy(ids).cuda(), torch.from_numpy(g).cuda(), score=score, scale=2.5)
+    want = route.route_bwd(xd.double().cpu().numpy(), ids, g, score, True, 2.5)
+    assert (np.abs(want[:4]).max(axis=1) > 0.1).all()
+    # as in test_gradient
+    slack = 2.0 ** -44 * 2.5 * np.abs(g).sum(1, keepdims=True)
+    half = HALF["f32"] + (HALF["bf16"] if dtype == "bf16" else 0.0)
+    assert np.all(np.abs(d.double().cpu().numpy() - want) <= half * (1 + 2.0 ** -8) * np.abs(want) + slack + TINY)
+
+
 def test_no_tokens():
     import torch
     import fp8_fine_grained_online_amd as F

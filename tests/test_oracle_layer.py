@@ -35,6 +35,39 @@ def test_route_gradient_against_differences(score, renormalize):
             assert abs((value(up) - value(down)) / (2 * h) - d[t, e]) < 1e-8
 
 
+def decimal_weights(x, ids, score, renormalize):
+    """The weights by the formula, in 60 decimal digits."""
+    from decimal import Decimal as D, getcontext
+    getcontext().prec, getcontext().Emin = 60, -10 ** 6
+    e = [D(float(v)) for v in x]
+    if score == "sigmoid":
+        p = [1 / (1 + (-v).exp()) for v in e]
+    else:
+        top = max(e)
+        p = [(v - top).exp() for v in e]
+        p = [v / sum(p) for v in p]
+    w = [p[i] for i in ids]
+    return [v / sum(w) for v in w] if renormalize else w
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_gradient_of_far_logits(score):
+    """Against the formula in 60 digits: dw_j / dl_e = q_j (delta - q_e), times 1 - p_e for sigmoids."""
+    from decimal import Decimal as D
+    g = np.array([[200.0, -200.0]])
+    for pair in ((-707.0, -706.0), (-720.0, -721.0), (-745.5, -744.0), (-800.0, -801.0), (0.0, -750.0)):
+        x = np.array([[1.0, pair[0], pair[1]]])
+        ids = np.array([[2, 1]], np.int32)
+        q = decimal_weights(x[0], ids[0], score, True)
+        p = decimal_weights(x[0], ids[0], score, False)
+        mean = sum(D(float(a)) * b for a, b in zip(g[0], q))
+        want = [float(b * (D(float(a)) - mean) * ((1 - c) if score == "sigmoid" else 1)) for a, b, c in zip(g[0], q, p)]
+        d = route.route_bwd(x, ids, g, score, True, 1.0)[0]
+        assert d[0] == 0
+        # float64: a few tens of roundings against |g|
+        assert abs(d[2] - want[0]) < 1e-12 and abs(d[1] - want[1]) < 1e-12, (pair, d, want)
+
+
 def test_route_ties_groups_and_masks():
     x = np.zeros((4, 8))
     ids, w = route.route(x, 3)
