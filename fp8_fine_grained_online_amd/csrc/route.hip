@@ -89,8 +89,10 @@ __device__ __forceinline__ double recip64(double d) {
 }
 
 __device__ __forceinline__ double sigmoid64(float x) {
-  // e^709 + 1 still has a reciprocal; past it the formula's value is below 2^-1022
-  return x < -709.0f ? 0.0 : recip64(1.0 + exp64(-(double)x));
+  // e^709 + 1 still has a reciprocal; before that, 1 + e^x is 1 in float64
+  const bool far = x < -700.0f;
+  const double e = exp64(far ? (double)x : -(double)x);
+  return far ? e : recip64(1.0 + e);
 }
 
 // 64-bit key ordered like the double; 0 (below every finite value's key) marks

@@ -16,9 +16,11 @@ import numpy as np
 def scores(logits, score):
     x = np.asarray(logits, np.float64)
     live = x > -np.inf  # False for NaN
-    with np.errstate(over="ignore"):
+    with np.errstate(over="ignore", under="ignore"):
         if score == "sigmoid":
-            return np.where(live, 1.0 / (1.0 + np.exp(-np.where(live, x, 0.0))), 0.0)
+            v = np.where(live, x, 0.0)
+            # (1 + e^v is 1 in float64 below -700, and e^-v would overflow below -709)
+            return np.where(live, np.where(v < -700.0, np.exp(np.minimum(v, 0.0)), 1.0 / (1.0 + np.exp(-v))), 0.0)
         p = np.zeros_like(x)
         for t in range(x.shape[0]):
             at = live[t]

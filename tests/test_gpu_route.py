@@ -171,6 +171,15 @@ def test_renormalized_gradient_of_far_logits(score, dtype):
     assert np.all(np.abs(d.double().cpu().numpy() - want) <= half * (1 + 2.0 ** -8) * np.abs(want) + slack + TINY)
 
 
+def test_sigmoid_of_far_logits():
+    """Probabilities below 2^-1022 order the experts down to float64's smallest; then they tie."""
+    import torch
+    x = np.array([[-709.5, -709.25, -720, -715, -744, -746, -800, -3e38], [-701, -700, -699, -700.5, -1, 1, 30, -30]],
+                 np.float32)
+    ids, want = check(torch.from_numpy(x).cuda(), x.astype(np.float64), 8, score="sigmoid", renormalize=False)
+    assert want[0].tolist() == [1, 0, 3, 2, 4, 5, 6, 7]
+
+
 def test_no_tokens():
     import torch
     import fp8_fine_grained_online_amd as F

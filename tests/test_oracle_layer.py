@@ -68,6 +68,13 @@ def test_route_gradient_of_far_logits(score):
         assert abs(d[2] - want[0]) < 1e-12 and abs(d[1] - want[1]) < 1e-12, (pair, d, want)
 
 
+def test_sigmoid_of_far_logits():
+    x = np.array([-699.5, -700.5, -709.25, -709.75, -720.0, -744.0, -1.0, 30.0])
+    want = decimal_weights(x, range(8), "sigmoid", False)
+    # float64, and one unit of the smallest subnormal number
+    assert all(abs(a - float(b)) <= 1e-15 * float(b) + 5e-324 for a, b in zip(route.scores(x[None], "sigmoid")[0], want))
+
+
 def test_route_ties_groups_and_masks():
     x = np.zeros((4, 8))
     ids, w = route.route(x, 3)
