@@ -183,16 +183,18 @@ __device__ __forceinline__ double wave_top(const float (&x)[E]) {
 
 // Renormalized weights are ratios p_j / sum_i p_i of the chosen. Probabilities below
 // this have lost bits to underflow, or are about to; their ratios are formed from
-// shifted_sigmoid instead.
+// shifted_score instead.
 constexpr double kSmallScore = 0x1p-960;
 
-// The chosen logits' sigmoids, one per lane (masked: 0), without the factor e^top
-// that all share where the largest chosen logit, top, is negative.
-__device__ __forceinline__ double shifted_sigmoid(float x) {
+// The chosen logits' probabilities, one per lane (masked: 0), without a factor that
+// all share: e^top / sum of the softmax; e^top of sigmoids where the largest chosen
+// logit, top, is negative.
+__device__ __forceinline__ double shifted_score(float x, bool sigmoid) {
   const float one[1] = {x};
-  const double top = __builtin_fmin(wave_top<1>(one), 0.0);
-  const double v = (double)x;
-  return x > -__builtin_huge_valf() ? exp64(__builtin_fmin(v, 0.0) - top) * recip64(1.0 + exp64(-__builtin_fabs(v))) : 0.0;
+  const double top = wave_top<1>(one), v = (double)x;
+  double s = exp64(sigmoid ? __builtin_fmin(v, 0.0) - __builtin_fmin(top, 0.0) : v - top);
+  if (sigmoid) s *= recip64(1.0 + exp64(-__builtin_fabs(v)));
+  return x > -__builtin_huge_valf() ? s : 0.0;
 }
 
 // Numerators of the softmax (all over `sum`), or sigmoids; masked logits have 0.
@@ -316,6 +318,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   const int my_id = ids[lane];  // lane j: choice j
   double w = my_id >= 0 ? __longlong_as_double((long long)tab[my_id]) : 0.0;
   if (a.renorm) {
+    if (__ballot(my_id >= 0 && w < kSmallScore))  // rare: the logits are read again
+      w = shifted_score(my_id >= 0 ? as_logit(((const Tin*)a.logits)[(int64_t)t * a.G + my_id]) : -__builtin_huge_valf(),
+                        a.sigmoid);
     const double sum = wave_sum_f64(w);
     w = sum > 0.0 ? w / sum : 0.0;
   }
@@ -398,7 +403,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_bwd_kernel(RouteBwdArg
     const double rest = !live ? 0.0 : xj >= 0.0f ? small : big;
     if (a.renorm) {
       // q and q (g - sum g q) are ordinary numbers; 1 / sum may not be one
-      const double part = __ballot(live && pj < kSmallScore) ? shifted_sigmoid(xj) : pj;
+      const double part = __ballot(live && pj < kSmallScore) ? shifted_score(xj, true) : pj;
       const double sum = wave_sum_f64(part);
       const double q = sum > 0.0 ? part / sum : 0.0;
       const double gq = wave_sum_f64(g * q);

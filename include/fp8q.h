@@ -475,10 +475,12 @@ typedef enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 } fp8q_score;
  *     topk_groups best groups may be chosen;
  *   topk_ids[t, :] = the topk experts with the largest z, largest first;
  *   weights[t, j] = scale * p[t, id_j], divided by sum_j p[t, id_j] when
- *     renormalize is 1 (0 when that sum is 0).
+ *     renormalize is 1. These ratios hold however small the probabilities
+ *     are: all chosen may lie far below the row's largest logit.
  * Ties go to the lowest index, for groups as for experts. All of it is
  * computed in float64, so that the choice between nearly equal experts does
- * not depend on rounding; weights are rounded once to binary32.
+ * not depend on rounding (experts whose p is below float64's smallest number
+ * tie); weights are rounded once to binary32.
  *
  * An expert whose logit is -infinity or NaN (or whose bias is) has p = 0 and
  * is never chosen. When fewer than topk experts can be chosen, the remaining

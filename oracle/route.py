@@ -4,7 +4,7 @@
   or NaN, or a bias that makes z so) cannot be chosen;
   groups: the score of a group is the sum of its (up to) two largest z; the best
   topk_groups stay;  ids = the topk largest z, ties to the lowest index;
-  w_j = scale p_j, or scale p_j / sum_i p_i (0 when that sum is 0);
+  w_j = scale p_j, or scale p_j / sum_i p_i, a ratio that holds where the p underflow;
   choices that cannot be filled are -1 with weight 0.
 
 TEST INFRASTRUCTURE ONLY (see the package docstring).
@@ -69,10 +69,7 @@ def route(logits, topk, bias=None, score="softmax", renormalize=True, scale=1.0,
             can &= np.array([e // gs in kept for e in range(G)])
         order = sorted((e for e in range(G) if can[e]), key=lambda e: (-z[t, e], e))[:topk]
         ids[t, :len(order)] = order
-        pj = p[t, order]
-        if renormalize:
-            pj = pj / pj.sum() if pj.sum() > 0 else np.zeros_like(pj)
-        w[t, :len(order)] = scale * pj
+        w[t, :len(order)] = scale * (ratios(x[t, order], score) if renormalize else p[t, order])
     return ids, w
 
 
@@ -82,11 +79,10 @@ def weights_of(logits, ids, score, renormalize, scale):
     ids = np.asarray(ids)
     T, G = p.shape
     on = (ids >= 0) & (ids < G)
-    pj = np.where(on, np.take_along_axis(p, np.where(on, ids, 0), 1), 0.0)
     if renormalize:
-        s = pj.sum(1, keepdims=True)
-        pj = np.where(s > 0, pj / np.where(s > 0, s, 1.0), 0.0)
-    return scale * pj
+        chosen = np.take_along_axis(np.asarray(logits, np.float64), np.where(on, ids, 0), 1)
+        return scale * np.stack([ratios(v, score) for v in np.where(on, chosen, -np.inf)])
+    return scale * np.where(on, np.take_along_axis(p, np.where(on, ids, 0), 1), 0.0)
 
 
 def route_bwd(logits, ids, dweights, score="softmax", renormalize=True, scale=1.0):

@@ -180,6 +180,25 @@ def test_sigmoid_of_far_logits():
     assert want[0].tolist() == [1, 0, 3, 2, 4, 5, 6, 7]
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_renormalized_weights_that_underflow(score):
+    """A bias steers the choice to experts whose probabilities are 0 in float64: their weights are still the ratios."""
+    import torch
+    x = np.array([(1.0, a, 0.25, b, -2.0, a - 0.5) for a, b in FAR]).astype(np.float32)
+    bias = np.array([-9.0, 0, -9.0, 0, -9.0, 0])
+    xd = torch.from_numpy(x).cuda()
+    x64 = x.astype(np.float64)
+    ids, want = check(xd, x64, 2, bias, score=score)
+    assert set(want[3]) <= {1, 3, 5}
+    check(xd, x64, 3, bias, score=score, scale=2.5)
+    check(xd, x64, 6, bias, score=score)          # beside experts with ordinary probabilities
+    check(xd, x64, 2, score=score, bias=np.array([-9.0, -9, 0, 0, -9, 0]), n_groups=3, topk_groups=2)
+    x = np.array([[-709.5, -709.25, -720, -715, -744, -746, -800, -3e38], [-701, -700, -699, -700.5, -1, 1, 30, -30]],
+                 np.float32)
+    for topk in (2, 8):
+        check(torch.from_numpy(x).cuda(), x.astype(np.float64), topk, score=score)
+
+
 def test_no_tokens():
     import torch
     import fp8_fine_grained_online_amd as F

@@ -68,6 +68,19 @@ def test_route_gradient_of_far_logits(score):
         assert abs(d[2] - want[0]) < 1e-12 and abs(d[1] - want[1]) < 1e-12, (pair, d, want)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_renormalized_weights_that_underflow(score):
+    """A bias steers the choice to experts whose probabilities are 0 in float64."""
+    bias = np.array([-9.0, 0, 0])
+    for pair in ((-707.0, -706.0), (-720.0, -721.0), (-745.5, -744.0), (-800.0, -801.0), (0.0, -750.0), (-3.0, 0.5)):
+        x = np.array([[1.0, *pair]])
+        ids, w = route.route(x, 2, bias, score=score)
+        assert sorted(ids[0]) == [1, 2]
+        want = [float(v) for v in decimal_weights(x[0], ids[0], score, True)]
+        assert np.allclose(w[0], want, rtol=1e-13, atol=1e-300)
+        assert np.allclose(route.weights_of(x, ids, score, True, 1.0)[0], want, rtol=1e-13, atol=1e-300)
+
+
 def test_sigmoid_of_far_logits():
     x = np.array([-699.5, -700.5, -709.25, -709.75, -720.0, -744.0, -1.0, 30.0])
     want = decimal_weights(x, range(8), "sigmoid", False)
