@@ -354,7 +354,15 @@ struct RouteBwdArgs {
 
 __device__ __forceinline__ void store_logit(float* p, double v) { *p = (float)v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, double v) {
-  const __bf16 b = (__bf16)(float)v;
+  // By way of binary32, whose own rounding shows only if it lands in the middle
+  // between two bfloat16 numbers (one value in 2^16): then v tells the side.
+  uint32_t u = __float_as_uint((float)v);
+  if ((u & 0xFFFF) == 0x8000) {
+    const double mid = __builtin_fabs((double)__uint_as_float(u));
+    if (mid < __builtin_fabs(v)) u += 1;
+    else if (mid > __builtin_fabs(v)) u -= 1;
+  }
+  const __bf16 b = (__bf16)__uint_as_float(u);
   *p = __builtin_bit_cast(uint16_t, b);
 }
 

@@ -171,6 +171,38 @@ def test_renormalized_gradient_of_far_logits(score, dtype):
     assert np.all(np.abs(d.double().cpu().numpy() - want) <= half * (1 + 2.0 ** -8) * np.abs(want) + slack + TINY)
 
 
+@pytest.mark.parametrize("score,renormalize", [("softmax", False), ("sigmoid", True)])
+def test_bfloat16_gradient_is_rounded_once(score, renormalize):
+    """Gradients go from float64 to bfloat16 in one rounding: two (by way of binary32) would move about one value in
+    2^17 across the middle between two bfloat16 numbers."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    T, G, topk = 8192, 256, 8
+    gen = torch.Generator("cuda").manual_seed(7)
+    x = (1.5 * torch.randn(T, G, device="cuda", generator=gen)).to(torch.bfloat16)
+    ids = torch.rand(T, G, device="cuda", generator=gen).topk(topk, 1).indices.int().contiguous()
+    g = torch.randn(T, topk, device="cuda", generator=gen)
+    if renormalize:  # few gradients of a row are not 0: more rows
+        ids, topk = torch.arange(G, device="cuda").int().repeat(T, 1)[:, :64].contiguous(), 64
+        g = torch.randn(T, topk, device="cuda", generator=gen)
+    d = F.fp8q_moe_route_bwd(x, ids, g, score=score, renormalize=renormalize).double().cpu().numpy()
+    x64, at, g64 = x.double().cpu().numpy(), ids.cpu().numpy(), g.double().cpu().numpy()
+    p = route.scores(x64, score)
+    pj = np.take_along_axis(p, at, 1)
+    want = np.zeros_like(p)
+    if renormalize:
+        q = pj / pj.sum(1, keepdims=True)
+        np.put_along_axis(want, at, q * (1 - pj) * (g64 - (g64 * q).sum(1, keepdims=True)), 1)
+    else:
+        dp = np.zeros_like(p)
+        np.put_along_axis(dp, at, g64, 1)
+        want = p * (dp - (dp * p).sum(1, keepdims=True))
+    # half a step of a value 1.b 2^e is 2^(e-8); beyond it only float64's own errors
+    step = np.exp2(np.floor(np.log2(np.maximum(np.abs(want), 2.0 ** -120))) - 7)
+    slack = 2.0 ** -44 * np.abs(g64).sum(1, keepdims=True)
+    assert np.all(np.abs(d - want) <= step / 2 + slack)
+
+
 def test_sigmoid_of_far_logits():
     """Probabilities below 2^-1022 order the experts down to float64's smallest; then they tie."""
     import torch
