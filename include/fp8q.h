@@ -482,8 +482,9 @@ typedef enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 } fp8q_score;
  * not depend on rounding (experts whose p is below float64's smallest number
  * tie); weights are rounded once to binary32.
  *
- * An expert whose logit is -infinity or NaN (or whose bias is) has p = 0 and
- * is never chosen. When fewer than topk experts can be chosen, the remaining
+ * An expert whose logit is -infinity or NaN has p = 0 and is never chosen. One
+ * whose bias is -infinity or NaN is never chosen either, but its logit counts in
+ * the softmax like any other: the bias steers the choice alone. When fewer than topk experts can be chosen, the remaining
  * choices are -1 with weight 0 (fp8q_moe_dispatch_1x128, fp8q_moe_permute
  * drop those, and the other calls skip them). Logits of +infinity are outside
  * the contract (ids stay in range).

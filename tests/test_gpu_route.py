@@ -85,6 +85,28 @@ def test_masked_logits_and_empty_rows():
         assert np.isfinite(d).all() and not d[3].any() and not d[5].any()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_masked_bias_bars_the_choice_alone(score, renormalize):
+    """An expert with a bias of -infinity or NaN is never chosen, and its logit still counts in the softmax."""
+    xd, x = logits_of(50, 40, "f32", 2406)
+    bias = 0.1 * S.rng_for(2407, 0).standard_normal(40)
+    bias[[3, 17, 18, 19]] = -np.inf
+    bias[[5, 30]] = np.nan
+    for kw in ({}, {"n_groups": 8, "topk_groups": 3}, {"n_groups": 20, "topk_groups": 4}):
+        _, want = check(xd, x, 5, bias, score=score, renormalize=renormalize, **kw)
+        assert not np.isin(want, [3, 17, 18, 19, 5, 30]).any()
+    p = route.scores(x, score)
+    if score == "softmax" and not renormalize:
+        import fp8_fine_grained_online_amd as F
+        import torch
+        b = torch.from_numpy(bias).float().cuda()
+        ids, w = F.fp8q_moe_route(xd, 34, bias=b, score=score, renormalize=False)
+        free = np.setdiff1d(np.arange(40), [3, 17, 18, 19, 5, 30])
+        # 34 weights rounded to binary32, and their sum in float64
+        assert np.allclose(w.double().cpu().numpy().sum(1), p[:, free].sum(1), rtol=2.0 ** -24 + 2.0 ** -44, atol=0)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_logits_at_any_element(dtype):
     """Contiguous logits that start one element past an aligned address."""
