@@ -62,6 +62,22 @@ def test_groups(G, groups, kept, topk, ties):
     check(xd, x, topk, score="softmax", renormalize=False, n_groups=groups, topk_groups=kept)
 
 
+@pytest.mark.parametrize("G,groups,kept,topk", [(88, 4, 2, 8), (96, 8, 3, 9), (160, 32, 7, 10), (360, 8, 4, 8),
+                                                (520, 4, 2, 10), (1000, 8, 5, 64), (1024, 64, 9, 8), (1023, 31, 8, 12),
+                                                (66, 33, 12, 10), (300, 2, 1, 3)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_that_end_inside_lanes(G, groups, kept, topk, score):
+    """Several experts per lane and groups that are no power-of-two run of whole lanes (and one that is, of 16 per
+    lane): with ties, masked logits and a bias."""
+    for seed, ties, masked in ((2410, False, 0.0), (2411, True, 0.0), (2412, False, 0.6), (2413, True, 0.97)):
+        xd, x = logits_of(41, G, "f32" if seed % 2 else "bf16", seed + G, ties=ties, masked=masked)
+        bias = S.rng_for(seed, G).standard_normal(G)
+        if ties:
+            bias = np.round(bias)
+        check(xd, x, topk, score=score, n_groups=groups, topk_groups=kept)
+        check(xd, x, topk, 0.2 * bias, score=score, renormalize=False, scale=2.5, n_groups=groups, topk_groups=kept)
+
+
 def test_ties_go_to_the_lowest_index():
     xd, x = logits_of(200, 100, "bf16", 2400, ties=True)
     check(xd, x, 9, score="softmax")
