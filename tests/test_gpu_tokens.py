@@ -155,6 +155,47 @@ def test_rows_beyond_the_cache():
     assert torch.all((dw.double() - torch.where(on, norm, 0.0)).abs() <= (K / 64 + 24) * EPS32 * norm)
 
 
+def padding_of(rows, off, M):
+    """(rows below off[G] that nothing maps, rows from off[G] on), as masks over M rows."""
+    import torch
+    mapped = torch.zeros(M, dtype=torch.bool, device="cuda")
+    mapped[rows[rows >= 0].long()] = True
+    behind = torch.arange(M, device="cuda") >= off[-1]
+    return ~mapped & ~behind, behind
+
+
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+@pytest.mark.parametrize("T,topk,G,K", [(2600, 8, 16, 7168), (5600, 3, 300, 64), (16385, 1, 7, 200), (2048, 8, 40, 4096),
+                                        (300, 8, 256, 4096), (9000, 2, 1024, 24)])
+def test_padding_rows_are_zero_and_rows_behind_stay(T, topk, G, K, name):
+    """Sixteen and four zeroing workgroups per expert (up to 16384 slots, and more), rows that fit the cache and that
+    do not (stored another way), blocks without a row: padding is zero in every element, rows behind are not written."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    ids = routing(T, topk, G, 2660 + T, drop=5)
+    ids[ids == G - 2] = G - 1  # an expert without rows
+    ids = torch.from_numpy(ids).cuda()
+    x, dy = randn((T, K), name, 2661), randn((T, K), name, 2662)
+    cap = F.lib().fp8q_moe_dispatch_max_rows(T, topk, G)
+    xp = torch.full((cap, K), float("nan"), dtype=dtype(name), device="cuda")
+    _, off, rows = F.fp8q_moe_permute(x, ids, G, xp=xp)
+    padding, behind = padding_of(rows, off, cap)
+    assert padding.any() and behind.any()
+    assert torch.count_nonzero(xp[padding]) == 0 and torch.isnan(xp[behind]).all()
+    w = torch.rand(T, topk, device="cuda", generator=torch.Generator("cuda").manual_seed(8))
+    c = torch.where(padding.unsqueeze(1), float("nan"), xp.float()).to(dtype(name))  # padding is never read
+    want = (w.unsqueeze(2) * dy.float().unsqueeze(1)).to(dtype(name)) if T * topk * K < 1 << 28 else None
+    for with_dw in (True, False):
+        dc = torch.full((cap, K), float("nan"), dtype=dtype(name), device="cuda")
+        _, dw = F.fp8q_moe_combine_bwd(dy, c, rows, w, off, dc=dc, with_dw=with_dw)
+        assert torch.count_nonzero(dc[padding]) == 0 and torch.isnan(dc[behind]).all()
+        on = rows >= 0
+        if want is not None:
+            assert torch.equal(dc[rows[on].long()], want[on])
+        if with_dw:
+            assert torch.isfinite(dw).all() and torch.count_nonzero(dw[~on]) == 0
+
+
 def test_combine_skips_rows_outside():
     import torch
     import fp8_fine_grained_online_amd as F
