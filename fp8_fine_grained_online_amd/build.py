@@ -1,5 +1,6 @@
-"""Build libfp8q.so (HIP, gfx950) in-tree with hipcc, and the Python binding beside
-it (host code, against the installed torch) with g++.
+"""Build libfp8q.so (HIP, gfx950) in-tree with hipcc, and beside it the native part
+of the Python binding (host code, against the installed torch). Where torch or
+Python's headers are not installed the library is built alone.
 
 Usage: python -m fp8_fine_grained_online_amd.build [--verbose]
 """
@@ -60,7 +61,11 @@ def build(verbose: bool = False) -> str:
     tmp = LIB_PATH + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
-    build_binding(verbose)
+    missing = binding_needs()
+    if missing:
+        print(f"{missing}: the native part of the binding is not built", file=sys.stderr)
+    else:
+        build_binding(verbose)
     build_probes(verbose)
     return LIB_PATH
 
@@ -68,11 +73,23 @@ def build(verbose: bool = False) -> str:
 BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 
+def binding_needs() -> str:
+    """What the binding's native part needs and does not find ('' for nothing)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return "torch is not installed"
+    for folder, header in ((os.path.join(spec.submodule_search_locations[0], "include"), "ATen/core/Tensor.h"),
+                           (sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(os.path.join(folder, header)):
+            return f"{os.path.join(folder, header)} is missing"
+    return ""
+
+
 def build_binding(verbose: bool = False) -> str:
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     libs = os.path.join(torch_dir, "lib")
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+    _run([HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM", "-I", sysconfig.get_paths()["include"],
           "-I", os.path.join(torch_dir, "include"), "-I", os.path.join(rocm, "include"),
           os.path.join(CSRC, "binding.cpp"), "-o", BINDING_PATH + ".tmp",
