@@ -170,8 +170,10 @@ PyObject* moe_route(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   const int64_t score = c.integer(3), renorm = c.truth(4), groups = c.integer(6), kept = c.integer(7);
   const float scale = (float)c.number(5);
-  const at::Tensor ids = c.out(8, "topk_ids", {T, topk < 0 ? 0 : topk}, ScalarType::Int);
-  const at::Tensor w = c.out(9, "weights", {T, topk < 0 ? 0 : topk}, ScalarType::Float);
+  // (more choices than experts are refused by the library: nothing is allocated for them)
+  auto cols = [&](int i) { return topk < 0 || (topk > G && c.none(i)) ? 0 : topk; };
+  const at::Tensor ids = c.out(8, "topk_ids", {T, cols(8)}, ScalarType::Int);
+  const at::Tensor w = c.out(9, "weights", {T, cols(9)}, ScalarType::Float);
   void* s = c.stream();
   const int status = launch([&] {
     return fp8q_moe_route(ptr(x), code(x), (const float*)ptr(bias), T, G, topk, groups, kept, (int)score, (int)renorm,

@@ -295,3 +295,17 @@ def test_refusals():
         F.fp8q_moe_route(x.t(), 2)
     with pytest.raises(ValueError):
         F.fp8q_moe_route(x, 2, bias=torch.zeros(15, device="cuda"))
+
+
+def test_too_many_choices_allocate_nothing():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = torch.zeros(4, 16, device="cuda")
+    for topk in (17, 10 ** 12, 2 ** 62):
+        before = torch.cuda.memory_reserved()
+        with pytest.raises(F.Fp8qError):
+            F.fp8q_moe_route(x, topk)
+        assert torch.cuda.memory_reserved() == before
+    with pytest.raises(F.Fp8qError):
+        F.fp8q_moe_route(x, 17, topk_ids=torch.zeros(4, 17, dtype=torch.int32, device="cuda"),
+                         weights=torch.zeros(4, 17, device="cuda"))
