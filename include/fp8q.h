@@ -592,7 +592,9 @@ FP8Q_API int fp8q_moe_combine_bwd(const void* dy, int dy_dtype, const void* c, i
  * channels of an N x K weight; G experts' weights are G * N rows).
  *   amax = max |x[m, :]|, s[m] = fl32(amax / 127),
  *   q[m, k] = clamp(RNE(fl32(x[m, k] / s[m])), -127, 127);
- * a zero row has scale 0 and zero codes.
+ * a zero row has scale 0 and zero codes. A row that holds an infinity or NaN gets
+ * that as its scale and unspecified codes, so that what a product makes of it is
+ * not finite either; other rows do not notice.
  *   x_bf16 : in,  M x K bfloat16, 16-byte aligned
  *   q      : out, M x K int8, 16-byte aligned;   s : out, M float32
  * Requires K % 16 == 0. M == 0 is a no-op; K == 0 writes zero scales.

@@ -88,6 +88,28 @@ def test_quant_codes_beyond_the_cache():
         assert torch.equal(q[m:m + 8000], torch.round(xf / want_s.unsqueeze(1)).to(torch.int8))
 
 
+@pytest.mark.parametrize("K", [16, 1040, 4112, 40000])
+def test_quant_rows_that_are_not_finite(K):
+    """An infinite or NaN row has that as its scale, a product's row from it is not finite, and other rows are exact."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    M = 21
+    x = torch.from_numpy(S.rng_for(2715, K).standard_normal((M, K), dtype=np.float32)).to(torch.bfloat16)
+    bad = {2: float("inf"), 5: -float("inf"), 6: float("nan"), 20: float("inf")}
+    for row, v in bad.items():
+        x[row, (row * 7) % K] = v
+    x[20, 3] = float("nan")
+    q, s = F.fp8q_quant_int8_rows(x.cuda())
+    good = [m for m in range(M) if m not in bad]
+    want_q, want_s = int8.quant_rows(x[good].float().numpy())
+    assert np.array_equal(s.cpu().numpy()[good], want_s) and np.array_equal(q.cpu().numpy()[good], want_q)
+    assert s[[2, 5]].eq(float("inf")).all() and s[[6, 20]].isnan().all()
+    b, sb = codes((70, K), 2716), scales(70, 2717)
+    c = F.int8_gemm_scaled(q, s, dev(b), dev(sb), "f32").cpu()
+    assert not torch.isfinite(c[list(bad)]).any()
+    same(c[good], rounded(int8.gemm(want_q, want_s, b, sb), "f32"))
+
+
 def test_quant_weights_of_experts():
     import torch
     import fp8_fine_grained_online_amd as F
