@@ -497,11 +497,21 @@ __global__ __launch_bounds__(256 * S, S) void gemm_i8_kernel(I8Args p) {
 // fragments straight from global memory to registers, kAhead pieces ahead; the
 // int32 partial blocks are added through LDS. For products too small to give
 // every CU a large tile, and for few rows, where B is read once.
+//
+// kAhead keeps 6 to 8 loads per lane in flight, whatever MB and NB. us on MI355X
+// for 1, 2, 4, 6 pieces ahead, operands beyond the Infinity Cache:
+//   16 x 16  1 x 4096 x 8192    11.09   9.41   8.41   8.67
+//            1 x 4096 x 1024     3.27   3.21   3.24   3.31
+//   16 x 32  1 x 7168 x 7168    14.17  11.43  13.25  13.21
+//            8 x 16384 x 2048    9.74   9.07   9.20   9.24
+//   32 x 16  32 x 4096 x 8192   16.22  14.95  15.81  15.85
+//   32 x 32  256 x 1024 x 2032   5.85   5.70   5.95   5.96
 // ---------------------------------------------------------------------------
 constexpr int kPiece = 64;
 
-template <int MB, int NB, int W, int kAhead, bool kBf16>
+template <int MB, int NB, int W, bool kBf16>
 __global__ __launch_bounds__(64 * W) void gemm_i8_small_kernel(I8Args p) {
+  constexpr int kAhead = 8 / (MB + NB);
   __shared__ __attribute__((aligned(16))) v4i part[W][MB * NB][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -625,13 +635,13 @@ static hipError_t launch_tiles(const I8Args& a, bool bf16, int64_t m_tiles, hipS
   return hipGetLastError();
 }
 
-template <int MB, int NB, int W, int kAhead>
+template <int MB, int NB, int W>
 static hipError_t launch_small(const I8Args& a, bool bf16, hipStream_t stream) {
   const int64_t wgs = (int64_t)((a.M + 16 * MB - 1) / (16 * MB)) * ((a.N + 16 * NB - 1) / (16 * NB));
   if (bf16)
-    hipLaunchKernelGGL((gemm_i8_small_kernel<MB, NB, W, kAhead, true>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_small_kernel<MB, NB, W, true>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
   else
-    hipLaunchKernelGGL((gemm_i8_small_kernel<MB, NB, W, kAhead, false>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_small_kernel<MB, NB, W, false>), dim3((unsigned)wgs), dim3(64 * W), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -644,18 +654,18 @@ hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, c
   // that, CUs idle while others load twice the operand bytes (a CU loads about
   // 90 GB/s whatever its tile); above it, some CUs work twice. Measured on
   // MI355X, us for the chosen tile against its neighbours in size:
-  //   64 x 512 x 512         16x16 2.70   32x16 2.98   32x32 3.24
-  //   256 x 512 x 2048       32x16 5.10   32x32 5.92   64x64 6.33
-  //   256 x 1024 x 512       32x32 3.40   32x16 3.90   64x64 4.64
-  //   333 x 2050 x 2064      64x64 8.3    64x128 10.6  32x32 15.4
-  //   1024 x 2048 x 2048     64x128 9.0   64x64 12.6   128x128 11.3
-  //   1024 x 4096 x 4096     128x128 20.1 64x128 26.7  256x256 45.7
-  // Long K is better shared through LDS: 32 x 7168 x 7168 takes 12.4 us in
-  // 64x64 tiles and 15.4 in 32x32; at K = 2048 6.4 and 6.9.
-  if (M <= 16 && wgs(16, 16) > kCus) return launch_small<1, 2, 8, 7>(p, bf16, stream);
-  if (wgs(16, 16) <= kCus) return launch_small<1, 1, 8, 4>(p, bf16, stream);
-  if (wgs(32, 16) <= kCus) return launch_small<2, 1, 8, 6>(p, bf16, stream);
-  if (wgs(32, 32) <= kCus && K < 2048) return launch_small<2, 2, 8, 4>(p, bf16, stream);
+  //   64 x 512 x 512         16x16 2.64   32x16 2.81   32x32 3.15
+  //   256 x 512 x 2048       32x16 4.87   32x32 5.79   64x64 6.66
+  //   256 x 1024 x 512       32x32 3.27   32x16 3.64   64x64 4.03
+  //   333 x 2050 x 2064      64x64 8.6    64x128 11.0  32x32 14.4
+  //   1024 x 2048 x 2048     64x128 9.0   64x64 12.7   128x128 11.3
+  //   1024 x 4096 x 4096     128x128 21.2 64x128 24.1  256x256 47.8
+  // Long K is better shared through LDS: 32 x 7168 x 7168 takes 12.5 us in
+  // 64x64 tiles and 15.5 in 32x32; at K = 2048 they are equal, 6.5 and 6.3.
+  if (M <= 16 && wgs(16, 16) > kCus) return launch_small<1, 2, 8>(p, bf16, stream);
+  if (wgs(16, 16) <= kCus) return launch_small<1, 1, 8>(p, bf16, stream);
+  if (wgs(32, 16) <= kCus) return launch_small<2, 1, 8>(p, bf16, stream);
+  if (wgs(32, 32) <= kCus && K < 2048) return launch_small<2, 2, 8>(p, bf16, stream);
   if (wgs(64, 64) <= kCus) {
     // Two groups of waves that share K start with half the steps but have their
     // sums to add. 200 x 4096, us at K = 256, 992, 2048, 4096, 8192: one group, 5
