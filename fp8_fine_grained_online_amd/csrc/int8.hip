@@ -667,11 +667,22 @@ hipError_t launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, c
   if (wgs(32, 16) <= kCus) return launch_small<2, 1, 8>(p, bf16, stream);
   if (wgs(32, 32) <= kCus && K < 2048) return launch_small<2, 2, 8>(p, bf16, stream);
   if (wgs(64, 64) <= kCus) {
-    // Two groups of waves that share K start with half the steps but have their
-    // sums to add. 200 x 4096, us at K = 256, 992, 2048, 4096, 8192: one group, 5
-    // buffers 3.7, 5.4, 7.1, 10.7, 17.7; two groups, 3 buffers 4.2, 6.0, 7.1, 9.7,
-    // 17.2 (4 buffers: the same). 17 steps do not halve: 333 x 2050 x 2064 7.8, 8.1.
-    if (K <= 17 * kStepK) return launch_tiles<64, 64, 5, 1, false>(p, bf16, (M + 63) / 64, stream);
+    // Two groups of waves that share K have half the steps each but their sums to
+    // add, and twice the loads in flight. That pays from K = 2048 on where rows
+    // start at whole 128-byte lines; else every copy touches two lines, the cache is
+    // what is waited for, and it pays from about 8192 on. us, one group with 5
+    // buffers / two groups with 3 (4 buffers: the same), MI355X:
+    //     K    200 x 4096     333 x 2050     500 x 1000     1024 x 1024
+    //   1536   6.15 /  6.06   6.37 /  6.42   5.98 /  5.76   6.62 /  6.71
+    //   1792   6.65 /  6.53   6.91 /  6.91   6.39 /  6.03   7.03 /  7.11
+    //   2048   7.31 /  6.95   7.45 /  7.29   6.88 /  6.47   7.50 /  7.38
+    //   8192  17.95 / 14.83  17.54 / 15.29  17.94 / 14.64  17.54 / 15.48
+    //   2064   8.33 /  8.43   8.55 /  8.79   7.23 /  6.87   8.81 /  9.10
+    //   4112  12.86 / 12.85  13.06 / 13.21  12.36 / 12.32  13.13 / 13.55
+    //   6208  14.88 / 15.04  14.90 / 15.57  14.94 / 14.60  14.96 / 15.85
+    //   8208  21.76 / 21.03  21.92 / 21.78  21.04 / 20.57  22.01 / 22.24
+    //  16400  38.31 / 36.41  39.42 / 37.43  37.36 / 34.88  39.33 / 38.63
+    if (K < (K % kStepK == 0 ? 2048 : 8192)) return launch_tiles<64, 64, 5, 1, false>(p, bf16, (M + 63) / 64, stream);
     return launch_tiles<64, 64, 3, 2, false>(p, bf16, (M + 63) / 64, stream);
   }
   if (wgs(64, 128) <= kCus) return launch_tiles<64, 128, 3, 1, false>(p, bf16, (M + 63) / 64, stream);

@@ -141,7 +141,8 @@ def test_dense(M, N, K, out):
     same(c, rounded(int8.gemm(a, sa, b, sb), out))
 
 
-@pytest.mark.parametrize("M,N,K", [(129, 1025, 2320), (1025, 129, 4112), (64, 4097, 6160), (65, 4033, 2576)])
+@pytest.mark.parametrize("M,N,K", [(129, 1025, 2320), (1025, 129, 4112), (64, 4097, 6160), (65, 4033, 2576),
+                                   (129, 1025, 8208), (1025, 129, 8464), (64, 4097, 16400), (65, 4033, 8272)])
 def test_last_rows_alone_in_their_tiles(M, N, K):
     """One row of a, of b or of both in a 64 x 64 tile, and a K that two groups of waves do not halve: the second
     group's last step lies past K, where its copies must read zeros."""
@@ -152,6 +153,20 @@ def test_last_rows_alone_in_their_tiles(M, N, K):
     c = torch.full((M, N), float("nan"), device="cuda")
     F.int8_gemm_scaled(dev(a), dev(sa), dev(b), dev(sb), "f32", c=c)
     same(c, rounded(int8.gemm(a, sa, b, sb), "f32"))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(333, 514, 1920), (333, 514, 2048), (200, 1030, 2176), (500, 1000, 2432),
+                                   (200, 1030, 8176), (200, 1030, 8208), (333, 514, 8320), (100, 4097, 9232)])
+def test_one_and_two_groups_of_waves(M, N, K, out):
+    """64 x 64 tiles on both sides of the limits of K, with whole 128-byte steps and without, even and odd."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    a, b = codes((M, K), 2770 + M), codes((N, K), 2771 + N)
+    sa, sb = scales(M, 2772), scales(N, 2773)
+    c = torch.full((M, N), float("nan"), dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    F.int8_gemm_scaled(dev(a), dev(sa), dev(b), dev(sb), out, c=c)
+    same(c, rounded(int8.gemm(a, sa, b, sb), out))
 
 
 def test_largest_sums():
