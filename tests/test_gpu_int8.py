@@ -255,6 +255,20 @@ def test_grouped(rows, N, K, out):
     same(c, rounded(int8.gemm_grouped(a, sa, b, sb, off), out))  # NaN where nothing is written
 
 
+def test_grouped_with_fewer_rows_than_given():
+    """M_total below a's rows: offsets are held to it, and c has M_total rows."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    a, b = codes((640, 96), 2740), codes((3, 70, 96), 2741)
+    sa, sb = scales(700, 2742), scales((3, 70), 2743)
+    off = np.array([0, 128, 256, 384], np.int32)
+    c = F.int8_gemm_grouped(dev(a), dev(sa), dev(b), dev(sb), dev(off), "f32", M_total=384)
+    assert c.shape == (384, 70)
+    same(c, rounded(int8.gemm_grouped(a[:384], sa[:384], b, sb, off), "f32"))
+    with pytest.raises(ValueError):
+        F.int8_gemm_grouped(dev(a), dev(sa), dev(b), dev(sb), dev(off), "f32", M_total=768)
+
+
 def test_grouped_without_k():
     import torch
     import fp8_fine_grained_online_amd as F

@@ -89,6 +89,30 @@ def test_permute_is_the_dispatch_layout():
         assert torch.equal(off, off2) and torch.equal(rows, rows2)
 
 
+def test_permute_with_the_callers_buffers():
+    """A workspace of exactly the stated size, kept between calls of each of the three sorting paths, and its end
+    left alone; one byte less is refused."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    for T, topk, G in ((200, 2, 9), (2000, 8, 40), (9000, 2, 16)):
+        need = F.lib().fp8q_moe_dispatch_workspace_bytes(T, topk, G)
+        buffer = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+        x = randn((T, 16), "f32", 2613)
+        for seed in (1, 2):
+            ids = routing(T, topk, G, 2614 + seed, drop=6)
+            off = torch.full((G + 1,), -7, dtype=torch.int32, device="cuda")
+            rows = torch.full((T, topk), -7, dtype=torch.int32, device="cuda")
+            xp, off2, rows2 = F.fp8q_moe_permute(x, torch.from_numpy(ids).cuda(), G, m_offsets=off, row_of_slot=rows,
+                                                 workspace=buffer[:need])
+            assert off2 is off and rows2 is rows
+            want, want_off, want_rows = tokens.permute(x.cpu().numpy(), ids, G)
+            assert np.array_equal(off.cpu().numpy(), want_off) and np.array_equal(rows.cpu().numpy(), want_rows)
+            assert np.array_equal(xp[:len(want)].cpu().numpy(), want)
+            assert (buffer[need:] == 0xA5).all()
+        with pytest.raises(F.Fp8qError):
+            F.fp8q_moe_permute(x, torch.from_numpy(ids).cuda(), G, workspace=buffer[:need - 1])
+
+
 def test_permute_without_tokens_or_columns():
     import torch
     import fp8_fine_grained_online_amd as F
