@@ -13,14 +13,16 @@
 // float64: whether an expert is chosen is a comparison of two nearly equal
 // numbers, and its answer should be that of the formula, not of the rounding.
 //
-// Few bytes move (at most 17 MB below, 3.5 us), so the time is mostly that of one
-// launch (1.8 us for an empty kernel) and of one wavefront's chain: a load, the
-// softmax, its choices (0.15 us each). MI355X, us: 16 tokens of 256 experts in 8
-// groups, top-8, sigmoid 5.6; 8192 of 64, top-6 5.6; 100 of 1024, top-64 23.2 (41.6
-// with the places of a lane's experts moved up one by one); gradient, 8192 of 256
-// 5.3. (With every choice searched through all keys, the library's exponential,
-// and gradient shares passed from lane to lane the first took 8.8 and the gradient
-// 8.3.)
+// Few bytes move (at most 17 MB below, 3.5 us): what the time goes into are
+// instructions. For few tokens it is one wavefront's chain (a load, the scores in
+// float64, its choices, 0.15 us each) on top of a launch (1.8 us for an empty
+// kernel); for batches the vector ALUs are busy 70 to 80% of the time. MI355X, us,
+// in a captured graph: 16 tokens of 256 experts in 8 groups, top-8, sigmoid 5.7;
+// 8192 of 64, top-6 6.0; 8192 of 256 in 8 groups 14.1; 4096 of 512, top-10 10.2;
+// 100 of 1024, top-64 21.2 (41.6 with the places of a lane's experts moved up one by
+// one); gradient, 8192 of 256, sigmoid 5.4, softmax 7.6. (With every choice searched
+// through all keys, the library's exponential, and gradient shares passed from lane
+// to lane the first took 8.8 and the gradient 8.3.)
 #include <type_traits>
 
 #include "common.hpp"
