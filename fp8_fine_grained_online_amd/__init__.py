@@ -34,6 +34,12 @@ MoE layer around the experts' products, with gradients:
   fp8q_quant_int8_rows(x)                    -> (q, s)
   int8_gemm_scaled(a, sa, b, sb, out_dtype)  -> c
   int8_gemm_grouped(a, sa, b, sb, m_offsets, out_dtype)  -> c
+A training step around the products, with gradients:
+  fp8q_norm(x, gamma, eps, beta, centred, residual)      -> y [, h]   rows that stay in 16 or 32 bits
+  fp8q_norm_bwd(dy, x, gamma, eps, centred, dres)        -> (dx, dgamma, dbeta)
+  fp8q_swiglu(gu, out_dtype)                             -> y   gated activation
+  fp8q_swiglu_quant_act_1x128(gu)                        -> (q, sa)   the same, straight to FP8 tiles
+  fp8q_swiglu_bwd(dy, gu)                                -> dgu
 """
 
 from ._lib import (  # noqa: F401
@@ -61,7 +67,12 @@ from ._lib import (  # noqa: F401
     fp8q_moe_permute,
     fp8q_moe_route,
     fp8q_moe_route_bwd,
+    fp8q_norm,
+    fp8q_norm_bwd,
     fp8q_quant_int8_rows,
+    fp8q_swiglu,
+    fp8q_swiglu_bwd,
+    fp8q_swiglu_quant_act_1x128,
     fp8q_version,
     int8_gemm_grouped,
     int8_gemm_scaled,
@@ -77,4 +88,5 @@ __all__ = [
     "fp8_gemm_rowscaled",
     "fp8q_moe_route", "fp8q_moe_route_bwd", "fp8q_moe_permute", "fp8q_moe_combine", "fp8q_moe_combine_bwd",
     "fp8q_quant_int8_rows", "int8_gemm_scaled", "int8_gemm_grouped",
+    "fp8q_norm", "fp8q_norm_bwd", "fp8q_swiglu", "fp8q_swiglu_quant_act_1x128", "fp8q_swiglu_bwd",
 ]

@@ -98,6 +98,19 @@ def lib() -> ctypes.CDLL:
         L.int8_gemm_scaled.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]
         L.int8_gemm_grouped.restype = i32
         L.int8_gemm_grouped.argtypes = [vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, i64, vp]
+        L.fp8q_norm.restype = i32
+        L.fp8q_norm.argtypes = [vp, i32, i64, vp, i64, vp, vp, i32, f32, i32, i64, i64, vp, i32, vp, vp]
+        L.fp8q_norm_bwd_workspace_bytes.restype = i64
+        L.fp8q_norm_bwd_workspace_bytes.argtypes = [i64, i64, i32]
+        L.fp8q_norm_bwd.restype = i32
+        L.fp8q_norm_bwd.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, vp, i64, f32, i32, i64, i64, vp, vp,
+                                    vp, vp, i64, vp]
+        L.fp8q_swiglu.restype = i32
+        L.fp8q_swiglu.argtypes = [vp, i32, i64, vp, i64, i64, i64, vp, i32, vp]
+        L.fp8q_swiglu_quant_act_1x128.restype = i32
+        L.fp8q_swiglu_quant_act_1x128.argtypes = [vp, i32, i64, vp, i64, i64, i64, vp, vp, vp]
+        L.fp8q_swiglu_bwd.restype = i32
+        L.fp8q_swiglu_bwd.argtypes = [vp, i32, i64, vp, i32, i64, vp, i64, i64, i64, vp, vp]
         _lib = L
     return _lib
 
@@ -483,7 +496,7 @@ def fp8_gemm_rowscaled(a, sa, b, sb, out_dtype="f32", c=None, stream=None):
     return c
 
 
-# ---- MoE layer around the experts' products, and the 8-bit integer product ----
+# ---- MoE layer around the experts' products, the 8-bit integer product, a training step ----
 #
 # These calls are short enough for a binding's own time to count, so their
 # argument checks and allocations are native (csrc/binding.cpp).
@@ -608,3 +621,44 @@ def int8_gemm_grouped(a, sa, b, sb, m_offsets, out_dtype="bf16", c=None, M_total
         return _on_stream(stream, int8_gemm_grouped, a, sa, b, sb, m_offsets, out_dtype, c, M_total)
     return (_native or _binding()).int8_gemm_grouped(a, sa, b, sb, m_offsets, _out_code(out_dtype), c,
                                                       M_total)
+
+
+def fp8q_norm(x, gamma, eps, beta=None, centred=False, residual=None, out_dtype="bf16", y=None, h=None, stream=None):
+    """Rows of x (M x K, bfloat16 or float32), or of x + residual, normalized: RMS, or centred with an
+    optional beta -> y (M x K of out_dtype); with a residual (y, h), h the sum in x's type. Rows of x
+    and residual may lie apart; gamma and beta are of one type, bfloat16 or float32."""
+    if stream is not None:
+        return _on_stream(stream, fp8q_norm, x, gamma, eps, beta, centred, residual, out_dtype, y, h)
+    return (_native or _binding()).fp8q_norm(x, gamma, eps, beta, centred, residual, _out_code(out_dtype), y, h)
+
+
+def fp8q_norm_bwd(dy, x, gamma, eps, centred=False, dres=None, dx=None, dgamma=None, dbeta=None, workspace=None,
+                  stream=None):
+    """Gradient of fp8q_norm, or of the normalization in fp8q_norm_quant_act_1x128, of x (fp8q_norm's h
+    where it had a residual): dy M x K -> (dx M x K like x, dgamma float32 K, dbeta float32 K or None
+    where not centred). dres (like x) is added to dx: the residual stream's own gradient."""
+    if stream is not None:
+        return _on_stream(stream, fp8q_norm_bwd, dy, x, gamma, eps, centred, dres, dx, dgamma, dbeta, workspace)
+    return (_native or _binding()).fp8q_norm_bwd(dy, x, gamma, eps, centred, dres, dx, dgamma, dbeta, workspace)
+
+
+def fp8q_swiglu(gu, out_dtype="bf16", m_offsets=None, y=None, stream=None):
+    """gu = [gate | up] (M x 2I, bfloat16 or float32) -> y = silu(gate) * up (M x I of out_dtype). With
+    m_offsets (int32[G+1], device) rows from m_offsets[G] on are neither read nor written."""
+    if stream is not None:
+        return _on_stream(stream, fp8q_swiglu, gu, out_dtype, m_offsets, y)
+    return (_native or _binding()).fp8q_swiglu(gu, m_offsets, _out_code(out_dtype), y)
+
+
+def fp8q_swiglu_quant_act_1x128(gu, m_offsets=None, q=None, sa=None, stream=None):
+    """fp8q_swiglu's binary32 result in 1x128 FP8 tiles -> (q uint8 M x I, sa float32 M x I/128)."""
+    if stream is not None:
+        return _on_stream(stream, fp8q_swiglu_quant_act_1x128, gu, m_offsets, q, sa)
+    return (_native or _binding()).fp8q_swiglu_quant_act_1x128(gu, m_offsets, q, sa)
+
+
+def fp8q_swiglu_bwd(dy, gu, m_offsets=None, dgu=None, stream=None):
+    """Gradient of fp8q_swiglu: dy M x I -> dgu = [dgate | dup] (M x 2I, like gu)."""
+    if stream is not None:
+        return _on_stream(stream, fp8q_swiglu_bwd, dy, gu, m_offsets, dgu)
+    return (_native or _binding()).fp8q_swiglu_bwd(dy, gu, m_offsets, dgu)

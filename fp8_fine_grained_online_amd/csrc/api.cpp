@@ -74,6 +74,22 @@ hipError_t launch_int8_gemm_grouped(const int8_t* a, const float* sa, const int8
                                     const float* sb, void* c, bool bf16, const int32_t* m_offsets,
                                     int64_t G, int64_t M_total, int64_t N, int64_t K,
                                     hipStream_t stream);
+hipError_t launch_norm_rows(const void* x, bool x_bf16, int64_t ldx, const void* res, int64_t ldr,
+                            const void* gamma, const void* beta, bool weights_bf16, float eps,
+                            bool centred, int64_t M, int64_t K, void* y, bool y_bf16, void* h,
+                            hipStream_t stream);
+int64_t norm_bwd_workspace_bytes(int64_t M, int64_t K, bool centred);
+hipError_t launch_norm_rows_bwd(const void* dy, bool dy_bf16, int64_t ldy, const void* x, bool x_bf16,
+                                int64_t ldx, const void* gamma, bool weights_bf16, const void* dres,
+                                int64_t ldr, float eps, bool centred, int64_t M, int64_t K, void* dx,
+                                float* dgamma, float* dbeta, void* ws, hipStream_t stream);
+hipError_t launch_swiglu(const void* gu, bool gu_bf16, int64_t ld, const int32_t* last, int64_t M,
+                         int64_t I, void* y, bool y_bf16, hipStream_t stream);
+hipError_t launch_swiglu_quant(const void* gu, bool gu_bf16, int64_t ld, const int32_t* last,
+                               int64_t M, int64_t I, uint8_t* q, float* sa, hipStream_t stream);
+hipError_t launch_swiglu_bwd(const void* dy, bool dy_bf16, int64_t ldy, const void* gu, bool gu_bf16,
+                             int64_t ld, const int32_t* last, int64_t M, int64_t I, void* dgu,
+                             hipStream_t stream);
 }  // namespace fp8q
 
 namespace {
@@ -156,6 +172,30 @@ int check_int8(const int8_t* a, const float* sa, const int8_t* b, const float* s
   if (!aligned(c, 16)) return FP8Q_ERR_ALIGN;
   if (K > 0 && (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4)))
     return FP8Q_ERR_ALIGN;
+  return FP8Q_OK;
+}
+
+uintptr_t element(int dtype) { return dtype == FP8Q_OUT_BF16 ? 2 : 4; }
+
+// Sizes shared by the normalization's calls.
+int check_norm(float eps, int centred, int64_t M, int64_t K) {
+  if (M < 0 || K < 0) return FP8Q_ERR_SHAPE;
+  if (centred != 0 && centred != 1) return FP8Q_ERR_SHAPE;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return FP8Q_ERR_SHAPE;  // NaN, negative or infinite
+  // up to a workgroup of 512 threads per row
+  if (M > kMaxDim || K > kNormMaxK || !launchable(M, 512)) return FP8Q_ERR_TOO_LARGE;
+  return FP8Q_OK;
+}
+
+// Sizes and offsets shared by the gated activation's calls.
+int check_swiglu(int gu_dtype, int64_t ld, const int32_t* m_offsets, int64_t G, int64_t M, int64_t I) {
+  if (M < 0 || I < 0 || (m_offsets && G < 1)) return FP8Q_ERR_SHAPE;
+  if (!known_dtype(gu_dtype)) return FP8Q_ERR_DTYPE;
+  if (M > kMaxDim || I > kMaxDim / 2 || (m_offsets && G > kMaxDim)) return FP8Q_ERR_TOO_LARGE;
+  if (!launchable((M * ((I + 7) / 8) + 255) / 256, 256)) return FP8Q_ERR_TOO_LARGE;
+  if (M == 0 || I == 0) return -1;  // valid no-op
+  if (ld < 2 * I) return FP8Q_ERR_SHAPE;
+  if (!aligned(m_offsets, 4)) return FP8Q_ERR_ALIGN;
   return FP8Q_OK;
 }
 
@@ -553,6 +593,100 @@ int int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b, const f
   if ((s = check_device())) return s;
   return launched(fp8q::launch_int8_gemm_grouped(a, sa, b, sb, c, out_dtype == FP8Q_OUT_BF16,
                                                  m_offsets, G, M_total, N, K, (hipStream_t)stream));
+}
+
+int fp8q_norm(const void* x, int x_dtype, int64_t ldx, const void* residual, int64_t ldr,
+              const void* gamma, const void* beta, int weights_dtype, float eps, int centred, int64_t M,
+              int64_t K, void* y, int y_dtype, void* h, void* stream) {
+  int s = check_norm(eps, centred, M, K);
+  if (s) return s;
+  if (!known_dtype(x_dtype) || !known_dtype(weights_dtype) || !known_dtype(y_dtype)) return FP8Q_ERR_DTYPE;
+  if (beta && !centred) return FP8Q_ERR_SHAPE;
+  if (M == 0 || K == 0) return FP8Q_OK;
+  if (!x || !gamma || !y || (residual == nullptr) != (h == nullptr)) return FP8Q_ERR_NULL;
+  if (ldx < K || (residual && ldr < K)) return FP8Q_ERR_SHAPE;
+  const uintptr_t ex = element(x_dtype), ew = element(weights_dtype);
+  if (!aligned(x, ex) || !aligned(residual, ex) || !aligned(h, ex) || !aligned(gamma, ew) ||
+      !aligned(beta, ew) || !aligned(y, element(y_dtype)))
+    return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_norm_rows(x, x_dtype == FP8Q_OUT_BF16, ldx, residual, ldr, gamma, beta,
+                                         weights_dtype == FP8Q_OUT_BF16, eps, centred == 1, M, K, y,
+                                         y_dtype == FP8Q_OUT_BF16, h, (hipStream_t)stream));
+}
+
+int64_t fp8q_norm_bwd_workspace_bytes(int64_t M, int64_t K, int centred) {
+  if (check_norm(0.0f, centred, M, K)) return -1;
+  return fp8q::norm_bwd_workspace_bytes(M, K, centred == 1);
+}
+
+int fp8q_norm_bwd(const void* dy, int dy_dtype, int64_t ldy, const void* x, int x_dtype, int64_t ldx,
+                  const void* gamma, int weights_dtype, const void* dres, int64_t ldr, float eps,
+                  int centred, int64_t M, int64_t K, void* dx, float* dgamma, float* dbeta,
+                  void* workspace, int64_t workspace_bytes, void* stream) {
+  int s = check_norm(eps, centred, M, K);
+  if (s) return s;
+  if (!known_dtype(dy_dtype) || !known_dtype(x_dtype) || !known_dtype(weights_dtype)) return FP8Q_ERR_DTYPE;
+  if (K == 0) return FP8Q_OK;
+  if (!gamma || !dgamma || (dbeta != nullptr) != (centred == 1)) return FP8Q_ERR_NULL;
+  const int64_t need = fp8q::norm_bwd_workspace_bytes(M, K, centred == 1);
+  if (M > 0) {
+    if (!dy || !x || !dx || !workspace) return FP8Q_ERR_NULL;
+    if (ldy < K || ldx < K || (dres && ldr < K) || workspace_bytes < need) return FP8Q_ERR_SHAPE;
+  }
+  const uintptr_t ex = element(x_dtype);
+  if (!aligned(dy, element(dy_dtype)) || !aligned(x, ex) || !aligned(dres, ex) || !aligned(dx, ex) ||
+      !aligned(gamma, element(weights_dtype)) || !aligned(dgamma, 4) || !aligned(dbeta, 4) ||
+      !aligned(workspace, 16))
+    return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_norm_rows_bwd(dy, dy_dtype == FP8Q_OUT_BF16, ldy, x, x_dtype == FP8Q_OUT_BF16,
+                                             ldx, gamma, weights_dtype == FP8Q_OUT_BF16, dres, ldr, eps,
+                                             centred == 1, M, K, dx, dgamma, dbeta, workspace,
+                                             (hipStream_t)stream));
+}
+
+int fp8q_swiglu(const void* gu, int gu_dtype, int64_t ld, const int32_t* m_offsets, int64_t G, int64_t M,
+                int64_t I, void* y, int y_dtype, void* stream) {
+  if (!known_dtype(y_dtype)) return FP8Q_ERR_DTYPE;
+  int s = check_swiglu(gu_dtype, ld, m_offsets, G, M, I);
+  if (s == -1) return FP8Q_OK;
+  if (s) return s;
+  if (!gu || !y) return FP8Q_ERR_NULL;
+  if (!aligned(gu, element(gu_dtype)) || !aligned(y, element(y_dtype))) return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_swiglu(gu, gu_dtype == FP8Q_OUT_BF16, ld, m_offsets ? m_offsets + G : nullptr,
+                                      M, I, y, y_dtype == FP8Q_OUT_BF16, (hipStream_t)stream));
+}
+
+int fp8q_swiglu_quant_act_1x128(const void* gu, int gu_dtype, int64_t ld, const int32_t* m_offsets,
+                                int64_t G, int64_t M, int64_t I, uint8_t* q, float* sa, void* stream) {
+  if (I % kGroup) return FP8Q_ERR_SHAPE;
+  int s = check_swiglu(gu_dtype, ld, m_offsets, G, M, I);
+  if (s == -1) return FP8Q_OK;
+  if (s) return s;
+  if (!gu || !q || !sa) return FP8Q_ERR_NULL;
+  if (!aligned(gu, element(gu_dtype)) || !aligned(q, 16) || !aligned(sa, 4)) return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_swiglu_quant(gu, gu_dtype == FP8Q_OUT_BF16, ld,
+                                            m_offsets ? m_offsets + G : nullptr, M, I, q, sa,
+                                            (hipStream_t)stream));
+}
+
+int fp8q_swiglu_bwd(const void* dy, int dy_dtype, int64_t ldy, const void* gu, int gu_dtype, int64_t ld,
+                    const int32_t* m_offsets, int64_t G, int64_t M, int64_t I, void* dgu, void* stream) {
+  if (!known_dtype(dy_dtype)) return FP8Q_ERR_DTYPE;
+  int s = check_swiglu(gu_dtype, ld, m_offsets, G, M, I);
+  if (s == -1) return FP8Q_OK;
+  if (s) return s;
+  if (ldy < I) return FP8Q_ERR_SHAPE;
+  if (!dy || !gu || !dgu) return FP8Q_ERR_NULL;
+  if (!aligned(dy, element(dy_dtype)) || !aligned(gu, element(gu_dtype)) || !aligned(dgu, element(gu_dtype)))
+    return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_swiglu_bwd(dy, dy_dtype == FP8Q_OUT_BF16, ldy, gu, gu_dtype == FP8Q_OUT_BF16,
+                                          ld, m_offsets ? m_offsets + G : nullptr, M, I, dgu,
+                                          (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,4 +1,5 @@
-// Python binding of the MoE layer's calls and of the 8-bit integer product, as
+// Python binding of the MoE layer's calls, of the 8-bit integer product and of a
+// training step's calls around the products, as
 // a CPython extension over the C ABI: argument checks, outputs, device and
 // stream, and the call. A serving step's kernels take a few microseconds each,
 // so the binding's own time is part of the latency: the same checks and
@@ -58,7 +59,8 @@ struct Call {
   bool none(int i) const { return args[i] == Py_None; }
 
   // Argument i: a contiguous tensor of one of `types` with `dims` dimensions
-  const at::Tensor& tensor(int i, const char* name, std::initializer_list<ScalarType> types, int64_t dims) {
+  const at::Tensor& tensor(int i, const char* name, std::initializer_list<ScalarType> types, int64_t dims,
+                           bool contiguous = true) {
     if (!THPVariable_Check(args[i])) refuse(PyExc_TypeError, "%s must be a torch.Tensor", name);
     const at::Tensor& t = THPVariable_Unpack(args[i]);
     if (!t.is_cuda() || (device >= 0 && t.get_device() != device))
@@ -70,7 +72,17 @@ struct Call {
     if (!known) refuse(PyExc_TypeError, "%s must not be of type %s here (the first allowed is %s)", name,
                                        at::toString(t.scalar_type()), at::toString(*types.begin()));
     if (t.dim() != dims) refuse(PyExc_ValueError, "%s must have %d dims, got %d", name, (int)dims, (int)t.dim());
-    if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
+    if (contiguous && !t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
+    return t;
+  }
+
+  // Argument i: a 2-dimensional tensor of one of `types` whose rows are dense but may
+  // lie apart; `ld` gets the elements from one row to the next
+  const at::Tensor& rows(int i, const char* name, std::initializer_list<ScalarType> types, int64_t& ld) {
+    const at::Tensor& t = tensor(i, name, types, 2, false);
+    const int64_t M = t.size(0), K = t.size(1);
+    ld = M > 1 ? t.stride(0) : K;
+    if ((K > 1 && t.stride(1) != 1) || ld < K) refuse(PyExc_ValueError, "%s must have dense rows that do not overlap", name);
     return t;
   }
 
@@ -338,6 +350,143 @@ PyObject* int8_gemm_experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A weight of K entries, or none where `optional` and None is given
+at::Tensor weight(Call& c, int i, const char* name, int64_t K, bool optional) {
+  if (optional && c.none(i)) return {};
+  const at::Tensor& w = c.tensor(i, name, kFloats, 1);
+  if (w.size(0) != K) refuse(PyExc_ValueError, "%s must have K entries", name);
+  return w;
+}
+
+// x, gamma, eps, beta, centred, residual, out_dtype, y, h
+PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c("fp8q_norm", args, n, 9);
+  int64_t ldx, ldr = 0;
+  const at::Tensor& x = c.rows(0, "x", kFloats, ldx);
+  const int64_t M = x.size(0), K = x.size(1), out = c.integer(6);
+  const at::Tensor gamma = weight(c, 1, "gamma", K, false), beta = weight(c, 3, "beta", K, true);
+  if (beta.defined() && beta.scalar_type() != gamma.scalar_type())
+    refuse(PyExc_TypeError, "gamma and beta must be of one type");
+  const float eps = (float)c.number(2);
+  const int centred = c.truth(4);
+  at::Tensor res, h;
+  if (!c.none(5)) {
+    res = c.rows(5, "residual", {x.scalar_type()}, ldr);
+    if (res.sizes() != x.sizes()) refuse(PyExc_ValueError, "residual must have x's shape");
+    h = c.out(8, "h", {M, K}, x.scalar_type());
+  } else if (!c.none(8)) {
+    refuse(PyExc_ValueError, "h goes with a residual");
+  }
+  const at::Tensor y = c.out(7, "y", {M, K}, type_of(out));
+  void* s = c.stream();
+  const int status = launch([&] {
+    return fp8q_norm(ptr(x), code(x), ldx, ptr(res), ldr, ptr(gamma), ptr(beta), code(gamma), eps, centred, M, K, ptr(y),
+                     (int)out, ptr(h), s);
+  });
+  if (!h.defined()) return result(status, c, {7}, {&y});
+  return result(status, c, {7, 8}, {&y, &h});
+  END_HANDLE_TH_ERRORS
+}
+
+// dy, x, gamma, eps, centred, dres, dx, dgamma, dbeta, workspace
+PyObject* norm_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c("fp8q_norm_bwd", args, n, 10);
+  int64_t ldy, ldx, ldr = 0;
+  const at::Tensor& dy = c.rows(0, "dy", kFloats, ldy);
+  const at::Tensor& x = c.rows(1, "x", kFloats, ldx);
+  if (dy.sizes() != x.sizes()) refuse(PyExc_ValueError, "dy must have x's shape");
+  const int64_t M = x.size(0), K = x.size(1);
+  const at::Tensor gamma = weight(c, 2, "gamma", K, false);
+  const float eps = (float)c.number(3);
+  const int centred = c.truth(4);
+  at::Tensor res, dbeta;
+  if (!c.none(5)) {
+    res = c.rows(5, "dres", {x.scalar_type()}, ldr);
+    if (res.sizes() != x.sizes()) refuse(PyExc_ValueError, "dres must have x's shape");
+  }
+  const int64_t bytes = fp8q_norm_bwd_workspace_bytes(M, K, centred);
+  if (bytes < 0) refuse(PyExc_ValueError, "invalid normalization sizes");
+  const at::Tensor dx = c.out(6, "dx", {M, K}, x.scalar_type());
+  const at::Tensor dgamma = c.out(7, "dgamma", {K}, ScalarType::Float);
+  if (centred) dbeta = c.out(8, "dbeta", {K}, ScalarType::Float);
+  else if (!c.none(8)) refuse(PyExc_ValueError, "dbeta goes with the centred form");
+  const at::Tensor ws = c.none(9) ? c.out(9, "workspace", {bytes}, ScalarType::Byte)
+                                  : c.tensor(9, "workspace", {ScalarType::Byte}, 1);
+  void* s = c.stream();
+  const int status = launch([&] {
+    return fp8q_norm_bwd(ptr(dy), code(dy), ldy, ptr(x), code(x), ldx, ptr(gamma), code(gamma), ptr(res), ldr, eps,
+                         centred, M, K, ptr(dx), (float*)ptr(dgamma), (float*)ptr(dbeta), ptr(ws), ws.numel(), s);
+  });
+  return result(status, c, {6, 7, 8}, {&dx, &dgamma, &dbeta});
+  END_HANDLE_TH_ERRORS
+}
+
+// gu's rows as [gate | up]; the offsets of the experts' blocks, where given
+struct Gated {
+  const at::Tensor& gu;
+  at::Tensor off;
+  int64_t ld, M, I, G = 0;
+
+  Gated(Call& c, int i, int i_off) : gu(c.rows(i, "gu", kFloats, ld)), M(gu.size(0)), I(gu.size(1) / 2) {
+    if (gu.size(1) % 2) refuse(PyExc_ValueError, "gu must have 2 I columns, gate and up");
+    if (c.none(i_off)) return;
+    off = c.tensor(i_off, "m_offsets", {ScalarType::Int}, 1);
+    G = off.size(0) - 1;
+    if (G < 1) refuse(PyExc_ValueError, "m_offsets must have G+1 entries");
+  }
+};
+
+// gu, m_offsets, out_dtype, y
+PyObject* swiglu(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c("fp8q_swiglu", args, n, 4);
+  const Gated g(c, 0, 1);
+  const int64_t out = c.integer(2);
+  const at::Tensor y = c.out(3, "y", {g.M, g.I}, type_of(out));
+  void* s = c.stream();
+  const int status = launch([&] {
+    return fp8q_swiglu(ptr(g.gu), code(g.gu), g.ld, (const int32_t*)ptr(g.off), g.G, g.M, g.I, ptr(y), (int)out, s);
+  });
+  return result(status, c, {3}, {&y});
+  END_HANDLE_TH_ERRORS
+}
+
+// gu, m_offsets, q, sa
+PyObject* swiglu_quant(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c("fp8q_swiglu_quant_act_1x128", args, n, 4);
+  const Gated g(c, 0, 1);
+  const at::Tensor q = c.out(2, "q", {g.M, g.I}, ScalarType::Byte);
+  const at::Tensor sa = c.out(3, "sa", {g.M, g.I / 128}, ScalarType::Float);
+  void* s = c.stream();
+  const int status = launch([&] {
+    return fp8q_swiglu_quant_act_1x128(ptr(g.gu), code(g.gu), g.ld, (const int32_t*)ptr(g.off), g.G, g.M, g.I,
+                                       (uint8_t*)ptr(q), (float*)ptr(sa), s);
+  });
+  return result(status, c, {2, 3}, {&q, &sa});
+  END_HANDLE_TH_ERRORS
+}
+
+// dy, gu, m_offsets, dgu
+PyObject* swiglu_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call c("fp8q_swiglu_bwd", args, n, 4);
+  int64_t ldy;
+  const at::Tensor& dy = c.rows(0, "dy", kFloats, ldy);
+  const Gated g(c, 1, 2);
+  if (dy.size(0) != g.M || dy.size(1) != g.I) refuse(PyExc_ValueError, "dy must be M x I for gu's M x 2I");
+  const at::Tensor dgu = c.out(3, "dgu", {g.M, 2 * g.I}, g.gu.scalar_type());
+  void* s = c.stream();
+  const int status = launch([&] {
+    return fp8q_swiglu_bwd(ptr(dy), code(dy), ldy, ptr(g.gu), code(g.gu), g.ld, (const int32_t*)ptr(g.off), g.G, g.M, g.I,
+                           ptr(dgu), s);
+  });
+  return result(status, c, {3}, {&dgu});
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* on_status(PyObject*, PyObject* handler) {
   Py_INCREF(handler);
   Py_XDECREF(status_handler);
@@ -355,6 +504,11 @@ PyMethodDef methods[] = {
     FP8Q_METHOD("fp8q_quant_int8_rows", quant_int8_rows),
     FP8Q_METHOD("int8_gemm_scaled", int8_gemm_dense),
     FP8Q_METHOD("int8_gemm_grouped", int8_gemm_experts),
+    FP8Q_METHOD("fp8q_norm", norm),
+    FP8Q_METHOD("fp8q_norm_bwd", norm_bwd),
+    FP8Q_METHOD("fp8q_swiglu", swiglu),
+    FP8Q_METHOD("fp8q_swiglu_quant_act_1x128", swiglu_quant),
+    FP8Q_METHOD("fp8q_swiglu_bwd", swiglu_bwd),
     {"on_status", on_status, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

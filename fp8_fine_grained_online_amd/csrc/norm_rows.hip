@@ -1,0 +1,460 @@
+// Normalization of rows that stay in bfloat16 or binary32, and its gradient with
+// the reduction of the weights' gradients, for gfx950.
+//
+//   h = x + residual (rounded to x's type, where a residual is given), else x
+//   centred: mu = sum h / K, var = sum (h - mu)^2 / K;  RMS: mu = 0
+//   r = 1 / sqrt(var + eps),  hat = (h - mu) r,  y = hat gamma + beta
+//
+//   dg = dy gamma
+//   dx = r (dg - [centred: sum dg / K] - hat sum(dg hat) / K) + dres
+//   dgamma = sum over rows of dy hat,  dbeta = sum over rows of dy
+//
+// Both are bound by memory: a row is read once, held in registers by one
+// wavefront or by a workgroup's, and reduced twice there (the mean, then the
+// deviations). The second reduction also sums the deviations themselves, whose
+// mean is what the rounded mean is off by: var and hat are put right with it, so
+// rows with a mean far larger than their spread lose nothing to the mean's
+// rounding. Sums are in binary32; a row whose statistics leave binary32's range
+// (squares that overflow, or underflow where eps does not cover them) is done
+// again in float64, from the registers.
+#include "common.hpp"
+#include "rows.hpp"
+#include "wave.hpp"
+
+namespace fp8q {
+
+// kThreads per row (64: a wavefront; else a whole number of them), kChunks of
+// eight values per thread: value 8 (t + kThreads i) + e belongs to thread t.
+template <int kThreads, int kChunks>
+struct RowShape {
+  static constexpr int kT = kThreads, kC = kChunks;
+  static constexpr int kMaxK = 8 * kThreads * kChunks;
+};
+
+// Sums over the threads of a row, the same bits in all of them. `slot`: LDS for
+// kN sums of each of the row's wavefronts; a barrier separates two calls' uses of
+// one slot.
+template <int kThreads, int kN, typename S>
+__device__ __forceinline__ void row_sums(S (&v)[kN], S (*slot)[kN]) {
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    if constexpr (sizeof(S) == 8) v[n] = wave_sum_f64(v[n]);
+    else v[n] = wave_sum_f32(v[n]);
+  }
+  if constexpr (kThreads > 64) {
+    const int wave = (threadIdx.x % kThreads) >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) slot[wave][n] = v[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      S s = slot[0][n];
+#pragma unroll
+      for (int w = 1; w < kThreads / 64; ++w) s += slot[w][n];
+      v[n] = s;
+    }
+  }
+}
+
+// LDS of one row's sums, a slot per reduction so that none waits for another's readers
+template <int kThreads>
+struct RowLds {
+  float one[kThreads / 64][1], two[kThreads / 64][2];
+  double wide[2][kThreads / 64][1];
+};
+
+struct RowStats {
+  float mu, shift, r;  // hat = (h - mu) r - shift, shift = (what mu is off by) r
+  double wide_mu, wide_r;
+  bool wide;  // the statistics are in the doubles
+};
+
+// Statistics of the row whose values are in v; absent values are zeros.
+// `present(i)`: how many of chunk i's values exist (0 to 8). kTogether: other rows
+// of the workgroup meet the same barriers, so one that needs the wide way takes all
+// along (who did not need it keeps what it had).
+template <typename Shape, bool kCentred, bool kTogether, typename Present>
+__device__ __forceinline__ RowStats row_stats(const float (&v)[Shape::kC][8], Present present, int K, float eps,
+                                              RowLds<Shape::kT>& lds) {
+  constexpr int T = Shape::kT, C = Shape::kC;
+  RowStats s;
+  s.mu = s.shift = 0.0f;
+  s.wide_mu = 0.0, s.wide_r = 0.0;
+  const float inv_k = 1.0f / (float)K;
+  float stat[2] = {0.0f, 0.0f};  // sum of squared deviations, of deviations
+  if constexpr (kCentred) {
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[0] += v[i][e];
+    row_sums<T, 1>(sum, lds.one);
+    s.mu = sum[0] * inv_k;
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int have = present(i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = kCentred ? (e < have ? v[i][e] - s.mu : 0.0f) : v[i][e];
+      stat[0] = __builtin_fmaf(d, d, stat[0]);
+      if constexpr (kCentred) stat[1] += d;
+    }
+  }
+  row_sums<T, 2>(stat, lds.two);
+  const float off = stat[1] * inv_k;  // the true mean is mu + off
+  const float raw = stat[0] * inv_k - off * off;  // NaN where both overflow
+  s.wide = !(raw <= 1e36f) || (raw < 1e-30f && eps < 1e-25f);
+  const float var = fmaxf(raw, 0.0f);
+  s.r = (float)(1.0 / __dsqrt_rn((double)var + (double)eps));
+  s.shift = off * s.r;
+  if (!(kTogether ? __syncthreads_or(s.wide) : s.wide)) return s;
+  if constexpr (kCentred) {
+    double sum[1] = {0.0};
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[0] += (double)v[i][e];
+    row_sums<T, 1>(sum, lds.wide[0]);
+    s.wide_mu = sum[0] / (double)K;
+  }
+  double sq[1] = {0.0};
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int have = present(i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double d = e < have ? (double)v[i][e] - s.wide_mu : 0.0;
+      sq[0] = __builtin_fma(d, d, sq[0]);
+    }
+  }
+  row_sums<T, 1>(sq, lds.wide[1]);
+  s.wide_r = 1.0 / __dsqrt_rn(sq[0] / (double)K + (double)eps);
+  if (s.wide) s.r = (float)s.wide_r;
+  return s;
+}
+
+template <bool kCentred>
+__device__ __forceinline__ float hat(float v, const RowStats& s) {
+  if (s.wide) return (float)(((double)v - s.wide_mu) * s.wide_r);
+  if constexpr (kCentred) return __builtin_fmaf(v - s.mu, s.r, -s.shift);
+  return v * s.r;
+}
+
+// ---------------------------------------------------------------------------
+// Forward. One row per kT threads; rows of up to 2048 values take a wavefront
+// each, four to a workgroup.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  const void *x, *res, *gamma, *beta;
+  void *y, *h;
+  int64_t ldx, ldr;
+  int M, K;
+  float eps;
+  bool weights_bf16;
+};
+
+template <typename Shape>
+constexpr int kRowThreads = Shape::kT < 256 ? 256 : Shape::kT;  // of a workgroup
+
+template <typename Shape, typename X, typename Y, bool kCentred>
+__global__ __launch_bounds__(kRowThreads<Shape>) void norm_rows_kernel(NormArgs p) {
+  constexpr int T = Shape::kT, C = Shape::kC, kRows = kRowThreads<Shape> / T;
+  __shared__ RowLds<T> lds[kRows];
+  const int tid = threadIdx.x % T, sub = threadIdx.x / T;
+  const int64_t m = (int64_t)blockIdx.x * kRows + sub;
+  if (m >= p.M) return;  // (kRows > 1: rows are single wavefronts, which meet no barrier)
+  const int chunks = (p.K + 7) / 8;
+  auto at = [&](int i) { return 8 * (tid + T * i); };
+  auto present = [&](int i) { return min(max(p.K - at(i), 0), 8); };
+  const X* const x = (const X*)p.x + m * p.ldx;
+  Chunk<X> raw[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    raw[i] = tid + T * i < chunks ? load_chunk(x + at(i), present(i)) : zero_chunk(X{});
+  float v[C][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i) values(raw[i], v[i]);
+  if (p.res) {
+    const X* const res = (const X*)p.res + m * p.ldr;
+    X* const h = (X*)p.h + m * (int64_t)p.K;
+#pragma unroll
+    for (int i = 0; i < C; ++i) raw[i] = tid + T * i < chunks ? load_chunk(res + at(i), present(i)) : zero_chunk(X{});
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float r[8];
+      values(raw[i], r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] += r[e];
+      to_chunk(v[i], raw[i]);  // what is kept is what is normalized
+      values(raw[i], v[i]);
+      if (tid + T * i < chunks) store_chunk(h + at(i), raw[i], present(i));
+    }
+  }
+  const RowStats s = row_stats<Shape, kCentred, false>(v, present, p.K, p.eps, lds[sub]);
+  Y* const y = (Y*)p.y + m * (int64_t)p.K;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if (tid + T * i >= chunks) break;
+    const int have = present(i);
+    float g[8], b[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    load_weights(p.gamma, p.weights_bf16, at(i), have, g);
+    if (kCentred && p.beta) load_weights(p.beta, p.weights_bf16, at(i), have, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[e] *= hat<kCentred>(v[i][e], s);
+      if (kCentred && p.beta) g[e] += b[e];
+    }
+    Chunk<Y> out;
+    to_chunk(g, out);
+    store_chunk(y + at(i), out, have);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient. A workgroup of kBwdThreads takes rows in turn, kRows at once; a
+// thread's columns are the same in each, so the weights' gradients are sums in
+// its registers, joined at the end over the workgroup's rows in LDS and written
+// as one row of partial sums. A second kernel adds those in order: no atomics,
+// and the same bits every time.
+// ---------------------------------------------------------------------------
+constexpr int kBwdThreads = 512;
+
+struct NormBwdArgs {
+  const void *dy, *x, *gamma, *dres;
+  void* dx;
+  float* partial;  // [workgroups][centred ? 2 : 1][K]
+  int64_t ldy, ldx, ldr;
+  int M, K;
+  float eps;
+  bool weights_bf16;
+};
+
+template <typename Shape, typename X, typename D, bool kCentred>
+__global__ __launch_bounds__(kBwdThreads) void norm_rows_bwd_kernel(NormBwdArgs p) {
+  constexpr int T = Shape::kT, C = Shape::kC, kRows = kBwdThreads / T;
+  constexpr int kSums = kCentred ? 2 : 1;
+  constexpr int kJoin = kRows > 1 ? kSums * 8 * T * C : 1;  // one row's columns
+  struct Lds {
+    RowLds<T> row[kRows];
+    float two[kRows][T / 64][2];
+  };
+  __shared__ union {
+    Lds rows;
+    float join[kJoin];
+  } lds;
+  const int tid = threadIdx.x % T, sub = threadIdx.x / T;
+  const int chunks = (p.K + 7) / 8;
+  auto at = [&](int i) { return 8 * (tid + T * i); };
+  auto present = [&](int i) { return min(max(p.K - at(i), 0), 8); };
+  float dgamma[C][8], dbeta[kCentred ? C : 1][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dgamma[i][e] = 0.0f;
+      if constexpr (kCentred) dbeta[i][e] = 0.0f;
+    }
+  const float inv_k = 1.0f / (float)p.K;
+  // every thread of the workgroup makes the same number of rounds (barriers inside)
+  for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < p.M; m0 += (int64_t)gridDim.x * kRows) {
+    const int64_t m = m0 + sub;
+    const bool row = m < p.M;
+    Chunk<X> rx[C];
+    Chunk<D> rd[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const bool have = row && tid + T * i < chunks;
+      rx[i] = have ? load_chunk((const X*)p.x + m * p.ldx + at(i), present(i)) : zero_chunk(X{});
+      rd[i] = have ? load_chunk((const D*)p.dy + m * p.ldy + at(i), present(i)) : zero_chunk(D{});
+    }
+    float v[C][8];
+#pragma unroll
+    for (int i = 0; i < C; ++i) values(rx[i], v[i]);
+    const RowStats s = row_stats<Shape, kCentred, (T > 64 && kRows > 1)>(v, present, p.K, p.eps, lds.rows.row[sub]);
+    // v becomes hat
+    float sums[2] = {0.0f, 0.0f};  // of dg hat, of dg
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float d[8], g[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      const int have = present(i);
+      if (have) load_weights(p.gamma, p.weights_bf16, at(i), have, g);
+      values(rd[i], d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] = hat<kCentred>(v[i][e], s);
+        if (row && e < have) dgamma[i][e] = __builtin_fmaf(d[e], v[i][e], dgamma[i][e]);
+        if constexpr (kCentred) dbeta[i][e] += d[e];
+        const float dg = d[e] * g[e];
+        if (e < have) sums[0] = __builtin_fmaf(dg, v[i][e], sums[0]);
+        sums[1] += dg;
+      }
+    }
+    row_sums<T, 2>(sums, lds.rows.two[sub]);
+    const float c_hat = sums[0] * inv_k, c_one = kCentred ? sums[1] * inv_k : 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int have = present(i);
+      if (!row || !have) continue;
+      float d[8], g[8], o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      load_weights(p.gamma, p.weights_bf16, at(i), have, g);
+      values(rd[i], d);
+      if (p.dres) values(load_chunk((const X*)p.dres + m * p.ldr + at(i), have), o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = __builtin_fmaf(-v[i][e], c_hat, d[e] * g[e] - c_one);
+        o[e] = __builtin_fmaf(s.r, t, o[e]);
+      }
+      Chunk<X> out;
+      to_chunk(o, out);
+      store_chunk((X*)p.dx + m * (int64_t)p.K + at(i), out, have);
+    }
+    if constexpr (T > 64) __syncthreads();  // the slots are used again
+  }
+  // join the workgroup's rows, in order
+  if constexpr (kRows > 1) {
+    for (int r = 0; r < kRows; ++r) {
+      __syncthreads();
+      if (sub == r) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float* const to = lds.join + (i * 8 + e) * T + tid;
+            *to = r ? *to + dgamma[i][e] : dgamma[i][e];
+            if constexpr (kCentred) to[8 * T * C] = r ? to[8 * T * C] + dbeta[i][e] : dbeta[i][e];
+          }
+      }
+    }
+    if (sub != kRows - 1) return;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dgamma[i][e] = lds.join[(i * 8 + e) * T + tid];
+        if constexpr (kCentred) dbeta[i][e] = lds.join[8 * T * C + (i * 8 + e) * T + tid];
+      }
+  }
+  float* const part = p.partial + (int64_t)blockIdx.x * kSums * p.K;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int have = present(i);
+    if (!have) continue;
+    Chunk<float> c;
+    to_chunk(dgamma[i], c);
+    store_chunk(part + at(i), c, have);
+    if constexpr (kCentred) {
+      to_chunk(dbeta[i], c);
+      store_chunk(part + p.K + at(i), c, have);
+    }
+  }
+}
+
+// Sums of the partial rows: 64 columns and 16 runs of rows per workgroup.
+constexpr int kJoinCols = 64, kJoinRuns = 16;
+
+__global__ __launch_bounds__(kJoinCols* kJoinRuns) void join_partials_kernel(const float* __restrict__ partial, int rows,
+                                                                             int cols, int K, float* __restrict__ dgamma,
+                                                                             float* __restrict__ dbeta) {
+  __shared__ float runs[kJoinRuns][kJoinCols];
+  const int c = blockIdx.x * kJoinCols + threadIdx.x % kJoinCols, run = threadIdx.x / kJoinCols;
+  float s = 0.0f;
+  if (c < cols) {
+    for (int r = run; r < rows; r += kJoinRuns) s += partial[(int64_t)r * cols + c];
+  }
+  runs[run][threadIdx.x % kJoinCols] = s;
+  __syncthreads();
+  if (run || c >= cols) return;
+#pragma unroll
+  for (int r = 1; r < kJoinRuns; ++r) s += runs[r][threadIdx.x];
+  if (c < K) dgamma[c] = s;
+  else dbeta[c - K] = s;
+}
+
+// ---------------------------------------------------------------------------
+template <typename Shape, typename X, typename Y>
+static void launch_fwd(const NormArgs& a, bool centred, hipStream_t stream) {
+  constexpr int rows = kRowThreads<Shape> / Shape::kT;
+  const dim3 grid((unsigned)((a.M + rows - 1) / rows)), block(kRowThreads<Shape>);
+  if (centred) hipLaunchKernelGGL((norm_rows_kernel<Shape, X, Y, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((norm_rows_kernel<Shape, X, Y, false>), grid, block, 0, stream, a);
+}
+
+template <typename X, typename Y>
+static void launch_fwd_shape(const NormArgs& a, bool centred, hipStream_t stream) {
+  if (a.K <= RowShape<64, 1>::kMaxK) return launch_fwd<RowShape<64, 1>, X, Y>(a, centred, stream);
+  if (a.K <= RowShape<64, 2>::kMaxK) return launch_fwd<RowShape<64, 2>, X, Y>(a, centred, stream);
+  if (a.K <= RowShape<64, 4>::kMaxK) return launch_fwd<RowShape<64, 4>, X, Y>(a, centred, stream);
+  if (a.K <= RowShape<256, 2>::kMaxK) return launch_fwd<RowShape<256, 2>, X, Y>(a, centred, stream);
+  if (a.K <= RowShape<256, 4>::kMaxK) return launch_fwd<RowShape<256, 4>, X, Y>(a, centred, stream);
+  launch_fwd<RowShape<512, 4>, X, Y>(a, centred, stream);
+}
+
+hipError_t launch_norm_rows(const void* x, bool x_bf16, int64_t ldx, const void* res, int64_t ldr, const void* gamma,
+                            const void* beta, bool weights_bf16, float eps, bool centred, int64_t M, int64_t K, void* y,
+                            bool y_bf16, void* h, hipStream_t stream) {
+  const NormArgs a{x, res, gamma, beta, y, h, ldx, ldr, (int)M, (int)K, eps, weights_bf16};
+  if (x_bf16) {
+    if (y_bf16) launch_fwd_shape<bf16_t, bf16_t>(a, centred, stream);
+    else launch_fwd_shape<bf16_t, float>(a, centred, stream);
+  } else {
+    if (y_bf16) launch_fwd_shape<float, bf16_t>(a, centred, stream);
+    else launch_fwd_shape<float, float>(a, centred, stream);
+  }
+  return hipGetLastError();
+}
+
+// Workgroups of the gradient: one per CU, fewer for few rows. `threads`: of a row.
+static int bwd_threads(int64_t K) { return K <= 2048 ? 64 : K <= 8192 ? 256 : 512; }
+static int64_t bwd_workgroups(int64_t M, int64_t K) {
+  const int rows = kBwdThreads / bwd_threads(K);
+  const int64_t need = (M + rows - 1) / rows;
+  return need < 256 ? need : 256;
+}
+
+int64_t norm_bwd_workspace_bytes(int64_t M, int64_t K, bool centred) {
+  return bwd_workgroups(M, K) * (centred ? 2 : 1) * K * (int64_t)sizeof(float);
+}
+
+template <typename Shape, typename X, typename D>
+static void launch_bwd(const NormBwdArgs& a, bool centred, hipStream_t stream) {
+  const dim3 grid((unsigned)bwd_workgroups(a.M, a.K)), block(kBwdThreads);
+  if (centred) hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, X, D, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, X, D, false>), grid, block, 0, stream, a);
+}
+
+template <typename X, typename D>
+static void launch_bwd_shape(const NormBwdArgs& a, bool centred, hipStream_t stream) {
+  if (a.K <= RowShape<64, 1>::kMaxK) return launch_bwd<RowShape<64, 1>, X, D>(a, centred, stream);
+  if (a.K <= RowShape<64, 2>::kMaxK) return launch_bwd<RowShape<64, 2>, X, D>(a, centred, stream);
+  if (a.K <= RowShape<64, 4>::kMaxK) return launch_bwd<RowShape<64, 4>, X, D>(a, centred, stream);
+  if (a.K <= RowShape<256, 2>::kMaxK) return launch_bwd<RowShape<256, 2>, X, D>(a, centred, stream);
+  if (a.K <= RowShape<256, 4>::kMaxK) return launch_bwd<RowShape<256, 4>, X, D>(a, centred, stream);
+  launch_bwd<RowShape<512, 4>, X, D>(a, centred, stream);
+}
+
+hipError_t launch_norm_rows_bwd(const void* dy, bool dy_bf16, int64_t ldy, const void* x, bool x_bf16, int64_t ldx,
+                                const void* gamma, bool weights_bf16, const void* dres, int64_t ldr, float eps,
+                                bool centred, int64_t M, int64_t K, void* dx, float* dgamma, float* dbeta, void* ws,
+                                hipStream_t stream) {
+  const NormBwdArgs a{dy, x, gamma, dres, dx, (float*)ws, ldy, ldx, ldr, (int)M, (int)K, eps, weights_bf16};
+  if (M > 0) {
+    if (x_bf16) {
+      if (dy_bf16) launch_bwd_shape<bf16_t, bf16_t>(a, centred, stream);
+      else launch_bwd_shape<bf16_t, float>(a, centred, stream);
+    } else {
+      if (dy_bf16) launch_bwd_shape<float, bf16_t>(a, centred, stream);
+      else launch_bwd_shape<float, float>(a, centred, stream);
+    }
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  const int cols = (int)K * (centred ? 2 : 1);
+  hipLaunchKernelGGL(join_partials_kernel, dim3((unsigned)((cols + kJoinCols - 1) / kJoinCols)),
+                     dim3(kJoinCols * kJoinRuns), 0, stream, (const float*)ws, (int)bwd_workgroups(M, K), cols, (int)K,
+                     dgamma, dbeta);
+  return hipGetLastError();
+}
+
+}  // namespace fp8q

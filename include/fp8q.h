@@ -627,6 +627,104 @@ FP8Q_API int int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b
                                void* c, int out_dtype, const int32_t* m_offsets, int64_t G,
                                int64_t M_total, int64_t N, int64_t K, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A training step around the products: normalization of rows that stay in 16 or
+ * 32 bits and its gradient (also that of fp8q_norm_quant_act_1x128, whose codes
+ * are taken as the values they stand for), and the gated activation between an
+ * MLP's two products with its gradient. "Six Reasons Deepseek Ai Is A Waste Of
+ * Time" keeps normalization in BF16 or FP32 while the products run in FP8.
+ *
+ * Element types are named by fp8q_out_dtype. Rows of inputs may lie apart (ld*:
+ * elements from one row to the next, at least the row's length); outputs are
+ * dense. Data pointers need their element's alignment only, and rows may have any
+ * length. Everything is deterministic (no floating-point atomics) and allocates
+ * nothing. No output or workspace may overlap an input or another output, and
+ * calls that may run at the same time need workspaces of their own.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Normalization, with the residual sum before it:
+ *   h = x + residual, rounded to x's type, or x where residual is NULL;
+ *   centred 1: mu = sum_k h / K, var = sum_k (h - mu)^2 / K;  centred 0: mu = 0;
+ *   y = (h - mu) / sqrt(var + eps) * gamma + beta, rounded once to y's type.
+ * Binary32 arithmetic; statistics that leave its range are formed in float64. A
+ * row that holds an infinity or NaN gives NaN there; other rows do not notice. With
+ * eps == 0 a row of zeros (centred: of equal values) gives NaN.
+ *
+ *   x, residual : in,  M x K of x_dtype (rows ldx, ldr apart); residual may be NULL
+ *   gamma, beta : in,  K of weights_dtype; beta NULL for none, and only with centred 1
+ *   y           : out, M x K of y_dtype
+ *   h           : out, M x K of x_dtype; NULL exactly where residual is
+ * 0 <= K <= 16384. M == 0 or K == 0 is a no-op. One kernel.
+ */
+FP8Q_API int fp8q_norm(const void* x, int x_dtype, int64_t ldx, const void* residual, int64_t ldr,
+                       const void* gamma, const void* beta, int weights_dtype, float eps,
+                       int centred, int64_t M, int64_t K, void* y, int y_dtype, void* h,
+                       void* stream);
+
+/*
+ * Gradient of the normalization of x (fp8q_norm's h where it had a residual),
+ * whose statistics are formed again from x:
+ *   hat = (x - mu) / sqrt(var + eps),  dg = dy * gamma,
+ *   dx = (dg - [centred: sum_k dg / K] - hat * sum_k(dg * hat) / K) / sqrt(var + eps) + dres,
+ *   dgamma[k] = sum_m dy * hat,  dbeta[k] = sum_m dy.
+ * Sums in binary32, over rows in a fixed order; dx is rounded once to x's type.
+ *
+ *   dy    : in,  M x K of dy_dtype;  x, dres : in, M x K of x_dtype (rows ldy, ldx, ldr
+ *           apart); dres may be NULL (the gradient that passes the norm by: of the
+ *           residual stream)
+ *   gamma : in,  K of weights_dtype
+ *   dx    : out, M x K of x_dtype
+ *   dgamma, dbeta : out, K float32, every element written; dbeta NULL exactly
+ *           where centred is 0
+ *   workspace : at least fp8q_norm_bwd_workspace_bytes(M, K, centred), 16-byte aligned
+ * 0 <= K <= 16384. K == 0 is a no-op; M == 0 writes zeros to dgamma and dbeta. Two kernels.
+ */
+FP8Q_API int64_t fp8q_norm_bwd_workspace_bytes(int64_t M, int64_t K, int centred);
+FP8Q_API int fp8q_norm_bwd(const void* dy, int dy_dtype, int64_t ldy, const void* x, int x_dtype,
+                           int64_t ldx, const void* gamma, int weights_dtype, const void* dres,
+                           int64_t ldr, float eps, int centred, int64_t M, int64_t K, void* dx,
+                           float* dgamma, float* dbeta, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+
+/*
+ * Gated activation: of a row gu = [gate | up] of 2 I values
+ *   y = gate / (1 + exp(-gate)) * up
+ * in binary32 (exp to about two units in the last place; sigmoids below 2^-126
+ * count as 0), rounded once to y's type. A gate of -infinity gives 0.
+ *
+ *   gu : in,  M x 2I of gu_dtype, rows ld apart
+ *   m_offsets : in, DEVICE int32[G + 1], or NULL for all M rows: rows from
+ *        m_offsets[G] (clamped to [0, M]) on are neither read nor written, as in
+ *        the grouped GEMMs; G >= 1 (ignored for NULL)
+ *   y  : out, M x I of y_dtype
+ * M == 0 or I == 0 is a no-op. One kernel.
+ */
+FP8Q_API int fp8q_swiglu(const void* gu, int gu_dtype, int64_t ld, const int32_t* m_offsets,
+                         int64_t G, int64_t M, int64_t I, void* y, int y_dtype, void* stream);
+
+/*
+ * The same, its binary32 result quantized per 1x128 tile with the activation rule
+ * of fp8q_quant_act_1x128 instead of being stored:
+ *   q : out, M x I E4M3 bytes, 16-byte aligned;  sa : out, M x (I/128) float32
+ * Requires I % 128 == 0.
+ */
+FP8Q_API int fp8q_swiglu_quant_act_1x128(const void* gu, int gu_dtype, int64_t ld,
+                                         const int32_t* m_offsets, int64_t G, int64_t M, int64_t I,
+                                         uint8_t* q, float* sa, void* stream);
+
+/*
+ * Gradient of the gated activation: with s = 1 / (1 + exp(-gate))
+ *   dgu = [dy * up * s * (1 + gate * (1 - s)) | dy * gate * s], rounded once.
+ *   dy  : in,  M x I of dy_dtype, rows ldy apart;  gu, m_offsets: as above
+ *   dgu : out, M x 2I of gu_dtype
+ */
+FP8Q_API int fp8q_swiglu_bwd(const void* dy, int dy_dtype, int64_t ldy, const void* gu,
+                             int gu_dtype, int64_t ld, const int32_t* m_offsets, int64_t G,
+                             int64_t M, int64_t I, void* dgu, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,7 @@ Modules:
   route    MoE router (scores, groups, top-k, weights) and its gradient.
   tokens   rows sorted by expert, the weighted way back and its gradient.
   int8     8-bit row quantization and the 8-bit integer product.
+  step     normalization and gated activation with gradients, orthogonalized updates.
 """
 
 from . import e4m3, bf16, quant, gemm, accsim  # noqa: F401
