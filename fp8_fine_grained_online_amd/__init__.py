@@ -40,6 +40,7 @@ A training step around the products, with gradients:
   fp8q_swiglu(gu, out_dtype)                             -> y   gated activation
   fp8q_swiglu_quant_act_1x128(gu)                        -> (q, sa)   the same, straight to FP8 tiles
   fp8q_swiglu_bwd(dy, gu)                                -> dgu
+  fp8q_orthogonalize(g, steps, coeffs, scale, out_dtype) -> out   a weight's update by Newton-Schulz products
 """
 
 from ._lib import (  # noqa: F401
@@ -69,6 +70,7 @@ from ._lib import (  # noqa: F401
     fp8q_moe_route_bwd,
     fp8q_norm,
     fp8q_norm_bwd,
+    fp8q_orthogonalize,
     fp8q_quant_int8_rows,
     fp8q_swiglu,
     fp8q_swiglu_bwd,
@@ -89,4 +91,5 @@ __all__ = [
     "fp8q_moe_route", "fp8q_moe_route_bwd", "fp8q_moe_permute", "fp8q_moe_combine", "fp8q_moe_combine_bwd",
     "fp8q_quant_int8_rows", "int8_gemm_scaled", "int8_gemm_grouped",
     "fp8q_norm", "fp8q_norm_bwd", "fp8q_swiglu", "fp8q_swiglu_quant_act_1x128", "fp8q_swiglu_bwd",
+    "fp8q_orthogonalize",
 ]

@@ -19,7 +19,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libfp8q.so")
 
 SOURCES = ["quant.hip", "retile.hip", "norm.hip", "moe.hip", "gemm.hip", "gemm_qa.hip", "route.hip",
-           "tokens.hip", "int8.hip", "norm_rows.hip", "swiglu.hip", "api.cpp"]
+           "tokens.hip", "int8.hip", "norm_rows.hip", "swiglu.hip",
+           "ortho.hip", "api.cpp"]
 HEADERS = ["common.hpp", "tiles.hpp", "wave.hpp", "rows.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

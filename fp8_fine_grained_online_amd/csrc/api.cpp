@@ -2,6 +2,7 @@
 // Every check runs before the first HIP call, so a rejected call touches no
 // device state and can be exercised without a GPU.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -90,6 +91,10 @@ hipError_t launch_swiglu_quant(const void* gu, bool gu_bf16, int64_t ld, const i
 hipError_t launch_swiglu_bwd(const void* dy, bool dy_bf16, int64_t ldy, const void* gu, bool gu_bf16,
                              int64_t ld, const int32_t* last, int64_t M, int64_t I, void* dgu,
                              hipStream_t stream);
+int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool bf16);
+hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M, int64_t N, int steps,
+                                float a, float b, float c, float scale, void* out, bool out_bf16,
+                                void* ws, hipStream_t stream);
 }  // namespace fp8q
 
 namespace {
@@ -197,6 +202,46 @@ int check_swiglu(int gu_dtype, int64_t ld, const int32_t* m_offsets, int64_t G, 
   if (ld < 2 * I) return FP8Q_ERR_SHAPE;
   if (!aligned(m_offsets, 4)) return FP8Q_ERR_ALIGN;
   return FP8Q_OK;
+}
+
+// Sizes of the orthogonalization.
+int check_ortho(int64_t L, int64_t M, int64_t N) {
+  if (L < 0 || M < 0 || N < 0) return FP8Q_ERR_SHAPE;
+  if (L > 65535 || M > 65536 || N > 65536) return FP8Q_ERR_TOO_LARGE;
+  // one workgroup of 256 threads per 64 x 64 values, padded
+  if (!launchable(L * ((M + 63) / 64) * ((N + 63) / 64), 256)) return FP8Q_ERR_TOO_LARGE;
+  if (L == 0 || M == 0 || N == 0) return -1;  // valid no-op
+  return FP8Q_OK;
+}
+
+// Whether s <- a s + b s^3 + c s^5 keeps [0, 1] below 3, and b s^2 + c s^4 within 7.5,
+// for `steps` steps: the FP16 planes' scales count on it. The largest |p| over
+// [0, top] is at the end or where p' = a + 3 b s^2 + 5 c s^4 is zero, the other's at the
+// end or at s^2 = -b / 2c.
+bool bounded(int steps, double a, double b, double c) {
+  if (!isfinite(a) || !isfinite(b) || !isfinite(c)) return false;
+  auto p = [&](double s) { return fabs(s * (a + s * s * (b + s * s * c))); };
+  auto q = [&](double t) { return fabs(t * (b + t * c)); };
+  double top = 1.0;
+  for (int k = 0; k < steps; ++k) {
+    const double t1 = top * top;
+    double most = p(top), inner = q(t1);
+    if (c != 0.0) {
+      if (const double t = -b / (2 * c); t > 0 && t < t1) inner = fmax(inner, q(t));
+      const double disc = 9 * b * b - 20 * a * c;
+      if (disc >= 0) {
+        for (double sign : {-1.0, 1.0}) {
+          const double t = (-3 * b + sign * sqrt(disc)) / (10 * c);
+          if (t > 0 && t < t1) most = fmax(most, p(sqrt(t)));
+        }
+      }
+    } else if (b != 0.0) {
+      if (const double t = -a / (3 * b); t > 0 && t < t1) most = fmax(most, p(sqrt(t)));
+    }
+    if (inner > 7.5 || most > 3.0) return false;
+    top = most;
+  }
+  return true;
 }
 
 // worst-case m_offsets[G] of the MoE dispatch (every expert padded by 127
@@ -687,6 +732,30 @@ int fp8q_swiglu_bwd(const void* dy, int dy_dtype, int64_t ldy, const void* gu, i
   return launched(fp8q::launch_swiglu_bwd(dy, dy_dtype == FP8Q_OUT_BF16, ldy, gu, gu_dtype == FP8Q_OUT_BF16,
                                           ld, m_offsets ? m_offsets + G : nullptr, M, I, dgu,
                                           (hipStream_t)stream));
+}
+
+int64_t fp8q_orthogonalize_workspace_bytes(int64_t L, int64_t M, int64_t N, int out_dtype) {
+  const int s = check_ortho(L, M, N);
+  if (!known_dtype(out_dtype) || s > 0) return -1;
+  return s ? 0 : fp8q::ortho_workspace_bytes(L, M, N, out_dtype == FP8Q_OUT_BF16);
+}
+
+int fp8q_orthogonalize(const void* g, int g_dtype, int64_t L, int64_t M, int64_t N, int steps, float a,
+                       float b, float c, float scale, void* out, int out_dtype, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  if (!known_dtype(g_dtype) || !known_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
+  if (steps < 1 || steps > 100 || !isfinite(scale) || !bounded(steps, a, b, c)) return FP8Q_ERR_SHAPE;
+  int s = check_ortho(L, M, N);
+  if (s == -1) return FP8Q_OK;
+  if (s) return s;
+  if (!g || !out || !workspace) return FP8Q_ERR_NULL;
+  const bool bf16 = out_dtype == FP8Q_OUT_BF16;
+  if (workspace_bytes < fp8q::ortho_workspace_bytes(L, M, N, bf16)) return FP8Q_ERR_SHAPE;
+  if (!aligned(g, element(g_dtype)) || !aligned(out, element(out_dtype)) || !aligned(workspace, 16))
+    return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_orthogonalize(g, g_dtype == FP8Q_OUT_BF16, L, M, N, steps, a, b, c, scale,
+                                             out, bf16, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

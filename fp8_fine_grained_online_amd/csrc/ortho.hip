@@ -1,0 +1,583 @@
+// Newton-Schulz orthogonalization of weight gradients' updates, for gfx950.
+//
+//   X_0 = G / |G| (Frobenius),  A = X X^T,  B = b A + c A^2,  X <- a X + B X
+//
+// run `steps` times over m x n matrices, m <= n (a tall G is transposed on the way
+// in and out), as three matrix products a step on the FP16 matrix cores:
+//
+//   gram    A = X X^T         symmetric: tiles on and below the diagonal only
+//   square  B = b A + c A A   symmetric, and A A = A A^T
+//   update  X = a X + B X     the columns of X are the rows of X^T, kept beside it
+//
+// so that every operand is read along its rows. The products' epilogues do the
+// rest: a tile goes out in both orientations where both are read next.
+//
+// Numbers. X, A and B are kept as FP16 times a power of two that puts their
+// entries in FP16's normal range (the singular values of X stay below 3, checked
+// on the host). X is the sum of two such numbers, high and low: 22 bits, and the
+// term a X loses nothing that matters. For a float32 result (kSplit) so are A and
+// B, and a product is high high + high low + low high in one binary32 accumulator:
+// the result is as near the definition as one formed in binary32 (2e-6 to 4e-5,
+// growing with the spread of the singular values). For a bfloat16 result, whose own rounding is 1.7e-3, one product of the
+// high parts is enough (1e-4 to 1e-3), with two precautions against errors that do
+// not average out over an inner product, those of the diagonal:
+//
+//  * what FP16 cuts off the diagonals of A and B is kept in binary32 vectors and
+//    put back in the next epilogue (D A + A D in the square, D X in the update);
+//  * in the last two steps, where all singular values are near 1 and b A + c A A
+//    would cancel most of a, A is taken about its mean eigenvalue alpha = |X|^2 / m:
+//    with A = alpha I + A',  B' = (b + 2 c alpha) A' + c A' A'  and
+//    X <- (a + b alpha + c alpha^2) X + B' X. Exact for any alpha. (In earlier steps
+//    most eigenvalues are near 0, not near their mean, and the rounding of X in B' X
+//    would cost more than it saves.)
+//
+// Zero rows and columns pad m and n to multiples of 64; they stay zero.
+#include <type_traits>
+
+#include "common.hpp"
+#include "rows.hpp"
+#include "tiles.hpp"
+#include "wave.hpp"
+
+namespace fp8q {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f;  // X, and A and B, as they are stored
+constexpr int kPad = 64;                               // rows and columns are padded to
+constexpr int kOrthoStep = 128;                        // bytes of K per pipeline step: 64 values
+constexpr int kNormParts = 64;                         // partial sums of |G|^2 per matrix
+
+enum class Product { kGram, kSquare, kUpdate };
+
+struct OrthoArgs {
+  // planes of all matrices, one after the other; *_lo: low parts (of A, B and X^T for kSplit only)
+  _Float16 *x, *x_lo;          // m x n
+  const _Float16 *xt, *xt_lo;  // n x m, as read
+  _Float16 *xt_new, *xt_lo_new;
+  _Float16 *am, *am_lo, *bm, *bm_lo;  // m x m
+  float *da, *db;                     // what FP16 cut off their diagonals, m
+  float* alpha;                       // one per matrix
+  float* squares;                     // sums of X^2, parts per matrix; written by the update, read by the gram
+  void* out;                          // the result, from the last step
+  int m, n, m_true, n_true;           // padded and true sizes
+  int parts;
+  int count;    // tiles per matrix
+  float a, b, c, scale;
+  int pivot;    // this step takes A about its mean eigenvalue
+  int tall;     // the result is transposed
+};
+
+template <int BM, int BN, int D, bool kSplit>
+struct OrthoTile {
+  static constexpr int kWM = BM / 2, kWN = BN / 2;
+  static constexpr int kSlabA = BM * kOrthoStep, kSlabB = BN * kOrthoStep;
+  static constexpr int kRing = (D + 1) * kSlabA + D * kSlabB;
+  // a wave's staging of its part on the way out: 16 rows, and all of it transposed
+  static constexpr int kPitchR = kWN * 2 + 16, kPitchC = kWM * 2 + 16;
+  static constexpr int kStageR = 16 * kPitchR, kStageC = kWN * kPitchC;
+  static constexpr int kStage = 4 * (kStageR + (kSplit ? 2 : 1) * kStageC);
+  static constexpr int kLds = kRing > kStage ? kRing : kStage;
+  static constexpr int kLoadsA = BM * 8 / 256, kLoadsB = BN * 8 / 256;
+  static_assert(kWM % 16 == 0 && kWN % 16 == 0, "whole MFMA blocks");
+  static_assert(BM * 8 % 256 == 0 && BN * 8 % 256 == 0, "whole copies");
+  static_assert(kLds <= 160 * 1024 && D >= 2, "LDS");
+  static_assert((D - 1) * (kLoadsA + kLoadsB) <= 63, "the wait counter holds the copies in flight");
+};
+
+constexpr int ortho_wait_vm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int kOrthoWaitLds = 0xC07F;
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+
+enum class Result { kPlanes, kBf16, kF32 };
+
+// ---------------------------------------------------------------------------
+// One tile of one product. Four wavefronts, each a quarter of the tile; per step
+// of 64 values of K the slabs of both operands go straight from global memory to
+// LDS (16-byte chunk c of row r at position c ^ (r % 8)), and each step is
+// multiplied in two halves, the one's operands read from LDS while the other
+// multiplies; A's slabs rotate through D + 1 buffers, B's through D. Lane l
+// supplies row l % 16 of a 16-row block and 8 values of K at 8 (l / 16); B is the
+// first operand, so a lane holds C[l % 16][4 (l / 16) + r].
+// ---------------------------------------------------------------------------
+template <Product kWhat, Result kOut, bool kSplit, int BM, int BN, int D>
+__global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
+  using Cfg = OrthoTile<BM, BN, D, kSplit>;
+  constexpr int WM = Cfg::kWM, WN = Cfg::kWN, SUBM = WM / 16, SUBN = WN / 16, kMfmas = SUBM * SUBN;
+  constexpr bool kSymmetric = kWhat != Product::kUpdate;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Cfg::kLds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int lr = lane & 15, lk = lane >> 4;
+
+  // tiles of all matrices in one run, shared out to the XCDs
+  const int task = xcd_tile(blockIdx.x, gridDim.x);
+  const int64_t mat = task / p.count;
+  const int t = task % p.count;
+  int tm, tn;
+  if constexpr (kSymmetric) {
+    static_assert(!kSymmetric || BM == BN, "square tiles");
+    // t-th of the tiles on and below the diagonal, row by row
+    tm = (int)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (tm * (tm + 1) / 2 > t) --tm;
+    while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
+    tn = t - tm * (tm + 1) / 2;
+  } else {
+    band_tile(t, (p.m + BM - 1) / BM, (p.n + BN - 1) / BN, tm, tn);
+  }
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int64_t mm = mat * p.m * p.m, mn = mat * (int64_t)p.m * p.n;
+
+  // operands: rows m0.. of one, rows n0.. of the other, K values each
+  const _Float16 *a_hi, *a_lo, *b_hi, *b_lo;
+  int K, rows_total;
+  if constexpr (kWhat == Product::kGram) a_hi = b_hi = p.x + mn, a_lo = b_lo = p.x_lo + mn, K = p.n, rows_total = p.m;
+  if constexpr (kWhat == Product::kSquare) a_hi = b_hi = p.am + mm, a_lo = b_lo = p.am_lo + mm, K = p.m, rows_total = p.m;
+  if constexpr (kWhat == Product::kUpdate)
+    a_hi = p.bm + mm, a_lo = p.bm_lo + mm, b_hi = p.xt + mn, b_lo = p.xt_lo + mn, K = p.m, rows_total = p.n;
+  const int pitch = K * 2;  // bytes
+  const uint32_t bytes_a = (uint32_t)min(BM, p.m - m0) * (uint32_t)pitch;
+  const uint32_t bytes_b = (uint32_t)min(BN, rows_total - n0) * (uint32_t)pitch;
+  const int64_t at_a = (int64_t)m0 * K, at_b = (int64_t)n0 * K;
+  const int ksteps = pitch / kOrthoStep;
+  const int steps = kSplit ? 3 * ksteps : ksteps;
+  auto rsrc_a = [&](int seg) { return make_rsrc((kSplit && seg == 2 ? a_lo : a_hi) + at_a, bytes_a); };
+  auto rsrc_b = [&](int seg) { return make_rsrc((kSplit && seg == 1 ? b_lo : b_hi) + at_b, bytes_b); };
+
+  // copy q of thread tid brings row q * 32 + tid / 8, stored chunk tid % 8
+  const int row0 = tid >> 3, lc0 = (tid & 7) ^ (row0 & 7);
+  constexpr int kRows = Cfg::kLoadsA > Cfg::kLoadsB ? Cfg::kLoadsA : Cfg::kLoadsB;
+  uint32_t off[kRows];
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) off[q] = (uint32_t)(row0 + q * 32) * (uint32_t)pitch + lc0 * 16;
+  auto copy_a = [&](int q, __amdgpu_buffer_rsrc_t r, int k, uint8_t* __restrict__ to) {
+    load_lds(r, to + (q * 256 + wave * 64) * 16, 16, off[q], k);
+  };
+  auto copy_b = copy_a;
+
+  v4f acc[SUBM][SUBN];
+#pragma unroll
+  for (int i = 0; i < SUBM; ++i)
+#pragma unroll
+    for (int j = 0; j < SUBN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  f16x8 ra[2][SUBM], rb[2][SUBN];
+  const int a_off[2] = {(wm * WM + lr) * kOrthoStep + ((lk ^ (lr & 7)) << 4),
+                        (wm * WM + lr) * kOrthoStep + (((4 + lk) ^ (lr & 7)) << 4)};
+  const int b_off[2] = {a_off[0] + (wn * WN - wm * WM) * kOrthoStep, a_off[1] + (wn * WN - wm * WM) * kOrthoStep};
+  auto read_operand = [&](int u, int h, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ sb) {
+    if (u < SUBN) rb[h][u] = *(const f16x8*)(sb + b_off[h] + u * 16 * kOrthoStep);
+    else ra[h][u - SUBN] = *(const f16x8*)(sa + a_off[h] + (u - SUBN) * 16 * kOrthoStep);
+  };
+  constexpr int kEvery = kMfmas >= 2 * (SUBM + SUBN) ? 2 : 1;
+  auto half = [&](int h, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ sb, __amdgpu_buffer_rsrc_t r, int k,
+                  uint8_t* __restrict__ to, bool copy_is_a) {
+#pragma unroll
+    for (int u = 0; u < kMfmas; ++u) {
+      const int i = u / SUBN, j = u % SUBN;
+      if (u % kEvery == 0 && u / kEvery < SUBM + SUBN) read_operand(u / kEvery, 1 - h, sa, sb);
+      if (u % kEvery == kEvery - 1) {
+        const int q = u / kEvery;
+        if (copy_is_a) { if (q < Cfg::kLoadsA) copy_a(q, r, k, to); }
+        else { if (q < Cfg::kLoadsB) copy_b(q, r, k, to); }
+      }
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(rb[h][j], ra[h][i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  static_assert(kMfmas / kEvery >= SUBM + SUBN && kMfmas / kEvery >= kRows, "reads and copies fit between the MFMAs");
+
+  // step g: byte of K and, for kSplit, which parts are multiplied
+  auto seg_of = [&](int g) { return !kSplit || g < ksteps ? 0 : g < 2 * ksteps ? 1 : 2; };
+  auto k_of = [&](int g) { return (g - seg_of(g) * ksteps) * kOrthoStep; };
+  uint8_t* const lds_b = lds + (D + 1) * Cfg::kSlabA;
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    const int g = min(d, steps - 1);
+#pragma unroll
+    for (int q = 0; q < Cfg::kLoadsA; ++q) copy_a(q, rsrc_a(seg_of(g)), k_of(g), lds + d * Cfg::kSlabA);
+#pragma unroll
+    for (int q = 0; q < Cfg::kLoadsB; ++q) copy_b(q, rsrc_b(seg_of(g)), k_of(g), lds_b + d * Cfg::kSlabB);
+  }
+  __builtin_amdgcn_s_waitcnt(ortho_wait_vm((D - 1) * (Cfg::kLoadsA + Cfg::kLoadsB)));
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int u = 0; u < SUBM + SUBN; ++u) read_operand(u, 0, lds, lds_b);
+  int a0 = 0, a1 = Cfg::kSlabA, a2 = D * Cfg::kSlabA;
+  int b0 = 0, b1 = Cfg::kSlabB;
+  for (int g = 0; g < steps; ++g) {
+    const int gn = min(g + D, steps - 1);  // past the end the last step is copied again, unread
+    const int seg = seg_of(gn), kn = k_of(gn);
+    half(0, lds + a0, lds_b + b0, rsrc_a(seg), kn, lds + a2, true);
+    // this wave has read all of step g, and its copies of step g + 1 have landed
+    __builtin_amdgcn_s_waitcnt(kOrthoWaitLds);
+    __builtin_amdgcn_s_waitcnt(ortho_wait_vm((D - 1) * Cfg::kLoadsA + (D - 2) * Cfg::kLoadsB));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    half(1, lds + a1, lds_b + b1, rsrc_b(seg), kn, lds_b + b0, false);
+    a2 = a0, a0 = a1, b0 = b1;
+    a1 = a1 == D * Cfg::kSlabA ? 0 : a1 + Cfg::kSlabA;
+    b1 = b1 == (D - 1) * Cfg::kSlabB ? 0 : b1 + Cfg::kSlabB;
+  }
+  // the last copies may still be writing the LDS that is used again below
+  __builtin_amdgcn_s_waitcnt(ortho_wait_vm(0));
+  __syncthreads();
+
+  // ---- the tile's values ----
+  const int mw = m0 + wm * WM, nw = n0 + wn * WN;  // this wave's part
+  const bool on_diagonal = kSymmetric && tm == tn;
+  float alpha = 0.0f;
+  if (kWhat == Product::kGram && p.pivot && on_diagonal) {
+    float s = 0.0f;
+    float* const sums = (float*)lds;
+    for (int i = tid; i < p.parts; i += 256) s += p.squares[mat * p.parts + i];
+    s = wave_sum_f32(s);
+    if (lane == 0) sums[wave] = s;
+    __syncthreads();
+    alpha = ((sums[0] + sums[1]) + (sums[2] + sums[3])) / (float)p.m_true;
+    if (t == 0 && tid == 0) p.alpha[mat] = alpha;
+    __syncthreads();
+  }
+  if (kWhat != Product::kGram && p.pivot) alpha = p.alpha[mat];
+
+  // four values of a row of a plane, as binary32
+  auto four = [&](const _Float16* from, float (&v)[4]) {
+    const f16x4 h = *(const f16x4*)from;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = (float)h[r];
+  };
+  constexpr int kPitchR = Cfg::kPitchR, kPitchC = Cfg::kPitchC;
+  uint8_t* const st_r = lds + wave * (Cfg::kStage / 4);
+  uint8_t* const st_c = st_r + Cfg::kStageR;
+  uint8_t* const st_c_lo = st_c + Cfg::kStageC;  // kSplit
+  // `kR` rows of `kC` 16-bit values from the wave's LDS to `to` (ld apart), up to the ends of its rows and columns
+  auto flush = [&](auto r_c, auto c_c, const uint8_t* st, int pitch_st, uint16_t* to, int64_t ld, int row, int col, int row_end,
+                   int col_end) {
+    constexpr int kR = decltype(r_c)::value, kCh = decltype(c_c)::value / 8;
+    static_assert(kR * kCh % 64 == 0, "whole wave stores");
+    __builtin_amdgcn_s_waitcnt(kOrthoWaitLds);  // a wave reads back only its own part
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+    for (int k = 0; k < kR * kCh / 64; ++k) {
+      const int r = (k * 64 + lane) / kCh, ch = (k * 64 + lane) % kCh;
+      const u32x4 v = *(const u32x4*)(st + r * pitch_st + ch * 16);
+      if (row + r < row_end && col + ch * 8 < col_end)
+        store_chunk((bf16_t*)to + (row + r) * ld + col + ch * 8, {v}, col_end - col - ch * 8);
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  using std::integral_constant;
+  constexpr integral_constant<int, 16> k16{};
+  constexpr integral_constant<int, WM> kWMc{};
+  constexpr integral_constant<int, WN> kWNc{};
+  auto put_row = [&](int j, uint32_t p0, uint32_t p1) {  // block j's four values of this lane's row
+    *(uint2*)(st_r + lr * kPitchR + (j * 16 + 4 * lk) * 2) = make_uint2(p0, p1);
+  };
+  // transposed: neighbouring lanes hold neighbouring rows; the even one writes the first two columns of both, the odd one the others
+  auto put_col = [&](uint8_t* st, int i, int j, uint32_t p0, uint32_t p1) {
+    const bool odd = lr & 1;
+    const uint32_t own = odd ? p1 : p0, got = dpp_u32<0xB1>(odd ? p0 : p1);
+    const uint32_t first = odd ? got : own, second = odd ? own : got;
+    uint8_t* const to = st + (j * 16 + 4 * lk + (odd ? 2 : 0)) * kPitchC + (i * 16 + (lr & ~1)) * 2;
+    *(uint32_t*)to = (first & 0xFFFFu) | (second << 16);
+    *(uint32_t*)(to + kPitchC) = (first >> 16) | (second & 0xFFFF0000u);
+  };
+
+  // where rows of the tile go, and columns
+  uint16_t *to_r = nullptr, *to_r_lo = nullptr, *to_c = nullptr, *to_c_lo = nullptr;
+  int64_t ld_r = 0, ld_c = 0;
+  int end_m = p.m, end_n = rows_total;
+  if constexpr (kSymmetric) {
+    to_r = (uint16_t*)((kWhat == Product::kGram ? p.am : p.bm) + mm);
+    to_r_lo = (uint16_t*)((kWhat == Product::kGram ? p.am_lo : p.bm_lo) + mm);
+    if (!on_diagonal) to_c = to_r, to_c_lo = to_r_lo;
+    ld_r = ld_c = p.m;
+  } else if constexpr (kOut == Result::kPlanes) {
+    to_r = (uint16_t*)(p.x + mn), to_r_lo = (uint16_t*)(p.x_lo + mn);
+    to_c = (uint16_t*)(p.xt_new + mn), to_c_lo = (uint16_t*)(p.xt_lo_new + mn);
+    ld_r = p.n, ld_c = p.m;
+  } else {
+    end_m = p.m_true, end_n = p.n_true;
+    if constexpr (kOut == Result::kBf16) (p.tall ? to_c : to_r) = (uint16_t*)p.out + mat * (int64_t)p.m_true * p.n_true;
+    ld_r = p.n_true, ld_c = p.m_true;
+  }
+  constexpr bool kLowRows = kSplit || kWhat == Product::kUpdate;  // low parts are kept of X always
+  float* const cut = (kWhat == Product::kGram ? p.da : p.db) + mat * p.m;
+
+  float square = 0.0f;
+#pragma unroll
+  for (int i = 0; i < SUBM; ++i) {
+    const int gm = mw + i * 16 + lr;
+    float cut_m = 0.0f;  // of the diagonal, row gm
+    if (!kSplit && gm < p.m) {
+      if constexpr (kWhat == Product::kSquare) cut_m = p.da[mat * p.m + gm];
+      if constexpr (kWhat == Product::kUpdate) cut_m = p.db[mat * p.m + gm];
+    }
+    float val[SUBN][4];
+#pragma unroll
+    for (int j = 0; j < SUBN; ++j) {
+      const int gn = nw + j * 16 + 4 * lk;
+      const bool inside = gm < p.m && gn < rows_total;
+      if constexpr (kWhat == Product::kGram) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          val[j][r] = acc[i][j][r] * (kScaleA / (kScaleX * kScaleX));
+          if (on_diagonal && gm == gn + r) val[j][r] -= kScaleA * alpha;
+        }
+      } else if constexpr (kWhat == Product::kSquare) {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lo[4] = {0.0f, 0.0f, 0.0f, 0.0f}, cut_n[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (inside) {
+          four(p.am + mm + (int64_t)gm * p.m + gn, v);
+          if constexpr (kSplit) {
+            four(p.am_lo + mm + (int64_t)gm * p.m + gn, lo);
+          } else {
+            const v4f d = *(const v4f*)(p.da + mat * p.m + gn);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) cut_n[r] = d[r];
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float whole = v[r] + (kSplit ? lo[r] : gm == gn + r ? cut_m : 0.0f);
+          const float sq = __builtin_fmaf(cut_m + cut_n[r], v[r], acc[i][j][r]) * (1.0f / kScaleA);
+          val[j][r] = __builtin_fmaf(p.c, sq, (p.b + 2.0f * p.c * alpha) * whole);
+        }
+      } else {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lo[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (inside) {
+          four(p.x + mn + (int64_t)gm * p.n + gn, v);
+          four(p.x_lo + mn + (int64_t)gm * p.n + gn, lo);
+        }
+        const float q = p.a + alpha * (p.b + alpha * p.c) + cut_m * (1.0f / kScaleA);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          val[j][r] = __builtin_fmaf(q, v[r] + lo[r], acc[i][j][r] * (1.0f / kScaleA));
+          square = __builtin_fmaf(val[j][r], val[j][r], square);
+        }
+      }
+    }
+    if constexpr (!kSplit && kSymmetric) {
+      if (on_diagonal && wm == wn && i < SUBN) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (4 * lk + r == lr && gm < p.m) cut[gm] = val[i][r] - (float)(_Float16)val[i][r];
+      }
+    }
+    if constexpr (kOut == Result::kF32) {
+      float* const to = (float*)p.out + mat * (int64_t)p.m_true * p.n_true;
+#pragma unroll
+      for (int j = 0; j < SUBN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int gn = nw + j * 16 + 4 * lk + r;
+          if (gm < end_m && gn < end_n)
+            to[p.tall ? (int64_t)gn * p.m_true + gm : (int64_t)gm * p.n_true + gn] = val[j][r] * (p.scale * (1.0f / kScaleX));
+        }
+    } else {
+      uint32_t lo[SUBN][2];
+#pragma unroll
+      for (int j = 0; j < SUBN; ++j) {
+        uint32_t hi[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float u = val[j][2 * h], v = val[j][2 * h + 1];
+          if constexpr (kOut == Result::kBf16) {
+            const float f = p.scale * (1.0f / kScaleX);
+            hi[h] = pack_bf16(u * f, v * f);
+          } else {
+            hi[h] = pack_f16(u, v);
+            lo[j][h] = pack_f16(u - (float)(_Float16)u, v - (float)(_Float16)v);
+          }
+        }
+        if (to_r) put_row(j, hi[0], hi[1]);
+        if (to_c) {
+          put_col(st_c, i, j, hi[0], hi[1]);
+          if constexpr (kSplit && kOut == Result::kPlanes) put_col(st_c_lo, i, j, lo[j][0], lo[j][1]);
+        }
+      }
+      if (to_r) flush(k16, kWNc, st_r, kPitchR, to_r, ld_r, mw + i * 16, nw, end_m, end_n);
+      if constexpr (kLowRows && kOut == Result::kPlanes) {
+#pragma unroll
+        for (int j = 0; j < SUBN; ++j) put_row(j, lo[j][0], lo[j][1]);
+        flush(k16, kWNc, st_r, kPitchR, to_r_lo, ld_r, mw + i * 16, nw, end_m, end_n);
+      }
+    }
+    // one row block at a time: with more of their loads ahead the registers do not hold
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if constexpr (kOut != Result::kF32) {
+    if (to_c) {
+      flush(kWNc, kWMc, st_c, kPitchC, to_c, ld_c, nw, mw, end_n, end_m);
+      if constexpr (kSplit && kOut == Result::kPlanes) flush(kWNc, kWMc, st_c_lo, kPitchC, to_c_lo, ld_c, nw, mw, end_n, end_m);
+    }
+  }
+  if constexpr (kWhat == Product::kUpdate && kOut == Result::kPlanes && !kSplit) {
+    square = wave_sum_f32(square) * (1.0f / (kScaleX * kScaleX));
+    if (lane == 0) p.squares[mat * p.parts + t * 4 + wave] = square;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The way in. Sums of G's squares, kNormParts per matrix, in float64 (no input's
+// squares leave its range), then G / |G| to the planes of X and X^T.
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float element_of(const T* p, int64_t i);
+template <>
+__device__ __forceinline__ float element_of<float>(const float* p, int64_t i) { return p[i]; }
+template <>
+__device__ __forceinline__ float element_of<bf16_t>(const bf16_t* p, int64_t i) { return bf16_lo(p[i].bits); }
+
+template <typename T>
+__global__ __launch_bounds__(256) void ortho_squares_kernel(const T* __restrict__ g, int64_t size, double* __restrict__ parts) {
+  __shared__ double sums[4];
+  const int64_t chunks = (size + 7) / 8;
+  const T* const from = g + blockIdx.y * size;
+  double s = 0.0;
+  for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < chunks; c += kNormParts * 256) {
+    float v[8];
+    values(load_chunk(from + 8 * c, (int)min(size - 8 * c, (int64_t)8)), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fma((double)v[e], (double)v[e], s);
+  }
+  s = wave_sum_f64(s);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) parts[blockIdx.y * kNormParts + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+// A 64 x 64 block of G (M x N) to the planes: X takes it as it lies or, where G is
+// tall, transposed, and X^T the other way round.
+template <typename T, bool kSplit>
+__global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__ g, const double* __restrict__ parts, int M, int N,
+                                                           int tiles_n, int tiles, OrthoArgs p) {
+  __shared__ float block[64][65];
+  const int mat = blockIdx.x / tiles, t = blockIdx.x % tiles;
+  const int r0 = t / tiles_n * 64, c0 = t % tiles_n * 64;
+  const double sum = wave_sum_f64(parts[mat * kNormParts + (threadIdx.x & 63)]);
+  const double f = sum > 0.0 ? (double)kScaleX / __dsqrt_rn(sum) : sum;  // (a NaN goes on)
+  const T* const from = g + (int64_t)mat * M * N;
+  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+    const int r = r0 + i / 64, c = c0 + i % 64;
+    block[i / 64][i % 64] = r < M && c < N ? (float)((double)element_of(from, (int64_t)r * N + c) * f) : 0.0f;
+  }
+  __syncthreads();
+  const int64_t base = (int64_t)mat * p.m * p.n;
+  // rows of G as they lie: M by N padded; columns: N by M padded
+  _Float16* const straight = (p.tall ? p.xt_new : p.x) + base;
+  _Float16* const straight_lo = (p.tall ? p.xt_lo_new : p.x_lo) + base;
+  _Float16* const turned = (p.tall ? p.x : p.xt_new) + base;
+  _Float16* const turned_lo = (p.tall ? p.x_lo : p.xt_lo_new) + base;
+  const int64_t ld_s = p.tall ? p.m : p.n, ld_t = p.tall ? p.n : p.m;
+  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+    const int r = i / 64, c = i % 64;
+    const float v = block[r][c], w = block[c][r];
+    straight[(r0 + r) * ld_s + c0 + c] = (_Float16)v;
+    turned[(c0 + r) * ld_t + r0 + c] = (_Float16)w;
+    if (kSplit || !p.tall) straight_lo[(r0 + r) * ld_s + c0 + c] = (_Float16)(v - (float)(_Float16)v);
+    if (kSplit || p.tall) turned_lo[(c0 + r) * ld_t + r0 + c] = (_Float16)(w - (float)(_Float16)w);
+  }
+}
+
+// ---------------------------------------------------------------------------
+struct OrthoPlan {
+  int64_t m, n;  // padded
+  bool split;
+  int tile;      // of all three products
+  int64_t symmetric, whole;
+  int64_t bytes;
+};
+
+static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
+  OrthoPlan o;
+  const int64_t lo = M < N ? M : N, hi = M < N ? N : M;
+  o.m = (lo + kPad - 1) / kPad * kPad;
+  o.n = (hi + kPad - 1) / kPad * kPad;
+  o.split = !bf16 || lo <= 128;
+  auto side = [&](int64_t v, int64_t t) { return (v + t - 1) / t; };
+  o.tile = L * side(o.m, 64) * side(o.n, 64) <= kCus ? 64 : L * side(o.m, 256) * side(o.n, 256) < 200 || o.split ? 128 : 256;
+  const int64_t r = side(o.m, o.tile);
+  o.symmetric = r * (r + 1) / 2;
+  o.whole = r * side(o.n, o.tile);
+  const int64_t mn = L * o.m * o.n * 2, mm = L * o.m * o.m * 2;
+  o.bytes = mn * (o.split ? 6 : 4) + mm * (o.split ? 4 : 2);
+  o.bytes += L * (kNormParts * 8 + 2 * o.m * 4 + o.whole * 16 + 16);
+  return o;
+}
+
+int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool bf16) { return ortho_plan(L, M, N, bf16).bytes; }
+
+template <Product kWhat, Result kOut, bool kSplit>
+static void launch_product(const OrthoArgs& a, int64_t L, int tile, hipStream_t stream) {
+  const dim3 grid((unsigned)(L * a.count)), block(256);
+  if (tile == 64) hipLaunchKernelGGL((ortho_product_kernel<kWhat, kOut, kSplit, 64, 64, 5>), grid, block, 0, stream, a);
+  else if (tile == 128) hipLaunchKernelGGL((ortho_product_kernel<kWhat, kOut, kSplit, 128, 128, 2>), grid, block, 0, stream, a);
+  else if constexpr (!kSplit) hipLaunchKernelGGL((ortho_product_kernel<kWhat, kOut, kSplit, 256, 256, 2>), grid, block, 0, stream, a);
+}
+
+template <bool kSplit>
+static hipError_t run_ortho(const void* g, bool g_bf16, int64_t L, int64_t M, int64_t N, int steps, bool bf16,
+                            const OrthoPlan& o, OrthoArgs p, double* parts, _Float16* xt[2], _Float16* xt_lo[2], hipStream_t stream) {
+  auto both = [&](auto squares, auto spread, auto from) {
+    hipLaunchKernelGGL(squares, dim3(kNormParts, (unsigned)L), dim3(256), 0, stream, from, M * N, parts);
+    const int64_t tn = (p.tall ? o.m : o.n) / 64, tiles = o.m / 64 * (o.n / 64);
+    p.xt_new = xt[0], p.xt_lo_new = xt_lo[0];
+    hipLaunchKernelGGL(spread, dim3((unsigned)(L * tiles)), dim3(256), 0, stream, from, (const double*)parts, (int)M, (int)N, (int)tn,
+                       (int)tiles, p);
+  };
+  if (g_bf16) both(ortho_squares_kernel<bf16_t>, ortho_spread_kernel<bf16_t, kSplit>, (const bf16_t*)g);
+  else both(ortho_squares_kernel<float>, ortho_spread_kernel<float, kSplit>, (const float*)g);
+  for (int k = 0; k < steps; ++k) {
+    // (the first step has no sum of squares before it, and alpha = 1 / m there)
+    p.pivot = !kSplit && k >= 1 && k >= steps - 2;
+    p.xt = xt[k % 2], p.xt_lo = xt_lo[k % 2];
+    p.xt_new = xt[1 - k % 2], p.xt_lo_new = xt_lo[1 - k % 2];
+    p.count = (int)o.symmetric;
+    launch_product<Product::kGram, Result::kPlanes, kSplit>(p, L, o.tile, stream);
+    launch_product<Product::kSquare, Result::kPlanes, kSplit>(p, L, o.tile, stream);
+    p.count = (int)o.whole;
+    if (k < steps - 1) launch_product<Product::kUpdate, Result::kPlanes, kSplit>(p, L, o.tile, stream);
+    else if (bf16) launch_product<Product::kUpdate, Result::kBf16, kSplit>(p, L, o.tile, stream);
+    else if constexpr (kSplit) launch_product<Product::kUpdate, Result::kF32, kSplit>(p, L, o.tile, stream);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M, int64_t N, int steps, float a, float b,
+                                float c, float scale, void* out, bool out_bf16, void* ws, hipStream_t stream) {
+  const OrthoPlan o = ortho_plan(L, M, N, out_bf16);
+  OrthoArgs p{};
+  p.m = (int)o.m, p.n = (int)o.n;
+  p.tall = M > N;
+  p.m_true = (int)(p.tall ? N : M), p.n_true = (int)(p.tall ? M : N);
+  p.a = a, p.b = b, p.c = c, p.scale = scale, p.out = out;
+  p.parts = (int)o.whole * 4;
+  uint8_t* at = (uint8_t*)ws;
+  auto take = [&](int64_t bytes) {
+    void* r = at;
+    at += bytes;
+    return r;
+  };
+  const int64_t mn = L * o.m * o.n * 2, mm = L * o.m * o.m * 2;
+  _Float16 *xt[2], *xt_lo[2] = {nullptr, nullptr};
+  p.x = (_Float16*)take(mn), p.x_lo = (_Float16*)take(mn);
+  for (auto& v : xt) v = (_Float16*)take(mn);
+  p.am = (_Float16*)take(mm), p.bm = (_Float16*)take(mm);
+  if (o.split) {
+    for (auto& v : xt_lo) v = (_Float16*)take(mn);
+    p.am_lo = (_Float16*)take(mm), p.bm_lo = (_Float16*)take(mm);
+  }
+  double* const parts = (double*)take(L * kNormParts * 8);
+  p.da = (float*)take(L * o.m * 4), p.db = (float*)take(L * o.m * 4);
+  p.squares = (float*)take(L * o.whole * 16);
+  p.alpha = (float*)take(L * 16);
+  return o.split ? run_ortho<true>(g, g_bf16, L, M, N, steps, out_bf16, o, p, parts, xt, xt_lo, stream)
+                 : run_ortho<false>(g, g_bf16, L, M, N, steps, out_bf16, o, p, parts, xt, xt_lo, stream);
+}
+
+}  // namespace fp8q

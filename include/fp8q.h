@@ -725,6 +725,40 @@ FP8Q_API int fp8q_swiglu_bwd(const void* dy, int dy_dtype, int64_t ldy, const vo
                              int gu_dtype, int64_t ld, const int32_t* m_offsets, int64_t G,
                              int64_t M, int64_t I, void* dgu, void* stream);
 
+/*
+ * Orthogonalized updates: what an optimizer that steps along the orthogonal factor
+ * of a weight's gradient makes of it (fp8_gemm_rowscaled's product, or a momentum
+ * of such), by Newton-Schulz products. For each of L matrices G (M x N):
+ *   X_0 = G / sqrt(sum G^2);  steps times:  A = X X^T,  X = a X + (b A + c A A) X
+ *   out = scale * X_steps
+ * The singular vectors stay, each singular value s (of X_0, so at most 1) becomes
+ * scale * p(p(...p(s))) with p(s) = a s + b s^3 + c s^5. A zero matrix gives zeros (so
+ * no small number is added to the norm); one that holds an infinity or NaN gives
+ * NaN; the other matrices do not notice.
+ *
+ * The products run on the FP16 matrix cores with binary32 sums. For a float32 out
+ * every operand is two FP16 numbers, 22 bits: out is as near the definition as if
+ * formed in binary32. For a bfloat16 out the operands of matrices larger than 128 in
+ * both directions are one FP16 number (X itself two): out is within 2e-3 of the
+ * definition (relative, over the matrix), most often 2e-4 to 8e-4, before its own
+ * rounding.
+ *
+ * a, b, c have to keep singular values of [0, 1] below 3 and |b s^2 + c s^4| below
+ * 7.5 in every step, which holds for (3.4445, -4.7750, 2.0315) and for polynomials
+ * that stay in [0, 1], such as (2, -1.5, 0.5); otherwise FP8Q_ERR_SHAPE.
+ *
+ *   g   : in,  L x M x N of g_dtype;  out : L x M x N of out_dtype
+ *   workspace : at least fp8q_orthogonalize_workspace_bytes(L, M, N, out_dtype), 16-byte aligned
+ * g and out need their element's alignment only. 1 <= steps <= 100, scale finite,
+ * L <= 65535, M, N <= 65536, and L M N below about 2^36 (FP8Q_ERR_TOO_LARGE).
+ * L, M or N == 0 is a no-op. Deterministic; allocates nothing. 2 + 3 * steps kernels.
+ */
+FP8Q_API int64_t fp8q_orthogonalize_workspace_bytes(int64_t L, int64_t M, int64_t N, int out_dtype);
+FP8Q_API int fp8q_orthogonalize(const void* g, int g_dtype, int64_t L, int64_t M, int64_t N,
+                                int steps, float a, float b, float c, float scale, void* out,
+                                int out_dtype, void* workspace, int64_t workspace_bytes,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

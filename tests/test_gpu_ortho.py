@@ -1,0 +1,281 @@
+"""Newton-Schulz orthogonalization on the GPU against float64.
+
+What one step may be off by, in the Frobenius norm |.| (||.|| is the spectral norm), follows from what it
+rounds. h is the relative error of an operand's rounding (one FP16 number: 2^-11; two: 2^-21), e that of a
+binary32 sum of K products, 4 sqrt(K) 2^-24 of the sum of their magnitudes (roundings of either sign):
+
+  A   2 h |X| ||X|| + e ||X| |X|^T|, and h |A| as it is kept
+  B   (|b| + 2 |c| ||A||) of that, e |c| ||A| |A||, and h (|B| + |beta| sqrt(m)) as it is kept: about a
+      mean eigenvalue alpha the kept part is B - beta I, beta = b alpha + c alpha^2
+  X   ||X|| of that, (||B|| + |beta|) h |X| for X's rounding in the product, e ||B| |X||, and 2^-21 |X|
+
+A step turns an error E before it into at most sup |p'| E: the map of singular values is odd, and
+the sup is over [0, ||X||], widened by the error itself. That bounds the worst case; what the
+documentation says is held to as well: 2e-3 for one FP16 number, and for two about what binary32 gives,
+that is, at most four times what the same steps in binary32 are off by on the CPU or GPU."""
+
+import numpy as np
+import pytest
+
+from conftest import gpu_available
+from fp8_fine_grained_online_amd import synthetic as S
+from oracle import step
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def fro(x):
+    return float(np.linalg.norm(x))
+
+
+def slope(coeffs, top):
+    s = np.linspace(0, top, 4001)
+    a, b, c = coeffs
+    return float(np.abs(a + 3 * b * s ** 2 + 5 * c * s ** 4).max())
+
+
+def bound(g, steps, coeffs, single):
+    """The largest |X_steps - exact|, from the formulas above."""
+    a, b, c = coeffs
+    x = np.asarray(g, np.float64)
+    x = x.T if x.shape[0] > x.shape[1] else x
+    m, n = x.shape
+    h, h2 = 2.0 ** -11 if single else 2.0 ** -21, 2.0 ** -21
+    e_n, e_m = (4 * np.sqrt(k) * 2.0 ** -24 for k in (n, m))
+    norm = fro(x)
+    x = x / norm if norm else x
+    E = (h2 + 2.0 ** -23) * fro(x)
+    for k in range(steps):
+        A = x @ x.T
+        B = b * A + c * A @ A
+        s = float(np.linalg.norm(x, 2)) if norm else 0.0
+        alpha = np.trace(A) / m if single and k >= 1 and k >= steps - 2 else 0.0
+        beta = abs(b * alpha + c * alpha ** 2)
+        dA = 2 * h * fro(x) * s + e_n * fro(np.abs(x) @ np.abs(x).T) + h * fro(A)
+        dB = (abs(b) + 2 * abs(c) * s ** 2) * dA + e_m * abs(c) * fro(np.abs(A) @ np.abs(A)) + h * (fro(B) + beta * m ** 0.5)
+        dX = s * dB + (float(np.linalg.norm(B, 2)) + beta) * h * fro(x) + e_m * fro(np.abs(B) @ np.abs(x)) + h2 * fro(x)
+        E = slope(coeffs, s + E) * E + dX
+        x = a * x + B @ x
+    return E
+
+
+def matrix(M, N, kind, seed):
+    rng = S.rng_for(seed, M * 7 + N)
+    r = min(M, N)
+    if kind == "gauss":
+        return rng.standard_normal((M, N))
+    if kind == "decay":
+        return (rng.standard_normal((M, r)) * np.exp(-8.0 * np.arange(r) / r)) @ rng.standard_normal((r, N))
+    if kind == "few":  # a few directions, and noise
+        return rng.standard_normal((M, 4)) @ rng.standard_normal((4, N)) + 0.1 * rng.standard_normal((M, N))
+    if kind == "one":
+        g = np.zeros((M, N))
+        g[M // 2, N // 3] = -3.0
+        return g
+    q, _ = np.linalg.qr(rng.standard_normal((max(M, N), r)))  # equal singular values
+    return q if M > N else q.T
+
+
+def dev(g, dtype):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(g, np.float32)).to({"bf16": torch.bfloat16, "f32": torch.float32}[dtype]).cuda()
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def binary32(g, steps, coeffs):
+    """The steps in binary32."""
+    a, b, c = (np.float32(v) for v in coeffs)
+    x = np.asarray(g / max(fro(g), 2.0 ** -200), np.float32)
+    x = x.T if x.shape[0] > x.shape[1] else x
+    for _ in range(steps):
+        A = x @ x.T
+        x = a * x + (b * A + c * (A @ A)) @ x
+    return x.T if g.shape[0] > g.shape[1] else x
+
+
+def check(g, got, out, steps=5, coeffs=COEFFS, scale=1.0):
+    coeffs = tuple(float(np.float32(v)) for v in coeffs)
+    single = out == "bf16" and min(g.shape) > 128
+    want = step.orthogonalize(g, steps, coeffs)
+    promise = 2e-3 * fro(want) if single else 4 * fro(binary32(g, steps, coeffs) - want) + 2.0 ** -22 * fro(want)
+    tol = abs(scale) * min(bound(g, steps, coeffs, single), promise)
+    want = scale * want
+    tol += (2.0 ** -8 if out == "bf16" else 2.0 ** -23) * fro(want)
+    assert fro(got - want) <= tol, (fro(got - want) / fro(want), tol / fro(want))
+    # and no single value far from its place
+    assert np.abs(got - want).max() <= 0.5 * tol / max(1.0, np.sqrt(min(g.shape)) / 8) + 2.0 ** -8 * np.abs(want).max()
+
+
+SHAPES = [(1, 1), (1, 200), (7, 7), (64, 64), (65, 63), (16, 100), (130, 16), (128, 700), (129, 130), (200, 333),
+          (333, 200), (512, 512), (150, 1100)]
+
+
+@pytest.mark.parametrize("M,N", SHAPES)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_shapes(M, N, dtype, out):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    kinds = ["gauss", "decay", "few"] if min(M, N) > 4 else ["gauss"]
+    for kind in kinds:
+        g = dev(matrix(M, N, kind, 3300), dtype)
+        o = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+        F.fp8q_orthogonalize(g, out_dtype=out, out=o[:M])
+        check(host(g), host(o[:M]), out)
+        assert torch.all(o[M] == 7.0)
+
+
+@pytest.mark.parametrize("kind", ["one", "equal"])
+@pytest.mark.parametrize("M,N", [(40, 60), (300, 180)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_spectra_at_the_ends(kind, M, N, out):
+    import fp8_fine_grained_online_amd as F
+    g = dev(matrix(M, N, kind, 3310), "f32")
+    check(host(g), host(F.fp8q_orthogonalize(g, out_dtype=out)), out)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 7])
+@pytest.mark.parametrize("coeffs,scale", [(COEFFS, -0.2), ((2.0, -1.5, 0.5), 1.0), ((1.5, -0.5, 0.0), 3.0)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_steps_and_polynomials(steps, coeffs, scale, out):
+    import fp8_fine_grained_online_amd as F
+    for M, N in ((50, 90), (260, 140)):
+        g = dev(matrix(M, N, "few", 3320), "f32")
+        got = host(F.fp8q_orthogonalize(g, steps=steps, coeffs=coeffs, scale=scale, out_dtype=out))
+        check(host(g), got, out, steps, coeffs, scale)
+
+
+@pytest.mark.parametrize("L,M,N", [(1, 64, 64), (3, 96, 160), (5, 300, 150), (40, 20, 30), (0, 8, 8)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_several_matrices(L, M, N, out):
+    import fp8_fine_grained_online_amd as F
+    g = dev(np.stack([matrix(M, N, "gauss", 3330 + i) * 10.0 ** (i - 2) for i in range(L)] or [np.zeros((M, N))])[:L], "f32")
+    got = F.fp8q_orthogonalize(g, out_dtype=out)
+    assert got.shape == g.shape
+    for a, b in zip(host(g), host(got)):
+        check(a, b, out)
+
+
+@pytest.mark.parametrize("M,N,dtype", [(1024, 4096, "bf16"), (2100, 1900, "f32"), (4096, 700, "bf16")])
+@pytest.mark.parametrize("kind", ["gauss", "few"])
+def test_large(M, N, dtype, kind):
+    """The larger tiles, against float64 on the GPU: what the documentation says."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    gen = torch.Generator("cuda").manual_seed(M + N)
+    g = torch.randn(M, N, device="cuda", generator=gen)
+    if kind == "few":
+        g = 0.05 * g + torch.randn(M, 8, device="cuda", generator=gen) @ torch.randn(8, N, device="cuda", generator=gen)
+    g = g.to({"bf16": torch.bfloat16, "f32": torch.float32}[dtype])
+    a, b, c = COEFFS
+
+    def steps(x):
+        x = x / torch.linalg.norm(x)
+        x = x.t().contiguous() if M > N else x
+        for _ in range(5):
+            A = x @ x.t().contiguous()
+            x = a * x + (b * A + c * (A @ A)) @ x
+        return x.t() if M > N else x
+
+    x = steps(g.double())
+
+    def off(y):
+        return float(torch.linalg.norm(y.double() - x) / torch.linalg.norm(x))
+
+    assert off(F.fp8q_orthogonalize(g)) <= 2e-3 + 2.0 ** -8
+    assert off(F.fp8q_orthogonalize(g, out_dtype="f32")) <= 4 * off(steps(g.float())) + 2.0 ** -22
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N", [(30, 40), (200, 300)])
+def test_magnitudes_zeros_and_what_is_not_finite(M, N, out):
+    """Any magnitude of g gives the same; zero gives zeros; an infinity or NaN stays with its matrix."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    base = dev(np.round(matrix(M, N, "gauss", 3340) * 64) / 64, "f32")
+    g = torch.stack([base, base * 2.0 ** 100, base * 2.0 ** -120, torch.zeros_like(base), base.clone(), base.clone()])
+    g[4, M // 2, 3] = float("nan")
+    g[5, 0, N - 1] = float("inf")
+    got = F.fp8q_orthogonalize(g, out_dtype=out)
+    again = F.fp8q_orthogonalize(g, out_dtype=out)
+    assert torch.equal(got[:4], again[:4])
+    check(host(g[0]), host(got[0]), out)
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])  # powers of two change nothing
+    assert not got[3].any() and torch.isnan(got[4]).any() and torch.isnan(got[5]).any()
+
+
+def test_odd_addresses():
+    """Neither g nor out needs more than its element's alignment."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    M, N = 131, 77
+    src = dev(matrix(M, N, "gauss", 3350), "bf16")
+    room = torch.zeros(M * N + 9, dtype=torch.bfloat16, device="cuda")
+    g = room[3:3 + M * N].view(M, N)
+    g.copy_(src)
+    o = torch.zeros(M * N + 9, dtype=torch.bfloat16, device="cuda")
+    F.fp8q_orthogonalize(g, out=o[5:5 + M * N].view(M, N))
+    assert torch.equal(o[5:5 + M * N].view(M, N), F.fp8q_orthogonalize(src))
+    assert not o[:5].any() and not o[5 + M * N:].any()
+
+
+def test_streams_and_the_callers_workspace():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    gs = [dev(matrix(300, 200, "gauss", 3360 + i), "f32") for i in range(2)]
+    want = [F.fp8q_orthogonalize(g) for g in gs]
+    need = F.lib().fp8q_orthogonalize_workspace_bytes(1, 300, 200, F.FP8Q_OUT_BF16)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in gs]
+    spaces = [torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda") for _ in gs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [F.fp8q_orthogonalize(g, workspace=w[:need], stream=s) for g, w, s in zip(gs, spaces, streams)]
+        torch.cuda.synchronize()
+        for a, b, w in zip(got, want, spaces):
+            assert torch.equal(a, b) and torch.all(w[need:] == 0xFF)
+
+
+@pytest.mark.parametrize("M,N,out", [(200, 300, "bf16"), (100, 60, "f32")])
+def test_in_a_captured_graph(M, N, out):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    g = torch.randn(M, N, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        F.fp8q_orthogonalize(g, out_dtype=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = F.fp8q_orthogonalize(g, out_dtype=out)
+    for _ in range(4):
+        g.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, F.fp8q_orthogonalize(g, out_dtype=out))
+        torch.randn(1 << 20, device="cuda").sum().item()
+
+
+def test_refusals():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    g = torch.randn(8, 8, device="cuda")
+    for call in (lambda: F.fp8q_orthogonalize(g[:, :4]), lambda: F.fp8q_orthogonalize(g[0]), lambda: F.fp8q_orthogonalize(g, steps=0),
+                 lambda: F.fp8q_orthogonalize(g, steps=101), lambda: F.fp8q_orthogonalize(g, coeffs=(1.0, 2.0)),
+                 lambda: F.fp8q_orthogonalize(g, out=g[:4].bfloat16()), lambda: F.fp8q_orthogonalize(g.cpu()),
+                 lambda: F.fp8q_orthogonalize(g, out_dtype="f16")):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        F.fp8q_orthogonalize(g.half())
+    for call in (lambda: F.fp8q_orthogonalize(g, coeffs=(9.0, 0.0, 0.0)), lambda: F.fp8q_orthogonalize(g, scale=float("inf")),
+                 lambda: F.fp8q_orthogonalize(g, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(F.Fp8qError):
+            call()
+    for shape in ((0, 5), (5, 0), (2, 0, 3)):
+        assert F.fp8q_orthogonalize(torch.empty(shape, device="cuda")).shape == shape

@@ -94,12 +94,48 @@ def test_swiglu_bwd():
     assert f(None, F32, 0, None, BF16, 0, None, 0, 0, 33, None, None) == 0
 
 
+def test_orthogonalize():
+    L = _lib()
+    f, need = L.fp8q_orthogonalize, L.fp8q_orthogonalize_workspace_bytes(2, 33, 70, BF16)
+    size = L.fp8q_orthogonalize_workspace_bytes
+    # X and both X^T, high parts at least
+    assert need >= 3 * 2 * 64 * 128 * 2 and size(2, 33, 70, F32) >= need and size(0, 33, 70, F32) == 0
+    assert size(2, 33, 70, 2) == -1 and size(-1, 33, 70, F32) == -1 and size(1, 65537, 4, F32) == -1
+    assert size(65536, 4, 4, F32) == -1 and size(65535, 4096, 4096, BF16) == -1
+    #       0  1    2  3   4   5  6       7       8       9    10 11    12  13    14
+    good = [X, F32, 2, 33, 70, 5, 3.4445, -4.775, 2.0315, 0.5, Y, BF16, WS, need, None]
+    refuses(f, good, [
+        (1, 2, DTYPE), (11, -1, DTYPE), (2, -1, SHAPE), (3, -1, SHAPE), (4, -1, SHAPE), (5, 0, SHAPE), (5, 101, SHAPE),
+        (6, NAN, SHAPE), (7, INF, SHAPE), (8, NAN, SHAPE), (9, INF, SHAPE), (9, NAN, SHAPE), (13, need - 1, SHAPE),
+        (3, 65537, LARGE), (4, 65537, LARGE), (2, 65536, LARGE), (0, None, NULL), (10, None, NULL), (12, None, NULL),
+        (0, X + 2, ALIGN), (10, Y + 1, ALIGN), (12, WS + 8, ALIGN)])
+    assert f(None, F32, 0, 33, 70, 5, 2.0, -1.5, 0.5, 1.0, None, BF16, None, 0, None) == 0
+    assert f(None, F32, 2, 33, 0, 5, 2.0, -1.5, 0.5, 1.0, None, BF16, None, 0, None) == 0
+
+
+def test_orthogonalize_refuses_polynomials_that_grow():
+    """Singular values above 3 or an inner polynomial above 7.5 in any step; those below pass on to the NULL check."""
+    f = _lib().fp8q_orthogonalize
+
+    def status(steps, a, b, c):
+        return f(None, F32, 1, 4, 4, steps, a, b, c, 1.0, Y, F32, WS, 1 << 40, None)
+    for ok in ((5, 3.4445, -4.775, 2.0315), (100, 3.4445, -4.775, 2.0315), (9, 2.0, -1.5, 0.5), (9, 1.5, -0.5, 0.0),
+               (3, 1.0, 0.0, 0.0), (1, 3.0, 0.0, 0.0), (1, 4.0848, -6.8946, 2.9270)):
+        assert status(*ok) == NULL, ok
+    for bad in ((2, 3.0, 0.0, 0.0), (1, 3.1, 0.0, 0.0), (1, 1.0, -8.0, 0.0), (2, 5.0, -3.0, 0.0), (3, 3.4445, -4.775, 4.0),
+                (1, 10.0, -20.0, 10.0)):
+        assert status(*bad) == SHAPE, bad
+    # the largest value inside the interval: s (1 - s^2) 7.9 has its top, 3.04, at s^2 = 1/3
+    assert status(1, 7.9, -7.9, 0.0) == SHAPE and status(1, 7.5, -7.5, 0.0) == NULL
+
+
 def test_binding_refuses_before_any_device_call():
     import torch
     import fp8_fine_grained_online_amd as F
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.ones(64)
     for call in (lambda: F.fp8q_norm(x, w, 1e-6), lambda: F.fp8q_norm_bwd(x, x, w, 1e-6), lambda: F.fp8q_swiglu(x),
-                 lambda: F.fp8q_swiglu_quant_act_1x128(x), lambda: F.fp8q_swiglu_bwd(x, x)):
+                 lambda: F.fp8q_swiglu_quant_act_1x128(x), lambda: F.fp8q_swiglu_bwd(x, x),
+                 lambda: F.fp8q_orthogonalize(x)):
         with pytest.raises(ValueError, match="device tensor"):
             call()
     with pytest.raises(TypeError):
