@@ -32,6 +32,7 @@
 //    would cost more than it saves.)
 //
 // Zero rows and columns pad m and n to multiples of 64; they stay zero.
+#include <initializer_list>
 #include <type_traits>
 
 #include "common.hpp"
@@ -47,7 +48,7 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f;  // X, and A and B, as they are stored
 constexpr int kPad = 64;                               // rows and columns are padded to
 constexpr int kOrthoStep = 128;                        // bytes of K per pipeline step: 64 values
-constexpr int kNormParts = 64;                         // partial sums of |G|^2 per matrix
+constexpr int kNormParts = 512;                        // partial sums of |G|^2 per matrix
 
 enum class Product { kGram, kSquare, kUpdate };
 
@@ -74,8 +75,9 @@ struct OrthoTile {
   static constexpr int kWM = BM / 2, kWN = BN / 2;
   static constexpr int kSlabA = BM * kOrthoStep, kSlabB = BN * kOrthoStep;
   static constexpr int kRing = (D + 1) * kSlabA + D * kSlabB;
-  // a wave's staging of its part on the way out: 16 rows, and all of it transposed
-  static constexpr int kPitchR = kWN * 2 + 16, kPitchC = kWM * 2 + 16;
+  // a wave's staging of its part on the way out: 16 rows (16-byte chunk c of row r at
+  // c ^ r), and all of it transposed (rows a chunk apart)
+  static constexpr int kPitchR = kWN * 2, kPitchC = kWM * 2 + 16;
   static constexpr int kStageR = 16 * kPitchR, kStageC = kWN * kPitchC;
   static constexpr int kStage = 4 * (kStageR + (kSplit ? 2 : 1) * kStageC);
   static constexpr int kLds = kRing > kStage ? kRing : kStage;
@@ -93,6 +95,10 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
 }
+
+// Where chunk c of a staged row r lies, of n: another place in each of the rows that
+// are written at once, also where n is no power of two
+__device__ __forceinline__ int swz_chunk(int r, int c, int n) { return (n & (n - 1)) ? (c + r) % n : c ^ (r & (n - 1)); }
 
 enum class Result { kPlanes, kBf16, kF32 };
 
@@ -245,27 +251,55 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   }
   if (kWhat != Product::kGram && p.pivot) alpha = p.alpha[mat];
 
-  // four values of a row of a plane, as binary32
-  auto four = [&](const _Float16* from, float (&v)[4]) {
-    const f16x4 h = *(const f16x4*)from;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = (float)h[r];
+  // What the epilogue reads of row block i: the tile's values of X or A, and what
+  // FP16 cut off the diagonal there. Loaded a row block ahead of its use.
+  struct Before {
+    f16x4 hi[SUBN], lo[SUBN];
+    float cut;
   };
+  constexpr bool kLowBefore = kWhat == Product::kUpdate || (kWhat == Product::kSquare && kSplit);
+  auto read_before = [&](int i, Before& f) {
+    if constexpr (kWhat == Product::kGram) return;
+    const int gm = mw + i * 16 + lr;
+    f.cut = !kSplit && gm < p.m ? (kWhat == Product::kSquare ? p.da : p.db)[mat * p.m + gm] : 0.0f;
+    const int64_t at = (kWhat == Product::kSquare ? mm : mn) + (int64_t)gm * rows_total + nw + 4 * lk;
+    const _Float16* const hi = (kWhat == Product::kSquare ? p.am : p.x) + at;
+    const _Float16* const lo = (kWhat == Product::kSquare ? p.am_lo : p.x_lo) + at;
+#pragma unroll
+    for (int j = 0; j < SUBN; ++j) {
+      const bool inside = gm < p.m && nw + j * 16 + 4 * lk < rows_total;
+      const f16x4 none = {0, 0, 0, 0};
+      f.hi[j] = inside ? *(const f16x4*)(hi + j * 16) : none;
+      f.lo[j] = kLowBefore && inside ? *(const f16x4*)(lo + j * 16) : none;
+    }
+  };
+  float cut_n[kWhat == Product::kSquare && !kSplit ? SUBN : 1][4];  // of the columns' diagonals
+  if constexpr (kWhat == Product::kSquare && !kSplit) {
+#pragma unroll
+    for (int j = 0; j < SUBN; ++j) {
+      const int gn = nw + j * 16 + 4 * lk;
+      const v4f d = gn < p.m ? *(const v4f*)(p.da + mat * p.m + gn) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) cut_n[j][r] = d[r];
+    }
+  }
   constexpr int kPitchR = Cfg::kPitchR, kPitchC = Cfg::kPitchC;
   uint8_t* const st_r = lds + wave * (Cfg::kStage / 4);
   uint8_t* const st_c = st_r + Cfg::kStageR;
   uint8_t* const st_c_lo = st_c + Cfg::kStageC;  // kSplit
   // `kR` rows of `kC` 16-bit values from the wave's LDS to `to` (ld apart), up to the ends of its rows and columns
-  auto flush = [&](auto r_c, auto c_c, const uint8_t* st, int pitch_st, uint16_t* to, int64_t ld, int row, int col, int row_end,
+  auto flush = [&](auto r_c, auto c_c, const uint8_t* st, uint16_t* to, int64_t ld, int row, int col, int row_end,
                    int col_end) {
     constexpr int kR = decltype(r_c)::value, kCh = decltype(c_c)::value / 8;
+    constexpr bool kSwizzled = kR == 16;
+    constexpr int kPitch = kCh * 16 + (kSwizzled ? 0 : 16);
     static_assert(kR * kCh % 64 == 0, "whole wave stores");
     __builtin_amdgcn_s_waitcnt(kOrthoWaitLds);  // a wave reads back only its own part
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 4
     for (int k = 0; k < kR * kCh / 64; ++k) {
       const int r = (k * 64 + lane) / kCh, ch = (k * 64 + lane) % kCh;
-      const u32x4 v = *(const u32x4*)(st + r * pitch_st + ch * 16);
+      const u32x4 v = *(const u32x4*)(st + r * kPitch + (kSwizzled ? swz_chunk(r, ch, kCh) : ch) * 16);
       if (row + r < row_end && col + ch * 8 < col_end)
         store_chunk((bf16_t*)to + (row + r) * ld + col + ch * 8, {v}, col_end - col - ch * 8);
     }
@@ -276,7 +310,7 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   constexpr integral_constant<int, WM> kWMc{};
   constexpr integral_constant<int, WN> kWNc{};
   auto put_row = [&](int j, uint32_t p0, uint32_t p1) {  // block j's four values of this lane's row
-    *(uint2*)(st_r + lr * kPitchR + (j * 16 + 4 * lk) * 2) = make_uint2(p0, p1);
+    *(uint2*)(st_r + lr * kPitchR + swz_chunk(lr, 2 * j + (lk >> 1), WN / 8) * 16 + (lk & 1) * 8) = make_uint2(p0, p1);
   };
   // transposed: neighbouring lanes hold neighbouring rows; the even one writes the first two columns of both, the odd one the others
   auto put_col = [&](uint8_t* st, int i, int j, uint32_t p0, uint32_t p1) {
@@ -310,53 +344,32 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   float* const cut = (kWhat == Product::kGram ? p.da : p.db) + mat * p.m;
 
   float square = 0.0f;
+  Before before[2];
+  read_before(0, before[0]);
 #pragma unroll
   for (int i = 0; i < SUBM; ++i) {
     const int gm = mw + i * 16 + lr;
-    float cut_m = 0.0f;  // of the diagonal, row gm
-    if (!kSplit && gm < p.m) {
-      if constexpr (kWhat == Product::kSquare) cut_m = p.da[mat * p.m + gm];
-      if constexpr (kWhat == Product::kUpdate) cut_m = p.db[mat * p.m + gm];
-    }
+    const Before& f = before[i % 2];
+    if (i + 1 < SUBM) read_before(i + 1, before[(i + 1) % 2]);
+    __builtin_amdgcn_sched_barrier(0);
     float val[SUBN][4];
 #pragma unroll
     for (int j = 0; j < SUBN; ++j) {
       const int gn = nw + j * 16 + 4 * lk;
-      const bool inside = gm < p.m && gn < rows_total;
-      if constexpr (kWhat == Product::kGram) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (kWhat == Product::kGram) {
           val[j][r] = acc[i][j][r] * (kScaleA / (kScaleX * kScaleX));
           if (on_diagonal && gm == gn + r) val[j][r] -= kScaleA * alpha;
-        }
-      } else if constexpr (kWhat == Product::kSquare) {
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lo[4] = {0.0f, 0.0f, 0.0f, 0.0f}, cut_n[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (inside) {
-          four(p.am + mm + (int64_t)gm * p.m + gn, v);
-          if constexpr (kSplit) {
-            four(p.am_lo + mm + (int64_t)gm * p.m + gn, lo);
-          } else {
-            const v4f d = *(const v4f*)(p.da + mat * p.m + gn);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) cut_n[r] = d[r];
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float whole = v[r] + (kSplit ? lo[r] : gm == gn + r ? cut_m : 0.0f);
-          const float sq = __builtin_fmaf(cut_m + cut_n[r], v[r], acc[i][j][r]) * (1.0f / kScaleA);
+        } else if constexpr (kWhat == Product::kSquare) {
+          const float v = (float)f.hi[j][r];
+          const float whole = v + (kSplit ? (float)f.lo[j][r] : gm == gn + r ? f.cut : 0.0f);
+          const float cut = kSplit ? 0.0f : f.cut + cut_n[kSplit ? 0 : j][r];
+          const float sq = __builtin_fmaf(cut, v, acc[i][j][r]) * (1.0f / kScaleA);
           val[j][r] = __builtin_fmaf(p.c, sq, (p.b + 2.0f * p.c * alpha) * whole);
-        }
-      } else {
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lo[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (inside) {
-          four(p.x + mn + (int64_t)gm * p.n + gn, v);
-          four(p.x_lo + mn + (int64_t)gm * p.n + gn, lo);
-        }
-        const float q = p.a + alpha * (p.b + alpha * p.c) + cut_m * (1.0f / kScaleA);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          val[j][r] = __builtin_fmaf(q, v[r] + lo[r], acc[i][j][r] * (1.0f / kScaleA));
+        } else {
+          const float q = p.a + alpha * (p.b + alpha * p.c) + f.cut * (1.0f / kScaleA);
+          val[j][r] = __builtin_fmaf(q, (float)f.hi[j][r] + (float)f.lo[j][r], acc[i][j][r] * (1.0f / kScaleA));
           square = __builtin_fmaf(val[j][r], val[j][r], square);
         }
       }
@@ -400,11 +413,11 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
           if constexpr (kSplit && kOut == Result::kPlanes) put_col(st_c_lo, i, j, lo[j][0], lo[j][1]);
         }
       }
-      if (to_r) flush(k16, kWNc, st_r, kPitchR, to_r, ld_r, mw + i * 16, nw, end_m, end_n);
+      if (to_r) flush(k16, kWNc, st_r, to_r, ld_r, mw + i * 16, nw, end_m, end_n);
       if constexpr (kLowRows && kOut == Result::kPlanes) {
 #pragma unroll
         for (int j = 0; j < SUBN; ++j) put_row(j, lo[j][0], lo[j][1]);
-        flush(k16, kWNc, st_r, kPitchR, to_r_lo, ld_r, mw + i * 16, nw, end_m, end_n);
+        flush(k16, kWNc, st_r, to_r_lo, ld_r, mw + i * 16, nw, end_m, end_n);
       }
     }
     // one row block at a time: with more of their loads ahead the registers do not hold
@@ -412,8 +425,8 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   }
   if constexpr (kOut != Result::kF32) {
     if (to_c) {
-      flush(kWNc, kWMc, st_c, kPitchC, to_c, ld_c, nw, mw, end_n, end_m);
-      if constexpr (kSplit && kOut == Result::kPlanes) flush(kWNc, kWMc, st_c_lo, kPitchC, to_c_lo, ld_c, nw, mw, end_n, end_m);
+      flush(kWNc, kWMc, st_c, to_c, ld_c, nw, mw, end_n, end_m);
+      if constexpr (kSplit && kOut == Result::kPlanes) flush(kWNc, kWMc, st_c_lo, to_c_lo, ld_c, nw, mw, end_n, end_m);
     }
   }
   if constexpr (kWhat == Product::kUpdate && kOut == Result::kPlanes && !kSplit) {
@@ -459,7 +472,10 @@ __global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__
   __shared__ float block[64][65];
   const int mat = blockIdx.x / tiles, t = blockIdx.x % tiles;
   const int r0 = t / tiles_n * 64, c0 = t % tiles_n * 64;
-  const double sum = wave_sum_f64(parts[mat * kNormParts + (threadIdx.x & 63)]);
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < kNormParts / 64; ++i) sum += parts[mat * kNormParts + i * 64 + (threadIdx.x & 63)];
+  sum = wave_sum_f64(sum);
   const double f = sum > 0.0 ? (double)kScaleX / __dsqrt_rn(sum) : sum;  // (a NaN goes on)
   const T* const from = g + (int64_t)mat * M * N;
   for (int i = threadIdx.x; i < 64 * 64; i += 256) {
@@ -488,7 +504,7 @@ __global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__
 struct OrthoPlan {
   int64_t m, n;  // padded
   bool split;
-  int tile;      // of all three products
+  int tile_sym, tile;  // of the gram and the square, and of the update
   int64_t symmetric, whole;
   int64_t bytes;
 };
@@ -500,10 +516,26 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   o.n = (hi + kPad - 1) / kPad * kPad;
   o.split = !bf16 || lo <= 128;
   auto side = [&](int64_t v, int64_t t) { return (v + t - 1) / t; };
-  o.tile = L * side(o.m, 64) * side(o.n, 64) <= kCus ? 64 : L * side(o.m, 256) * side(o.n, 256) < 200 || o.split ? 128 : 256;
-  const int64_t r = side(o.m, o.tile);
-  o.symmetric = r * (r + 1) / 2;
-  o.whole = r * side(o.n, o.tile);
+  auto sym = [&](int64_t t) { return side(o.m, t) * (side(o.m, t) + 1) / 2; };
+  auto all = [&](int64_t t) { return side(o.m, t) * side(o.n, t); };
+  // The tile with the least cost, in rounds of a workgroup per CU (two for 128 x 128)
+  auto choose = [&](auto count, std::initializer_list<int> tiles) {
+    int best = 64;
+    double least = 0;
+    for (int t : tiles) {
+      const double rounds = (double)(L * count(t)) / (t == 128 ? 2 * kCus : kCus), whole = (double)(int64_t)rounds;
+      const double part = rounds - whole;
+      const double cost = (whole + (part > 0 ? (t == 128 ? (part > 0.5 ? part : 0.5) : 0.9) : 0)) * (t == 128 ? 0.55 : t / 256.0 * t / 256.0 * (t == 192 ? 1.06 : 1.0));
+      if (least == 0 || cost < least) least = cost, best = t;
+    }
+    return best;
+  };
+  if (L * all(64) <= kCus) o.tile = 64;
+  else o.tile = o.split ? 128 : choose(all, {256, 128});
+  if (L * sym(64) <= kCus) o.tile_sym = 64;
+  else o.tile_sym = o.split ? 128 : choose(sym, {256, 192, 128});
+  o.symmetric = sym(o.tile_sym);
+  o.whole = all(o.tile);
   const int64_t mn = L * o.m * o.n * 2, mm = L * o.m * o.m * 2;
   o.bytes = mn * (o.split ? 6 : 4) + mm * (o.split ? 4 : 2);
   o.bytes += L * (kNormParts * 8 + 2 * o.m * 4 + o.whole * 16 + 16);
@@ -514,10 +546,15 @@ int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool bf16) { retu
 
 template <Product kWhat, Result kOut, bool kSplit>
 static void launch_product(const OrthoArgs& a, int64_t L, int tile, hipStream_t stream) {
-  const dim3 grid((unsigned)(L * a.count)), block(256);
-  if (tile == 64) hipLaunchKernelGGL((ortho_product_kernel<kWhat, kOut, kSplit, 64, 64, 5>), grid, block, 0, stream, a);
-  else if (tile == 128) hipLaunchKernelGGL((ortho_product_kernel<kWhat, kOut, kSplit, 128, 128, 2>), grid, block, 0, stream, a);
-  else if constexpr (!kSplit) hipLaunchKernelGGL((ortho_product_kernel<kWhat, kOut, kSplit, 256, 256, 2>), grid, block, 0, stream, a);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)(L * a.count)), dim3(256), 0, stream, a); };
+  if (tile == 64) return go(ortho_product_kernel<kWhat, kOut, kSplit, 64, 64, 5>);
+  if (tile == 128) return go(ortho_product_kernel<kWhat, kOut, kSplit, 128, 128, 2>);
+  if constexpr (!kSplit) {
+    if constexpr (kWhat != Product::kUpdate) {
+      if (tile == 192) return go(ortho_product_kernel<kWhat, kOut, kSplit, 192, 192, 2>);
+    }
+    go(ortho_product_kernel<kWhat, kOut, kSplit, 256, 256, 2>);
+  }
 }
 
 template <bool kSplit>
@@ -538,8 +575,8 @@ static hipError_t run_ortho(const void* g, bool g_bf16, int64_t L, int64_t M, in
     p.xt = xt[k % 2], p.xt_lo = xt_lo[k % 2];
     p.xt_new = xt[1 - k % 2], p.xt_lo_new = xt_lo[1 - k % 2];
     p.count = (int)o.symmetric;
-    launch_product<Product::kGram, Result::kPlanes, kSplit>(p, L, o.tile, stream);
-    launch_product<Product::kSquare, Result::kPlanes, kSplit>(p, L, o.tile, stream);
+    launch_product<Product::kGram, Result::kPlanes, kSplit>(p, L, o.tile_sym, stream);
+    launch_product<Product::kSquare, Result::kPlanes, kSplit>(p, L, o.tile_sym, stream);
     p.count = (int)o.whole;
     if (k < steps - 1) launch_product<Product::kUpdate, Result::kPlanes, kSplit>(p, L, o.tile, stream);
     else if (bf16) launch_product<Product::kUpdate, Result::kBf16, kSplit>(p, L, o.tile, stream);
