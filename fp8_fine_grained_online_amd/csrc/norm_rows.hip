@@ -23,13 +23,35 @@
 
 namespace fp8q {
 
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr int64_t kBwdWorkgroups = 256;  // of the gradient: one per CU
+
 // kThreads per row (64: a wavefront; else a whole number of them), kChunks of
 // eight values per thread: value 8 (t + kThreads i) + e belongs to thread t.
 template <int kThreads, int kChunks>
 struct RowShape {
   static constexpr int kT = kThreads, kC = kChunks;
   static constexpr int kMaxK = 8 * kThreads * kChunks;
+  static constexpr bool kFew = false;
 };
+// Rows of 1 to 7 values: one thread has them all
+struct FewShape : RowShape<64, 1> {
+  static constexpr bool kFew = true;
+};
+
+template <typename Shape, typename T>
+__device__ __forceinline__ Chunk<T> load_row_chunk(const T* row, int at, int K) {
+  if constexpr (Shape::kFew) return load_few(row + at, K);
+  else return load_in_row(row, at, K);
+}
+
+// Eight weights, whose type is known at run time only
+template <typename Shape>
+__device__ __forceinline__ void row_weights(const void* w, bool bf16, int at, int K, float (&f)[8]) {
+  if (bf16) values(load_row_chunk<Shape>((const bf16_t*)w, at, K), f);
+  else values(load_row_chunk<Shape>((const float*)w, at, K), f);
+}
 
 // Sums over the threads of a row, the same bits in all of them. `slot`: LDS for
 // kN sums of each of the row's wavefronts; a barrier separates two calls' uses of
@@ -71,12 +93,22 @@ struct RowStats {
   bool wide;  // the statistics are in the doubles
 };
 
+// An empty asm that "modifies" the values: what was computed from them before, their
+// float64 forms above all, cannot be kept in registers for a later pass.
+template <int C>
+__device__ __forceinline__ void forget(float (&v)[C][8]) {
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(v[i][e]));
+}
+
 // Statistics of the row whose values are in v; absent values are zeros.
 // `present(i)`: how many of chunk i's values exist (0 to 8). kTogether: other rows
 // of the workgroup meet the same barriers, so one that needs the wide way takes all
 // along (who did not need it keeps what it had).
 template <typename Shape, bool kCentred, bool kTogether, typename Present>
-__device__ __forceinline__ RowStats row_stats(const float (&v)[Shape::kC][8], Present present, int K, float eps,
+__device__ __forceinline__ RowStats row_stats(float (&v)[Shape::kC][8], Present present, int K, float eps,
                                               RowLds<Shape::kT>& lds) {
   constexpr int T = Shape::kT, C = Shape::kC;
   RowStats s;
@@ -111,6 +143,7 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[Shape::kC][8], Pr
   s.r = (float)(1.0 / __dsqrt_rn((double)var + (double)eps));
   s.shift = off * s.r;
   if (!(kTogether ? __syncthreads_or(s.wide) : s.wide)) return s;
+  forget(v);
   if constexpr (kCentred) {
     double sum[1] = {0.0};
 #pragma unroll
@@ -119,6 +152,7 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[Shape::kC][8], Pr
       for (int e = 0; e < 8; ++e) sum[0] += (double)v[i][e];
     row_sums<T, 1>(sum, lds.wide[0]);
     s.wide_mu = sum[0] / (double)K;
+    forget(v);
   }
   double sq[1] = {0.0};
 #pragma unroll
@@ -133,14 +167,24 @@ __device__ __forceinline__ RowStats row_stats(const float (&v)[Shape::kC][8], Pr
   row_sums<T, 1>(sq, lds.wide[1]);
   s.wide_r = 1.0 / __dsqrt_rn(sq[0] / (double)K + (double)eps);
   if (s.wide) s.r = (float)s.wide_r;
+  forget(v);
   return s;
 }
 
-template <bool kCentred>
-__device__ __forceinline__ float hat(float v, const RowStats& s) {
-  if (s.wide) return (float)(((double)v - s.wide_mu) * s.wide_r);
-  if constexpr (kCentred) return __builtin_fmaf(v - s.mu, s.r, -s.shift);
-  return v * s.r;
+// v becomes hat. The branch is the row's, so the wavefront's.
+template <bool kCentred, int C>
+__device__ __forceinline__ void to_hat(float (&v)[C][8], const RowStats& s) {
+  if (__builtin_amdgcn_readfirstlane(s.wide)) {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = (float)(((double)v[i][e] - s.wide_mu) * s.wide_r);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = kCentred ? __builtin_fmaf(v[i][e] - s.mu, s.r, -s.shift) : v[i][e] * s.r;
 }
 
 // ---------------------------------------------------------------------------
@@ -163,7 +207,7 @@ template <typename Shape, typename X, typename Y, bool kCentred>
 __global__ __launch_bounds__(kRowThreads<Shape>) void norm_rows_kernel(NormArgs p) {
   constexpr int T = Shape::kT, C = Shape::kC, kRows = kRowThreads<Shape> / T;
   __shared__ RowLds<T> lds[kRows];
-  const int tid = threadIdx.x % T, sub = threadIdx.x / T;
+  const int tid = threadIdx.x % T, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
   const int64_t m = (int64_t)blockIdx.x * kRows + sub;
   if (m >= p.M) return;  // (kRows > 1: rows are single wavefronts, which meet no barrier)
   const int chunks = (p.K + 7) / 8;
@@ -173,7 +217,7 @@ __global__ __launch_bounds__(kRowThreads<Shape>) void norm_rows_kernel(NormArgs 
   Chunk<X> raw[C];
 #pragma unroll
   for (int i = 0; i < C; ++i)
-    raw[i] = tid + T * i < chunks ? load_chunk(x + at(i), present(i)) : zero_chunk(X{});
+    raw[i] = tid + T * i < chunks ? load_row_chunk<Shape>(x, at(i), p.K) : zero_chunk(X{});
   float v[C][8];
 #pragma unroll
   for (int i = 0; i < C; ++i) values(raw[i], v[i]);
@@ -181,7 +225,7 @@ __global__ __launch_bounds__(kRowThreads<Shape>) void norm_rows_kernel(NormArgs 
     const X* const res = (const X*)p.res + m * p.ldr;
     X* const h = (X*)p.h + m * (int64_t)p.K;
 #pragma unroll
-    for (int i = 0; i < C; ++i) raw[i] = tid + T * i < chunks ? load_chunk(res + at(i), present(i)) : zero_chunk(X{});
+    for (int i = 0; i < C; ++i) raw[i] = tid + T * i < chunks ? load_row_chunk<Shape>(res, at(i), p.K) : zero_chunk(X{});
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float r[8];
@@ -194,17 +238,18 @@ __global__ __launch_bounds__(kRowThreads<Shape>) void norm_rows_kernel(NormArgs 
     }
   }
   const RowStats s = row_stats<Shape, kCentred, false>(v, present, p.K, p.eps, lds[sub]);
+  to_hat<kCentred>(v, s);
   Y* const y = (Y*)p.y + m * (int64_t)p.K;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     if (tid + T * i >= chunks) break;
     const int have = present(i);
     float g[8], b[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    load_weights(p.gamma, p.weights_bf16, at(i), have, g);
-    if (kCentred && p.beta) load_weights(p.beta, p.weights_bf16, at(i), have, b);
+    row_weights<Shape>(p.gamma, p.weights_bf16, at(i), p.K, g);
+    if (kCentred && p.beta) row_weights<Shape>(p.beta, p.weights_bf16, at(i), p.K, b);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      g[e] *= hat<kCentred>(v[i][e], s);
+      g[e] *= v[i][e];
       if (kCentred && p.beta) g[e] += b[e];
     }
     Chunk<Y> out;
@@ -214,14 +259,13 @@ __global__ __launch_bounds__(kRowThreads<Shape>) void norm_rows_kernel(NormArgs 
 }
 
 // ---------------------------------------------------------------------------
-// Gradient. A workgroup of kBwdThreads takes rows in turn, kRows at once; a
-// thread's columns are the same in each, so the weights' gradients are sums in
-// its registers, joined at the end over the workgroup's rows in LDS and written
+// Gradient. A workgroup of kWg threads takes rows in turn, kWg / kT at once, the
+// next ones' loads on their way while it works on these; gamma stays in LDS. A
+// thread's columns are the same in every row, so the weights' gradients are sums
+// in its registers, joined at the end over the workgroup's rows in LDS and written
 // as one row of partial sums. A second kernel adds those in order: no atomics,
 // and the same bits every time.
 // ---------------------------------------------------------------------------
-constexpr int kBwdThreads = 512;
-
 struct NormBwdArgs {
   const void *dy, *x, *gamma, *dres;
   void* dx;
@@ -232,23 +276,31 @@ struct NormBwdArgs {
   bool weights_bf16;
 };
 
-template <typename Shape, typename X, typename D, bool kCentred>
-__global__ __launch_bounds__(kBwdThreads) void norm_rows_bwd_kernel(NormBwdArgs p) {
-  constexpr int T = Shape::kT, C = Shape::kC, kRows = kBwdThreads / T;
+template <typename Shape, int kWg, typename X, typename D, bool kCentred>
+__global__ __launch_bounds__(kWg) void norm_rows_bwd_kernel(NormBwdArgs p) {
+  constexpr int T = Shape::kT, C = Shape::kC, kRows = kWg / T;
   constexpr int kSums = kCentred ? 2 : 1;
-  constexpr int kJoin = kRows > 1 ? kSums * 8 * T * C : 1;  // one row's columns
-  struct Lds {
-    RowLds<T> row[kRows];
-    float two[kRows][T / 64][2];
+  struct Slots {
+    RowLds<T> row;
+    float sums[T / 64][2];
   };
-  __shared__ union {
-    Lds rows;
-    float join[kJoin];
-  } lds;
-  const int tid = threadIdx.x % T, sub = threadIdx.x / T;
+  __shared__ Slots slots[kRows];
+  extern __shared__ __attribute__((aligned(16))) float shared[];  // gamma, padded to whole chunks; then sums to join
+  const int tid = threadIdx.x % T, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
   const int chunks = (p.K + 7) / 8;
   auto at = [&](int i) { return 8 * (tid + T * i); };
   auto present = [&](int i) { return min(max(p.K - at(i), 0), 8); };
+  for (int c = threadIdx.x; c < chunks; c += kWg) {
+    float g[8];
+    row_weights<Shape>(p.gamma, p.weights_bf16, 8 * c, p.K, g);  // absent ones are zeros
+    *(v4f*)(shared + 8 * c) = v4f{g[0], g[1], g[2], g[3]};
+    *(v4f*)(shared + 8 * c + 4) = v4f{g[4], g[5], g[6], g[7]};
+  }
+  auto gamma_of = [&](int i, float (&g)[8]) {
+    const v4f a = *(const v4f*)(shared + at(i)), b = *(const v4f*)(shared + at(i) + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) g[e] = a[e], g[4 + e] = b[e];
+  };
   float dgamma[C][8], dbeta[kCentred ? C : 1][8];
 #pragma unroll
   for (int i = 0; i < C; ++i)
@@ -257,64 +309,82 @@ __global__ __launch_bounds__(kBwdThreads) void norm_rows_bwd_kernel(NormBwdArgs 
       dgamma[i][e] = 0.0f;
       if constexpr (kCentred) dbeta[i][e] = 0.0f;
     }
+  Chunk<X> rx[C], rr[C];
+  Chunk<D> rd[C];
+  auto read_rows = [&](int64_t m) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const bool have = m < p.M && tid + T * i < chunks;
+      rx[i] = have ? load_row_chunk<Shape>((const X*)p.x + m * p.ldx, at(i), p.K) : zero_chunk(X{});
+      rd[i] = have ? load_row_chunk<Shape>((const D*)p.dy + m * p.ldy, at(i), p.K) : zero_chunk(D{});
+      rr[i] = have && p.dres ? load_row_chunk<Shape>((const X*)p.dres + m * p.ldr, at(i), p.K) : zero_chunk(X{});
+    }
+  };
   const float inv_k = 1.0f / (float)p.K;
+  read_rows((int64_t)blockIdx.x * kRows + sub);
+  __syncthreads();
   // every thread of the workgroup makes the same number of rounds (barriers inside)
   for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < p.M; m0 += (int64_t)gridDim.x * kRows) {
     const int64_t m = m0 + sub;
-    const bool row = m < p.M;
-    Chunk<X> rx[C];
-    Chunk<D> rd[C];
+    float v[C][8];
+    Chunk<D> d_now[C];
+    Chunk<X> r_now[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const bool have = row && tid + T * i < chunks;
-      rx[i] = have ? load_chunk((const X*)p.x + m * p.ldx + at(i), present(i)) : zero_chunk(X{});
-      rd[i] = have ? load_chunk((const D*)p.dy + m * p.ldy + at(i), present(i)) : zero_chunk(D{});
+      values(rx[i], v[i]);
+      d_now[i] = rd[i];
+      r_now[i] = rr[i];
     }
-    float v[C][8];
-#pragma unroll
-    for (int i = 0; i < C; ++i) values(rx[i], v[i]);
-    const RowStats s = row_stats<Shape, kCentred, (T > 64 && kRows > 1)>(v, present, p.K, p.eps, lds.rows.row[sub]);
-    // v becomes hat
+    read_rows(m + (int64_t)gridDim.x * kRows);
+    const RowStats s = row_stats<Shape, kCentred, (T > 64 && kRows > 1)>(v, present, p.K, p.eps, slots[sub].row);
+    to_hat<kCentred>(v, s);
     float sums[2] = {0.0f, 0.0f};  // of dg hat, of dg
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      float d[8], g[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      const int have = present(i);
-      if (have) load_weights(p.gamma, p.weights_bf16, at(i), have, g);
-      values(rd[i], d);
+      if (tid + T * i >= chunks) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+        continue;
+      }
+      float d[8], g[8];
+      gamma_of(i, g);
+      values(d_now[i], d);
+      // (dy and gamma are zero past the row's end, and a row that is not there has zeros throughout,
+      // but its hat may not be finite)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[i][e] = hat<kCentred>(v[i][e], s);
-        if (row && e < have) dgamma[i][e] = __builtin_fmaf(d[e], v[i][e], dgamma[i][e]);
+        if (m < p.M) dgamma[i][e] = __builtin_fmaf(d[e], v[i][e], dgamma[i][e]);
         if constexpr (kCentred) dbeta[i][e] += d[e];
         const float dg = d[e] * g[e];
-        if (e < have) sums[0] = __builtin_fmaf(dg, v[i][e], sums[0]);
+        sums[0] = __builtin_fmaf(dg, v[i][e], sums[0]);
         sums[1] += dg;
       }
     }
-    row_sums<T, 2>(sums, lds.rows.two[sub]);
+    row_sums<T, 2>(sums, slots[sub].sums);
     const float c_hat = sums[0] * inv_k, c_one = kCentred ? sums[1] * inv_k : 0.0f;
+    if (m < p.M) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int have = present(i);
-      if (!row || !have) continue;
-      float d[8], g[8], o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      load_weights(p.gamma, p.weights_bf16, at(i), have, g);
-      values(rd[i], d);
-      if (p.dres) values(load_chunk((const X*)p.dres + m * p.ldr + at(i), have), o);
+      for (int i = 0; i < C; ++i) {
+        if (tid + T * i >= chunks) break;
+        float d[8], g[8], o[8];
+        gamma_of(i, g);
+        values(d_now[i], d);
+        values(r_now[i], o);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float t = __builtin_fmaf(-v[i][e], c_hat, d[e] * g[e] - c_one);
-        o[e] = __builtin_fmaf(s.r, t, o[e]);
+        for (int e = 0; e < 8; ++e) {
+          const float t = __builtin_fmaf(-v[i][e], c_hat, d[e] * g[e] - c_one);
+          o[e] = __builtin_fmaf(s.r, t, o[e]);
+        }
+        Chunk<X> out;
+        to_chunk(o, out);
+        store_chunk((X*)p.dx + m * (int64_t)p.K + at(i), out, present(i));
       }
-      Chunk<X> out;
-      to_chunk(o, out);
-      store_chunk((X*)p.dx + m * (int64_t)p.K + at(i), out, have);
     }
     if constexpr (T > 64) __syncthreads();  // the slots are used again
   }
   // join the workgroup's rows, in order
   if constexpr (kRows > 1) {
+    float* const join = shared;  // (gamma has been read)
     for (int r = 0; r < kRows; ++r) {
       __syncthreads();
       if (sub == r) {
@@ -322,20 +392,13 @@ __global__ __launch_bounds__(kBwdThreads) void norm_rows_bwd_kernel(NormBwdArgs 
         for (int i = 0; i < C; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float* const to = lds.join + (i * 8 + e) * T + tid;
-            *to = r ? *to + dgamma[i][e] : dgamma[i][e];
-            if constexpr (kCentred) to[8 * T * C] = r ? to[8 * T * C] + dbeta[i][e] : dbeta[i][e];
+            float* const to = join + (i * 8 + e) * T + tid;
+            dgamma[i][e] = *to = r ? *to + dgamma[i][e] : dgamma[i][e];
+            if constexpr (kCentred) dbeta[i][e] = to[8 * T * C] = r ? to[8 * T * C] + dbeta[i][e] : dbeta[i][e];
           }
       }
     }
     if (sub != kRows - 1) return;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dgamma[i][e] = lds.join[(i * 8 + e) * T + tid];
-        if constexpr (kCentred) dbeta[i][e] = lds.join[8 * T * C + (i * 8 + e) * T + tid];
-      }
   }
   float* const part = p.partial + (int64_t)blockIdx.x * kSums * p.K;
 #pragma unroll
@@ -352,8 +415,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_rows_bwd_kernel(NormBwdArgs 
   }
 }
 
-// Sums of the partial rows: 64 columns and 16 runs of rows per workgroup.
-constexpr int kJoinCols = 64, kJoinRuns = 16;
+// Sums of the partial rows: 32 columns and 32 runs of rows per workgroup.
+constexpr int kJoinCols = 32, kJoinRuns = 32;
 
 __global__ __launch_bounds__(kJoinCols* kJoinRuns) void join_partials_kernel(const float* __restrict__ partial, int rows,
                                                                              int cols, int K, float* __restrict__ dgamma,
@@ -362,6 +425,7 @@ __global__ __launch_bounds__(kJoinCols* kJoinRuns) void join_partials_kernel(con
   const int c = blockIdx.x * kJoinCols + threadIdx.x % kJoinCols, run = threadIdx.x / kJoinCols;
   float s = 0.0f;
   if (c < cols) {
+#pragma unroll 8
     for (int r = run; r < rows; r += kJoinRuns) s += partial[(int64_t)r * cols + c];
   }
   runs[run][threadIdx.x % kJoinCols] = s;
@@ -384,6 +448,7 @@ static void launch_fwd(const NormArgs& a, bool centred, hipStream_t stream) {
 
 template <typename X, typename Y>
 static void launch_fwd_shape(const NormArgs& a, bool centred, hipStream_t stream) {
+  if (a.K < 8) return launch_fwd<FewShape, X, Y>(a, centred, stream);
   if (a.K <= RowShape<64, 1>::kMaxK) return launch_fwd<RowShape<64, 1>, X, Y>(a, centred, stream);
   if (a.K <= RowShape<64, 2>::kMaxK) return launch_fwd<RowShape<64, 2>, X, Y>(a, centred, stream);
   if (a.K <= RowShape<64, 4>::kMaxK) return launch_fwd<RowShape<64, 4>, X, Y>(a, centred, stream);
@@ -406,33 +471,58 @@ hipError_t launch_norm_rows(const void* x, bool x_bf16, int64_t ldx, const void*
   return hipGetLastError();
 }
 
-// Workgroups of the gradient: one per CU, fewer for few rows. `threads`: of a row.
-static int bwd_threads(int64_t K) { return K <= 2048 ? 64 : K <= 8192 ? 256 : 512; }
-static int64_t bwd_workgroups(int64_t M, int64_t K) {
-  const int rows = kBwdThreads / bwd_threads(K);
+// The gradient's threads per row and per workgroup, and its workgroups: up to one
+// per CU and 512 threads, fewer for few rows. float32 rows are shared by twice as
+// many threads as bfloat16 ones from 2048 values on, since a thread holds its part
+// of two rows at a time.
+struct BwdPlan {
+  int threads, group;
+  int64_t workgroups;
+};
+static BwdPlan bwd_plan(int64_t M, int64_t K, bool wide) {
+  BwdPlan b;
+  b.threads = K <= 1024 || (K <= 2048 && !wide) ? 64 : K <= 2048 ? 128 : K <= 4096 || (K <= 8192 && !wide) ? 256 : K <= 8192 || !wide ? 512 : 1024;
+  b.group = b.threads > 512 ? b.threads : 512;
+  const int rows = b.group / b.threads;
   const int64_t need = (M + rows - 1) / rows;
-  return need < 256 ? need : 256;
+  b.workgroups = need < kBwdWorkgroups ? need : kBwdWorkgroups;
+  return b;
 }
 
+// (of either type: a workspace fits both)
 int64_t norm_bwd_workspace_bytes(int64_t M, int64_t K, bool centred) {
-  return bwd_workgroups(M, K) * (centred ? 2 : 1) * K * (int64_t)sizeof(float);
+  const int64_t a = bwd_plan(M, K, false).workgroups, b = bwd_plan(M, K, true).workgroups;
+  return (a > b ? a : b) * (centred ? 2 : 1) * K * (int64_t)sizeof(float);
 }
 
 template <typename Shape, typename X, typename D>
-static void launch_bwd(const NormBwdArgs& a, bool centred, hipStream_t stream) {
-  const dim3 grid((unsigned)bwd_workgroups(a.M, a.K)), block(kBwdThreads);
-  if (centred) hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, X, D, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, X, D, false>), grid, block, 0, stream, a);
+static void launch_bwd(const NormBwdArgs& a, bool centred, const BwdPlan& b, hipStream_t stream) {
+  constexpr int kT = Shape::kT;
+  constexpr int kWg = kT > 512 ? kT : 512;
+  const dim3 grid((unsigned)b.workgroups), block(kWg);
+  const size_t gamma = (size_t)(a.K + 7) / 8 * 32, join = kWg > kT ? (size_t)(centred ? 2 : 1) * Shape::kMaxK * 4 : 0;
+  const size_t lds = gamma > join ? gamma : join;
+  if (centred) hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, kWg, X, D, true>), grid, block, lds, stream, a);
+  else hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, kWg, X, D, false>), grid, block, lds, stream, a);
 }
 
 template <typename X, typename D>
-static void launch_bwd_shape(const NormBwdArgs& a, bool centred, hipStream_t stream) {
-  if (a.K <= RowShape<64, 1>::kMaxK) return launch_bwd<RowShape<64, 1>, X, D>(a, centred, stream);
-  if (a.K <= RowShape<64, 2>::kMaxK) return launch_bwd<RowShape<64, 2>, X, D>(a, centred, stream);
-  if (a.K <= RowShape<64, 4>::kMaxK) return launch_bwd<RowShape<64, 4>, X, D>(a, centred, stream);
-  if (a.K <= RowShape<256, 2>::kMaxK) return launch_bwd<RowShape<256, 2>, X, D>(a, centred, stream);
-  if (a.K <= RowShape<256, 4>::kMaxK) return launch_bwd<RowShape<256, 4>, X, D>(a, centred, stream);
-  launch_bwd<RowShape<512, 4>, X, D>(a, centred, stream);
+static void launch_bwd_shape(const NormBwdArgs& a, bool centred, const BwdPlan& b, hipStream_t stream) {
+  constexpr bool kWide = sizeof(X) == 4 || sizeof(D) == 4;
+  if (a.K < 8) return launch_bwd<FewShape, X, D>(a, centred, b, stream);
+  if (a.K <= 512) return launch_bwd<RowShape<64, 1>, X, D>(a, centred, b, stream);
+  if (a.K <= 1024) return launch_bwd<RowShape<64, 2>, X, D>(a, centred, b, stream);
+  if constexpr (kWide) {
+    if (a.K <= 2048) return launch_bwd<RowShape<128, 2>, X, D>(a, centred, b, stream);
+    if (a.K <= 4096) return launch_bwd<RowShape<256, 2>, X, D>(a, centred, b, stream);
+    if (a.K <= 8192) return launch_bwd<RowShape<512, 2>, X, D>(a, centred, b, stream);
+    launch_bwd<RowShape<1024, 2>, X, D>(a, centred, b, stream);
+  } else {
+    if (a.K <= 2048) return launch_bwd<RowShape<64, 4>, X, D>(a, centred, b, stream);
+    if (a.K <= 4096) return launch_bwd<RowShape<256, 2>, X, D>(a, centred, b, stream);
+    if (a.K <= 8192) return launch_bwd<RowShape<256, 4>, X, D>(a, centred, b, stream);
+    launch_bwd<RowShape<512, 4>, X, D>(a, centred, b, stream);
+  }
 }
 
 hipError_t launch_norm_rows_bwd(const void* dy, bool dy_bf16, int64_t ldy, const void* x, bool x_bf16, int64_t ldx,
@@ -440,19 +530,20 @@ hipError_t launch_norm_rows_bwd(const void* dy, bool dy_bf16, int64_t ldy, const
                                 bool centred, int64_t M, int64_t K, void* dx, float* dgamma, float* dbeta, void* ws,
                                 hipStream_t stream) {
   const NormBwdArgs a{dy, x, gamma, dres, dx, (float*)ws, ldy, ldx, ldr, (int)M, (int)K, eps, weights_bf16};
+  const BwdPlan b = bwd_plan(M, K, !x_bf16 || !dy_bf16);
   if (M > 0) {
     if (x_bf16) {
-      if (dy_bf16) launch_bwd_shape<bf16_t, bf16_t>(a, centred, stream);
-      else launch_bwd_shape<bf16_t, float>(a, centred, stream);
+      if (dy_bf16) launch_bwd_shape<bf16_t, bf16_t>(a, centred, b, stream);
+      else launch_bwd_shape<bf16_t, float>(a, centred, b, stream);
     } else {
-      if (dy_bf16) launch_bwd_shape<float, bf16_t>(a, centred, stream);
-      else launch_bwd_shape<float, float>(a, centred, stream);
+      if (dy_bf16) launch_bwd_shape<float, bf16_t>(a, centred, b, stream);
+      else launch_bwd_shape<float, float>(a, centred, b, stream);
     }
     if (hipError_t e = hipGetLastError()) return e;
   }
   const int cols = (int)K * (centred ? 2 : 1);
   hipLaunchKernelGGL(join_partials_kernel, dim3((unsigned)((cols + kJoinCols - 1) / kJoinCols)),
-                     dim3(kJoinCols * kJoinRuns), 0, stream, (const float*)ws, (int)bwd_workgroups(M, K), cols, (int)K,
+                     dim3(kJoinCols * kJoinRuns), 0, stream, (const float*)ws, (int)b.workgroups, cols, (int)K,
                      dgamma, dbeta);
   return hipGetLastError();
 }

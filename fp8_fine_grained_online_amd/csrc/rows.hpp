@@ -29,28 +29,64 @@ struct Chunk<float> {
 __device__ __forceinline__ Chunk<bf16_t> zero_chunk(bf16_t) { return {u32x4{0, 0, 0, 0}}; }
 __device__ __forceinline__ Chunk<float> zero_chunk(float) { return {{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}}}; }
 
-// `have` values (1 to 8) at p; those beyond are zero
-__device__ __forceinline__ Chunk<bf16_t> load_chunk(const bf16_t* p, int have) {
+// A whole chunk at p
+__device__ __forceinline__ Chunk<bf16_t> load_whole(const bf16_t* p) { return {*(const u32x4_by2*)p}; }
+__device__ __forceinline__ Chunk<float> load_whole(const float* p) {
+  return {{*(const u32x4_by4*)p, *(const u32x4_by4*)(p + 4)}};
+}
+
+// `have` values (0 to 7) at p, one by one; those beyond are zero
+__device__ __forceinline__ Chunk<bf16_t> load_few(const bf16_t* p, int have) {
   Chunk<bf16_t> c = zero_chunk(bf16_t{});
-  if (have >= 8) {
-    c.v = *(const u32x4_by2*)p;
-  } else {
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (e < have) c.v[e / 2] |= (uint32_t)p[e].bits << (16 * (e & 1));
-  }
+  for (int e = 0; e < 7; ++e)
+    if (e < have) c.v[e / 2] |= (uint32_t)p[e].bits << (16 * (e & 1));
   return c;
 }
-__device__ __forceinline__ Chunk<float> load_chunk(const float* p, int have) {
+__device__ __forceinline__ Chunk<float> load_few(const float* p, int have) {
   Chunk<float> c = zero_chunk(0.0f);
-  if (have >= 8) {
-    c.v[0] = *(const u32x4_by4*)p;
-    c.v[1] = *(const u32x4_by4*)(p + 4);
-  } else {
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (e < have) c.v[e / 4][e % 4] = __float_as_uint(p[e]);
-  }
+  for (int e = 0; e < 7; ++e)
+    if (e < have) c.v[e / 4][e % 4] = __float_as_uint(p[e]);
+  return c;
+}
+
+// `have` values (1 to 8) at p; those beyond are zero
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_chunk(const T* p, int have) {
+  return have >= 8 ? load_whole(p) : load_few(p, have);
+}
+
+// The chunk without its first n values (0 to 7), zeros behind
+__device__ __forceinline__ Chunk<bf16_t> shifted(const Chunk<bf16_t>& c, int n) {
+  uint64_t lo = (uint64_t)c.v[1] << 32 | c.v[0], hi = (uint64_t)c.v[3] << 32 | c.v[2];
+  if (n & 4) lo = hi, hi = 0;
+  const int bits = 16 * (n & 3);
+  if (bits) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
+  return {u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)}};
+}
+__device__ __forceinline__ Chunk<float> shifted(const Chunk<float>& c, int n) {
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = c.v[e / 4][e % 4];
+#pragma unroll
+  for (int b = 1; b <= 4; b <<= 1)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = n & b ? (e + b < 8 ? w[e + b] : 0u) : w[e];
+  Chunk<float> o;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o.v[e / 4][e % 4] = w[e];
+  return o;
+}
+
+// Values at .. at + 7 of a row of K >= 8; zeros past its end. The chunk that ends
+// past the row is loaded whole all the same, so that it ends with the row, and
+// shifted into place.
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_in_row(const T* row, int at, int K) {
+  const int past = at + 8 - K;
+  Chunk<T> c = load_whole(row + (past > 0 ? K - 8 : at));
+  if (past > 0) c = shifted(c, past);
   return c;
 }
 
@@ -98,12 +134,6 @@ __device__ __forceinline__ void store_chunk(float* p, const Chunk<float>& c, int
     for (int e = 0; e < 7; ++e)
       if (e < have) p[e] = __uint_as_float(c.v[e / 4][e % 4]);
   }
-}
-
-// eight weights, whose type is known at run time only
-__device__ __forceinline__ void load_weights(const void* w, bool bf16, int64_t at, int have, float (&f)[8]) {
-  if (bf16) values(load_chunk((const bf16_t*)w + at, have), f);
-  else values(load_chunk((const float*)w + at, have), f);
 }
 
 }  // namespace fp8q
