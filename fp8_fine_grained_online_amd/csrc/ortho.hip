@@ -102,6 +102,101 @@ __device__ __forceinline__ int swz_chunk(int r, int c, int n) { return (n & (n -
 
 enum class Result { kPlanes, kBf16, kF32 };
 
+// One value of a product's result, scaled as it is stored: from the product, and what
+// the result's place held before (high and low part of X or A; the diagonal's cuts of its
+// row and column).
+template <Product kWhat, bool kSplit>
+__device__ __forceinline__ float ortho_value(const OrthoArgs& p, float acc, float hi, float lo, float cut_m, float cut_n,
+                                             bool diagonal, float alpha) {
+  if constexpr (kWhat == Product::kGram) {
+    const float v = acc * (kScaleA / (kScaleX * kScaleX));
+    return diagonal ? v - kScaleA * alpha : v;
+  } else if constexpr (kWhat == Product::kSquare) {
+    const float whole = hi + (kSplit ? lo : diagonal ? cut_m : 0.0f);
+    const float sq = __builtin_fmaf(kSplit ? 0.0f : cut_m + cut_n, hi, acc) * (1.0f / kScaleA);
+    return __builtin_fmaf(p.c, sq, (p.b + 2.0f * p.c * alpha) * whole);
+  } else {
+    const float q = p.a + alpha * (p.b + alpha * p.c) + cut_m * (1.0f / kScaleA);
+    return __builtin_fmaf(q, hi + lo, acc * (1.0f / kScaleA));
+  }
+}
+
+// t-th of the tiles on and below the diagonal, row by row
+__device__ __forceinline__ void triangle_tile(int t, int& tm, int& tn) {
+  tm = (int)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+  while (tm * (tm + 1) / 2 > t) --tm;
+  while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
+  tn = t - tm * (tm + 1) / 2;
+}
+
+// Operands and result of a product for matrix `mat`: rows m0.. of a, rows n0.. of b, K values each
+struct OrthoOperands {
+  const _Float16 *a_hi, *a_lo, *b_hi, *b_lo;
+  int K, rows;  // `rows`: of b
+  int64_t mm, mn;
+};
+template <Product kWhat>
+__device__ __forceinline__ OrthoOperands ortho_operands(const OrthoArgs& p, int64_t mat) {
+  OrthoOperands o;
+  o.mm = mat * p.m * p.m, o.mn = mat * (int64_t)p.m * p.n;
+  if constexpr (kWhat == Product::kGram) o.a_hi = o.b_hi = p.x + o.mn, o.a_lo = o.b_lo = p.x_lo + o.mn, o.K = p.n, o.rows = p.m;
+  if constexpr (kWhat == Product::kSquare) o.a_hi = o.b_hi = p.am + o.mm, o.a_lo = o.b_lo = p.am_lo + o.mm, o.K = p.m, o.rows = p.m;
+  if constexpr (kWhat == Product::kUpdate)
+    o.a_hi = p.bm + o.mm, o.a_lo = p.bm_lo + o.mm, o.b_hi = p.xt + o.mn, o.b_lo = p.xt_lo + o.mn, o.K = p.m, o.rows = p.n;
+  return o;
+}
+
+// Where a result goes: rows of it, and columns (transposed); NULL for neither
+struct OrthoPlaces {
+  uint16_t *r, *r_lo, *c, *c_lo;
+  int64_t ld_r, ld_c;
+  int end_m, end_n;
+};
+template <Product kWhat, Result kOut>
+__device__ __forceinline__ OrthoPlaces ortho_places(const OrthoArgs& p, const OrthoOperands& o, int64_t mat, bool on_diagonal) {
+  OrthoPlaces w{nullptr, nullptr, nullptr, nullptr, 0, 0, p.m, o.rows};
+  if constexpr (kWhat != Product::kUpdate) {
+    w.r = (uint16_t*)((kWhat == Product::kGram ? p.am : p.bm) + o.mm);
+    w.r_lo = (uint16_t*)((kWhat == Product::kGram ? p.am_lo : p.bm_lo) + o.mm);
+    if (!on_diagonal) w.c = w.r, w.c_lo = w.r_lo;
+    w.ld_r = w.ld_c = p.m;
+  } else if constexpr (kOut == Result::kPlanes) {
+    w.r = (uint16_t*)(p.x + o.mn), w.r_lo = (uint16_t*)(p.x_lo + o.mn);
+    w.c = (uint16_t*)(p.xt_new + o.mn), w.c_lo = (uint16_t*)(p.xt_lo_new + o.mn);
+    w.ld_r = p.n, w.ld_c = p.m;
+  } else {
+    w.end_m = p.m_true, w.end_n = p.n_true;
+    if constexpr (kOut == Result::kBf16) (p.tall ? w.c : w.r) = (uint16_t*)p.out + mat * (int64_t)p.m_true * p.n_true;
+    w.ld_r = p.n_true, w.ld_c = p.m_true;
+  }
+  return w;
+}
+
+// alpha = |X|^2 / m from the last update's partial sums, by a whole workgroup
+__device__ __forceinline__ float ortho_alpha(const OrthoArgs& p, int64_t mat, float* sums, int threads) {
+  float s = 0.0f;
+  for (int i = threadIdx.x; i < p.parts; i += threads) s += p.squares[mat * p.parts + i];
+  s = wave_sum_f32(s);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = sums[0];
+  for (int w = 1; w < threads / 64; ++w) s += sums[w];
+  __syncthreads();
+  return s / (float)p.m_true;
+}
+
+// Neighbouring lanes (l ^ 1) hold four columns of neighbouring rows, packed in two
+// numbers of two: the even lane gets both rows' first two columns, the odd one the
+// others, each as a pair along the column.
+struct Turned {
+  uint32_t first, second;  // of columns 2 odd, 2 odd + 1
+};
+__device__ __forceinline__ Turned turn_pairs(bool odd, uint32_t p0, uint32_t p1) {
+  const uint32_t own = odd ? p1 : p0, got = dpp_u32<0xB1>(odd ? p0 : p1);
+  const uint32_t a = odd ? got : own, b = odd ? own : got;
+  return {(a & 0xFFFFu) | (b << 16), (a >> 16) | (b & 0xFFFF0000u)};
+}
+
 // ---------------------------------------------------------------------------
 // One tile of one product. Four wavefronts, each a quarter of the tile; per step
 // of 64 values of K the slabs of both operands go straight from global memory to
@@ -129,24 +224,15 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   int tm, tn;
   if constexpr (kSymmetric) {
     static_assert(!kSymmetric || BM == BN, "square tiles");
-    // t-th of the tiles on and below the diagonal, row by row
-    tm = (int)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-    while (tm * (tm + 1) / 2 > t) --tm;
-    while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
-    tn = t - tm * (tm + 1) / 2;
+    triangle_tile(t, tm, tn);
   } else {
     band_tile(t, (p.m + BM - 1) / BM, (p.n + BN - 1) / BN, tm, tn);
   }
   const int m0 = tm * BM, n0 = tn * BN;
-  const int64_t mm = mat * p.m * p.m, mn = mat * (int64_t)p.m * p.n;
-
-  // operands: rows m0.. of one, rows n0.. of the other, K values each
-  const _Float16 *a_hi, *a_lo, *b_hi, *b_lo;
-  int K, rows_total;
-  if constexpr (kWhat == Product::kGram) a_hi = b_hi = p.x + mn, a_lo = b_lo = p.x_lo + mn, K = p.n, rows_total = p.m;
-  if constexpr (kWhat == Product::kSquare) a_hi = b_hi = p.am + mm, a_lo = b_lo = p.am_lo + mm, K = p.m, rows_total = p.m;
-  if constexpr (kWhat == Product::kUpdate)
-    a_hi = p.bm + mm, a_lo = p.bm_lo + mm, b_hi = p.xt + mn, b_lo = p.xt_lo + mn, K = p.m, rows_total = p.n;
+  const OrthoOperands o = ortho_operands<kWhat>(p, mat);
+  const int64_t mm = o.mm, mn = o.mn;
+  const _Float16 *const a_hi = o.a_hi, *const a_lo = o.a_lo, *const b_hi = o.b_hi, *const b_lo = o.b_lo;
+  const int K = o.K, rows_total = o.rows;
   const int pitch = K * 2;  // bytes
   const uint32_t bytes_a = (uint32_t)min(BM, p.m - m0) * (uint32_t)pitch;
   const uint32_t bytes_b = (uint32_t)min(BN, rows_total - n0) * (uint32_t)pitch;
@@ -239,15 +325,8 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   const bool on_diagonal = kSymmetric && tm == tn;
   float alpha = 0.0f;
   if (kWhat == Product::kGram && p.pivot && on_diagonal) {
-    float s = 0.0f;
-    float* const sums = (float*)lds;
-    for (int i = tid; i < p.parts; i += 256) s += p.squares[mat * p.parts + i];
-    s = wave_sum_f32(s);
-    if (lane == 0) sums[wave] = s;
-    __syncthreads();
-    alpha = ((sums[0] + sums[1]) + (sums[2] + sums[3])) / (float)p.m_true;
+    alpha = ortho_alpha(p, mat, (float*)lds, 256);
     if (t == 0 && tid == 0) p.alpha[mat] = alpha;
-    __syncthreads();
   }
   if (kWhat != Product::kGram && p.pivot) alpha = p.alpha[mat];
 
@@ -259,7 +338,10 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   };
   constexpr bool kLowBefore = kWhat == Product::kUpdate || (kWhat == Product::kSquare && kSplit);
   auto read_before = [&](int i, Before& f) {
-    if constexpr (kWhat == Product::kGram) return;
+    if constexpr (kWhat == Product::kGram) {
+      f = Before{};
+      return;
+    }
     const int gm = mw + i * 16 + lr;
     f.cut = !kSplit && gm < p.m ? (kWhat == Product::kSquare ? p.da : p.db)[mat * p.m + gm] : 0.0f;
     const int64_t at = (kWhat == Product::kSquare ? mm : mn) + (int64_t)gm * rows_total + nw + 4 * lk;
@@ -273,8 +355,9 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
       f.lo[j] = kLowBefore && inside ? *(const f16x4*)(lo + j * 16) : none;
     }
   };
-  float cut_n[kWhat == Product::kSquare && !kSplit ? SUBN : 1][4];  // of the columns' diagonals
-  if constexpr (kWhat == Product::kSquare && !kSplit) {
+  constexpr bool kCutN = kWhat == Product::kSquare && !kSplit;
+  float cut_n[kCutN ? SUBN : 1][4] = {};  // of the columns' diagonals
+  if constexpr (kCutN) {
 #pragma unroll
     for (int j = 0; j < SUBN; ++j) {
       const int gn = nw + j * 16 + 4 * lk;
@@ -315,31 +398,16 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   // transposed: neighbouring lanes hold neighbouring rows; the even one writes the first two columns of both, the odd one the others
   auto put_col = [&](uint8_t* st, int i, int j, uint32_t p0, uint32_t p1) {
     const bool odd = lr & 1;
-    const uint32_t own = odd ? p1 : p0, got = dpp_u32<0xB1>(odd ? p0 : p1);
-    const uint32_t first = odd ? got : own, second = odd ? own : got;
+    const Turned w = turn_pairs(odd, p0, p1);
     uint8_t* const to = st + (j * 16 + 4 * lk + (odd ? 2 : 0)) * kPitchC + (i * 16 + (lr & ~1)) * 2;
-    *(uint32_t*)to = (first & 0xFFFFu) | (second << 16);
-    *(uint32_t*)(to + kPitchC) = (first >> 16) | (second & 0xFFFF0000u);
+    *(uint32_t*)to = w.first;
+    *(uint32_t*)(to + kPitchC) = w.second;
   };
 
-  // where rows of the tile go, and columns
-  uint16_t *to_r = nullptr, *to_r_lo = nullptr, *to_c = nullptr, *to_c_lo = nullptr;
-  int64_t ld_r = 0, ld_c = 0;
-  int end_m = p.m, end_n = rows_total;
-  if constexpr (kSymmetric) {
-    to_r = (uint16_t*)((kWhat == Product::kGram ? p.am : p.bm) + mm);
-    to_r_lo = (uint16_t*)((kWhat == Product::kGram ? p.am_lo : p.bm_lo) + mm);
-    if (!on_diagonal) to_c = to_r, to_c_lo = to_r_lo;
-    ld_r = ld_c = p.m;
-  } else if constexpr (kOut == Result::kPlanes) {
-    to_r = (uint16_t*)(p.x + mn), to_r_lo = (uint16_t*)(p.x_lo + mn);
-    to_c = (uint16_t*)(p.xt_new + mn), to_c_lo = (uint16_t*)(p.xt_lo_new + mn);
-    ld_r = p.n, ld_c = p.m;
-  } else {
-    end_m = p.m_true, end_n = p.n_true;
-    if constexpr (kOut == Result::kBf16) (p.tall ? to_c : to_r) = (uint16_t*)p.out + mat * (int64_t)p.m_true * p.n_true;
-    ld_r = p.n_true, ld_c = p.m_true;
-  }
+  const OrthoPlaces w = ortho_places<kWhat, kOut>(p, o, mat, on_diagonal);
+  uint16_t *const to_r = w.r, *const to_r_lo = w.r_lo, *const to_c = w.c, *const to_c_lo = w.c_lo;
+  const int64_t ld_r = w.ld_r, ld_c = w.ld_c;
+  const int end_m = w.end_m, end_n = w.end_n;
   constexpr bool kLowRows = kSplit || kWhat == Product::kUpdate;  // low parts are kept of X always
   float* const cut = (kWhat == Product::kGram ? p.da : p.db) + mat * p.m;
 
@@ -358,20 +426,9 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
       const int gn = nw + j * 16 + 4 * lk;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        if constexpr (kWhat == Product::kGram) {
-          val[j][r] = acc[i][j][r] * (kScaleA / (kScaleX * kScaleX));
-          if (on_diagonal && gm == gn + r) val[j][r] -= kScaleA * alpha;
-        } else if constexpr (kWhat == Product::kSquare) {
-          const float v = (float)f.hi[j][r];
-          const float whole = v + (kSplit ? (float)f.lo[j][r] : gm == gn + r ? f.cut : 0.0f);
-          const float cut = kSplit ? 0.0f : f.cut + cut_n[kSplit ? 0 : j][r];
-          const float sq = __builtin_fmaf(cut, v, acc[i][j][r]) * (1.0f / kScaleA);
-          val[j][r] = __builtin_fmaf(p.c, sq, (p.b + 2.0f * p.c * alpha) * whole);
-        } else {
-          const float q = p.a + alpha * (p.b + alpha * p.c) + f.cut * (1.0f / kScaleA);
-          val[j][r] = __builtin_fmaf(q, (float)f.hi[j][r] + (float)f.lo[j][r], acc[i][j][r] * (1.0f / kScaleA));
-          square = __builtin_fmaf(val[j][r], val[j][r], square);
-        }
+        val[j][r] = ortho_value<kWhat, kSplit>(p, acc[i][j][r], (float)f.hi[j][r], (float)f.lo[j][r], f.cut,
+                                               cut_n[kCutN ? j : 0][r], kSymmetric && gm == gn + r, alpha);
+        if constexpr (kWhat == Product::kUpdate) square = __builtin_fmaf(val[j][r], val[j][r], square);
       }
     }
     if constexpr (!kSplit && kSymmetric) {
@@ -432,6 +489,164 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   if constexpr (kWhat == Product::kUpdate && kOut == Result::kPlanes && !kSplit) {
     square = wave_sum_f32(square) * (1.0f / (kScaleX * kScaleX));
     if (lane == 0) p.squares[mat * p.parts + t * 4 + wave] = square;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Small products: a workgroup owns 16 S x 16 S values and its W wavefronts split K
+// between them in pieces of 32 values (one MFMA deep), each streaming its fragments
+// straight from global memory to registers, kAhead pieces ahead; the partial
+// blocks are added through LDS, in the wavefronts' order. What the epilogue reads is
+// loaded before the loop. For products whose tiles would leave most CUs without
+// work, where a tile's own chain of copies, barriers and short runs of MFMAs is what is
+// waited for.
+// ---------------------------------------------------------------------------
+template <Product kWhat, Result kOut, bool kSplit, int S, int W>
+__global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
+  constexpr bool kSymmetric = kWhat != Product::kUpdate;
+  constexpr int kAhead = 2;
+  static_assert(S * S <= W, "a wave per block");
+  __shared__ __attribute__((aligned(16))) v4f part[W][S * S][64];
+  const int lane = threadIdx.x & 63, lr = lane & 15, lk = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t mat = blockIdx.x / p.count;
+  const int t = blockIdx.x % p.count;
+  int tm, tn;
+  if constexpr (kSymmetric) {
+    triangle_tile(t, tm, tn);
+  } else {
+    const int across = p.n / (16 * S);
+    tm = t / across, tn = t % across;
+  }
+  const int m0 = tm * 16 * S, n0 = tn * 16 * S;
+  const bool on_diagonal = kSymmetric && tm == tn;
+  const OrthoOperands o = ortho_operands<kWhat>(p, mat);
+  const int pieces = o.K / 32;
+  const int g_begin = pieces * wave / W, g_end = pieces * (wave + 1) / W;
+  struct Frags {
+    f16x8 a[S], b[S], a_lo[kSplit ? S : 1], b_lo[kSplit ? S : 1];
+  };
+  const int64_t at_a = (int64_t)(m0 + lr) * o.K + 8 * lk, at_b = (int64_t)(n0 + lr) * o.K + 8 * lk;
+  auto load = [&](int g, Frags& f) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const int64_t off = (int64_t)i * 16 * o.K + g * 32;
+      f.a[i] = *(const f16x8*)(o.a_hi + at_a + off);
+      f.b[i] = *(const f16x8*)(o.b_hi + at_b + off);
+      if constexpr (kSplit) {
+        f.a_lo[i] = *(const f16x8*)(o.a_lo + at_a + off);
+        f.b_lo[i] = *(const f16x8*)(o.b_lo + at_b + off);
+      }
+    }
+  };
+  v4f acc[S][S];
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < S; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  auto compute = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+        if constexpr (kSplit) {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.b_lo[j], f.a[i], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.b[j], f.a_lo[i], acc[i][j], 0, 0, 0);
+        }
+      }
+  };
+  Frags f[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (g_begin + u < g_end) load(g_begin + u, f[u]);
+
+  // wave b finishes block b: what its places held before
+  const int bi = wave / S, bj = wave % S;
+  const int gm = m0 + bi * 16 + lr, gn = n0 + bj * 16 + 4 * lk;
+  const bool finishes = wave < S * S;
+  f16x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
+  float cut_m = 0.0f, alpha = 0.0f;
+  v4f cut_n = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (finishes) {
+    if constexpr (kWhat == Product::kSquare) {
+      hi = *(const f16x4*)(p.am + o.mm + (int64_t)gm * p.m + gn);
+      if constexpr (kSplit) lo = *(const f16x4*)(p.am_lo + o.mm + (int64_t)gm * p.m + gn);
+      else cut_m = p.da[mat * p.m + gm], cut_n = *(const v4f*)(p.da + mat * p.m + gn);
+    }
+    if constexpr (kWhat == Product::kUpdate) {
+      hi = *(const f16x4*)(p.x + o.mn + (int64_t)gm * p.n + gn);
+      lo = *(const f16x4*)(p.x_lo + o.mn + (int64_t)gm * p.n + gn);
+      if constexpr (!kSplit) cut_m = p.db[mat * p.m + gm];
+    }
+    if (kWhat != Product::kGram && p.pivot) alpha = p.alpha[mat];
+  }
+
+  for (int g = g_begin; g < g_end; g += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (g + u < g_end) compute(f[u]);
+      if (g + u + kAhead < g_end) load(g + u + kAhead, f[u]);
+    }
+  }
+  if (kWhat == Product::kGram && p.pivot && on_diagonal) {
+    alpha = ortho_alpha(p, mat, (float*)part, 64 * W);
+    if (t == 0 && threadIdx.x == 0) p.alpha[mat] = alpha;
+  }
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < S; ++j) part[wave][i * S + j][lane] = acc[i][j];
+  __syncthreads();
+  if (!finishes) return;
+  v4f sum = part[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < W; ++w) sum += part[w][wave][lane];
+
+  float val[4], square = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    val[r] = ortho_value<kWhat, kSplit>(p, sum[r], (float)hi[r], (float)lo[r], cut_m, cut_n[r], kSymmetric && gm == gn + r, alpha);
+    square = __builtin_fmaf(val[r], val[r], square);
+  }
+  if constexpr (!kSplit && kSymmetric) {
+    float* const cut = (kWhat == Product::kGram ? p.da : p.db) + mat * p.m;
+    if (on_diagonal && bi == bj) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (4 * lk + r == lr) cut[gm] = val[r] - (float)(_Float16)val[r];
+    }
+  }
+  if constexpr (kWhat == Product::kUpdate && kOut == Result::kPlanes && !kSplit) {
+    square = wave_sum_f32(square) * (1.0f / (kScaleX * kScaleX));
+    if (lane == 0) p.squares[mat * p.parts + t * (S * S) + wave] = square;
+  }
+  const float scale = p.scale * (1.0f / kScaleX);
+  if constexpr (kOut == Result::kPlanes) {
+    const OrthoPlaces to = ortho_places<kWhat, kOut>(p, o, mat, on_diagonal);
+    auto put = [&](uint16_t* rows, uint16_t* cols, uint32_t p0, uint32_t p1) {
+      if (rows) *(uint2*)(rows + (int64_t)gm * to.ld_r + gn) = make_uint2(p0, p1);
+      if (cols) {
+        const bool odd = lr & 1;
+        const Turned v = turn_pairs(odd, p0, p1);
+        uint16_t* const at = cols + (int64_t)(gn + (odd ? 2 : 0)) * to.ld_c + (gm & ~1);
+        *(uint32_t*)at = v.first;
+        *(uint32_t*)(at + to.ld_c) = v.second;
+      }
+    };
+    auto low = [](float v) { return v - (float)(_Float16)v; };
+    put(to.r, to.c, pack_f16(val[0], val[1]), pack_f16(val[2], val[3]));
+    if constexpr (kSplit || kWhat == Product::kUpdate)
+      put(to.r_lo, kSplit ? to.c_lo : nullptr, pack_f16(low(val[0]), low(val[1])), pack_f16(low(val[2]), low(val[3])));
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (gm >= p.m_true || gn + r >= p.n_true) continue;
+      const int64_t at = mat * (int64_t)p.m_true * p.n_true +
+                         (p.tall ? (int64_t)(gn + r) * p.m_true + gm : (int64_t)gm * p.n_true + gn + r);
+      if constexpr (kOut == Result::kBf16) ((__bf16*)p.out)[at] = (__bf16)(val[r] * scale);
+      else ((float*)p.out)[at] = val[r] * scale;
+    }
   }
 }
 
@@ -501,6 +716,8 @@ __global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__
 }
 
 // ---------------------------------------------------------------------------
+constexpr int64_t kOrthoSmall = 512;  // blocks of 32 x 32 up to which a product is small
+
 struct OrthoPlan {
   int64_t m, n;  // padded
   bool split;
@@ -530,9 +747,11 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
     }
     return best;
   };
-  if (L * all(64) <= kCus) o.tile = 64;
+  if (L * all(32) <= kOrthoSmall) o.tile = 32;
+  else if (L * all(64) <= kCus) o.tile = 64;
   else o.tile = o.split ? 128 : choose(all, {256, 128});
-  if (L * sym(64) <= kCus) o.tile_sym = 64;
+  if (L * sym(32) <= kOrthoSmall) o.tile_sym = 32;
+  else if (L * sym(64) <= kCus) o.tile_sym = 64;
   else o.tile_sym = o.split ? 128 : choose(sym, {256, 192, 128});
   o.symmetric = sym(o.tile_sym);
   o.whole = all(o.tile);
@@ -547,6 +766,10 @@ int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool bf16) { retu
 template <Product kWhat, Result kOut, bool kSplit>
 static void launch_product(const OrthoArgs& a, int64_t L, int tile, hipStream_t stream) {
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)(L * a.count)), dim3(256), 0, stream, a); };
+  if (tile == 32) {
+    hipLaunchKernelGGL((ortho_small_kernel<kWhat, kOut, kSplit, 2, 8>), dim3((unsigned)(L * a.count)), dim3(512), 0, stream, a);
+    return;
+  }
   if (tile == 64) return go(ortho_product_kernel<kWhat, kOut, kSplit, 64, 64, 5>);
   if (tile == 128) return go(ortho_product_kernel<kWhat, kOut, kSplit, 128, 128, 2>);
   if constexpr (!kSplit) {
