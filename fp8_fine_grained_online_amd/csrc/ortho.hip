@@ -655,13 +655,6 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
 // squares leave its range), then G / |G| to the planes of X and X^T.
 // ---------------------------------------------------------------------------
 template <typename T>
-__device__ __forceinline__ float element_of(const T* p, int64_t i);
-template <>
-__device__ __forceinline__ float element_of<float>(const float* p, int64_t i) { return p[i]; }
-template <>
-__device__ __forceinline__ float element_of<bf16_t>(const bf16_t* p, int64_t i) { return bf16_lo(p[i].bits); }
-
-template <typename T>
 __global__ __launch_bounds__(256) void ortho_squares_kernel(const T* __restrict__ g, int64_t size, double* __restrict__ parts) {
   __shared__ double sums[4];
   const int64_t chunks = (size + 7) / 8;
@@ -693,31 +686,39 @@ __global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__
   sum = wave_sum_f64(sum);
   const double f = sum > 0.0 ? (double)kScaleX / __dsqrt_rn(sum) : sum;  // (a NaN goes on)
   const T* const from = g + (int64_t)mat * M * N;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int r = r0 + i / 64, c = c0 + i % 64;
-    block[i / 64][i % 64] = r < M && c < N ? (float)((double)element_of(from, (int64_t)r * N + c) * f) : 0.0f;
+  const int ch = threadIdx.x % 8;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const int r = pass * 32 + threadIdx.x / 8, have = r0 + r < M ? N - c0 - ch * 8 : 0;
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (have > 0) values(load_chunk(from + (int64_t)(r0 + r) * N + c0 + ch * 8, have), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) block[r][ch * 8 + e] = (float)((double)v[e] * f);  // (0 f is NaN where f is)
   }
   __syncthreads();
   const int64_t base = (int64_t)mat * p.m * p.n;
   // rows of G as they lie: M by N padded; columns: N by M padded
-  _Float16* const straight = (p.tall ? p.xt_new : p.x) + base;
-  _Float16* const straight_lo = (p.tall ? p.xt_lo_new : p.x_lo) + base;
-  _Float16* const turned = (p.tall ? p.x : p.xt_new) + base;
-  _Float16* const turned_lo = (p.tall ? p.x_lo : p.xt_lo_new) + base;
   const int64_t ld_s = p.tall ? p.m : p.n, ld_t = p.tall ? p.n : p.m;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int r = i / 64, c = i % 64;
-    const float v = block[r][c], w = block[c][r];
-    straight[(r0 + r) * ld_s + c0 + c] = (_Float16)v;
-    turned[(c0 + r) * ld_t + r0 + c] = (_Float16)w;
-    if (kSplit || !p.tall) straight_lo[(r0 + r) * ld_s + c0 + c] = (_Float16)(v - (float)(_Float16)v);
-    if (kSplit || p.tall) turned_lo[(c0 + r) * ld_t + r0 + c] = (_Float16)(w - (float)(_Float16)w);
+  const int64_t straight = base + r0 * ld_s + c0, turned = base + c0 * ld_t + r0;
+  auto put = [&](_Float16* hi, _Float16* lo, bool low, int64_t at, const float (&v)[8]) {
+    f16x8 h, l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[e], l[e] = (_Float16)(v[e] - (float)h[e]);
+    *(f16x8*)(hi + at) = h;
+    if (low) *(f16x8*)(lo + at) = l;
+  };
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const int r = pass * 32 + threadIdx.x / 8;
+    float v[8], w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = block[r][ch * 8 + e], w[e] = block[ch * 8 + e][r];
+    put(p.tall ? p.xt_new : p.x, p.tall ? p.xt_lo_new : p.x_lo, kSplit || !p.tall, straight + r * ld_s + ch * 8, v);
+    put(p.tall ? p.x : p.xt_new, p.tall ? p.x_lo : p.xt_lo_new, kSplit || p.tall, turned + r * ld_t + ch * 8, w);
   }
 }
 
 // ---------------------------------------------------------------------------
-constexpr int64_t kOrthoSmall = 512;  // blocks of 32 x 32 up to which a product is small
-
 struct OrthoPlan {
   int64_t m, n;  // padded
   bool split;
@@ -747,10 +748,18 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
     }
     return best;
   };
-  if (L * all(32) <= kOrthoSmall) o.tile = 32;
+  // Small products, for few blocks of 16 x 16 or 32 x 32; else tiles. us for five steps, MI355X, with
+  // the symmetric products in 16 x 16 blocks / 32 x 32 blocks / 64 x 64 tiles:
+  //   256 x 1024 float32 92 / 116 / 147    256 x 4096 120 / 158 / 147    333 x 1000 99 / 102 / 108
+  //   400 x 400 85 / 85 / 94    512 x 512 97 / 90 / 95    700 x 2000 float32 - / 283 / 336    1024 x 1024 - / 204 / 144
+  // and the update:
+  //   100 x 200 63 / 68 / 79    256 x 1024 81 / 76 / 85    333 x 1000 111 / 99 / 104    600 x 600 - / 117 / 113
+  if (L * all(16) <= kCus) o.tile = 16;
+  else if (L * all(32) <= kCus * 3 / 2) o.tile = 32;
   else if (L * all(64) <= kCus) o.tile = 64;
   else o.tile = o.split ? 128 : choose(all, {256, 128});
-  if (L * sym(32) <= kOrthoSmall) o.tile_sym = 32;
+  if (L * sym(16) <= kCus * 3 / 2) o.tile_sym = 16;
+  else if (L * sym(32) <= kCus) o.tile_sym = 32;
   else if (L * sym(64) <= kCus) o.tile_sym = 64;
   else o.tile_sym = o.split ? 128 : choose(sym, {256, 192, 128});
   o.symmetric = sym(o.tile_sym);
@@ -766,10 +775,9 @@ int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool bf16) { retu
 template <Product kWhat, Result kOut, bool kSplit>
 static void launch_product(const OrthoArgs& a, int64_t L, int tile, hipStream_t stream) {
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)(L * a.count)), dim3(256), 0, stream, a); };
-  if (tile == 32) {
-    hipLaunchKernelGGL((ortho_small_kernel<kWhat, kOut, kSplit, 2, 8>), dim3((unsigned)(L * a.count)), dim3(512), 0, stream, a);
-    return;
-  }
+  auto small = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)(L * a.count)), dim3(512), 0, stream, a); };
+  if (tile == 16) return small(ortho_small_kernel<kWhat, kOut, kSplit, 1, 8>);
+  if (tile == 32) return small(ortho_small_kernel<kWhat, kOut, kSplit, 2, 8>);
   if (tile == 64) return go(ortho_product_kernel<kWhat, kOut, kSplit, 64, 64, 5>);
   if (tile == 128) return go(ortho_product_kernel<kWhat, kOut, kSplit, 128, 128, 2>);
   if constexpr (!kSplit) {
@@ -816,7 +824,7 @@ hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M
   p.tall = M > N;
   p.m_true = (int)(p.tall ? N : M), p.n_true = (int)(p.tall ? M : N);
   p.a = a, p.b = b, p.c = c, p.scale = scale, p.out = out;
-  p.parts = (int)o.whole * 4;
+  p.parts = (int)o.whole * (o.tile == 16 ? 1 : 4);
   uint8_t* at = (uint8_t*)ws;
   auto take = [&](int64_t bytes) {
     void* r = at;
