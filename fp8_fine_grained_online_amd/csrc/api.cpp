@@ -187,8 +187,8 @@ int check_norm(float eps, int centred, int64_t M, int64_t K) {
   if (M < 0 || K < 0) return FP8Q_ERR_SHAPE;
   if (centred != 0 && centred != 1) return FP8Q_ERR_SHAPE;
   if (!(eps >= 0.0f) || eps > 3.0e38f) return FP8Q_ERR_SHAPE;  // NaN, negative or infinite
-  // up to a workgroup of 512 threads per row
-  if (M > kMaxDim || K > kNormMaxK || !launchable(M, 512)) return FP8Q_ERR_TOO_LARGE;
+  // up to a workgroup of 1024 threads per row
+  if (M > kMaxDim || K > kNormMaxK || !launchable(M, 1024)) return FP8Q_ERR_TOO_LARGE;
   return FP8Q_OK;
 }
 
@@ -197,7 +197,7 @@ int check_swiglu(int gu_dtype, int64_t ld, const int32_t* m_offsets, int64_t G, 
   if (M < 0 || I < 0 || (m_offsets && G < 1)) return FP8Q_ERR_SHAPE;
   if (!known_dtype(gu_dtype)) return FP8Q_ERR_DTYPE;
   if (M > kMaxDim || I > kMaxDim / 2 || (m_offsets && G > kMaxDim)) return FP8Q_ERR_TOO_LARGE;
-  if (!launchable((M * ((I + 7) / 8) + 255) / 256, 256)) return FP8Q_ERR_TOO_LARGE;
+  if (M * ((I + 7) / 8) > kMaxDim - 256) return FP8Q_ERR_TOO_LARGE;  // chunks of 8, numbered with 31 bits
   if (M == 0 || I == 0) return -1;  // valid no-op
   if (ld < 2 * I) return FP8Q_ERR_SHAPE;
   if (!aligned(m_offsets, 4)) return FP8Q_ERR_ALIGN;

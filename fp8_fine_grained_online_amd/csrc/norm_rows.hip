@@ -17,6 +17,8 @@
 // rounding. Sums are in binary32; a row whose statistics leave binary32's range
 // (squares that overflow, or underflow where eps does not cover them) is done
 // again in float64, from the registers.
+#include <type_traits>
+
 #include "common.hpp"
 #include "rows.hpp"
 #include "wave.hpp"
@@ -24,8 +26,6 @@
 namespace fp8q {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
-
-constexpr int64_t kBwdWorkgroups = 256;  // of the gradient: one per CU
 
 // kThreads per row (64: a wavefront; else a whole number of them), kChunks of
 // eight values per thread: value 8 (t + kThreads i) + e belongs to thread t.
@@ -40,10 +40,10 @@ struct FewShape : RowShape<64, 1> {
   static constexpr bool kFew = true;
 };
 
-template <typename Shape, typename T>
+template <typename Shape, bool kNt = false, typename T>
 __device__ __forceinline__ Chunk<T> load_row_chunk(const T* row, int at, int K) {
   if constexpr (Shape::kFew) return load_few(row + at, K);
-  else return load_in_row(row, at, K);
+  else return load_in_row<kNt>(row, at, K);
 }
 
 // Eight weights, whose type is known at run time only
@@ -198,7 +198,13 @@ struct NormArgs {
   int M, K;
   float eps;
   bool weights_bf16;
+  bool nt;  // more is read and written than stays cached
 };
+
+// Reads that pass the caches by from 96 MiB of reads and writes on, which neither
+// leaves nor finds them there whole: 8192 x 7168 with a residual 86.6 -> 83.0 us, its
+// gradient 95.5 -> 93.1, 16384 x 1024 25.6 -> 23.9; but 4096 x 2048 12.0 -> 12.4.
+static bool beyond_cache(int64_t bytes) { return bytes > (int64_t(96) << 20); }
 
 template <typename Shape>
 constexpr int kRowThreads = Shape::kT < 256 ? 256 : Shape::kT;  // of a workgroup
@@ -215,17 +221,23 @@ __global__ __launch_bounds__(kRowThreads<Shape>) void norm_rows_kernel(NormArgs 
   auto present = [&](int i) { return min(max(p.K - at(i), 0), 8); };
   const X* const x = (const X*)p.x + m * p.ldx;
   Chunk<X> raw[C];
+  auto read = [&](const X* row) {
+    if (p.nt) {
 #pragma unroll
-  for (int i = 0; i < C; ++i)
-    raw[i] = tid + T * i < chunks ? load_row_chunk<Shape>(x, at(i), p.K) : zero_chunk(X{});
+      for (int i = 0; i < C; ++i) raw[i] = tid + T * i < chunks ? load_row_chunk<Shape, true>(row, at(i), p.K) : zero_chunk(X{});
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) raw[i] = tid + T * i < chunks ? load_row_chunk<Shape>(row, at(i), p.K) : zero_chunk(X{});
+    }
+  };
+  read(x);
   float v[C][8];
 #pragma unroll
   for (int i = 0; i < C; ++i) values(raw[i], v[i]);
   if (p.res) {
     const X* const res = (const X*)p.res + m * p.ldr;
     X* const h = (X*)p.h + m * (int64_t)p.K;
-#pragma unroll
-    for (int i = 0; i < C; ++i) raw[i] = tid + T * i < chunks ? load_row_chunk<Shape>(res, at(i), p.K) : zero_chunk(X{});
+    read(res);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float r[8];
@@ -259,13 +271,15 @@ __global__ __launch_bounds__(kRowThreads<Shape>) void norm_rows_kernel(NormArgs 
 }
 
 // ---------------------------------------------------------------------------
-// Gradient. A workgroup of kWg threads takes rows in turn, kWg / kT at once, the
+// Gradient. A workgroup of kBwdThreads takes rows in turn, 512 / kT at once, the
 // next ones' loads on their way while it works on these; gamma stays in LDS. A
 // thread's columns are the same in every row, so the weights' gradients are sums
 // in its registers, joined at the end over the workgroup's rows in LDS and written
 // as one row of partial sums. A second kernel adds those in order: no atomics,
 // and the same bits every time.
 // ---------------------------------------------------------------------------
+constexpr int kBwdThreads = 512;  // of a workgroup
+
 struct NormBwdArgs {
   const void *dy, *x, *gamma, *dres;
   void* dx;
@@ -273,12 +287,12 @@ struct NormBwdArgs {
   int64_t ldy, ldx, ldr;
   int M, K;
   float eps;
-  bool weights_bf16;
+  bool weights_bf16, nt;
 };
 
-template <typename Shape, int kWg, typename X, typename D, bool kCentred>
-__global__ __launch_bounds__(kWg) void norm_rows_bwd_kernel(NormBwdArgs p) {
-  constexpr int T = Shape::kT, C = Shape::kC, kRows = kWg / T;
+template <typename Shape, typename X, typename D, bool kCentred>
+__global__ __launch_bounds__(kBwdThreads) void norm_rows_bwd_kernel(NormBwdArgs p) {
+  constexpr int kWg = kBwdThreads, T = Shape::kT, C = Shape::kC, kRows = kWg / T;
   constexpr int kSums = kCentred ? 2 : 1;
   struct Slots {
     RowLds<T> row;
@@ -290,12 +304,6 @@ __global__ __launch_bounds__(kWg) void norm_rows_bwd_kernel(NormBwdArgs p) {
   const int chunks = (p.K + 7) / 8;
   auto at = [&](int i) { return 8 * (tid + T * i); };
   auto present = [&](int i) { return min(max(p.K - at(i), 0), 8); };
-  for (int c = threadIdx.x; c < chunks; c += kWg) {
-    float g[8];
-    row_weights<Shape>(p.gamma, p.weights_bf16, 8 * c, p.K, g);  // absent ones are zeros
-    *(v4f*)(shared + 8 * c) = v4f{g[0], g[1], g[2], g[3]};
-    *(v4f*)(shared + 8 * c + 4) = v4f{g[4], g[5], g[6], g[7]};
-  }
   auto gamma_of = [&](int i, float (&g)[8]) {
     const v4f a = *(const v4f*)(shared + at(i)), b = *(const v4f*)(shared + at(i) + 4);
 #pragma unroll
@@ -311,17 +319,28 @@ __global__ __launch_bounds__(kWg) void norm_rows_bwd_kernel(NormBwdArgs p) {
     }
   Chunk<X> rx[C], rr[C];
   Chunk<D> rd[C];
-  auto read_rows = [&](int64_t m) {
+  auto read_as = [&](auto nt, int64_t m) {
+    constexpr bool kNt = decltype(nt)::value;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const bool have = m < p.M && tid + T * i < chunks;
-      rx[i] = have ? load_row_chunk<Shape>((const X*)p.x + m * p.ldx, at(i), p.K) : zero_chunk(X{});
-      rd[i] = have ? load_row_chunk<Shape>((const D*)p.dy + m * p.ldy, at(i), p.K) : zero_chunk(D{});
-      rr[i] = have && p.dres ? load_row_chunk<Shape>((const X*)p.dres + m * p.ldr, at(i), p.K) : zero_chunk(X{});
+      rx[i] = have ? load_row_chunk<Shape, kNt>((const X*)p.x + m * p.ldx, at(i), p.K) : zero_chunk(X{});
+      rd[i] = have ? load_row_chunk<Shape, kNt>((const D*)p.dy + m * p.ldy, at(i), p.K) : zero_chunk(D{});
+      rr[i] = have && p.dres ? load_row_chunk<Shape, kNt>((const X*)p.dres + m * p.ldr, at(i), p.K) : zero_chunk(X{});
     }
+  };
+  auto read_rows = [&](int64_t m) {  // (longer parts of a row than two chunks leave no registers for both forms)
+    if (C <= 2 && p.nt) read_as(std::true_type{}, m);
+    else read_as(std::false_type{}, m);
   };
   const float inv_k = 1.0f / (float)p.K;
   read_rows((int64_t)blockIdx.x * kRows + sub);
+  for (int c = threadIdx.x; c < chunks; c += kWg) {
+    float g[8];
+    row_weights<Shape>(p.gamma, p.weights_bf16, 8 * c, p.K, g);  // absent ones are zeros
+    *(v4f*)(shared + 8 * c) = v4f{g[0], g[1], g[2], g[3]};
+    *(v4f*)(shared + 8 * c + 4) = v4f{g[4], g[5], g[6], g[7]};
+  }
   __syncthreads();
   // every thread of the workgroup makes the same number of rounds (barriers inside)
   for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < p.M; m0 += (int64_t)gridDim.x * kRows) {
@@ -448,19 +467,27 @@ static void launch_fwd(const NormArgs& a, bool centred, hipStream_t stream) {
 
 template <typename X, typename Y>
 static void launch_fwd_shape(const NormArgs& a, bool centred, hipStream_t stream) {
+  // Few chunks per thread: more rows in flight beat longer parts of a row (8192 x 7168 with
+  // 512 x 2 / 256 x 4 82.4 / 83.3 us, 333 x 7168 6.2 / 6.7; with 1024 x 2 / 512 x 4 100 x
+  // 16384 5.4 / 6.3, but 6000 x 10240 86.7 / 84.3). 512 threads of one chunk beat 256 of two where they
+  // are nearly all used: 16384 x 4096 89.2 / 92.8, but 4000 x 2049 (float32) 17.3 / 15.1.
   if (a.K < 8) return launch_fwd<FewShape, X, Y>(a, centred, stream);
-  if (a.K <= RowShape<64, 1>::kMaxK) return launch_fwd<RowShape<64, 1>, X, Y>(a, centred, stream);
-  if (a.K <= RowShape<64, 2>::kMaxK) return launch_fwd<RowShape<64, 2>, X, Y>(a, centred, stream);
-  if (a.K <= RowShape<64, 4>::kMaxK) return launch_fwd<RowShape<64, 4>, X, Y>(a, centred, stream);
-  if (a.K <= RowShape<256, 2>::kMaxK) return launch_fwd<RowShape<256, 2>, X, Y>(a, centred, stream);
-  if (a.K <= RowShape<256, 4>::kMaxK) return launch_fwd<RowShape<256, 4>, X, Y>(a, centred, stream);
-  launch_fwd<RowShape<512, 4>, X, Y>(a, centred, stream);
+  if (a.K <= 512) return launch_fwd<RowShape<64, 1>, X, Y>(a, centred, stream);
+  if (a.K <= 1024) return launch_fwd<RowShape<64, 2>, X, Y>(a, centred, stream);
+  if (a.K <= 2048) return launch_fwd<RowShape<128, 2>, X, Y>(a, centred, stream);
+  if (a.K <= 3584) return launch_fwd<RowShape<256, 2>, X, Y>(a, centred, stream);
+  if (a.K <= 4096) return launch_fwd<RowShape<512, 1>, X, Y>(a, centred, stream);
+  if (a.K <= 8192) return launch_fwd<RowShape<512, 2>, X, Y>(a, centred, stream);
+  if (a.K <= 12288) return launch_fwd<RowShape<512, 4>, X, Y>(a, centred, stream);
+  launch_fwd<RowShape<1024, 2>, X, Y>(a, centred, stream);
 }
 
 hipError_t launch_norm_rows(const void* x, bool x_bf16, int64_t ldx, const void* res, int64_t ldr, const void* gamma,
                             const void* beta, bool weights_bf16, float eps, bool centred, int64_t M, int64_t K, void* y,
                             bool y_bf16, void* h, hipStream_t stream) {
-  const NormArgs a{x, res, gamma, beta, y, h, ldx, ldr, (int)M, (int)K, eps, weights_bf16};
+  const int64_t ex = x_bf16 ? 2 : 4, ey = y_bf16 ? 2 : 4;
+  const NormArgs a{x, res, gamma, beta, y, h, ldx, ldr, (int)M, (int)K, eps, weights_bf16,
+                   beyond_cache(M * K * (ex * (res ? 3 : 1) + ey))};
   if (x_bf16) {
     if (y_bf16) launch_fwd_shape<bf16_t, bf16_t>(a, centred, stream);
     else launch_fwd_shape<bf16_t, float>(a, centred, stream);
@@ -471,66 +498,62 @@ hipError_t launch_norm_rows(const void* x, bool x_bf16, int64_t ldx, const void*
   return hipGetLastError();
 }
 
-// The gradient's threads per row and per workgroup, and its workgroups: up to one
-// per CU and 512 threads, fewer for few rows. float32 rows are shared by twice as
-// many threads as bfloat16 ones from 2048 values on, since a thread holds its part
-// of two rows at a time.
+// The gradient's threads per row and per workgroup, and its workgroups: as many as are
+// resident, fewer for few rows. us, MI355X, threads x chunks and workgroups against others:
+//   8192 x 7168   512 x 2, 512  89.9    256 workgroups 111    256 x 4, 256  94.2
+//   16384 x 4096  512 x 1, 512  90.1    256 x 2, 512  90.6    256 x 2, 256  124
+//   4096 x 2048   256 x 1, 512  20.2    128 x 2, 512  20.4    64 x 4, 256  over 22
+//   16384 x 1024  64 x 2, 512  28.9     64 x 2, 256  31.7     128 x 1, 512  33.4
+//   6000 x 10240  512 x 3, 256  98.5    512 x 4, 256  96.8    1024 x 2, 256  109
+//   3000 x 10240 (float32)  512 x 3, 256  90.4    512 x 4, 256  174    1024 x 2, 256  260
+//   4000 x 16384  512 x 4, 256  110     512 x 4, 512  117     1024 x 2, 256  110
 struct BwdPlan {
-  int threads, group;
+  int threads;
   int64_t workgroups;
 };
-static BwdPlan bwd_plan(int64_t M, int64_t K, bool wide) {
+static BwdPlan bwd_plan(int64_t M, int64_t K) {
   BwdPlan b;
-  b.threads = K <= 1024 || (K <= 2048 && !wide) ? 64 : K <= 2048 ? 128 : K <= 4096 || (K <= 8192 && !wide) ? 256 : K <= 8192 || !wide ? 512 : 1024;
-  b.group = b.threads > 512 ? b.threads : 512;
-  const int rows = b.group / b.threads;
-  const int64_t need = (M + rows - 1) / rows;
-  b.workgroups = need < kBwdWorkgroups ? need : kBwdWorkgroups;
+  b.threads = K <= 1024 ? 64 : K <= 2048 ? 256 : 512;
+  const int rows = kBwdThreads / b.threads;
+  const int64_t need = (M + rows - 1) / rows, most = K <= 8192 ? 512 : 256;
+  b.workgroups = need < most ? need : most;
   return b;
 }
 
-// (of either type: a workspace fits both)
 int64_t norm_bwd_workspace_bytes(int64_t M, int64_t K, bool centred) {
-  const int64_t a = bwd_plan(M, K, false).workgroups, b = bwd_plan(M, K, true).workgroups;
-  return (a > b ? a : b) * (centred ? 2 : 1) * K * (int64_t)sizeof(float);
+  return bwd_plan(M, K).workgroups * (centred ? 2 : 1) * K * (int64_t)sizeof(float);
 }
 
 template <typename Shape, typename X, typename D>
 static void launch_bwd(const NormBwdArgs& a, bool centred, const BwdPlan& b, hipStream_t stream) {
-  constexpr int kT = Shape::kT;
-  constexpr int kWg = kT > 512 ? kT : 512;
+  constexpr int kT = Shape::kT, kWg = kBwdThreads;
   const dim3 grid((unsigned)b.workgroups), block(kWg);
   const size_t gamma = (size_t)(a.K + 7) / 8 * 32, join = kWg > kT ? (size_t)(centred ? 2 : 1) * Shape::kMaxK * 4 : 0;
   const size_t lds = gamma > join ? gamma : join;
-  if (centred) hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, kWg, X, D, true>), grid, block, lds, stream, a);
-  else hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, kWg, X, D, false>), grid, block, lds, stream, a);
+  if (centred) hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, X, D, true>), grid, block, lds, stream, a);
+  else hipLaunchKernelGGL((norm_rows_bwd_kernel<Shape, X, D, false>), grid, block, lds, stream, a);
 }
 
 template <typename X, typename D>
 static void launch_bwd_shape(const NormBwdArgs& a, bool centred, const BwdPlan& b, hipStream_t stream) {
-  constexpr bool kWide = sizeof(X) == 4 || sizeof(D) == 4;
   if (a.K < 8) return launch_bwd<FewShape, X, D>(a, centred, b, stream);
   if (a.K <= 512) return launch_bwd<RowShape<64, 1>, X, D>(a, centred, b, stream);
   if (a.K <= 1024) return launch_bwd<RowShape<64, 2>, X, D>(a, centred, b, stream);
-  if constexpr (kWide) {
-    if (a.K <= 2048) return launch_bwd<RowShape<128, 2>, X, D>(a, centred, b, stream);
-    if (a.K <= 4096) return launch_bwd<RowShape<256, 2>, X, D>(a, centred, b, stream);
-    if (a.K <= 8192) return launch_bwd<RowShape<512, 2>, X, D>(a, centred, b, stream);
-    launch_bwd<RowShape<1024, 2>, X, D>(a, centred, b, stream);
-  } else {
-    if (a.K <= 2048) return launch_bwd<RowShape<64, 4>, X, D>(a, centred, b, stream);
-    if (a.K <= 4096) return launch_bwd<RowShape<256, 2>, X, D>(a, centred, b, stream);
-    if (a.K <= 8192) return launch_bwd<RowShape<256, 4>, X, D>(a, centred, b, stream);
-    launch_bwd<RowShape<512, 4>, X, D>(a, centred, b, stream);
-  }
+  if (a.K <= 2048) return launch_bwd<RowShape<256, 1>, X, D>(a, centred, b, stream);
+  if (a.K <= 4096) return launch_bwd<RowShape<512, 1>, X, D>(a, centred, b, stream);
+  if (a.K <= 8192) return launch_bwd<RowShape<512, 2>, X, D>(a, centred, b, stream);
+  if (a.K <= 12288) return launch_bwd<RowShape<512, 3>, X, D>(a, centred, b, stream);
+  launch_bwd<RowShape<512, 4>, X, D>(a, centred, b, stream);
 }
 
 hipError_t launch_norm_rows_bwd(const void* dy, bool dy_bf16, int64_t ldy, const void* x, bool x_bf16, int64_t ldx,
                                 const void* gamma, bool weights_bf16, const void* dres, int64_t ldr, float eps,
                                 bool centred, int64_t M, int64_t K, void* dx, float* dgamma, float* dbeta, void* ws,
                                 hipStream_t stream) {
-  const NormBwdArgs a{dy, x, gamma, dres, dx, (float*)ws, ldy, ldx, ldr, (int)M, (int)K, eps, weights_bf16};
-  const BwdPlan b = bwd_plan(M, K, !x_bf16 || !dy_bf16);
+  const int64_t ex = x_bf16 ? 2 : 4, ed = dy_bf16 ? 2 : 4;
+  const NormBwdArgs a{dy, x, gamma, dres, dx, (float*)ws, ldy, ldx, ldr, (int)M, (int)K, eps, weights_bf16,
+                      beyond_cache(M * K * (ex * (dres ? 3 : 2) + ed))};
+  const BwdPlan b = bwd_plan(M, K);
   if (M > 0) {
     if (x_bf16) {
       if (dy_bf16) launch_bwd_shape<bf16_t, bf16_t>(a, centred, b, stream);

@@ -29,10 +29,17 @@ struct Chunk<float> {
 __device__ __forceinline__ Chunk<bf16_t> zero_chunk(bf16_t) { return {u32x4{0, 0, 0, 0}}; }
 __device__ __forceinline__ Chunk<float> zero_chunk(float) { return {{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}}}; }
 
-// A whole chunk at p
-__device__ __forceinline__ Chunk<bf16_t> load_whole(const bf16_t* p) { return {*(const u32x4_by2*)p}; }
+// A whole chunk at p; kNt: read once, so it need not stay cached
+template <bool kNt = false>
+__device__ __forceinline__ Chunk<bf16_t> load_whole(const bf16_t* p) {
+  const u32x4_by2* const q = (const u32x4_by2*)p;
+  return {kNt ? (u32x4)__builtin_nontemporal_load(q) : (u32x4)*q};
+}
+template <bool kNt = false>
 __device__ __forceinline__ Chunk<float> load_whole(const float* p) {
-  return {{*(const u32x4_by4*)p, *(const u32x4_by4*)(p + 4)}};
+  const u32x4_by4* const q = (const u32x4_by4*)p;
+  if constexpr (kNt) return {{__builtin_nontemporal_load(q), __builtin_nontemporal_load(q + 1)}};
+  else return {{q[0], q[1]}};
 }
 
 // `have` values (0 to 7) at p, one by one; those beyond are zero
@@ -52,9 +59,9 @@ __device__ __forceinline__ Chunk<float> load_few(const float* p, int have) {
 }
 
 // `have` values (1 to 8) at p; those beyond are zero
-template <typename T>
+template <bool kNt = false, typename T>
 __device__ __forceinline__ Chunk<T> load_chunk(const T* p, int have) {
-  return have >= 8 ? load_whole(p) : load_few(p, have);
+  return have >= 8 ? load_whole<kNt>(p) : load_few(p, have);
 }
 
 // The chunk without its first n values (0 to 7), zeros behind
@@ -82,10 +89,10 @@ __device__ __forceinline__ Chunk<float> shifted(const Chunk<float>& c, int n) {
 // Values at .. at + 7 of a row of K >= 8; zeros past its end. The chunk that ends
 // past the row is loaded whole all the same, so that it ends with the row, and
 // shifted into place.
-template <typename T>
+template <bool kNt = false, typename T>
 __device__ __forceinline__ Chunk<T> load_in_row(const T* row, int at, int K) {
   const int past = at + 8 - K;
-  Chunk<T> c = load_whole(row + (past > 0 ? K - 8 : at));
+  Chunk<T> c = load_whole<kNt>(row + (past > 0 ? K - 8 : at));
   if (past > 0) c = shifted(c, past);
   return c;
 }

@@ -692,15 +692,16 @@ FP8Q_API int fp8q_norm_bwd(const void* dy, int dy_dtype, int64_t ldy, const void
 /*
  * Gated activation: of a row gu = [gate | up] of 2 I values
  *   y = gate / (1 + exp(-gate)) * up
- * in binary32 (exp to about two units in the last place; sigmoids below 2^-126
- * count as 0), rounded once to y's type. A gate of -infinity gives 0.
+ * in binary32 (exp to about two units in the last place; a gate below -87 counts
+ * as -87, where y is below 2^-118 of up), rounded once to y's type.
  *
  *   gu : in,  M x 2I of gu_dtype, rows ld apart
  *   m_offsets : in, DEVICE int32[G + 1], or NULL for all M rows: rows from
  *        m_offsets[G] (clamped to [0, M]) on are neither read nor written, as in
  *        the grouped GEMMs; G >= 1 (ignored for NULL)
  *   y  : out, M x I of y_dtype
- * M == 0 or I == 0 is a no-op. One kernel.
+ * M * ceil(I / 8) stays below 2^31 - 256 (FP8Q_ERR_TOO_LARGE). M == 0 or I == 0 is a
+ * no-op. One kernel.
  */
 FP8Q_API int fp8q_swiglu(const void* gu, int gu_dtype, int64_t ld, const int32_t* m_offsets,
                          int64_t G, int64_t M, int64_t I, void* y, int y_dtype, void* stream);

@@ -1,8 +1,8 @@
 """Normalization of rows and its gradient on the GPU, against float64.
 
 u = 2^-24 is the largest relative error of a binary32 rounding. A row's sum over K <= 16384 values
-is a chain of at most 32 additions in a thread, 7 over its wavefront and 7 over the row's wavefronts:
-at most 46 roundings, so a sum of nonnegative terms is within 46 u. Hence
+is a chain of at most 32 additions in a thread, 7 over its wavefront and 15 over the row's wavefronts (of 512
+threads; of 1024 threads 16 in each): at most 46 roundings, so a sum of nonnegative terms is within 46 u. Hence
 
 * r = 1 / sqrt(var + eps) is within (46 + 3) / 2 u + u < 26 u (1 / K and the product with it are two
   more roundings), centred rows' deviations adding their own rounding, 2 u of var;
@@ -68,10 +68,10 @@ def check_norm(x, g, eps, b, centred, got, out):
     assert np.all(err <= tol), float(np.max(err / tol))
 
 
-# every shape of row that the kernel has (64, 256 and 512 threads; 1, 2 and 4 chunks each), its limits
+# every shape of row that the kernels have (64 to 1024 threads, 1 to 4 chunks each), its limits
 # and the sizes around them, odd sizes and the smallest
-SIZES = [(1, 1), (3, 7), (5, 8), (2, 9), (7, 512), (3, 513), (6, 1024), (1, 1025), (9, 2048), (4, 2049), (5, 4095), (2, 4097),
-         (1, 7168), (3, 8192), (2, 8193), (3, 16383), (2, 16384)]
+SIZES = [(1, 1), (3, 7), (5, 8), (2, 9), (7, 512), (3, 513), (6, 1024), (1, 1025), (9, 2048), (4, 2049), (2, 3585), (5, 4095),
+         (2, 4097), (1, 7168), (3, 8192), (2, 8193), (3, 12288), (2, 12289), (3, 16383), (2, 16384)]
 
 
 @pytest.mark.parametrize("M,K", SIZES)
