@@ -32,7 +32,6 @@
 //    would cost more than it saves.)
 //
 // Zero rows and columns pad m and n to multiples of 64; they stay zero.
-#include <initializer_list>
 #include <type_traits>
 
 #include "common.hpp"
@@ -727,6 +726,42 @@ struct OrthoPlan {
   int64_t bytes;
 };
 
+// The tile of the least estimated time. A kernel takes about 4 us, and per round of
+// its tiles (two at a time on a CU for 64 x 64 and 128 x 128, else one) an epilogue
+// and, per 64 values of K, what the chip needs to feed the round: the same for few
+// workgroups, then growing with the share p of the round that is filled. Fitted to
+// kernels of 1024 to 4096 rows; the estimates are within a tenth of these. us on MI355X
+// for 64 / 128 / 192 / 256 tiles:
+//   gram    2048 x 2048 23.5 / 18.4 / 32.0 / 47.6    2048 x 7168 73.5 / 46.5 / 78.4 / 126
+//           2900 x 2900 62.3 / 39.0 / 41.0 / 61.6    4096 x 4096 155 / 89.4 / 66.0 / 83.3
+//   update  1400 x 1400 15.8 / 21.2 / 37.4 / 58.1    2048 x 2048 38.2 / 30.1 / 47.2 / 69.6
+//           2900 x 2900 94.3 / 78.5 / 62.9 / 83.9    4096 x 4096 216 / 136 / 148 / 128
+template <typename Count>
+static int ortho_tile(int64_t L, Count count, int64_t K, bool symmetric, bool split) {
+  struct Kind {
+    int side, slots;
+    double epilogue, least, base, slope;  // us; per 64 of K: max(least, base + slope p)
+  };
+  static constexpr Kind kinds[] = {{64, 2 * kCus, 3, 0.21, 0.10, 0.32},
+                                   {128, 2 * kCus, 7, 0.35, 0.17, 0.75},
+                                   {192, kCus, 12, 0.70, 0.45, 0.50},
+                                   {256, kCus, 20, 1.10, 0.60, 1.00}};
+  const double steps = (double)(split ? 3 * K : K) / 64;
+  int best = 64;
+  double least = 0;
+  for (const Kind& k : kinds) {
+    if (split && k.side > 128) break;
+    const double rounds = (double)(L * count(k.side)) / k.slots, whole = (double)(int64_t)rounds;
+    auto round = [&](double p) {
+      const double feed = k.base + k.slope * p;
+      return k.epilogue * (symmetric ? 0.4 : 1.0) + steps * (feed > k.least ? feed : k.least);
+    };
+    const double us = whole * round(1.0) + (rounds > whole ? round(rounds - whole) : 0);
+    if (least == 0 || us < least) least = us, best = k.side;
+  }
+  return best;
+}
+
 static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   OrthoPlan o;
   const int64_t lo = M < N ? M : N, hi = M < N ? N : M;
@@ -736,18 +771,6 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   auto side = [&](int64_t v, int64_t t) { return (v + t - 1) / t; };
   auto sym = [&](int64_t t) { return side(o.m, t) * (side(o.m, t) + 1) / 2; };
   auto all = [&](int64_t t) { return side(o.m, t) * side(o.n, t); };
-  // The tile with the least cost, in rounds of a workgroup per CU (two for 128 x 128)
-  auto choose = [&](auto count, std::initializer_list<int> tiles) {
-    int best = 64;
-    double least = 0;
-    for (int t : tiles) {
-      const double rounds = (double)(L * count(t)) / (t == 128 ? 2 * kCus : kCus), whole = (double)(int64_t)rounds;
-      const double part = rounds - whole;
-      const double cost = (whole + (part > 0 ? (t == 128 ? (part > 0.5 ? part : 0.5) : 0.9) : 0)) * (t == 128 ? 0.55 : t / 256.0 * t / 256.0 * (t == 192 ? 1.06 : 1.0));
-      if (least == 0 || cost < least) least = cost, best = t;
-    }
-    return best;
-  };
   // Small products, for few blocks of 16 x 16 or 32 x 32; else tiles. us for five steps, MI355X, with
   // the symmetric products in 16 x 16 blocks / 32 x 32 blocks / 64 x 64 tiles:
   //   256 x 1024 float32 92 / 116 / 147    256 x 4096 120 / 158 / 147    333 x 1000 99 / 102 / 108
@@ -756,12 +779,10 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   //   100 x 200 63 / 68 / 79    256 x 1024 81 / 76 / 85    333 x 1000 111 / 99 / 104    600 x 600 - / 117 / 113
   if (L * all(16) <= kCus) o.tile = 16;
   else if (L * all(32) <= kCus * 3 / 2) o.tile = 32;
-  else if (L * all(64) <= kCus) o.tile = 64;
-  else o.tile = o.split ? 128 : choose(all, {256, 128});
+  else o.tile = ortho_tile(L, all, o.m, false, o.split);
   if (L * sym(16) <= kCus * 3 / 2) o.tile_sym = 16;
   else if (L * sym(32) <= kCus) o.tile_sym = 32;
-  else if (L * sym(64) <= kCus) o.tile_sym = 64;
-  else o.tile_sym = o.split ? 128 : choose(sym, {256, 192, 128});
+  else o.tile_sym = ortho_tile(L, sym, o.n, true, o.split);
   o.symmetric = sym(o.tile_sym);
   o.whole = all(o.tile);
   const int64_t mn = L * o.m * o.n * 2, mm = L * o.m * o.m * 2;
@@ -778,12 +799,13 @@ static void launch_product(const OrthoArgs& a, int64_t L, int tile, hipStream_t 
   auto small = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)(L * a.count)), dim3(512), 0, stream, a); };
   if (tile == 16) return small(ortho_small_kernel<kWhat, kOut, kSplit, 1, 8>);
   if (tile == 32) return small(ortho_small_kernel<kWhat, kOut, kSplit, 2, 8>);
-  if (tile == 64) return go(ortho_product_kernel<kWhat, kOut, kSplit, 64, 64, 5>);
+  // Slabs ahead: 64 x 64 tiles two to a CU beat one with a deeper ring (2048 x 2048 gram 23.5 / 29.8 us), a
+  // 128 x 128 one alone on its CU wants the ring (18.4 / 21.3)
+  if (tile == 64) return go(ortho_product_kernel<kWhat, kOut, kSplit, 64, 64, 3>);
+  if (tile == 128 && L * a.count <= kCus) return go(ortho_product_kernel<kWhat, kOut, kSplit, 128, 128, 3>);
   if (tile == 128) return go(ortho_product_kernel<kWhat, kOut, kSplit, 128, 128, 2>);
   if constexpr (!kSplit) {
-    if constexpr (kWhat != Product::kUpdate) {
-      if (tile == 192) return go(ortho_product_kernel<kWhat, kOut, kSplit, 192, 192, 2>);
-    }
+    if (tile == 192) return go(ortho_product_kernel<kWhat, kOut, kSplit, 192, 192, 2>);
     go(ortho_product_kernel<kWhat, kOut, kSplit, 256, 256, 2>);
   }
 }
