@@ -66,6 +66,7 @@ struct OrthoArgs {
   int count;    // tiles per matrix
   float a, b, c, scale;
   int pivot;    // this step takes A about its mean eigenvalue
+  int low_in, low_out;  // X's low part is there, and is kept
   int tall;     // the result is transposed
 };
 
@@ -238,8 +239,8 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   const int64_t at_a = (int64_t)m0 * K, at_b = (int64_t)n0 * K;
   const int ksteps = pitch / kOrthoStep;
   const int steps = kSplit ? 3 * ksteps : ksteps;
-  auto rsrc_a = [&](int seg) { return make_rsrc((kSplit && seg == 2 ? a_lo : a_hi) + at_a, bytes_a); };
-  auto rsrc_b = [&](int seg) { return make_rsrc((kSplit && seg == 1 ? b_lo : b_hi) + at_b, bytes_b); };
+  auto rsrc_a = [&](int seg, bool any = true) { return make_rsrc((kSplit && seg == 2 ? a_lo : a_hi) + at_a, any ? bytes_a : 0u); };
+  auto rsrc_b = [&](int seg, bool any = true) { return make_rsrc((kSplit && seg == 1 ? b_lo : b_hi) + at_b, any ? bytes_b : 0u); };
 
   // copy q of thread tid brings row q * 32 + tid / 8, stored chunk tid % 8
   const int row0 = tid >> 3, lc0 = (tid & 7) ^ (row0 & 7);
@@ -266,6 +267,8 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
     else ra[h][u - SUBN] = *(const f16x8*)(sa + a_off[h] + (u - SUBN) * 16 * kOrthoStep);
   };
   constexpr int kEvery = kMfmas >= 2 * (SUBM + SUBN) ? 2 : 1;
+  // Half h of a step: its MFMAs, and between them the other half's operands from (sa, sb)
+  // and one operand's copies. Scheduling barriers keep that order.
   auto half = [&](int h, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ sb, __amdgpu_buffer_rsrc_t r, int k,
                   uint8_t* __restrict__ to, bool copy_is_a) {
 #pragma unroll
@@ -301,36 +304,10 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   for (int u = 0; u < SUBM + SUBN; ++u) read_operand(u, 0, lds, lds_b);
   int a0 = 0, a1 = Cfg::kSlabA, a2 = D * Cfg::kSlabA;
   int b0 = 0, b1 = Cfg::kSlabB;
-  for (int g = 0; g < steps; ++g) {
-    const int gn = min(g + D, steps - 1);  // past the end the last step is copied again, unread
-    const int seg = seg_of(gn), kn = k_of(gn);
-    half(0, lds + a0, lds_b + b0, rsrc_a(seg), kn, lds + a2, true);
-    // this wave has read all of step g, and its copies of step g + 1 have landed
-    __builtin_amdgcn_s_waitcnt(kOrthoWaitLds);
-    __builtin_amdgcn_s_waitcnt(ortho_wait_vm((D - 1) * Cfg::kLoadsA + (D - 2) * Cfg::kLoadsB));
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    half(1, lds + a1, lds_b + b1, rsrc_b(seg), kn, lds_b + b0, false);
-    a2 = a0, a0 = a1, b0 = b1;
-    a1 = a1 == D * Cfg::kSlabA ? 0 : a1 + Cfg::kSlabA;
-    b1 = b1 == (D - 1) * Cfg::kSlabB ? 0 : b1 + Cfg::kSlabB;
-  }
-  // the last copies may still be writing the LDS that is used again below
-  __builtin_amdgcn_s_waitcnt(ortho_wait_vm(0));
-  __syncthreads();
-
-  // ---- the tile's values ----
   const int mw = m0 + wm * WM, nw = n0 + wn * WN;  // this wave's part
-  const bool on_diagonal = kSymmetric && tm == tn;
-  float alpha = 0.0f;
-  if (kWhat == Product::kGram && p.pivot && on_diagonal) {
-    alpha = ortho_alpha(p, mat, (float*)lds, 256);
-    if (t == 0 && tid == 0) p.alpha[mat] = alpha;
-  }
-  if (kWhat != Product::kGram && p.pivot) alpha = p.alpha[mat];
-
   // What the epilogue reads of row block i: the tile's values of X or A, and what
-  // FP16 cut off the diagonal there. Loaded a row block ahead of its use.
+  // FP16 cut off the diagonal there. Loaded a row block ahead of its use, the first under
+  // the last step's products.
   struct Before {
     f16x4 hi[SUBN], lo[SUBN];
     float cut;
@@ -351,7 +328,7 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
       const bool inside = gm < p.m && nw + j * 16 + 4 * lk < rows_total;
       const f16x4 none = {0, 0, 0, 0};
       f.hi[j] = inside ? *(const f16x4*)(hi + j * 16) : none;
-      f.lo[j] = kLowBefore && inside ? *(const f16x4*)(lo + j * 16) : none;
+      f.lo[j] = kLowBefore && inside && (kSplit || p.low_in) ? *(const f16x4*)(lo + j * 16) : none;
     }
   };
   constexpr bool kCutN = kWhat == Product::kSquare && !kSplit;
@@ -365,6 +342,37 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
       for (int r = 0; r < 4; ++r) cut_n[j][r] = d[r];
     }
   }
+  Before before[2];
+  for (int g = 0; g < steps; ++g) {
+    // past the end the copies read nothing: an empty descriptor gives zeros, unread
+    const bool more = g + D < steps;
+    const int gn = more ? g + D : 0, seg = seg_of(gn), kn = k_of(gn);
+    half(0, lds + a0, lds_b + b0, rsrc_a(seg, more), kn, lds + a2, true);
+    // this wave has read all of step g, and its copies of step g + 1 have landed
+    __builtin_amdgcn_s_waitcnt(kOrthoWaitLds);
+    __builtin_amdgcn_s_waitcnt(ortho_wait_vm((D - 1) * Cfg::kLoadsA + (D - 2) * Cfg::kLoadsB));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (!kSplit && g == steps - 1) read_before(0, before[0]);
+    half(1, lds + a1, lds_b + b1, rsrc_b(seg, more), kn, lds_b + b0, false);
+    a2 = a0, a0 = a1, b0 = b1;
+    a1 = a1 == D * Cfg::kSlabA ? 0 : a1 + Cfg::kSlabA;
+    b1 = b1 == (D - 1) * Cfg::kSlabB ? 0 : b1 + Cfg::kSlabB;
+  }
+  if constexpr (kSplit) read_before(0, before[0]);  // (three times as many steps: its loop is the faster without)
+  // the last copies may still be writing the LDS that is used again below
+  __builtin_amdgcn_s_waitcnt(ortho_wait_vm(0));
+  __syncthreads();
+
+  // ---- the tile's values ----
+  const bool on_diagonal = kSymmetric && tm == tn;
+  float alpha = 0.0f;
+  if (kWhat == Product::kGram && p.pivot && on_diagonal) {
+    alpha = ortho_alpha(p, mat, (float*)lds, 256);
+    if (t == 0 && tid == 0) p.alpha[mat] = alpha;
+  }
+  if (kWhat != Product::kGram && p.pivot) alpha = p.alpha[mat];
+
   constexpr int kPitchR = Cfg::kPitchR, kPitchC = Cfg::kPitchC;
   uint8_t* const st_r = lds + wave * (Cfg::kStage / 4);
   uint8_t* const st_c = st_r + Cfg::kStageR;
@@ -382,8 +390,11 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
     for (int k = 0; k < kR * kCh / 64; ++k) {
       const int r = (k * 64 + lane) / kCh, ch = (k * 64 + lane) % kCh;
       const u32x4 v = *(const u32x4*)(st + r * kPitch + (kSwizzled ? swz_chunk(r, ch, kCh) : ch) * 16);
-      if (row + r < row_end && col + ch * 8 < col_end)
-        store_chunk((bf16_t*)to + (row + r) * ld + col + ch * 8, {v}, col_end - col - ch * 8);
+      if (row + r < row_end && col + ch * 8 < col_end) {
+        uint16_t* const at = to + (row + r) * ld + col + ch * 8;
+        if constexpr (kOut == Result::kPlanes) *(u32x4*)at = v;  // planes are padded to whole chunks
+        else store_chunk((bf16_t*)at, {v}, col_end - col - ch * 8);
+      }
     }
     __builtin_amdgcn_wave_barrier();
   };
@@ -411,8 +422,6 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   float* const cut = (kWhat == Product::kGram ? p.da : p.db) + mat * p.m;
 
   float square = 0.0f;
-  Before before[2];
-  read_before(0, before[0]);
 #pragma unroll
   for (int i = 0; i < SUBM; ++i) {
     const int gm = mw + i * 16 + lr;
@@ -471,9 +480,11 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
       }
       if (to_r) flush(k16, kWNc, st_r, to_r, ld_r, mw + i * 16, nw, end_m, end_n);
       if constexpr (kLowRows && kOut == Result::kPlanes) {
+        if (kSplit || p.low_out) {
 #pragma unroll
-        for (int j = 0; j < SUBN; ++j) put_row(j, lo[j][0], lo[j][1]);
-        flush(k16, kWNc, st_r, to_r_lo, ld_r, mw + i * 16, nw, end_m, end_n);
+          for (int j = 0; j < SUBN; ++j) put_row(j, lo[j][0], lo[j][1]);
+          flush(k16, kWNc, st_r, to_r_lo, ld_r, mw + i * 16, nw, end_m, end_n);
+        }
       }
     }
     // one row block at a time: with more of their loads ahead the registers do not hold
@@ -575,7 +586,7 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
     }
     if constexpr (kWhat == Product::kUpdate) {
       hi = *(const f16x4*)(p.x + o.mn + (int64_t)gm * p.n + gn);
-      lo = *(const f16x4*)(p.x_lo + o.mn + (int64_t)gm * p.n + gn);
+      if (kSplit || p.low_in) lo = *(const f16x4*)(p.x_lo + o.mn + (int64_t)gm * p.n + gn);
       if constexpr (!kSplit) cut_m = p.db[mat * p.m + gm];
     }
     if (kWhat != Product::kGram && p.pivot) alpha = p.alpha[mat];
@@ -635,7 +646,7 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
     };
     auto low = [](float v) { return v - (float)(_Float16)v; };
     put(to.r, to.c, pack_f16(val[0], val[1]), pack_f16(val[2], val[3]));
-    if constexpr (kSplit || kWhat == Product::kUpdate)
+    if (kSplit || (kWhat == Product::kUpdate && p.low_out))
       put(to.r_lo, kSplit ? to.c_lo : nullptr, pack_f16(low(val[0]), low(val[1])), pack_f16(low(val[2]), low(val[3])));
   } else {
 #pragma unroll
@@ -825,6 +836,8 @@ static hipError_t run_ortho(const void* g, bool g_bf16, int64_t L, int64_t M, in
   for (int k = 0; k < steps; ++k) {
     // (the first step has no sum of squares before it, and alpha = 1 / m there)
     p.pivot = !kSplit && k >= 1 && k >= steps - 2;
+    // (X before the last step: its rounding is not amplified any more, high alone adds 0 to 3e-4)
+    p.low_in = k == 0 || k < steps - 1, p.low_out = k < steps - 2;
     p.xt = xt[k % 2], p.xt_lo = xt_lo[k % 2];
     p.xt_new = xt[1 - k % 2], p.xt_lo_new = xt_lo[1 - k % 2];
     p.count = (int)o.symmetric;
