@@ -748,9 +748,10 @@ int fp8q_orthogonalize(const void* g, int g_dtype, int64_t L, int64_t M, int64_t
   int s = check_ortho(L, M, N);
   if (s == -1) return FP8Q_OK;
   if (s) return s;
-  if (!g || !out || !workspace) return FP8Q_ERR_NULL;
   const bool bf16 = out_dtype == FP8Q_OUT_BF16;
-  if (workspace_bytes < fp8q::ortho_workspace_bytes(L, M, N, bf16)) return FP8Q_ERR_SHAPE;
+  const int64_t need = fp8q::ortho_workspace_bytes(L, M, N, bf16);
+  if (!g || !out || (need && !workspace)) return FP8Q_ERR_NULL;
+  if (workspace_bytes < need) return FP8Q_ERR_SHAPE;
   if (!aligned(g, element(g_dtype)) || !aligned(out, element(out_dtype)) || !aligned(workspace, 16))
     return FP8Q_ERR_ALIGN;
   if ((s = check_device())) return s;

@@ -193,8 +193,8 @@ struct Turned {
 };
 __device__ __forceinline__ Turned turn_pairs(bool odd, uint32_t p0, uint32_t p1) {
   const uint32_t own = odd ? p1 : p0, got = dpp_u32<0xB1>(odd ? p0 : p1);
-  const uint32_t a = odd ? got : own, b = odd ? own : got;
-  return {(a & 0xFFFFu) | (b << 16), (a >> 16) | (b & 0xFFFF0000u)};
+  // bytes 0 to 3 are own's, 4 to 7 got's; the even lane's row comes first
+  return {__builtin_amdgcn_perm(got, own, odd ? 0x01000504u : 0x05040100u), __builtin_amdgcn_perm(got, own, odd ? 0x03020706u : 0x07060302u)};
 }
 
 // ---------------------------------------------------------------------------
@@ -729,9 +729,215 @@ __global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__
 }
 
 // ---------------------------------------------------------------------------
+// A matrix that fits a CU's LDS: one workgroup of 16 wavefronts takes all the steps of
+// one matrix, m and n padded to 32. A wavefront keeps its units of X, of 16 S x 16 S values,
+// in registers as binary32; LDS holds X's high and low parts in both orientations, and A's
+// and then B's over X's rows, which only the gram reads, one unit to a wavefront. (All units of A
+// and B: a SIMD has work for four wavefronts at m = 128 either way, and writing one's mirror costs as
+// much as forming it.) The products are as for kSplit. One launch in place of two and three a step, which is
+// what small matrices wait for.
+// A step takes 1.1 us for 16 x 26, 2.9 us for 64 x 64 and 9.2 us for 128 x 128: there a half the
+// MFMAs and half the vector operations that form, split and place the values, in turn.
+// S = 1 where m is 32, whose A would be a single 32 x 32 unit.
+// ---------------------------------------------------------------------------
+constexpr int kWholeWaves = 16, kWholeLds = 160 * 1024, kWholeGap = 8;  // gap: after a row, against bank conflicts
+constexpr int64_t whole_lds(int64_t m, int64_t n) { return 4 * (m * (n + kWholeGap) + n * (m + kWholeGap)); }
+
+template <typename T, int S>
+__global__ __launch_bounds__(64 * kWholeWaves) void ortho_whole_kernel(const T* __restrict__ g, OrthoArgs p, int steps, bool out_bf16) {
+  constexpr int kSide = 16 * S, kOwn = S == 1 ? 5 : 2;  // units of X a wavefront has at most
+  __shared__ __attribute__((aligned(16))) _Float16 lds[kWholeLds / 2];
+  const int lane = threadIdx.x & 63;
+  int lr = lane & 15, lk = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = p.m, n = p.n, pitch_r = n + kWholeGap, pitch_c = m + kWholeGap;
+  _Float16 *const xr = lds, *const xr_lo = xr + m * pitch_r, *const xc = xr_lo + m * pitch_r, *const xc_lo = xc + n * pitch_c;
+  _Float16 *const am = lds, *const am_lo = am + m * pitch_c;
+  const int across = n / kSide, units = m / kSide * across;
+  const int across_a = m / kSide, am0 = wave / across_a * kSide, an0 = wave % across_a * kSide;
+  const bool has_a = wave < across_a * across_a;
+  const int64_t base = blockIdx.x * (int64_t)p.m_true * p.n_true;
+  // value r of this lane's four of block (i, j) of unit k: its place in X, and in G and the result
+  int row0[kOwn], col0[kOwn];  // of this wavefront's units
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k)
+    row0[k] = (wave + k * kWholeWaves) / across * kSide, col0[k] = (wave + k * kWholeWaves) % across * kSide;
+  auto row_of = [&](int k, int i) { return row0[k] + i * 16 + lr; };
+  auto col_of = [&](int k, int j) { return col0[k] + j * 16 + 4 * lk; };
+  const int ld_row = p.tall ? 1 : p.n_true, ld_col = p.tall ? p.m_true : 1;
+  auto place = [&](int row, int col) { return (uint32_t)(row * ld_row + col * ld_col); };
+
+  v4f x[kOwn][S][S];
+  double sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        x[k][i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (wave + k * kWholeWaves < units)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {  // past the matrix: its last row or column, so that no load waits in a branch
+            const T* const from = g + base + place(min(row_of(k, i), p.m_true - 1), min(col_of(k, j) + r, p.n_true - 1));
+            if constexpr (sizeof(T) == 2) x[k][i][j][r] = __uint_as_float((uint32_t)from->bits << 16);
+            else x[k][i][j][r] = *from;
+          }
+      }
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (row_of(k, i) >= p.m_true || col_of(k, j) + r >= p.n_true) x[k][i][j][r] = 0.0f;
+          sum = __builtin_fma((double)x[k][i][j][r], (double)x[k][i][j][r], sum);
+        }
+  sum = wave_sum_f64(sum);
+  double* const sums = (double*)lds;
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWholeWaves; ++w) sum += sums[w];
+  const double f = sum > 0.0 ? (double)kScaleX / __dsqrt_rn(sum) : sum;  // (a NaN goes on)
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[k][i][j][r] = (float)((double)x[k][i][j][r] * f);
+
+  // four values of a row to the planes of a matrix, and to those of its transpose
+  auto put = [&](_Float16* rows, _Float16* rows_lo, int ld_r, auto turned, _Float16* cols, _Float16* cols_lo, int ld_c, int row, int col,
+                 const v4f& v) {
+    const bool odd = lr & 1;
+    auto part = [&](_Float16* to_r, _Float16* to_c, uint32_t p0, uint32_t p1) {
+      *(uint2*)(to_r + row * ld_r + col) = make_uint2(p0, p1);
+      if constexpr (!decltype(turned)::value) return;
+      const Turned w = turn_pairs(odd, p0, p1);
+      _Float16* const at = to_c + (col + (odd ? 2 : 0)) * ld_c + (row & ~1);
+      *(uint32_t*)at = w.first;
+      *(uint32_t*)(at + ld_c) = w.second;
+    };
+    const f16x4 hi = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+    f16x4 lo;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) lo[r] = (_Float16)__builtin_fmaf((float)hi[r], -1.0f, v[r]);
+    const uint2 h = __builtin_bit_cast(uint2, hi), l = __builtin_bit_cast(uint2, lo);
+    part(rows, cols, h.x, h.y);
+    part(rows_lo, cols_lo, l.x, l.y);
+  };
+  // acc = rows a0.. of a times rows b0.. of b, K values each
+  auto multiply = [&](const _Float16* a, const _Float16* a_lo, const _Float16* b, const _Float16* b_lo, int ld, int a0, int b0, int K,
+                      v4f (&acc)[S][S]) {
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int at_a = (a0 + lr) * ld + 8 * lk, at_b = (b0 + lr) * ld + 8 * lk;
+    for (int k = 0; k < K; k += 32) {
+      f16x8 fa[S], fb[S], fa_lo[S], fb_lo[S];
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        fa[i] = *(const f16x8*)(a + at_a + i * 16 * ld + k), fa_lo[i] = *(const f16x8*)(a_lo + at_a + i * 16 * ld + k);
+        fb[i] = *(const f16x8*)(b + at_b + i * 16 * ld + k), fb_lo[i] = *(const f16x8*)(b_lo + at_b + i * 16 * ld + k);
+      }
+      auto add = [&](const f16x8 (&u)[S], const f16x8 (&v)[S]) {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int j = 0; j < S; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[j], u[i], acc[i][j], 0, 0, 0);
+      };
+      add(fa, fb), add(fa, fb_lo), add(fa_lo, fb);
+    }
+  };
+  auto put_a = [&](const v4f (&v)[S][S]) {
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+        put(am, am_lo, pitch_c, std::false_type{}, am, am_lo, 0, am0 + i * 16 + lr, an0 + j * 16 + 4 * lk, v[i][j]);
+  };
+
+  for (int s = 0; s < steps; ++s) {
+    if (S > 1) asm volatile("" : "+v"(lr), "+v"(lk));  // the addresses are formed anew each step: all of them would not fit the registers
+    __syncthreads();  // X's and B's readers are done
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+      if (wave + k * kWholeWaves < units)
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int j = 0; j < S; ++j)
+            put(xr, xr_lo, pitch_r, std::true_type{}, xc, xc_lo, pitch_c, row_of(k, i), col_of(k, j), x[k][i][j]);
+    __syncthreads();
+    v4f v[S][S];
+    if (has_a) multiply(xr, xr_lo, xr, xr_lo, pitch_r, am0, an0, n, v);
+    __syncthreads();
+    if (has_a) {
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int j = 0; j < S; ++j) v[i][j] *= kScaleA / (kScaleX * kScaleX);
+      put_a(v);
+    }
+    __syncthreads();
+    v4f acc[S][S];
+    if (has_a) multiply(am, am_lo, am, am_lo, pitch_c, am0, an0, m, acc);
+    __syncthreads();
+    if (has_a) {
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int j = 0; j < S; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v[i][j][r] = ortho_value<Product::kSquare, true>(p, acc[i][j][r], v[i][j][r], 0.0f, 0.0f, 0.0f, false, 0.0f);
+      put_a(v);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+      if (wave + k * kWholeWaves < units) {
+        multiply(am, am_lo, xc, xc_lo, pitch_c, row0[k], col0[k], m, acc);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int j = 0; j < S; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              x[k][i][j][r] = ortho_value<Product::kUpdate, true>(p, acc[i][j][r], x[k][i][j][r], 0.0f, 0.0f, 0.0f, false, 0.0f);
+      }
+  }
+  const float scale = p.scale * (1.0f / kScaleX);
+  auto store = [&](auto* out) {
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+      if (wave + k * kWholeWaves < units)
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int j = 0; j < S; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int row = row_of(k, i), col = col_of(k, j) + r;
+              if (row < p.m_true && col < p.n_true)
+                (out + base)[place(row, col)] = (std::remove_pointer_t<decltype(out)>)(x[k][i][j][r] * scale);
+            }
+  };
+  if (out_bf16) store((__bf16*)p.out);
+  else store((float*)p.out);
+}
+
+// ---------------------------------------------------------------------------
 struct OrthoPlan {
   int64_t m, n;  // padded
-  bool split;
+  bool split, in_lds;  // in_lds: one workgroup a matrix
   int tile_sym, tile;  // of the gram and the square, and of the update
   int64_t symmetric, whole;
   int64_t bytes;
@@ -774,8 +980,17 @@ static int ortho_tile(int64_t L, Count count, int64_t K, bool symmetric, bool sp
 }
 
 static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
-  OrthoPlan o;
+  OrthoPlan o{};
   const int64_t lo = M < N ? M : N, hi = M < N ? N : M;
+  o.m = (lo + 31) / 32 * 32;
+  o.n = (hi + 31) / 32 * 32;
+  // A matrix to a workgroup, where it fits (then X has at most 68 16 x 16 or 18 32 x 32 units) and unless few
+  // matrices are the larger ones. us for five steps against the products' launches, MI355X, L x m x n:
+  //   16 x 26 11 / 52    32 x 540 33 / 60    64 x 64 22 / 54    64 x 288 48 / 55    96 x 96 41 / 56    96 x 160 53 / 57
+  //   96 x 192 59 / 57    128 x 128 64 / 55    4 x 128 x 128 64 / 58    8 x 128 x 128 64 / 70    256 x 128 x 128 74 / 267
+  //   256 x 64 x 64 23 / 123
+  o.in_lds = whole_lds(o.m, o.n) <= kWholeLds && (o.m <= 64 || o.m * o.n <= 96 * 160 || L >= 8);
+  if (o.in_lds) return o;
   o.m = (lo + kPad - 1) / kPad * kPad;
   o.n = (hi + kPad - 1) / kPad * kPad;
   o.split = !bf16 || lo <= 128;
@@ -859,6 +1074,22 @@ hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M
   p.tall = M > N;
   p.m_true = (int)(p.tall ? N : M), p.n_true = (int)(p.tall ? M : N);
   p.a = a, p.b = b, p.c = c, p.scale = scale, p.out = out;
+  if (o.in_lds) {
+    auto go = [&](auto kernel, auto from) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)L), dim3(64 * kWholeWaves), 0, stream, from, p, steps, out_bf16);
+    };
+    auto of = [&](auto s, auto from) {
+      constexpr int S = decltype(s)::value;
+      go(ortho_whole_kernel<std::remove_const_t<std::remove_pointer_t<decltype(from)>>, S>, from);
+    };
+    auto sized = [&](auto from) {
+      if (o.m == 32) of(std::integral_constant<int, 1>{}, from);
+      else of(std::integral_constant<int, 2>{}, from);
+    };
+    if (g_bf16) sized((const bf16_t*)g);
+    else sized((const float*)g);
+    return hipGetLastError();
+  }
   p.parts = (int)o.whole * (o.tile == 16 ? 1 : 4);
   uint8_t* at = (uint8_t*)ws;
   auto take = [&](int64_t bytes) {

@@ -749,10 +749,12 @@ FP8Q_API int fp8q_swiglu_bwd(const void* dy, int dy_dtype, int64_t ldy, const vo
  * that stay in [0, 1], such as (2, -1.5, 0.5); otherwise FP8Q_ERR_SHAPE.
  *
  *   g   : in,  L x M x N of g_dtype;  out : L x M x N of out_dtype
- *   workspace : at least fp8q_orthogonalize_workspace_bytes(L, M, N, out_dtype), 16-byte aligned
+ *   workspace : at least fp8q_orthogonalize_workspace_bytes(L, M, N, out_dtype), 16-byte aligned;
+ *               may be NULL where that is 0 (matrices that a workgroup holds)
  * g and out need their element's alignment only. 1 <= steps <= 100, scale finite,
  * L <= 65535, M, N <= 65536, and L M N below about 2^36 (FP8Q_ERR_TOO_LARGE).
- * L, M or N == 0 is a no-op. Deterministic; allocates nothing. 2 + 3 * steps kernels.
+ * L, M or N == 0 is a no-op. Deterministic; allocates nothing. 2 + 3 * steps kernels, or one
+ * where no workspace is needed.
  */
 FP8Q_API int64_t fp8q_orthogonalize_workspace_bytes(int64_t L, int64_t M, int64_t N, int out_dtype);
 FP8Q_API int fp8q_orthogonalize(const void* g, int g_dtype, int64_t L, int64_t M, int64_t N,

@@ -160,6 +160,21 @@ def test_several_matrices(L, M, N, out):
         check(a, b, out)
 
 
+@pytest.mark.parametrize("L,M,N", [(1, 2, 545), (2, 32, 544), (1, 30, 512), (1, 64, 288), (1, 290, 64), (1, 161, 96), (1, 96, 160),
+                                   (8, 96, 192), (8, 190, 90), (9, 128, 128), (7, 128, 128), (8, 128, 129), (300, 33, 17)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32")])
+def test_matrices_about_what_a_workgroup_holds(L, M, N, dtype, out):
+    import torch
+    import fp8_fine_grained_online_amd as F
+    kinds = ("gauss", "few", "decay")
+    g = dev(np.stack([matrix(M, N, kinds[i % 3] if min(M, N) > 4 else "gauss", 3370 + i) for i in range(L)]), dtype)
+    o = torch.full((L * M * N + 5,), 7.0, dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    F.fp8q_orthogonalize(g, out_dtype=out, out=o[:L * M * N].view(L, M, N))
+    assert torch.all(o[L * M * N:] == 7.0)
+    for i in sorted({0, 1 % L, 2 % L, L // 2, L - 1}):
+        check(host(g[i]), host(o[:L * M * N].view(L, M, N)[i]), out)
+
+
 @pytest.mark.parametrize("M,N,dtype", [(1024, 4096, "bf16"), (2100, 1900, "f32"), (4096, 700, "bf16")])
 @pytest.mark.parametrize("kind", ["gauss", "few"])
 def test_large(M, N, dtype, kind):
@@ -274,7 +289,7 @@ def test_refusals():
     with pytest.raises(TypeError):
         F.fp8q_orthogonalize(g.half())
     for call in (lambda: F.fp8q_orthogonalize(g, coeffs=(9.0, 0.0, 0.0)), lambda: F.fp8q_orthogonalize(g, scale=float("inf")),
-                 lambda: F.fp8q_orthogonalize(g, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))):
+                 lambda: F.fp8q_orthogonalize(torch.randn(200, 300, device="cuda"), workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(F.Fp8qError):
             call()
     for shape in ((0, 5), (5, 0), (2, 0, 3)):

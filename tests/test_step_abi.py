@@ -96,19 +96,22 @@ def test_swiglu_bwd():
 
 def test_orthogonalize():
     L = _lib()
-    f, need = L.fp8q_orthogonalize, L.fp8q_orthogonalize_workspace_bytes(2, 33, 70, BF16)
+    f, need = L.fp8q_orthogonalize, L.fp8q_orthogonalize_workspace_bytes(2, 133, 270, BF16)
     size = L.fp8q_orthogonalize_workspace_bytes
     # X and both X^T, high parts at least
-    assert need >= 3 * 2 * 64 * 128 * 2 and size(2, 33, 70, F32) >= need and size(0, 33, 70, F32) == 0
+    assert need >= 3 * 2 * 192 * 320 * 2 and size(2, 133, 270, F32) >= need and size(0, 133, 270, F32) == 0
+    assert size(2, 33, 70, BF16) == 0  # small matrices need none
     assert size(2, 33, 70, 2) == -1 and size(-1, 33, 70, F32) == -1 and size(1, 65537, 4, F32) == -1
     assert size(65536, 4, 4, F32) == -1 and size(65535, 4096, 4096, BF16) == -1
     #       0  1    2  3   4   5  6       7       8       9    10 11    12  13    14
-    good = [X, F32, 2, 33, 70, 5, 3.4445, -4.775, 2.0315, 0.5, Y, BF16, WS, need, None]
+    good = [X, F32, 2, 133, 270, 5, 3.4445, -4.775, 2.0315, 0.5, Y, BF16, WS, need, None]
     refuses(f, good, [
         (1, 2, DTYPE), (11, -1, DTYPE), (2, -1, SHAPE), (3, -1, SHAPE), (4, -1, SHAPE), (5, 0, SHAPE), (5, 101, SHAPE),
         (6, NAN, SHAPE), (7, INF, SHAPE), (8, NAN, SHAPE), (9, INF, SHAPE), (9, NAN, SHAPE), (13, need - 1, SHAPE),
         (3, 65537, LARGE), (4, 65537, LARGE), (2, 65536, LARGE), (0, None, NULL), (10, None, NULL), (12, None, NULL),
         (0, X + 2, ALIGN), (10, Y + 1, ALIGN), (12, WS + 8, ALIGN)])
+    refuses(f, good[:3] + [33, 70] + good[5:12] + [None, 0, None], [
+        (0, None, NULL), (10, None, NULL), (13, -1, SHAPE), (12, WS + 8, ALIGN), (0, X + 2, ALIGN), (10, Y + 1, ALIGN)])
     assert f(None, F32, 0, 33, 70, 5, 2.0, -1.5, 0.5, 1.0, None, BF16, None, 0, None) == 0
     assert f(None, F32, 2, 33, 0, 5, 2.0, -1.5, 0.5, 1.0, None, BF16, None, 0, None) == 0
 
