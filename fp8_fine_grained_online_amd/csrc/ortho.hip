@@ -49,6 +49,14 @@ constexpr int kPad = 64;                               // rows and columns are p
 constexpr int kOrthoStep = 128;                        // bytes of K per pipeline step: 64 values
 constexpr int kNormParts = 512;                        // partial sums of |G|^2 per matrix
 
+// Where value (row, col) of a plane lies: blocks of 16 rows x 32 values, the operand of one
+// MFMA, one after the other along the rows; in a block, eight values of each of its 16 rows at a time.
+// A fragment is 1 KB in one piece whatever the pitch, where rows of 2^k bytes would all
+// come from the same few channels of the L2.
+__device__ __forceinline__ int64_t plane_at(int row, int col, int ld) {
+  return (int64_t)(row >> 4) * 16 * ld + (col >> 5) * 512 + ((col >> 3) & 3) * 128 + (row & 15) * 8 + (col & 7);
+}
+
 enum class Product { kGram, kSquare, kUpdate };
 
 struct OrthoArgs {
@@ -200,7 +208,7 @@ __device__ __forceinline__ Turned turn_pairs(bool odd, uint32_t p0, uint32_t p1)
 // ---------------------------------------------------------------------------
 // One tile of one product. Four wavefronts, each a quarter of the tile; per step
 // of 64 values of K the slabs of both operands go straight from global memory to
-// LDS (16-byte chunk c of row r at position c ^ (r % 8)), and each step is
+// LDS as they lie there, fragment by fragment, and each step is
 // multiplied in two halves, the one's operands read from LDS while the other
 // multiplies; A's slabs rotate through D + 1 buffers, B's through D. Lane l
 // supplies row l % 16 of a 16-row block and 8 values of K at 8 (l / 16); B is the
@@ -242,12 +250,12 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   auto rsrc_a = [&](int seg, bool any = true) { return make_rsrc((kSplit && seg == 2 ? a_lo : a_hi) + at_a, any ? bytes_a : 0u); };
   auto rsrc_b = [&](int seg, bool any = true) { return make_rsrc((kSplit && seg == 1 ? b_lo : b_hi) + at_b, any ? bytes_b : 0u); };
 
-  // copy q of thread tid brings row q * 32 + tid / 8, stored chunk tid % 8
-  const int row0 = tid >> 3, lc0 = (tid & 7) ^ (row0 & 7);
+  // copy q of wavefront w brings fragment 4 q + w of the slab: half w % 2 of row block 2 q + w / 2
+  const uint32_t first = (uint32_t)(wave >> 1) * 16 * (uint32_t)pitch + (wave & 1) * 1024 + lane * 16;
   constexpr int kRows = Cfg::kLoadsA > Cfg::kLoadsB ? Cfg::kLoadsA : Cfg::kLoadsB;
   uint32_t off[kRows];
 #pragma unroll
-  for (int q = 0; q < kRows; ++q) off[q] = (uint32_t)(row0 + q * 32) * (uint32_t)pitch + lc0 * 16;
+  for (int q = 0; q < kRows; ++q) off[q] = first + (uint32_t)(q * 32) * (uint32_t)pitch;
   auto copy_a = [&](int q, __amdgpu_buffer_rsrc_t r, int k, uint8_t* __restrict__ to) {
     load_lds(r, to + (q * 256 + wave * 64) * 16, 16, off[q], k);
   };
@@ -259,12 +267,10 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
 #pragma unroll
     for (int j = 0; j < SUBN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   f16x8 ra[2][SUBM], rb[2][SUBN];
-  const int a_off[2] = {(wm * WM + lr) * kOrthoStep + ((lk ^ (lr & 7)) << 4),
-                        (wm * WM + lr) * kOrthoStep + (((4 + lk) ^ (lr & 7)) << 4)};
-  const int b_off[2] = {a_off[0] + (wn * WN - wm * WM) * kOrthoStep, a_off[1] + (wn * WN - wm * WM) * kOrthoStep};
+  const int a_off = wm * WM * kOrthoStep + lane * 16, b_off = wn * WN * kOrthoStep + lane * 16;
   auto read_operand = [&](int u, int h, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ sb) {
-    if (u < SUBN) rb[h][u] = *(const f16x8*)(sb + b_off[h] + u * 16 * kOrthoStep);
-    else ra[h][u - SUBN] = *(const f16x8*)(sa + a_off[h] + (u - SUBN) * 16 * kOrthoStep);
+    if (u < SUBN) rb[h][u] = *(const f16x8*)(sb + b_off + u * 2048 + h * 1024);
+    else ra[h][u - SUBN] = *(const f16x8*)(sa + a_off + (u - SUBN) * 2048 + h * 1024);
   };
   constexpr int kEvery = kMfmas >= 2 * (SUBM + SUBN) ? 2 : 1;
   // Half h of a step: its MFMAs, and between them the other half's operands from (sa, sb)
@@ -288,7 +294,7 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
 
   // step g: byte of K and, for kSplit, which parts are multiplied
   auto seg_of = [&](int g) { return !kSplit || g < ksteps ? 0 : g < 2 * ksteps ? 1 : 2; };
-  auto k_of = [&](int g) { return (g - seg_of(g) * ksteps) * kOrthoStep; };
+  auto k_of = [&](int g) { return (g - seg_of(g) * ksteps) * (16 * kOrthoStep); };
   uint8_t* const lds_b = lds + (D + 1) * Cfg::kSlabA;
 #pragma unroll
   for (int d = 0; d < D; ++d) {
@@ -320,15 +326,15 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
     }
     const int gm = mw + i * 16 + lr;
     f.cut = !kSplit && gm < p.m ? (kWhat == Product::kSquare ? p.da : p.db)[mat * p.m + gm] : 0.0f;
-    const int64_t at = (kWhat == Product::kSquare ? mm : mn) + (int64_t)gm * rows_total + nw + 4 * lk;
-    const _Float16* const hi = (kWhat == Product::kSquare ? p.am : p.x) + at;
-    const _Float16* const lo = (kWhat == Product::kSquare ? p.am_lo : p.x_lo) + at;
+    const _Float16* const hi = (kWhat == Product::kSquare ? p.am + mm : p.x + mn);
+    const _Float16* const lo = (kWhat == Product::kSquare ? p.am_lo + mm : p.x_lo + mn);
 #pragma unroll
     for (int j = 0; j < SUBN; ++j) {
       const bool inside = gm < p.m && nw + j * 16 + 4 * lk < rows_total;
       const f16x4 none = {0, 0, 0, 0};
-      f.hi[j] = inside ? *(const f16x4*)(hi + j * 16) : none;
-      f.lo[j] = kLowBefore && inside && (kSplit || p.low_in) ? *(const f16x4*)(lo + j * 16) : none;
+      const int64_t at = plane_at(gm, nw + j * 16 + 4 * lk, rows_total);
+      f.hi[j] = inside ? *(const f16x4*)(hi + at) : none;
+      f.lo[j] = kLowBefore && inside && (kSplit || p.low_in) ? *(const f16x4*)(lo + at) : none;
     }
   };
   constexpr bool kCutN = kWhat == Product::kSquare && !kSplit;
@@ -388,12 +394,13 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 4
     for (int k = 0; k < kR * kCh / 64; ++k) {
-      const int r = (k * 64 + lane) / kCh, ch = (k * 64 + lane) % kCh;
+      // (planes: 16 rows of a chunk are one piece)
+      const int u = k * 64 + lane;
+      const int r = kOut == Result::kPlanes ? u / (16 * kCh) * 16 + u % 16 : u / kCh, ch = kOut == Result::kPlanes ? u / 16 % kCh : u % kCh;
       const u32x4 v = *(const u32x4*)(st + r * kPitch + (kSwizzled ? swz_chunk(r, ch, kCh) : ch) * 16);
       if (row + r < row_end && col + ch * 8 < col_end) {
-        uint16_t* const at = to + (row + r) * ld + col + ch * 8;
-        if constexpr (kOut == Result::kPlanes) *(u32x4*)at = v;  // planes are padded to whole chunks
-        else store_chunk((bf16_t*)at, {v}, col_end - col - ch * 8);
+        if constexpr (kOut == Result::kPlanes) *(u32x4*)(to + plane_at(row + r, col + ch * 8, (int)ld)) = v;  // padded to whole chunks
+        else store_chunk((bf16_t*)(to + (row + r) * ld + col + ch * 8), {v}, col_end - col - ch * 8);
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -502,6 +509,40 @@ __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
   }
 }
 
+// Four values of row gm from column gn on, from a lane of a 16 x 16 block's wavefront, to where a product's
+// result goes.
+template <Product kWhat, Result kOut, bool kSplit>
+__device__ __forceinline__ void ortho_put(const OrthoArgs& p, const OrthoOperands& o, int64_t mat, bool on_diagonal, int gm, int gn,
+                                          const float (&val)[4]) {
+  const float scale = p.scale * (1.0f / kScaleX);
+  if constexpr (kOut == Result::kPlanes) {
+    const OrthoPlaces to = ortho_places<kWhat, kOut>(p, o, mat, on_diagonal);
+    auto put = [&](uint16_t* rows, uint16_t* cols, uint32_t p0, uint32_t p1) {
+      if (rows) *(uint2*)(rows + plane_at(gm, gn, (int)to.ld_r)) = make_uint2(p0, p1);
+      if (cols) {
+        const bool odd = gm & 1;
+        const Turned v = turn_pairs(odd, p0, p1);
+        uint16_t* const at = cols + plane_at(gn + (odd ? 2 : 0), gm & ~1, (int)to.ld_c);
+        *(uint32_t*)at = v.first;
+        *(uint32_t*)(at + 8) = v.second;
+      }
+    };
+    auto low = [](float v) { return v - (float)(_Float16)v; };
+    put(to.r, to.c, pack_f16(val[0], val[1]), pack_f16(val[2], val[3]));
+    if (kSplit || (kWhat == Product::kUpdate && p.low_out))
+      put(to.r_lo, kSplit ? to.c_lo : nullptr, pack_f16(low(val[0]), low(val[1])), pack_f16(low(val[2]), low(val[3])));
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (gm >= p.m_true || gn + r >= p.n_true) continue;
+      const int64_t at = mat * (int64_t)p.m_true * p.n_true +
+                         (p.tall ? (int64_t)(gn + r) * p.m_true + gm : (int64_t)gm * p.n_true + gn + r);
+      if constexpr (kOut == Result::kBf16) ((__bf16*)p.out)[at] = (__bf16)(val[r] * scale);
+      else ((float*)p.out)[at] = val[r] * scale;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Small products: a workgroup owns 16 S x 16 S values and its W wavefronts split K
 // between them in pieces of 32 values (one MFMA deep), each streaming its fragments
@@ -536,11 +577,11 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
   struct Frags {
     f16x8 a[S], b[S], a_lo[kSplit ? S : 1], b_lo[kSplit ? S : 1];
   };
-  const int64_t at_a = (int64_t)(m0 + lr) * o.K + 8 * lk, at_b = (int64_t)(n0 + lr) * o.K + 8 * lk;
+  const int64_t at_a = (int64_t)m0 * o.K + lane * 8, at_b = (int64_t)n0 * o.K + lane * 8;
   auto load = [&](int g, Frags& f) {
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const int64_t off = (int64_t)i * 16 * o.K + g * 32;
+      const int64_t off = (int64_t)i * 16 * o.K + g * 512;
       f.a[i] = *(const f16x8*)(o.a_hi + at_a + off);
       f.b[i] = *(const f16x8*)(o.b_hi + at_b + off);
       if constexpr (kSplit) {
@@ -580,13 +621,15 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
   v4f cut_n = {0.0f, 0.0f, 0.0f, 0.0f};
   if (finishes) {
     if constexpr (kWhat == Product::kSquare) {
-      hi = *(const f16x4*)(p.am + o.mm + (int64_t)gm * p.m + gn);
-      if constexpr (kSplit) lo = *(const f16x4*)(p.am_lo + o.mm + (int64_t)gm * p.m + gn);
+      const int64_t at = o.mm + plane_at(gm, gn, p.m);
+      hi = *(const f16x4*)(p.am + at);
+      if constexpr (kSplit) lo = *(const f16x4*)(p.am_lo + at);
       else cut_m = p.da[mat * p.m + gm], cut_n = *(const v4f*)(p.da + mat * p.m + gn);
     }
     if constexpr (kWhat == Product::kUpdate) {
-      hi = *(const f16x4*)(p.x + o.mn + (int64_t)gm * p.n + gn);
-      if (kSplit || p.low_in) lo = *(const f16x4*)(p.x_lo + o.mn + (int64_t)gm * p.n + gn);
+      const int64_t at = o.mn + plane_at(gm, gn, p.n);
+      hi = *(const f16x4*)(p.x + at);
+      if (kSplit || p.low_in) lo = *(const f16x4*)(p.x_lo + at);
       if constexpr (!kSplit) cut_m = p.db[mat * p.m + gm];
     }
     if (kWhat != Product::kGram && p.pivot) alpha = p.alpha[mat];
@@ -631,32 +674,93 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
     square = wave_sum_f32(square) * (1.0f / (kScaleX * kScaleX));
     if (lane == 0) p.squares[mat * p.parts + t * (S * S) + wave] = square;
   }
-  const float scale = p.scale * (1.0f / kScaleX);
-  if constexpr (kOut == Result::kPlanes) {
-    const OrthoPlaces to = ortho_places<kWhat, kOut>(p, o, mat, on_diagonal);
-    auto put = [&](uint16_t* rows, uint16_t* cols, uint32_t p0, uint32_t p1) {
-      if (rows) *(uint2*)(rows + (int64_t)gm * to.ld_r + gn) = make_uint2(p0, p1);
-      if (cols) {
-        const bool odd = lr & 1;
-        const Turned v = turn_pairs(odd, p0, p1);
-        uint16_t* const at = cols + (int64_t)(gn + (odd ? 2 : 0)) * to.ld_c + (gm & ~1);
-        *(uint32_t*)at = v.first;
-        *(uint32_t*)(at + to.ld_c) = v.second;
-      }
-    };
-    auto low = [](float v) { return v - (float)(_Float16)v; };
-    put(to.r, to.c, pack_f16(val[0], val[1]), pack_f16(val[2], val[3]));
-    if (kSplit || (kWhat == Product::kUpdate && p.low_out))
-      put(to.r_lo, kSplit ? to.c_lo : nullptr, pack_f16(low(val[0]), low(val[1])), pack_f16(low(val[2]), low(val[3])));
-  } else {
+  ortho_put<kWhat, kOut, kSplit>(p, o, mat, on_diagonal, gm, gn, val);
+}
+
+// ---------------------------------------------------------------------------
+// Square and update in one, for few rows: B X = A (b X + c A X), so that a workgroup
+// needs no other one's part of B. It owns 16 columns of X, and each of its wavefronts 16
+// rows, whose part of A (32 P columns, all of it) it keeps in registers for both products;
+// the columns, and between the products W = b X + c A X, go through LDS. That is m^2 n products more
+// in place of m^3, but a launch less a step, and either launch takes about 4 us whatever it multiplies.
+// W is two FP16 numbers, times 2^9: its singular values |s (b + c s^2)|, and about a mean
+// eigenvalue at most |c| alpha s more, stay below a third of what that leaves, 128, for
+// every polynomial that passes the checks. (Its rounding to one would not be small beside what
+// b A + c A A cancels: 3e-3 for a matrix of rank one.)
+// ---------------------------------------------------------------------------
+template <Result kOut, bool kSplit, int P>
+__global__ __launch_bounds__(128 * P) void ortho_columns_kernel(OrthoArgs p) {
+  constexpr int kWaves = 2 * P, kParts = kSplit ? 2 : 1;
+  constexpr float kScaleW = 512.0f;
+  __shared__ __attribute__((aligned(16))) _Float16 columns[2][2 * P * 512];
+  const int lane = threadIdx.x & 63, lr = lane & 15, lk = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t mat = blockIdx.x / p.count;
+  const int t = blockIdx.x % p.count;
+  const OrthoOperands o = ortho_operands<Product::kUpdate>(p, mat);
+  f16x8 a[P], a_lo[kSplit ? P : 1];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (gm >= p.m_true || gn + r >= p.n_true) continue;
-      const int64_t at = mat * (int64_t)p.m_true * p.n_true +
-                         (p.tall ? (int64_t)(gn + r) * p.m_true + gm : (int64_t)gm * p.n_true + gn + r);
-      if constexpr (kOut == Result::kBf16) ((__bf16*)p.out)[at] = (__bf16)(val[r] * scale);
-      else ((float*)p.out)[at] = val[r] * scale;
+  for (int g = 0; g < P; ++g) {
+    const int64_t at = o.mm + (int64_t)wave * 16 * p.m + g * 512 + lane * 8;
+    a[g] = *(const f16x8*)(p.am + at);
+    if constexpr (kSplit) a_lo[g] = *(const f16x8*)(p.am_lo + at);
+  }
+  for (int g = wave; g < kParts * P; g += kWaves) {
+    const _Float16* const from = (g < P ? o.b_hi : o.b_lo) + (int64_t)t * 16 * p.m + g % P * 512 + lane * 8;
+    *(f16x8*)(columns[0] + g * 512 + lane * 8) = *(const f16x8*)from;
+  }
+  const int gm = wave * 16 + lr, gn = t * 16 + 4 * lk;
+  const int64_t at = o.mn + plane_at(gm, gn, p.n);
+  const f16x4 hi = *(const f16x4*)(p.x + at), lo = kSplit || p.low_in ? *(const f16x4*)(p.x_lo + at) : f16x4{0, 0, 0, 0};
+  const float cut = kSplit ? 0.0f : p.da[mat * p.m + gm] * (1.0f / kScaleA);
+  const float alpha = p.pivot ? p.alpha[mat] : 0.0f;
+  __syncthreads();
+  auto multiply = [&](const _Float16* v, auto low) {
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int g = 0; g < P; ++g) {
+      const f16x8 b = *(const f16x8*)(v + g * 512 + lane * 8);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a[g], acc, 0, 0, 0);
+      if constexpr (decltype(low)::value)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(*(const f16x8*)(v + (P + g) * 512 + lane * 8), a[g], acc, 0, 0, 0);
+      if constexpr (kSplit) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a_lo[g], acc, 0, 0, 0);
     }
+    return acc;
+  };
+  v4f acc = multiply(columns[0], std::bool_constant<kSplit>{});
+  float w[4];  // as stored
+  f16x4 h, l;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float x = (float)hi[r] + (float)lo[r];
+    const float y = __builtin_fmaf(cut, x, acc[r] * (1.0f / kScaleA));
+    w[r] = __builtin_fmaf(p.c, y, (p.b + 2.0f * p.c * alpha) * x) * (kScaleW / kScaleX);
+    h[r] = (_Float16)w[r];
+    l[r] = (_Float16)(w[r] - (float)h[r]);
+  }
+  auto put = [&](_Float16* to, uint2 v) {
+    const bool odd = lr & 1;
+    const Turned u = turn_pairs(odd, v.x, v.y);
+    _Float16* const at = to + plane_at(4 * lk + (odd ? 2 : 0), gm & ~1, 32 * P);
+    *(uint32_t*)at = u.first;
+    *(uint32_t*)(at + 8) = u.second;
+  };
+  put(columns[1], __builtin_bit_cast(uint2, h));
+  put(columns[1] + P * 512, __builtin_bit_cast(uint2, l));
+  __syncthreads();
+  acc = multiply(columns[1], std::true_type{});
+  const float q = p.a + alpha * (p.b + alpha * p.c);
+  float val[4], square = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float z = __builtin_fmaf(cut, w[r], acc[r] * (1.0f / kScaleA)) * (kScaleX / kScaleW);
+    val[r] = __builtin_fmaf(q, (float)hi[r] + (float)lo[r], z);
+    square = __builtin_fmaf(val[r], val[r], square);
+  }
+  ortho_put<Product::kUpdate, kOut, kSplit>(p, o, mat, false, gm, gn, val);
+  if constexpr (kOut == Result::kPlanes && !kSplit) {
+    square = wave_sum_f32(square) * (1.0f / (kScaleX * kScaleX));
+    if (lane == 0) p.squares[mat * p.parts + t * kWaves + wave] = square;
   }
 }
 
@@ -696,10 +800,9 @@ __global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__
   sum = wave_sum_f64(sum);
   const double f = sum > 0.0 ? (double)kScaleX / __dsqrt_rn(sum) : sum;  // (a NaN goes on)
   const T* const from = g + (int64_t)mat * M * N;
-  const int ch = threadIdx.x % 8;
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
-    const int r = pass * 32 + threadIdx.x / 8, have = r0 + r < M ? N - c0 - ch * 8 : 0;
+    const int ch = threadIdx.x % 8, r = pass * 32 + threadIdx.x / 8, have = r0 + r < M ? N - c0 - ch * 8 : 0;
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (have > 0) values(load_chunk(from + (int64_t)(r0 + r) * N + c0 + ch * 8, have), v);
 #pragma unroll
@@ -708,8 +811,7 @@ __global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__
   __syncthreads();
   const int64_t base = (int64_t)mat * p.m * p.n;
   // rows of G as they lie: M by N padded; columns: N by M padded
-  const int64_t ld_s = p.tall ? p.m : p.n, ld_t = p.tall ? p.n : p.m;
-  const int64_t straight = base + r0 * ld_s + c0, turned = base + c0 * ld_t + r0;
+  const int ld_s = p.tall ? p.m : p.n, ld_t = p.tall ? p.n : p.m;
   auto put = [&](_Float16* hi, _Float16* lo, bool low, int64_t at, const float (&v)[8]) {
     f16x8 h, l;
 #pragma unroll
@@ -719,12 +821,13 @@ __global__ __launch_bounds__(256) void ortho_spread_kernel(const T* __restrict__
   };
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
-    const int r = pass * 32 + threadIdx.x / 8;
+    // a wavefront writes 16 rows x 32 values, one piece of a plane
+    const int r = pass * 32 + threadIdx.x / 128 * 16 + threadIdx.x % 16, ch = threadIdx.x / 16 % 8;
     float v[8], w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = block[r][ch * 8 + e], w[e] = block[ch * 8 + e][r];
-    put(p.tall ? p.xt_new : p.x, p.tall ? p.xt_lo_new : p.x_lo, kSplit || !p.tall, straight + r * ld_s + ch * 8, v);
-    put(p.tall ? p.x : p.xt_new, p.tall ? p.x_lo : p.xt_lo_new, kSplit || p.tall, turned + r * ld_t + ch * 8, w);
+    put(p.tall ? p.xt_new : p.x, p.tall ? p.xt_lo_new : p.x_lo, kSplit || !p.tall, base + plane_at(r0 + r, c0 + ch * 8, ld_s), v);
+    put(p.tall ? p.x : p.xt_new, p.tall ? p.x_lo : p.xt_lo_new, kSplit || p.tall, base + plane_at(c0 + r, r0 + ch * 8, ld_t), w);
   }
 }
 
@@ -937,7 +1040,7 @@ __global__ __launch_bounds__(64 * kWholeWaves) void ortho_whole_kernel(const T* 
 // ---------------------------------------------------------------------------
 struct OrthoPlan {
   int64_t m, n;  // padded
-  bool split, in_lds;  // in_lds: one workgroup a matrix
+  bool split, in_lds, columns;  // in_lds: one workgroup a matrix; columns: square and update in one
   int tile_sym, tile;  // of the gram and the square, and of the update
   int64_t symmetric, whole;
   int64_t bytes;
@@ -947,12 +1050,13 @@ struct OrthoPlan {
 // its tiles (two at a time on a CU for 64 x 64 and 128 x 128, else one) an epilogue
 // and, per 64 values of K, what the chip needs to feed the round: the same for few
 // workgroups, then growing with the share p of the round that is filled. Fitted to
-// kernels of 1024 to 4096 rows; the estimates are within a tenth of these. us on MI355X
+// kernels of 1024 to 4096 rows; the tile it picks is the fastest of the four in 26 of 28 products of 1000 to
+// 4500 rows, and within 2% of it in the others. us on MI355X
 // for 64 / 128 / 192 / 256 tiles:
-//   gram    2048 x 2048 23.5 / 18.4 / 32.0 / 47.6    2048 x 7168 73.5 / 46.5 / 78.4 / 126
-//           2900 x 2900 62.3 / 39.0 / 41.0 / 61.6    4096 x 4096 155 / 89.4 / 66.0 / 83.3
-//   update  1400 x 1400 15.8 / 21.2 / 37.4 / 58.1    2048 x 2048 38.2 / 30.1 / 47.2 / 69.6
-//           2900 x 2900 94.3 / 78.5 / 62.9 / 83.9    4096 x 4096 216 / 136 / 148 / 128
+//   gram    2048 x 2048 23.0 / 19.4 / 32.3 / 50.2    2048 x 7168 75.6 / 55.9 / 84.0 / 141
+//           2900 x 2900 58.2 / 40.4 / 44.5 / 68.8    4096 x 4096 154 / 90.2 / 67.6 / 99.5
+//   update  1400 x 1400 15.0 / 19.2 / 34.0 / 52.3    2048 x 2048 34.6 / 26.5 / 42.2 / 62.9
+//           2900 x 2900 91.6 / 74.5 / 59.3 / 82.3    4096 x 4096 218 / 132 / 144 / 128
 template <typename Count>
 static int ortho_tile(int64_t L, Count count, int64_t K, bool symmetric, bool split) {
   struct Kind {
@@ -999,21 +1103,28 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   auto all = [&](int64_t t) { return side(o.m, t) * side(o.n, t); };
   // Small products, for few blocks of 16 x 16 or 32 x 32; else tiles. us for five steps, MI355X, with
   // the symmetric products in 16 x 16 blocks / 32 x 32 blocks / 64 x 64 tiles:
-  //   256 x 1024 float32 92 / 116 / 147    256 x 4096 120 / 158 / 147    333 x 1000 99 / 102 / 108
-  //   400 x 400 85 / 85 / 94    512 x 512 97 / 90 / 95    700 x 2000 float32 - / 283 / 336    1024 x 1024 - / 204 / 144
+  //   256 x 1024 float32 68 / 78 / 133    333 x 1000 70 / 72 / 90    512 x 512 68 / 69 / 84    600 x 600 92 / 89 / 104
+  //   800 x 800 118 / 109 / 122    1000 x 1000 135 / 120 / 132    1400 x 1400 242 / 186 / 170    1024 x 4096 - / 253 / 225
+  //   8 x 256 x 256 88 / 85 / 79
   // and the update:
-  //   100 x 200 63 / 68 / 79    256 x 1024 81 / 76 / 85    333 x 1000 111 / 99 / 104    600 x 600 - / 117 / 113
-  if (L * all(16) <= kCus) o.tile = 16;
-  else if (L * all(32) <= kCus * 3 / 2) o.tile = 32;
+  //   256 x 1024 float32 71 / 68 / 87    400 x 400 67 / 66 / 75    333 x 1000 75 / 69 / 78    600 x 600 88 / 83 / 88
+  //   700 x 700 98 / 90 / 94    800 x 800 134 / 122 / 122    700 x 2000 148 / 124 / 115    1000 x 1000 float32 283 / 239 / 258
+  if (L * all(16) <= 2 * kCus) o.tile = 16;
+  else if (L * all(32) <= (o.split ? 4 : 2) * kCus) o.tile = 32;
   else o.tile = ortho_tile(L, all, o.m, false, o.split);
-  if (L * sym(16) <= kCus * 3 / 2) o.tile_sym = 16;
-  else if (L * sym(32) <= kCus) o.tile_sym = 32;
+  if (L * sym(16) <= 2 * kCus) o.tile_sym = 16;
+  else if (L * sym(32) <= kCus || (L * sym(32) <= 9 * kCus / 4 && o.m >= 512 && o.n <= 2 * o.m)) o.tile_sym = 32;
   else o.tile_sym = ortho_tile(L, sym, o.n, true, o.split);
+  // Square and update in one where A's rows fit registers, and up to four rounds of columns. us for five steps,
+  // in one / apart: 26 x 1645 46 / 60    128 x 700 float32 48 / 59    128 x 16000 184 / 192    200 x 333 51 / 59
+  //   256 x 256 float32 61 / 61    256 x 1024 56 / 62    256 x 1024 float32 68 / 66    256 x 4096 float32 104 / 114
+  //   16 x 256 x 1024 136 / 140    333 x 1000 (with two row blocks to a wavefront) 71 / 68
+  o.columns = L * o.n <= 16 * 4 * kCus && (o.m <= 192 || (o.m == 256 && (!o.split || o.n >= 2048)));
   o.symmetric = sym(o.tile_sym);
-  o.whole = all(o.tile);
+  o.whole = o.columns ? o.n / 16 : all(o.tile);
   const int64_t mn = L * o.m * o.n * 2, mm = L * o.m * o.m * 2;
-  o.bytes = mn * (o.split ? 6 : 4) + mm * (o.split ? 4 : 2);
-  o.bytes += L * (kNormParts * 8 + 2 * o.m * 4 + o.whole * 16 + 16);
+  o.bytes = mn * (o.split ? 6 : 4) + mm * (o.split ? 2 : 1) * (o.columns ? 1 : 2);
+  o.bytes += L * (kNormParts * 8 + 2 * o.m * 4 + o.whole * (o.columns ? 64 : 16) + 16);
   return o;
 }
 
@@ -1034,6 +1145,21 @@ static void launch_product(const OrthoArgs& a, int64_t L, int tile, hipStream_t 
     if (tile == 192) return go(ortho_product_kernel<kWhat, kOut, kSplit, 192, 192, 2>);
     go(ortho_product_kernel<kWhat, kOut, kSplit, 256, 256, 2>);
   }
+}
+
+template <Result kOut, bool kSplit>
+static void launch_columns(const OrthoArgs& a, int64_t L, hipStream_t stream) {
+  auto go = [&](auto pieces) {
+    constexpr int P = decltype(pieces)::value;
+    hipLaunchKernelGGL((ortho_columns_kernel<kOut, kSplit, P>), dim3((unsigned)(L * a.count)), dim3(128 * P), 0, stream, a);
+  };
+  using std::integral_constant;
+  if constexpr (kSplit) {  // (for a bfloat16 result, m is more than 128)
+    if (a.m == 64) return go(integral_constant<int, 2>{});
+    if (a.m == 128) return go(integral_constant<int, 4>{});
+  }
+  if (a.m == 192) go(integral_constant<int, 6>{});
+  else go(integral_constant<int, 8>{});
 }
 
 template <bool kSplit>
@@ -1057,11 +1183,16 @@ static hipError_t run_ortho(const void* g, bool g_bf16, int64_t L, int64_t M, in
     p.xt_new = xt[1 - k % 2], p.xt_lo_new = xt_lo[1 - k % 2];
     p.count = (int)o.symmetric;
     launch_product<Product::kGram, Result::kPlanes, kSplit>(p, L, o.tile_sym, stream);
-    launch_product<Product::kSquare, Result::kPlanes, kSplit>(p, L, o.tile_sym, stream);
+    if (!o.columns) launch_product<Product::kSquare, Result::kPlanes, kSplit>(p, L, o.tile_sym, stream);
     p.count = (int)o.whole;
-    if (k < steps - 1) launch_product<Product::kUpdate, Result::kPlanes, kSplit>(p, L, o.tile, stream);
-    else if (bf16) launch_product<Product::kUpdate, Result::kBf16, kSplit>(p, L, o.tile, stream);
-    else if constexpr (kSplit) launch_product<Product::kUpdate, Result::kF32, kSplit>(p, L, o.tile, stream);
+    auto update = [&](auto out) {
+      constexpr Result kOut = decltype(out)::value;
+      if (o.columns) launch_columns<kOut, kSplit>(p, L, stream);
+      else launch_product<Product::kUpdate, kOut, kSplit>(p, L, o.tile, stream);
+    };
+    if (k < steps - 1) update(std::integral_constant<Result, Result::kPlanes>{});
+    else if (bf16) update(std::integral_constant<Result, Result::kBf16>{});
+    else if constexpr (kSplit) update(std::integral_constant<Result, Result::kF32>{});
   }
   return hipGetLastError();
 }
@@ -1090,7 +1221,7 @@ hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M
     else sized((const float*)g);
     return hipGetLastError();
   }
-  p.parts = (int)o.whole * (o.tile == 16 ? 1 : 4);
+  p.parts = (int)o.whole * (o.columns ? (int)o.m / 16 : o.tile == 16 ? 1 : 4);
   uint8_t* at = (uint8_t*)ws;
   auto take = [&](int64_t bytes) {
     void* r = at;
@@ -1101,14 +1232,16 @@ hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M
   _Float16 *xt[2], *xt_lo[2] = {nullptr, nullptr};
   p.x = (_Float16*)take(mn), p.x_lo = (_Float16*)take(mn);
   for (auto& v : xt) v = (_Float16*)take(mn);
-  p.am = (_Float16*)take(mm), p.bm = (_Float16*)take(mm);
+  p.am = (_Float16*)take(mm);
+  if (!o.columns) p.bm = (_Float16*)take(mm);
   if (o.split) {
     for (auto& v : xt_lo) v = (_Float16*)take(mn);
-    p.am_lo = (_Float16*)take(mm), p.bm_lo = (_Float16*)take(mm);
+    p.am_lo = (_Float16*)take(mm);
+    if (!o.columns) p.bm_lo = (_Float16*)take(mm);
   }
   double* const parts = (double*)take(L * kNormParts * 8);
   p.da = (float*)take(L * o.m * 4), p.db = (float*)take(L * o.m * 4);
-  p.squares = (float*)take(L * o.whole * 16);
+  p.squares = (float*)take(L * o.whole * (o.columns ? 64 : 16));
   p.alpha = (float*)take(L * 16);
   return o.split ? run_ortho<true>(g, g_bf16, L, M, N, steps, out_bf16, o, p, parts, xt, xt_lo, stream)
                  : run_ortho<false>(g, g_bf16, L, M, N, steps, out_bf16, o, p, parts, xt, xt_lo, stream);

@@ -175,6 +175,22 @@ def test_matrices_about_what_a_workgroup_holds(L, M, N, dtype, out):
         check(host(g[i]), host(o[:L * M * N].view(L, M, N)[i]), out)
 
 
+@pytest.mark.parametrize("L,M,N", [(1, 10, 700), (2, 64, 300), (1, 700, 128), (1, 150, 500), (3, 250, 140), (1, 256, 300), (1, 240, 2100),
+                                   (1, 2048, 256), (4, 20, 4100), (1, 257, 260), (1, 500, 350)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "bf16")])
+def test_few_rows(L, M, N, dtype, out):
+    """About where the products of a step go together, and one or several matrices."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    kinds = ("few", "decay", "gauss")
+    g = dev(np.stack([matrix(M, N, kinds[i % 3], 3380 + i) for i in range(L)]), dtype)
+    o = torch.full((L * M * N + 5,), 7.0, dtype=torch.bfloat16 if out == "bf16" else torch.float32, device="cuda")
+    F.fp8q_orthogonalize(g, out_dtype=out, out=o[:L * M * N].view(L, M, N))
+    assert torch.all(o[L * M * N:] == 7.0)
+    for i in range(L):
+        check(host(g[i]), host(o[:L * M * N].view(L, M, N)[i]), out)
+
+
 @pytest.mark.parametrize("M,N,dtype", [(1024, 4096, "bf16"), (2100, 1900, "f32"), (4096, 700, "bf16")])
 @pytest.mark.parametrize("kind", ["gauss", "few"])
 def test_large(M, N, dtype, kind):
