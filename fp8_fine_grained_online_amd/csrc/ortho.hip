@@ -1050,8 +1050,8 @@ struct OrthoPlan {
 // its tiles (two at a time on a CU for 64 x 64 and 128 x 128, else one) an epilogue
 // and, per 64 values of K, what the chip needs to feed the round: the same for few
 // workgroups, then growing with the share p of the round that is filled. Fitted to
-// kernels of 1024 to 4096 rows; the tile it picks is the fastest of the four in 26 of 28 products of 1000 to
-// 4500 rows, and within 2% of it in the others. us on MI355X
+// kernels of 1024 to 4096 rows; the tile it picks is the fastest of the four, or within 3% of it, in 28 products of 1000 to
+// 4500 rows. us on MI355X
 // for 64 / 128 / 192 / 256 tiles:
 //   gram    2048 x 2048 23.0 / 19.4 / 32.3 / 50.2    2048 x 7168 75.6 / 55.9 / 84.0 / 141
 //           2900 x 2900 58.2 / 40.4 / 44.5 / 68.8    4096 x 4096 154 / 90.2 / 67.6 / 99.5
@@ -1064,7 +1064,7 @@ static int ortho_tile(int64_t L, Count count, int64_t K, bool symmetric, bool sp
     double epilogue, least, base, slope;  // us; per 64 of K: max(least, base + slope p)
   };
   static constexpr Kind kinds[] = {{64, 2 * kCus, 3, 0.21, 0.10, 0.32},
-                                   {128, 2 * kCus, 7, 0.35, 0.17, 0.75},
+                                   {128, 2 * kCus, 7, 0.35, 0.17, 0.83},
                                    {192, kCus, 12, 0.70, 0.45, 0.50},
                                    {256, kCus, 20, 1.10, 0.60, 1.00}};
   const double steps = (double)(split ? 3 * K : K) / 64;
@@ -1090,10 +1090,10 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   o.n = (hi + 31) / 32 * 32;
   // A matrix to a workgroup, where it fits (then X has at most 68 16 x 16 or 18 32 x 32 units) and unless few
   // matrices are the larger ones. us for five steps against the products' launches, MI355X, L x m x n:
-  //   16 x 26 11 / 52    32 x 540 33 / 60    64 x 64 22 / 54    64 x 288 48 / 55    96 x 96 41 / 56    96 x 160 53 / 57
-  //   96 x 192 59 / 57    128 x 128 64 / 55    4 x 128 x 128 64 / 58    8 x 128 x 128 64 / 70    256 x 128 x 128 74 / 267
-  //   256 x 64 x 64 23 / 123
-  o.in_lds = whole_lds(o.m, o.n) <= kWholeLds && (o.m <= 64 || o.m * o.n <= 96 * 160 || L >= 8);
+  //   16 x 26 11 / 36    32 x 540 33 / 39    64 x 64 22 / 40    64 x 200 36 / 40    64 x 256 43 / 39    96 x 96 41 / 40
+  //   128 x 128 64 / 40    8 x 96 x 96 42 / 46    8 x 128 x 128 64 / 46    16 x 96 x 192 59 / 59    32 x 96 x 192 59 / 86
+  //   32 x 128 x 128 64 / 76    256 x 64 x 64 23 / 111    256 x 128 x 128 68 / 240
+  o.in_lds = whole_lds(o.m, o.n) <= kWholeLds && (o.m <= 32 || (o.m <= 64 && o.n <= 224) || L >= 24);
   if (o.in_lds) return o;
   o.m = (lo + kPad - 1) / kPad * kPad;
   o.n = (hi + kPad - 1) / kPad * kPad;

@@ -161,7 +161,8 @@ def test_several_matrices(L, M, N, out):
 
 
 @pytest.mark.parametrize("L,M,N", [(1, 2, 545), (2, 32, 544), (1, 30, 512), (1, 64, 288), (1, 290, 64), (1, 161, 96), (1, 96, 160),
-                                   (8, 96, 192), (8, 190, 90), (9, 128, 128), (7, 128, 128), (8, 128, 129), (300, 33, 17)])
+                                   (8, 96, 192), (8, 190, 90), (9, 128, 128), (7, 128, 128), (8, 128, 129), (300, 33, 17),
+                                   (1, 64, 224), (1, 225, 64), (23, 128, 128), (24, 128, 128), (25, 90, 190), (24, 129, 128)])
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32")])
 def test_matrices_about_what_a_workgroup_holds(L, M, N, dtype, out):
     import torch
