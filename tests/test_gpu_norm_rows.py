@@ -126,6 +126,24 @@ def test_rows_outside_the_ordinary_range(dtype, K, centred):
         check_norm(x[first:], g, eps, None, centred, y, "f32")
 
 
+@pytest.mark.parametrize("K", [300, 700, 1100, 2047, 3000, 4000, 10000, 16000])
+@pytest.mark.parametrize("centred", [False, True])
+def test_a_row_outside_the_range_leaves_its_neighbours_alone(K, centred):
+    """Also as the last row of an odd number."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = rows(5, K, 5160, "f32")
+    g, _ = weights(K, 5161, "f32")
+    want = F.fp8q_norm(x, g, 1e-6, centred=centred, out_dtype="f32")
+    for far in (1, 4):
+        z = x.clone()
+        z[far] *= 1e25
+        got = F.fp8q_norm(z, g, 1e-6, centred=centred, out_dtype="f32")
+        check_norm(z, g, 1e-6, None, centred, got, "f32")
+        keep = [i for i in range(5) if i != far]
+        assert torch.equal(got[keep], want[keep])
+
+
 def test_rows_that_are_not_finite():
     import torch
     import fp8_fine_grained_online_amd as F
