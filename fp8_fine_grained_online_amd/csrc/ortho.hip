@@ -213,6 +213,9 @@ __device__ __forceinline__ Turned turn_pairs(bool odd, uint32_t p0, uint32_t p1)
 // multiplies; A's slabs rotate through D + 1 buffers, B's through D. Lane l
 // supplies row l % 16 of a 16-row block and 8 values of K at 8 (l / 16); B is the
 // first operand, so a lane holds C[l % 16][4 (l / 16) + r].
+// The MFMAs bound it, at the clock that their power leaves: of 4096 x 4096 they are busy 64% of the
+// gram's time (72 us), 60% of the square's (75) and 56% of the update's (128), the rest being its
+// first copies and the epilogue's bursts (X, its low part and X^T, 101 MB).
 // ---------------------------------------------------------------------------
 template <Product kWhat, Result kOut, bool kSplit, int BM, int BN, int D>
 __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
@@ -550,7 +553,7 @@ __device__ __forceinline__ void ortho_put(const OrthoArgs& p, const OrthoOperand
 // blocks are added through LDS, in the wavefronts' order. What the epilogue reads is
 // loaded before the loop. For products whose tiles would leave most CUs without
 // work, where a tile's own chain of copies, barriers and short runs of MFMAs is what is
-// waited for.
+// waited for. A product of 256 x 1024 takes 3.5 to 4.8 us, an empty kernel 2 to 3.
 // ---------------------------------------------------------------------------
 template <Product kWhat, Result kOut, bool kSplit, int S, int W>
 __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
@@ -766,7 +769,8 @@ __global__ __launch_bounds__(128 * P) void ortho_columns_kernel(OrthoArgs p) {
 
 // ---------------------------------------------------------------------------
 // The way in. Sums of G's squares, kNormParts per matrix, in float64 (no input's
-// squares leave its range), then G / |G| to the planes of X and X^T.
+// squares leave its range), then G / |G| to the planes of X and X^T. Bound by memory: 4 x 4096
+// x 7168 (float32) 90 us, 5.2 TB/s, and 206 us, 5.7 TB/s.
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ __launch_bounds__(256) void ortho_squares_kernel(const T* __restrict__ g, int64_t size, double* __restrict__ parts) {
