@@ -72,6 +72,8 @@ struct OrthoArgs {
   int m, n, m_true, n_true;           // padded and true sizes
   int parts;
   int count;    // tiles per matrix
+  int splits;   // runs of K that a gram's blocks are formed in
+  v4f* partial;  // their sums, of a block one after the other
   float a, b, c, scale;
   int pivot;    // this step takes A about its mean eigenvalue
   int low_in, low_out;  // X's low part is there, and is kept
@@ -555,16 +557,19 @@ __device__ __forceinline__ void ortho_put(const OrthoArgs& p, const OrthoOperand
 // work, where a tile's own chain of copies, barriers and short runs of MFMAs is what is
 // waited for. A product of 256 x 1024 takes 3.5 to 4.8 us, an empty kernel 2 to 3.
 // ---------------------------------------------------------------------------
-template <Product kWhat, Result kOut, bool kSplit, int S, int W>
+// kRuns: a block's K is shared out to p.splits workgroups too, whose sums go to p.partial.
+template <Product kWhat, Result kOut, bool kSplit, int S, int W, bool kRuns = false>
 __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
   constexpr bool kSymmetric = kWhat != Product::kUpdate;
+  static_assert(!kRuns || (kWhat == Product::kGram && kSplit && S == 1), "as they are joined");
   constexpr int kAhead = 2;
   static_assert(S * S <= W, "a wave per block");
   __shared__ __attribute__((aligned(16))) v4f part[W][S * S][64];
   const int lane = threadIdx.x & 63, lr = lane & 15, lk = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t mat = blockIdx.x / p.count;
-  const int t = blockIdx.x % p.count;
+  const int runs = kRuns ? p.splits : 1;
+  const int64_t mat = blockIdx.x / runs / p.count;
+  const int t = blockIdx.x / runs % p.count;
   int tm, tn;
   if constexpr (kSymmetric) {
     triangle_tile(t, tm, tn);
@@ -576,7 +581,8 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
   const bool on_diagonal = kSymmetric && tm == tn;
   const OrthoOperands o = ortho_operands<kWhat>(p, mat);
   const int pieces = o.K / 32;
-  const int g_begin = pieces * wave / W, g_end = pieces * (wave + 1) / W;
+  const int share = blockIdx.x % runs * W + wave, shares = runs * W;
+  const int g_begin = pieces * share / shares, g_end = pieces * (share + 1) / shares;
   struct Frags {
     f16x8 a[S], b[S], a_lo[kSplit ? S : 1], b_lo[kSplit ? S : 1];
   };
@@ -658,6 +664,10 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
   v4f sum = part[0][wave][lane];
 #pragma unroll
   for (int w = 1; w < W; ++w) sum += part[w][wave][lane];
+  if constexpr (kRuns) {
+    p.partial[(int64_t)blockIdx.x * 64 + lane] = sum;
+    return;
+  }
 
   float val[4], square = 0.0f;
 #pragma unroll
@@ -678,6 +688,24 @@ __global__ __launch_bounds__(64 * W) void ortho_small_kernel(OrthoArgs p) {
     if (lane == 0) p.squares[mat * p.parts + t * (S * S) + wave] = square;
   }
   ortho_put<kWhat, kOut, kSplit>(p, o, mat, on_diagonal, gm, gn, val);
+}
+
+// The runs of K of a gram's 16 x 16 blocks, joined in their order; a wavefront per block. (Only kSplit's
+// matrices have so few rows.)
+__global__ __launch_bounds__(64) void ortho_join_kernel(OrthoArgs p) {
+  const int lane = threadIdx.x;
+  const int64_t mat = blockIdx.x / p.count;
+  int tm, tn;
+  triangle_tile(blockIdx.x % p.count, tm, tn);
+  const v4f* const from = p.partial + (int64_t)blockIdx.x * p.splits * 64 + lane;
+  v4f sum = from[0];
+#pragma unroll 4
+  for (int z = 1; z < p.splits; ++z) sum += from[z * 64];
+  float val[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) val[r] = ortho_value<Product::kGram, true>(p, sum[r], 0.0f, 0.0f, 0.0f, 0.0f, false, 0.0f);
+  ortho_put<Product::kGram, Result::kPlanes, true>(p, ortho_operands<Product::kGram>(p, mat), mat, tm == tn, tm * 16 + (lane & 15),
+                                                   tn * 16 + 4 * (lane >> 4), val);
 }
 
 // ---------------------------------------------------------------------------
@@ -1046,7 +1074,7 @@ struct OrthoPlan {
   int64_t m, n;  // padded
   bool split, in_lds, columns;  // in_lds: one workgroup a matrix; columns: square and update in one
   int tile_sym, tile;  // of the gram and the square, and of the update
-  int64_t symmetric, whole;
+  int64_t symmetric, whole, splits;
   int64_t bytes;
 };
 
@@ -1125,10 +1153,21 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   //   16 x 256 x 1024 136 / 140    333 x 1000 (with two row blocks to a wavefront) 71 / 68
   o.columns = L * o.n <= 16 * 4 * kCus && (o.m <= 192 || (o.m == 256 && (!o.split || o.n >= 2048)));
   o.symmetric = sym(o.tile_sym);
+  // A workgroup reads the 32 rows of its block of the gram at about 90 GB/s: from 8192 values of K on (in both parts),
+  // where most CUs would have none, runs of K of 16 pieces at least and another launch. us for five steps, with /
+  // without: 16 x 8192 60 / 87    100 x 4096 float32 66 / 77    128 x 16000 132 / 186    128 x 2000 (4096) 61 / 58
+  //   4 x 128 x 16000 (144 blocks) 330 / 321    256 x 4096 float32 (136) 115 / 104
+  o.splits = 1;
+  if (o.split && o.tile_sym == 16 && L * o.symmetric <= kCus / 4 && 2 * o.n >= 8192) {
+    o.splits = 2 * kCus / (L * o.symmetric);
+    if (o.splits > o.n / 512) o.splits = o.n / 512;
+    if (o.splits > 16) o.splits = 16;
+  }
   o.whole = o.columns ? o.n / 16 : all(o.tile);
   const int64_t mn = L * o.m * o.n * 2, mm = L * o.m * o.m * 2;
   o.bytes = mn * (o.split ? 6 : 4) + mm * (o.split ? 2 : 1) * (o.columns ? 1 : 2);
   o.bytes += L * (kNormParts * 8 + 2 * o.m * 4 + o.whole * (o.columns ? 64 : 16) + 16);
+  if (o.splits > 1) o.bytes += L * o.symmetric * o.splits * 1024;
   return o;
 }
 
@@ -1137,9 +1176,13 @@ int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool bf16) { retu
 template <Product kWhat, Result kOut, bool kSplit>
 static void launch_product(const OrthoArgs& a, int64_t L, int tile, hipStream_t stream) {
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)(L * a.count)), dim3(256), 0, stream, a); };
-  auto small = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)(L * a.count)), dim3(512), 0, stream, a); };
-  if (tile == 16) return small(ortho_small_kernel<kWhat, kOut, kSplit, 1, 8>);
-  if (tile == 32) return small(ortho_small_kernel<kWhat, kOut, kSplit, 2, 8>);
+  auto small = [&](auto kernel, int runs) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(L * a.count * runs)), dim3(512), 0, stream, a);
+  };
+  if constexpr (kWhat == Product::kGram && kSplit)
+    if (a.splits > 1) return small(ortho_small_kernel<kWhat, kOut, kSplit, 1, 8, true>, a.splits);
+  if (tile == 16) return small(ortho_small_kernel<kWhat, kOut, kSplit, 1, 8>, 1);
+  if (tile == 32) return small(ortho_small_kernel<kWhat, kOut, kSplit, 2, 8>, 1);
   // Slabs ahead: 64 x 64 tiles two to a CU beat one with a deeper ring (2048 x 2048 gram 23.5 / 29.8 us), a
   // 128 x 128 one alone on its CU wants the ring (18.4 / 21.3)
   if (tile == 64) return go(ortho_product_kernel<kWhat, kOut, kSplit, 64, 64, 3>);
@@ -1187,6 +1230,8 @@ static hipError_t run_ortho(const void* g, bool g_bf16, int64_t L, int64_t M, in
     p.xt_new = xt[1 - k % 2], p.xt_lo_new = xt_lo[1 - k % 2];
     p.count = (int)o.symmetric;
     launch_product<Product::kGram, Result::kPlanes, kSplit>(p, L, o.tile_sym, stream);
+    if constexpr (kSplit)
+      if (p.splits > 1) hipLaunchKernelGGL(ortho_join_kernel, dim3((unsigned)(L * p.count)), dim3(64), 0, stream, p);
     if (!o.columns) launch_product<Product::kSquare, Result::kPlanes, kSplit>(p, L, o.tile_sym, stream);
     p.count = (int)o.whole;
     auto update = [&](auto out) {
@@ -1247,6 +1292,8 @@ hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M
   p.da = (float*)take(L * o.m * 4), p.db = (float*)take(L * o.m * 4);
   p.squares = (float*)take(L * o.whole * (o.columns ? 64 : 16));
   p.alpha = (float*)take(L * 16);
+  p.splits = (int)o.splits;
+  if (o.splits > 1) p.partial = (v4f*)take(L * o.symmetric * o.splits * 1024);
   return o.split ? run_ortho<true>(g, g_bf16, L, M, N, steps, out_bf16, o, p, parts, xt, xt_lo, stream)
                  : run_ortho<false>(g, g_bf16, L, M, N, steps, out_bf16, o, p, parts, xt, xt_lo, stream);
 }

@@ -754,7 +754,7 @@ FP8Q_API int fp8q_swiglu_bwd(const void* dy, int dy_dtype, int64_t ldy, const vo
  * g and out need their element's alignment only. 1 <= steps <= 100, scale finite,
  * L <= 65535, M, N <= 65536, and L M N below about 2^36 (FP8Q_ERR_TOO_LARGE).
  * L, M or N == 0 is a no-op. Deterministic; allocates nothing. One kernel where no workspace is
- * needed, else two and two or three a step.
+ * needed, else two, and two or three a step.
  */
 FP8Q_API int64_t fp8q_orthogonalize_workspace_bytes(int64_t L, int64_t M, int64_t N, int out_dtype);
 FP8Q_API int fp8q_orthogonalize(const void* g, int g_dtype, int64_t L, int64_t M, int64_t N,

@@ -177,7 +177,8 @@ def test_matrices_about_what_a_workgroup_holds(L, M, N, dtype, out):
 
 
 @pytest.mark.parametrize("L,M,N", [(1, 10, 700), (2, 64, 300), (1, 700, 128), (1, 150, 500), (3, 250, 140), (1, 256, 300), (1, 240, 2100),
-                                   (1, 2048, 256), (4, 20, 4100), (1, 257, 260), (1, 500, 350)])
+                                   (1, 2048, 256), (4, 20, 4100), (1, 257, 260), (1, 500, 350), (1, 120, 4100),
+                                   (1, 9000, 30), (1, 130, 4200), (1, 600, 4200)])
 @pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "bf16")])
 def test_few_rows(L, M, N, dtype, out):
     """About where the products of a step go together, and one or several matrices."""
