@@ -115,6 +115,8 @@ def lib() -> ctypes.CDLL:
         L.fp8q_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64, i32]
         L.fp8q_orthogonalize.restype = i32
         L.fp8q_orthogonalize.argtypes = [vp, i32, i64, i64, i64, i32, f32, f32, f32, f32, vp, i32, vp, i64, vp]
+        L.fp8q_orthogonalize_f16.restype = i32
+        L.fp8q_orthogonalize_f16.argtypes = [vp, i32, i64, i64, i64, i32, f32, f32, f32, f32, vp, vp, i64, vp]
         _lib = L
     return _lib
 
@@ -669,11 +671,14 @@ def fp8q_swiglu_bwd(dy, gu, m_offsets=None, dgu=None, stream=None):
 
 
 def fp8q_orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), scale=1.0, out_dtype="bf16", out=None,
-                       workspace=None, stream=None):
+                       workspace=None, stream=None, single=False):
     """scale times the matrix that `steps` Newton-Schulz steps with p(s) = a s + b s^3 + c s^5, coeffs =
     (a, b, c), make of g / |g| (Frobenius): g M x N, or L x M x N for a matrix each (bfloat16 or float32)
-    -> out like g, of out_dtype. A zero matrix gives zeros."""
+    -> out like g, of out_dtype. A zero matrix gives zeros. As exact as in float32; `single`, for a bfloat16
+    out, multiplies FP16 numbers instead of pairs of them: up to 3.5 times as fast for large matrices, and
+    off by about 1e-3 before the rounding, by up to 1e-2 for matrices of few magnitudes."""
     if stream is not None:
-        return _on_stream(stream, fp8q_orthogonalize, g, steps, coeffs, scale, out_dtype, out, workspace)
+        return _on_stream(stream, fp8q_orthogonalize, g, steps, coeffs, scale, out_dtype, out, workspace, None, single)
     a, b, c = coeffs
-    return (_native or _binding()).fp8q_orthogonalize(g, steps, a, b, c, scale, _out_code(out_dtype), out, workspace)
+    return (_native or _binding()).fp8q_orthogonalize(g, steps, a, b, c, scale, _out_code(out_dtype), out, workspace,
+                                                      single)

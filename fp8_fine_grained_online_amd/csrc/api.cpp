@@ -91,10 +91,10 @@ hipError_t launch_swiglu_quant(const void* gu, bool gu_bf16, int64_t ld, const i
 hipError_t launch_swiglu_bwd(const void* dy, bool dy_bf16, int64_t ldy, const void* gu, bool gu_bf16,
                              int64_t ld, const int32_t* last, int64_t M, int64_t I, void* dgu,
                              hipStream_t stream);
-int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool bf16);
+int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool single);
 hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M, int64_t N, int steps,
                                 float a, float b, float c, float scale, void* out, bool out_bf16,
-                                void* ws, hipStream_t stream);
+                                bool single, void* ws, hipStream_t stream);
 }  // namespace fp8q
 
 namespace {
@@ -242,6 +242,24 @@ bool bounded(int steps, double a, double b, double c) {
     top = most;
   }
   return true;
+}
+
+// Both forms of the orthogonalization; `single`: of one FP16 number a value, for a bfloat16 out.
+int orthogonalize(const void* g, int g_dtype, int64_t L, int64_t M, int64_t N, int steps, float a, float b, float c,
+                  float scale, void* out, bool bf16, bool single, void* workspace, int64_t workspace_bytes,
+                  void* stream) {
+  if (!known_dtype(g_dtype)) return FP8Q_ERR_DTYPE;
+  if (steps < 1 || steps > 100 || !isfinite(scale) || !bounded(steps, a, b, c)) return FP8Q_ERR_SHAPE;
+  int s = check_ortho(L, M, N);
+  if (s == -1) return FP8Q_OK;
+  if (s) return s;
+  const int64_t need = fp8q::ortho_workspace_bytes(L, M, N, single);
+  if (!g || !out || (need && !workspace)) return FP8Q_ERR_NULL;
+  if (workspace_bytes < need) return FP8Q_ERR_SHAPE;
+  if (!aligned(g, element(g_dtype)) || !aligned(out, bf16 ? 2 : 4) || !aligned(workspace, 16)) return FP8Q_ERR_ALIGN;
+  if ((s = check_device())) return s;
+  return launched(fp8q::launch_orthogonalize(g, g_dtype == FP8Q_OUT_BF16, L, M, N, steps, a, b, c, scale, out, bf16,
+                                             single, workspace, (hipStream_t)stream));
 }
 
 // worst-case m_offsets[G] of the MoE dispatch (every expert padded by 127
@@ -737,26 +755,22 @@ int fp8q_swiglu_bwd(const void* dy, int dy_dtype, int64_t ldy, const void* gu, i
 int64_t fp8q_orthogonalize_workspace_bytes(int64_t L, int64_t M, int64_t N, int out_dtype) {
   const int s = check_ortho(L, M, N);
   if (!known_dtype(out_dtype) || s > 0) return -1;
-  return s ? 0 : fp8q::ortho_workspace_bytes(L, M, N, out_dtype == FP8Q_OUT_BF16);
+  return s ? 0 : fp8q::ortho_workspace_bytes(L, M, N, false);  // (one number a value takes less)
 }
 
 int fp8q_orthogonalize(const void* g, int g_dtype, int64_t L, int64_t M, int64_t N, int steps, float a,
                        float b, float c, float scale, void* out, int out_dtype, void* workspace,
                        int64_t workspace_bytes, void* stream) {
-  if (!known_dtype(g_dtype) || !known_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
-  if (steps < 1 || steps > 100 || !isfinite(scale) || !bounded(steps, a, b, c)) return FP8Q_ERR_SHAPE;
-  int s = check_ortho(L, M, N);
-  if (s == -1) return FP8Q_OK;
-  if (s) return s;
-  const bool bf16 = out_dtype == FP8Q_OUT_BF16;
-  const int64_t need = fp8q::ortho_workspace_bytes(L, M, N, bf16);
-  if (!g || !out || (need && !workspace)) return FP8Q_ERR_NULL;
-  if (workspace_bytes < need) return FP8Q_ERR_SHAPE;
-  if (!aligned(g, element(g_dtype)) || !aligned(out, element(out_dtype)) || !aligned(workspace, 16))
-    return FP8Q_ERR_ALIGN;
-  if ((s = check_device())) return s;
-  return launched(fp8q::launch_orthogonalize(g, g_dtype == FP8Q_OUT_BF16, L, M, N, steps, a, b, c, scale,
-                                             out, bf16, workspace, (hipStream_t)stream));
+  if (!known_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
+  return orthogonalize(g, g_dtype, L, M, N, steps, a, b, c, scale, out, out_dtype == FP8Q_OUT_BF16, false, workspace,
+                       workspace_bytes, stream);
+}
+
+int fp8q_orthogonalize_f16(const void* g, int g_dtype, int64_t L, int64_t M, int64_t N, int steps, float a,
+                           float b, float c, float scale, void* out, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  return orthogonalize(g, g_dtype, L, M, N, steps, a, b, c, scale, out, true, true, workspace, workspace_bytes,
+                       stream);
 }
 
 }  // extern "C"

@@ -487,15 +487,17 @@ PyObject* swiglu_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// g, steps, a, b, c, scale, out_dtype, out, workspace
+// g, steps, a, b, c, scale, out_dtype, out, workspace, single
 PyObject* orthogonalize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Call c("fp8q_orthogonalize", args, n, 9);
+  Call c("fp8q_orthogonalize", args, n, 10);
   const bool several = THPVariable_Check(args[0]) && THPVariable_Unpack(args[0]).dim() == 3;
   const at::Tensor& g = c.tensor(0, "g", kFloats, several ? 3 : 2);
   const int64_t L = several ? g.size(0) : 1, M = g.size(-2), N = g.size(-1), steps = c.integer(1), out = c.integer(6);
   if (steps < 1 || steps > 100) refuse(PyExc_ValueError, "steps must be 1 to 100");
   const float k[3] = {(float)c.number(2), (float)c.number(3), (float)c.number(4)}, scale = (float)c.number(5);
+  const bool single = c.truth(9);
+  if (single && out != FP8Q_OUT_BF16) refuse(PyExc_ValueError, "single goes with a bfloat16 out");
   const int64_t bytes = fp8q_orthogonalize_workspace_bytes(L, M, N, (int)out);
   if (bytes < 0) refuse(PyExc_ValueError, "invalid sizes to orthogonalize");
   const at::Tensor y = c.out(7, "out", g.sizes(), type_of(out));
@@ -503,6 +505,9 @@ PyObject* orthogonalize(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                   : c.tensor(8, "workspace", {ScalarType::Byte}, 1);
   void* s = c.stream();
   const int status = launch([&] {
+    if (single)
+      return fp8q_orthogonalize_f16(ptr(g), code(g), L, M, N, (int)steps, k[0], k[1], k[2], scale, ptr(y), ptr(ws),
+                                    ws.numel(), s);
     return fp8q_orthogonalize(ptr(g), code(g), L, M, N, (int)steps, k[0], k[1], k[2], scale, ptr(y), (int)out, ptr(ws),
                               ws.numel(), s);
   });

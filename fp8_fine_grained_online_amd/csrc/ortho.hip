@@ -14,13 +14,17 @@
 //
 // Numbers. X, A and B are kept as FP16 times a power of two that puts their
 // entries in FP16's normal range (the singular values of X stay below 3, checked
-// on the host). X is the sum of two such numbers, high and low: 22 bits, and the
-// term a X loses nothing that matters. For a float32 result (kSplit) so are A and
-// B, and a product is high high + high low + low high in one binary32 accumulator:
+// on the host). Each is the sum of two such numbers, high and low (kSplit): 22 bits,
+// and a product is high high + high low + low high in one binary32 accumulator:
 // the result is as near the definition as one formed in binary32 (2e-6 to 4e-5,
-// growing with the spread of the singular values). For a bfloat16 result, whose own rounding is 1.7e-3, one product of the
-// high parts is enough (1e-4 to 1e-3), with two precautions against errors that do
-// not average out over an inner product, those of the diagonal:
+// growing with the spread of the singular values), whatever its own type.
+//
+// Where the caller asks for it, a bfloat16 result comes from the high parts' product
+// alone (X keeps its low part, and the term a X loses nothing that matters): a third of
+// the MFMAs. It is off by 7e-4 to 2e-3, where values vary, and by up to 1e-2 where they
+// share a few magnitudes (a constant matrix, the identity, equal blocks), whose roundings
+// go the same way and add up; no form of one FP16 number a value is nearer there. Two
+// precautions against such errors of the diagonal:
 //
 //  * what FP16 cuts off the diagonals of A and B is kept in binary32 vectors and
 //    put back in the next epilogue (D A + A D in the square, D X in the update);
@@ -1115,7 +1119,7 @@ static int ortho_tile(int64_t L, Count count, int64_t K, bool symmetric, bool sp
   return best;
 }
 
-static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
+static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool single) {
   OrthoPlan o{};
   const int64_t lo = M < N ? M : N, hi = M < N ? N : M;
   o.m = (lo + 31) / 32 * 32;
@@ -1129,7 +1133,7 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   if (o.in_lds) return o;
   o.m = (lo + kPad - 1) / kPad * kPad;
   o.n = (hi + kPad - 1) / kPad * kPad;
-  o.split = !bf16 || lo <= 128;
+  o.split = !single || lo <= 128;  // (few rows: nothing to gain from one number)
   auto side = [&](int64_t v, int64_t t) { return (v + t - 1) / t; };
   auto sym = [&](int64_t t) { return side(o.m, t) * (side(o.m, t) + 1) / 2; };
   auto all = [&](int64_t t) { return side(o.m, t) * side(o.n, t); };
@@ -1171,7 +1175,7 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool bf16) {
   return o;
 }
 
-int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool bf16) { return ortho_plan(L, M, N, bf16).bytes; }
+int64_t ortho_workspace_bytes(int64_t L, int64_t M, int64_t N, bool single) { return ortho_plan(L, M, N, single).bytes; }
 
 template <Product kWhat, Result kOut, bool kSplit>
 static void launch_product(const OrthoArgs& a, int64_t L, int tile, hipStream_t stream) {
@@ -1247,8 +1251,8 @@ static hipError_t run_ortho(const void* g, bool g_bf16, int64_t L, int64_t M, in
 }
 
 hipError_t launch_orthogonalize(const void* g, bool g_bf16, int64_t L, int64_t M, int64_t N, int steps, float a, float b,
-                                float c, float scale, void* out, bool out_bf16, void* ws, hipStream_t stream) {
-  const OrthoPlan o = ortho_plan(L, M, N, out_bf16);
+                                float c, float scale, void* out, bool out_bf16, bool single, void* ws, hipStream_t stream) {
+  const OrthoPlan o = ortho_plan(L, M, N, single);  // single: of a bfloat16 result only
   OrthoArgs p{};
   p.m = (int)o.m, p.n = (int)o.n;
   p.tall = M > N;

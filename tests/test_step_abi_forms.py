@@ -1,0 +1,35 @@
+"""Host-side checks of the training step's calls: the orthogonalization with one FP16 number a value.
+
+Every call here fails validation or is a zero-size no-op, before the first HIP
+call; like the other ABI checks the module runs only where no GPU is visible."""
+
+import os
+
+import pytest
+
+from conftest import gpu_available
+from test_step_abi import ALIGN, BF16, DTYPE, F32, INF, LARGE, NAN, NULL, SHAPE, WS, X, Y, _lib, refuses
+
+pytestmark = pytest.mark.skipif(gpu_available() or os.path.exists("/dev/kfd"),
+                                reason="fake device addresses: runs only without a GPU")
+
+
+def test_orthogonalize_f16():
+    L = _lib()
+    f, need = L.fp8q_orthogonalize_f16, L.fp8q_orthogonalize_workspace_bytes(2, 133, 270, BF16)
+    #       0  1    2  3   4   5  6       7       8       9    10 11  12    13
+    good = [X, F32, 2, 133, 270, 5, 3.4445, -4.775, 2.0315, 0.5, Y, WS, need, None]
+    refuses(f, good, [
+        (1, 2, DTYPE), (2, -1, SHAPE), (3, -1, SHAPE), (4, -1, SHAPE), (5, 0, SHAPE), (5, 101, SHAPE),
+        (6, NAN, SHAPE), (7, INF, SHAPE), (8, 4.0, SHAPE), (9, INF, SHAPE), (12, need // 4, SHAPE),
+        (3, 65537, LARGE), (4, 65537, LARGE), (2, 65536, LARGE), (0, None, NULL), (10, None, NULL), (11, None, NULL),
+        (0, X + 2, ALIGN), (10, Y + 1, ALIGN), (11, WS + 8, ALIGN)])
+    assert f(None, F32, 0, 33, 70, 5, 2.0, -1.5, 0.5, 1.0, None, None, 0, None) == 0
+
+
+def test_the_workspace_is_that_of_two_numbers_a_value():
+    """X, both X^T, A and B, in two parts each, whatever out's type."""
+    size = _lib().fp8q_orthogonalize_workspace_bytes
+    for L, M, N in ((1, 512, 512), (2, 333, 1000), (1, 4096, 700)):
+        m, n = ((v + 63) // 64 * 64 for v in (min(M, N), max(M, N)))
+        assert size(L, M, N, BF16) == size(L, M, N, F32) >= L * 2 * (6 * m * n + 4 * m * m)
