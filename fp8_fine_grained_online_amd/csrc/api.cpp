@@ -226,17 +226,13 @@ bool bounded(int steps, double a, double b, double c) {
   for (int k = 0; k < steps; ++k) {
     const double t1 = top * top;
     double most = p(top), inner = q(t1);
-    if (c != 0.0) {
-      if (const double t = -b / (2 * c); t > 0 && t < t1) inner = fmax(inner, q(t));
-      const double disc = 9 * b * b - 20 * a * c;
-      if (disc >= 0) {
-        for (double sign : {-1.0, 1.0}) {
-          const double t = (-3 * b + sign * sqrt(disc)) / (10 * c);
-          if (t > 0 && t < t1) most = fmax(most, p(sqrt(t)));
-        }
-      }
-    } else if (b != 0.0) {
-      if (const double t = -a / (3 * b); t > 0 && t < t1) most = fmax(most, p(sqrt(t)));
+    if (const double t = -b / (2 * c); t > 0 && t < t1) inner = fmax(inner, q(t));
+    const double disc = 9 * b * b - 20 * a * c;
+    if (disc >= 0) {
+      // (5 c and a over the larger root's numerator: nothing cancels, whatever is near zero)
+      const double r = -0.5 * (3 * b + copysign(sqrt(disc), b));
+      for (double t : {r / (5 * c), a / r})
+        if (t > 0 && t < t1) most = fmax(most, p(sqrt(t)));
     }
     if (inner > 7.5 || most > 3.0) return false;
     top = most;

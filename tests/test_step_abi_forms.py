@@ -33,3 +33,18 @@ def test_the_workspace_is_that_of_two_numbers_a_value():
     for L, M, N in ((1, 512, 512), (2, 333, 1000), (1, 4096, 700)):
         m, n = ((v + 63) // 64 * 64 for v in (min(M, N), max(M, N)))
         assert size(L, M, N, BF16) == size(L, M, N, F32) >= L * 2 * (6 * m * n + 4 * m * m)
+
+
+def test_polynomials_with_a_vanishing_last_coefficient():
+    """s (8.4 - 7.4 s^2) has its top, 3.44, inside [0, 1]; a last coefficient near nothing changes neither that nor
+    that s (2 - 1.5 s^2) stays below 3. 0.1 s (1 - s^2)^2 is flat at its double root."""
+    f = _lib().fp8q_orthogonalize
+
+    def status(steps, a, b, c):
+        return f(None, F32, 1, 4, 4, steps, a, b, c, 1.0, Y, F32, WS, 1 << 40, None)
+    for c in (0.0, 1e-45, 1e-30, 1e-20, -1e-20, 1e-10, -1e-10, 1e-6):
+        assert status(1, 8.4, -7.4, c) == SHAPE, c
+        assert status(5, 2.0, -1.5, c) == NULL, c
+        assert status(1, -8.4, 7.4, c) == SHAPE, c
+    assert status(9, 0.1, -0.2, 0.1) == NULL and status(9, 0.0, 0.0, 0.0) == NULL and status(1, 0.0, 0.0, 2.9) == NULL
+    assert status(1, 0.0, 7.0, 1e-20) == SHAPE and status(1, 0.0, 2.9, 1e-20) == NULL
