@@ -135,8 +135,10 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_quant_kernel(SwigluArgs
   const float amax = __uint_as_float(row16_max_u32(__float_as_uint(top)));
   float s;
   uint2 codes;
-  if (__any(!(amax >= 0x1p-64f))) {
-    // tiles of nothing, or of so little that quotients have to be scaled and may pass 448
+  // (as bits, which order like the values: 2^-64 to the largest finite one)
+  if (__any(__float_as_uint(amax) - 0x1F800000u >= 0x7F800000u - 0x1F800000u)) {
+    // tiles of nothing, or of so little that quotients have to be scaled and may pass 448; and those with a
+    // product that overflowed, whose codes then do not depend on the tiles beside them
     s = tile_scale(amax);
     const TileDivisor d = make_divisor(s, amax);
     codes.x = pack4_e4m3(quotient(u[0], d), quotient(u[1], d), quotient(u[2], d), quotient(u[3], d));
