@@ -13,7 +13,10 @@
 // stay and walk along the rows 3 to 10%.
 //
 // With t = exp(-gate) the pair s, 1 - s is {1, t} / (1 + t). t is kept within
-// e^-87 .. e^87, so that none of it over- or underflows.
+// e^-87 .. e^87, so that none of it over- or underflows. Gates below -87, which ordinary
+// data does not have, put their wavefront on a way of its own with a factor exp(gate + 87).
+#include <type_traits>
+
 #include "common.hpp"
 #include "rows.hpp"
 
@@ -25,6 +28,7 @@ constexpr float kFar = 87.0f;  // beyond, a sigmoid or what it lacks to 1 is bel
 
 struct Gate {
   float s, c, y;  // sigmoid, 1 - sigmoid, gate sigmoid
+  float f;        // s and y are to be multiplied by it, last
 };
 
 // t = exp(-x), |x| <= 87, to about two units in the last place: 2^p by the hardware's
@@ -50,14 +54,43 @@ __device__ __forceinline__ float exp_neg(float x) {
 }
 
 // The reciprocal is the hardware's, to one unit: a correction would be two operations
-// of the FP8 form's budget. A gate below -87 counts as -87, whose silu is above -2^-118;
-// the clamp is the one that keeps a NaN.
-template <typename X>
+// of the FP8 form's budget. kBelow: some gate of the wavefront may be below -87. Such a one
+// counts as -87 in the sigmoid, and f is what its exponential lacks: none of the others'
+// factors is subnormal, so the products lose nothing before the last. (From -200 on f is 0; the
+// maximum is the one that keeps a NaN.)
+template <typename X, bool kBelow>
 __device__ __forceinline__ Gate gate_of(float g) {
-  const float low = __builtin_elementwise_maximum(g, -kFar);
+  const float low = kBelow ? __builtin_elementwise_maximum(g, -kFar) : g;
   const float t = exp_neg<X>(fminf(low, kFar));
   const float s = __builtin_amdgcn_rcpf(1.0f + t);
-  return {s, t * s, low * s};
+  if constexpr (!kBelow) return {s, t * s, g * s, 1.0f};
+  const float v = __builtin_elementwise_maximum(g, -200.0f);
+  return {s, t * s, v * s, v < -kFar ? exp_neg<float>(-kFar - v) : 1.0f};
+}
+
+// f(false), or f(true) where some gate of the wavefront is below -87: as bits, negative values order behind
+// all others, the farther from zero the later
+template <typename F>
+__device__ __forceinline__ void for_gates(const float (&g)[8], F&& f) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) most = umax(most, __float_as_uint(g[e]));
+  if (__any(most > 0xC2AE0000u)) f(std::true_type{});  // -87
+  else f(std::false_type{});
+}
+
+// u becomes gate sigmoid(gate) u
+template <typename X>
+__device__ __forceinline__ void activate(const float (&g)[8], float (&u)[8]) {
+  for_gates(g, [&](auto below) {
+    constexpr bool kBelow = decltype(below)::value;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const Gate k = gate_of<X, kBelow>(g[e]);
+      u[e] *= k.y;
+      if (kBelow) u[e] *= k.f;
+    }
+  });
 }
 
 // n / d for n below 2^31, by a multiplication: m = floor(2^k / d) + 1 for the k = 31 +
@@ -106,8 +139,7 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_kernel(SwigluArgs p) {
   float g[8], u[8];
   values(rg, g);
   values(ru, u);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) u[e] *= gate_of<X>(g[e]).y;
+  activate<X>(g, u);
   Chunk<Y> out;
   to_chunk(u, out);
   store_chunk((Y*)p.out + m * (int64_t)p.I + at, out, have);
@@ -126,12 +158,10 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_quant_kernel(SwigluArgs
   float g[8], u[8];
   values(rg, g);
   values(ru, u);
+  activate<X>(g, u);
   float top = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    u[e] *= gate_of<X>(g[e]).y;
-    top = fmaxf(top, fabsf(u[e]));
-  }
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(u[e]));
   const float amax = __uint_as_float(row16_max_u32(__float_as_uint(top)));
   float s;
   uint2 codes;
@@ -177,14 +207,18 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_bwd_kernel(SwigluArgs p
   values(rg, g);
   values(ru, u);
   values(rd, d);
+  for_gates(g, [&](auto below) {
+    constexpr bool kBelow = decltype(below)::value;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const Gate k = gate_of<X>(g[e]);
-    // s (1 + gate (1 - s)) = s + (gate s) (1 - s); beyond 87 it is 1 or counts as 0, whatever the gate
-    const float slope = g[e] > kFar ? k.s : g[e] < -kFar ? 0.0f : __builtin_fmaf(k.y, k.c, k.s);
-    g[e] = d[e] * u[e] * slope;
-    u[e] = d[e] * k.y;
-  }
+    for (int e = 0; e < 8; ++e) {
+      const Gate k = gate_of<X, kBelow>(g[e]);
+      // s (1 + gate (1 - s)) = s + (gate s) (1 - s); above 87 it is 1, whatever the gate
+      const float slope = g[e] > kFar ? k.s : __builtin_fmaf(k.y, k.c, k.s);
+      g[e] = d[e] * u[e] * slope;
+      u[e] = d[e] * k.y;
+      if (kBelow) g[e] *= k.f, u[e] *= k.f;
+    }
+  });
   X* const out = (X*)p.out + m * (int64_t)(2 * p.I) + at;
   Chunk<X> o;
   to_chunk(g, o);

@@ -692,8 +692,8 @@ FP8Q_API int fp8q_norm_bwd(const void* dy, int dy_dtype, int64_t ldy, const void
 /*
  * Gated activation: of a row gu = [gate | up] of 2 I values
  *   y = gate / (1 + exp(-gate)) * up
- * in binary32 (exp to about two units in the last place; a gate below -87 counts
- * as -87, where y is below 2^-118 of up), rounded once to y's type.
+ * in binary32 (exp to about two units in the last place; a y below 2^-240 of up is
+ * 0), rounded once to y's type.
  *
  *   gu : in,  M x 2I of gu_dtype, rows ld apart
  *   m_offsets : in, DEVICE int32[G + 1], or NULL for all M rows: rows from

@@ -44,3 +44,75 @@ def test_codes_of_a_tile_that_overflows_are_its_own(dtype):
     for m in range(1, 6):
         assert torch.equal(q[m, :128], q[0, :128]), m
     assert torch.equal(q[:, 128:], want[:, 128:])
+
+
+def far_gates(I, dtype):
+    """Gates about and below -87, and ordinary ones, with values of `up` that make the products ordinary numbers."""
+    import torch
+    rng = np.random.default_rng(38)
+    gate = np.concatenate([rng.uniform(-130, -80, I - 8), [-86.5, -87.0, -87.5, -88.0, -104.0, -3.0, 5.0, 90.0]])
+    exact = torch.from_numpy(gate.astype(np.float32)).to(dtype).double().numpy()
+    up = np.minimum(np.exp(np.minimum(-exact, 80.0)), 1e30) * rng.choice([-1.5, 0.75], I)
+    return torch.from_numpy(np.concatenate([gate, up])[None].astype(np.float32)).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("I", [128, 129])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_far_gates(I, dtype):
+    """The value is gate exp(gate) up to any distance: the sigmoid at -87 is within 7 u, exp(gate + 87) within 4 u and
+    what its argument lacks: gate + 87 is rounded where gate is a float32 beyond -174 only, which is not here. Four
+    products more: 16 u."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    gu = far_gates(I, t)
+    x = host(gu)
+    want = step.swiglu(x)
+    got = host(F.fp8q_swiglu(gu, out_dtype="f32"))
+    tol = 16 * U * np.abs(want) + 2.0 ** -149
+    assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
+    dy = torch.from_numpy(np.random.default_rng(39).standard_normal((1, I)).astype(np.float32)).cuda()
+    d, gate, up = host(dy), x[:, :I], x[:, I:]
+    got = host(F.fp8q_swiglu_bwd(dy, gu))
+    want = step.swiglu_bwd(d, x)
+    s, c = step.sigmoid(gate), step.sigmoid(-gate)
+    tol = np.concatenate([U * np.abs(d * up) * (11 * s + 21 * np.abs(gate * s * c) + 7 * np.abs(s + gate * s * c)), 16 * U * np.abs(d * gate * s)], 1)
+    tol += (2.0 ** -8 if dtype == "bf16" else 0.0) * (np.abs(want) + tol) + 2.0 ** -133
+    assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
+
+
+def test_the_farthest_gates_give_nothing():
+    import fp8_fine_grained_online_amd as F
+    inf = float("inf")
+    gu = tensor([[-200.0, -1e4, -3e38, -inf, 3e38, -3e38, 3e38, 2.0]])
+    assert not F.fp8q_swiglu(gu, out_dtype="f32").any()
+    import torch
+    assert not F.fp8q_swiglu_bwd(torch.ones(1, 4, device="cuda"), gu).any()
+
+
+def test_a_tile_of_far_gates_has_their_scale():
+    """1x128 tiles whose values all come from far gates."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    gu = far_gates(128, torch.float32)
+    gu[:, 120:128] = -95.0
+    want = np.abs(step.swiglu(host(gu))).max() / 448
+    q, sa = F.fp8q_swiglu_quant_act_1x128(gu)
+    assert abs(float(sa[0, 0]) - want) <= 18 * U * want
+    assert abs(q.view(torch.float8_e4m3fn).float().abs().max().item() - 448) == 0
+
+
+def test_one_far_gate_leaves_the_others_as_they_are():
+    import torch
+    import fp8_fine_grained_online_amd as F
+    for t in (torch.bfloat16, torch.float32):
+        gu = (3 * torch.randn(3, 512, device="cuda", generator=torch.Generator("cuda").manual_seed(40))).to(t)
+        far = gu.clone()
+        far[1, 77] = -99.0
+        dy = torch.randn(3, 256, device="cuda").to(t)
+        for f in (lambda x: F.fp8q_swiglu(x, out_dtype="f32"), lambda x: F.fp8q_swiglu_bwd(dy, x)):
+            a, b = f(gu), f(far)
+            b[1, 77] = a[1, 77]
+            if a.shape[1] == 512:
+                b[1, 256 + 77] = a[1, 256 + 77]
+            assert torch.equal(a, b)
