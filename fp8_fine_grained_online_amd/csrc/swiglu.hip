@@ -214,9 +214,10 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_bwd_kernel(SwigluArgs p
       const Gate k = gate_of<X, kBelow>(g[e]);
       // s (1 + gate (1 - s)) = s + (gate s) (1 - s); above 87 it is 1, whatever the gate
       const float slope = g[e] > kFar ? k.s : __builtin_fmaf(k.y, k.c, k.s);
-      g[e] = d[e] * u[e] * slope;
-      u[e] = d[e] * k.y;
-      if (kBelow) g[e] *= k.f, u[e] *= k.f;
+      // (where d u overflows both are above 1, and the slope, never subnormal, is taken to one of them first)
+      const float du = d[e] * u[e], f = kBelow ? k.f : 1.0f;
+      g[e] = fabsf(du) <= 3.402823466e38f ? du * slope * f : (d[e] * slope) * (u[e] * f);
+      u[e] = d[e] * k.y * f;
     }
   });
   X* const out = (X*)p.out + m * (int64_t)(2 * p.I) + at;

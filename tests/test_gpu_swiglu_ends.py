@@ -116,3 +116,23 @@ def test_one_far_gate_leaves_the_others_as_they_are():
             if a.shape[1] == 512:
                 b[1, 256 + 77] = a[1, 256 + 77]
             assert torch.equal(a, b)
+
+
+def test_gradients_whose_factors_overflow():
+    """dy up beyond binary32, the gradient within: three products and the slope, as elsewhere."""
+    import fp8_fine_grained_online_amd as F
+    gate = np.array([-40.0, -60.0, -86.0, -100.0, -120.0, -10.0, -5.0, -1.2784645])
+    up = np.array([1e20, 1e20, 3e38, 1e25, 3e38, -1e21, 2.0, 1e20])
+    d = np.array([1e20, -1e20, 1e20, 1e30, 3e38, 1e18, 3.3e38, 1e19])
+    gu = tensor(np.concatenate([gate, up])[None])
+    dy = tensor(d[None])
+    x, d = host(gu), host(dy)
+    gate, up = x[:, :8], x[:, 8:]
+    got = host(F.fp8q_swiglu_bwd(dy, gu))
+    want = step.swiglu_bwd(d, x)
+    s, c = step.sigmoid(gate), step.sigmoid(-gate)
+    tol = np.concatenate([U * np.abs(d * up) * (11 * s + 21 * np.abs(gate * s * c) + 7 * np.abs(s + gate * s * c)), 16 * U * np.abs(d * gate * s)], 1)
+    assert np.all(np.isfinite(got)) and np.all(np.abs(want) < 3e38)
+    assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
+    # what does overflow is an infinity
+    assert F.fp8q_swiglu_bwd(tensor([[1e20]]), tensor([[2.0, 1e20]]))[0, 0] == float("inf")
