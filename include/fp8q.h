@@ -657,7 +657,8 @@ FP8Q_API int int8_gemm_grouped(const int8_t* a, const float* sa, const int8_t* b
  *   gamma, beta : in,  K of weights_dtype; beta NULL for none, and only with centred 1
  *   y           : out, M x K of y_dtype
  *   h           : out, M x K of x_dtype; NULL exactly where residual is
- * 0 <= K <= 16384. M == 0 or K == 0 is a no-op. One kernel.
+ * 0 <= K <= 16384; M below 2^23, and below 2^22 for K > 12288. M == 0 or K == 0 is a no-op.
+ * One kernel.
  */
 FP8Q_API int fp8q_norm(const void* x, int x_dtype, int64_t ldx, const void* residual, int64_t ldr,
                        const void* gamma, const void* beta, int weights_dtype, float eps,
@@ -680,7 +681,8 @@ FP8Q_API int fp8q_norm(const void* x, int x_dtype, int64_t ldx, const void* resi
  *   dgamma, dbeta : out, K float32, every element written; dbeta NULL exactly
  *           where centred is 0
  *   workspace : at least fp8q_norm_bwd_workspace_bytes(M, K, centred), 16-byte aligned
- * 0 <= K <= 16384. K == 0 is a no-op; M == 0 writes zeros to dgamma and dbeta. Two kernels.
+ * K and M as for fp8q_norm. K == 0 is a no-op; M == 0 writes zeros to dgamma and dbeta. Two
+ * kernels.
  */
 FP8Q_API int64_t fp8q_norm_bwd_workspace_bytes(int64_t M, int64_t K, int centred);
 FP8Q_API int fp8q_norm_bwd(const void* dy, int dy_dtype, int64_t ldy, const void* x, int x_dtype,

@@ -1,0 +1,42 @@
+"""More of the normalization and its gradient: many short rows, several rounds of the gradient's row loop in every
+shape of row, rows that are not ordinary in them. The bounds are those of test_gpu_norm_rows; u = 2^-24."""
+
+import numpy as np
+import pytest
+
+from conftest import gpu_available
+from test_gpu_norm_rows import U, check_bwd, check_norm, rows, weights
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+
+@pytest.mark.parametrize("K", [64, 128])
+@pytest.mark.parametrize("centred", [False, True])
+def test_many_short_rows(K, centred):
+    """Every head of every token: more than 2^22 rows. Rows of any part of them are the smaller call's, bit for bit;
+    the weights' gradients are sums over M / 4096 rows in a thread, 8 in a workgroup, 512 partial rows in 32 runs."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    M = (1 << 22) + 3
+    gen = torch.Generator("cuda").manual_seed(K)
+    x, dy = (torch.randn(M, K, device="cuda", generator=gen, dtype=torch.bfloat16) for _ in range(2))
+    g, b = weights(K, 5200)
+    b = b if centred else None
+    y = F.fp8q_norm(x, g, 1e-6, beta=b, centred=centred)
+    dx, dgamma, dbeta = F.fp8q_norm_bwd(dy, x, g, 1e-6, centred=centred)
+    for part in (slice(0, 40), slice(M // 2, M // 2 + 40), slice(M - 41, M)):
+        check_norm(x[part], g, 1e-6, b, centred, y[part], "bf16")
+        assert torch.equal(y[part], F.fp8q_norm(x[part], g, 1e-6, beta=b, centred=centred))
+        assert torch.equal(dx[part], F.fp8q_norm_bwd(dy[part], x[part], g, 1e-6, centred=centred)[0])
+    sums = [torch.zeros(K, dtype=torch.float64, device="cuda") for _ in range(4)]
+    for at in range(0, M, 1 << 20):
+        h, d = x[at:at + (1 << 20)].double(), dy[at:at + (1 << 20)].double()
+        if centred:
+            h = h - h.mean(1, keepdim=True)
+        h = h / torch.sqrt((h * h).mean(1, keepdim=True) + float(np.float32(1e-6)))
+        for s, v in zip(sums, (d * h, (d * h).abs(), d, d.abs())):
+            s += v.sum(0)
+    n = M / 4096 + 8 + 16 + 32
+    assert torch.all((dgamma - sums[0]).abs() <= (n + 80) * U * sums[1])
+    if centred:
+        assert torch.all((dbeta - sums[2]).abs() <= n * U * sums[3])

@@ -48,3 +48,14 @@ def test_polynomials_with_a_vanishing_last_coefficient():
         assert status(1, -8.4, 7.4, c) == SHAPE, c
     assert status(9, 0.1, -0.2, 0.1) == NULL and status(9, 0.0, 0.0, 0.0) == NULL and status(1, 0.0, 0.0, 2.9) == NULL
     assert status(1, 0.0, 7.0, 1e-20) == SHAPE and status(1, 0.0, 2.9, 1e-20) == NULL
+
+
+def test_rows_of_the_normalization():
+    """2^22 rows are refused only where a row takes 1024 threads."""
+    L = _lib()
+    size, f = L.fp8q_norm_bwd_workspace_bytes, L.fp8q_norm
+    for M, K, ok in ((1 << 22, 64, True), ((1 << 23) - 1, 128, True), ((1 << 23) - 1, 12288, True), (1 << 23, 64, False),
+                     ((1 << 22) - 1, 16384, True), (1 << 22, 12289, False)):
+        assert (size(M, K, 1) > 0) == ok, (M, K)
+        # (the missing x is looked at after the sizes)
+        assert f(None, BF16, K, None, 0, X, None, F32, 1e-6, 1, M, K, Y, F32, None, None) == (NULL if ok else LARGE), (M, K)
