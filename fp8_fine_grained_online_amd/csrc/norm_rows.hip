@@ -89,6 +89,7 @@ struct RowLds {
 
 struct RowStats {
   float mu, shift, r;  // hat = (h - mu) r - shift, shift = (what mu is off by) r
+  float lift;             // 1 / std is r lift: 1, or 2^64 where it may pass binary32 (for the gradient)
   double wide_mu, wide_r;
   bool wide;  // the statistics are in the doubles
 };
@@ -112,7 +113,7 @@ __device__ __forceinline__ RowStats row_stats(float (&v)[Shape::kC][8], Present 
                                               RowLds<Shape::kT>& lds) {
   constexpr int T = Shape::kT, C = Shape::kC;
   RowStats s;
-  s.mu = s.shift = 0.0f;
+  s.mu = s.shift = 0.0f, s.lift = 1.0f;
   s.wide_mu = 0.0, s.wide_r = 0.0;
   const float inv_k = 1.0f / (float)K;
   float stat[2] = {0.0f, 0.0f};  // sum of squared deviations, of deviations
@@ -166,7 +167,10 @@ __device__ __forceinline__ RowStats row_stats(float (&v)[Shape::kC][8], Present 
   }
   row_sums<T, 1>(sq, lds.wide[1]);
   s.wide_r = 1.0 / __dsqrt_rn(sq[0] / (double)K + (double)eps);
-  if (s.wide) s.r = (float)s.wide_r;
+  if (s.wide) {
+    s.lift = s.wide_r > 0x1p100 ? 0x1p64f : 1.0f;
+    s.r = (float)(s.wide_r / (double)s.lift);
+  }
   forget(v);
   return s;
 }
@@ -383,6 +387,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_rows_bwd_kernel(NormBwdArgs 
     }
     row_sums<T, 2>(sums, slots[sub].sums);
     const float c_hat = sums[0] * inv_k, c_one = kCentred ? sums[1] * inv_k : 0.0f;
+    const float lift = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(s.lift)));
     if (m < p.M) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
@@ -394,7 +399,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_rows_bwd_kernel(NormBwdArgs 
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float t = __builtin_fmaf(-v[i][e], c_hat, d[e] * g[e] - c_one);
-          o[e] = __builtin_fmaf(s.r, t, o[e]);
+          o[e] = __builtin_fmaf(s.r, t * lift, o[e]);
         }
         Chunk<X> out;
         to_chunk(o, out);

@@ -40,3 +40,25 @@ def test_many_short_rows(K, centred):
     assert torch.all((dgamma - sums[0]).abs() <= (n + 80) * U * sums[1])
     if centred:
         assert torch.all((dbeta - sums[2]).abs() <= n * U * sums[3])
+
+
+@pytest.mark.parametrize("K", [1, 5, 40, 1000, 1100, 2047, 3000, 5000, 9000, 16000])
+@pytest.mark.parametrize("centred", [False, True])
+def test_bwd_of_the_smallest_rows(K, centred):
+    """eps 0 and rows whose 1 / std passes binary32: dx is finite where the formula is, beside ordinary rows."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x, dy = rows(7, K, 5210, "f32"), rows(7, K, 5211, "f32")
+    g, _ = weights(K, 5212, "f32")
+    ordinary = F.fp8q_norm_bwd(dy, x, g, 0.0, centred=centred)[0]
+    z, d = x.clone(), dy.clone()
+    for m in (2, 5, 6):
+        z[m] = (x[m] * 2.0 ** 9).round() * 2.0 ** -139  # whole multiples of 2^-139: subnormal, and centred ones too
+        d[m] *= 2.0 ** -16
+    if K == 1:
+        z[z == 0] = 2.0 ** -139
+    dx, dgamma, dbeta = F.fp8q_norm_bwd(d, z, g, 0.0, centred=centred)
+    keep = [0, 1, 3, 4]
+    assert torch.equal(dx[keep].nan_to_num(7.0), ordinary[keep].nan_to_num(7.0))
+    if K > 1 or not centred:  # (a single centred value has no deviation: 0 / 0)
+        check_bwd(d, z, g, 0.0, centred, None, (dx, dgamma, dbeta))
