@@ -62,3 +62,34 @@ def test_bwd_of_the_smallest_rows(K, centred):
     assert torch.equal(dx[keep].nan_to_num(7.0), ordinary[keep].nan_to_num(7.0))
     if K > 1 or not centred:  # (a single centred value has no deviation: 0 / 0)
         check_bwd(d, z, g, 0.0, centred, None, (dx, dgamma, dbeta))
+
+
+# one past two full rounds of the gradient's 512 (beyond 8192 values 256) workgroups, in every shape of row
+ROUNDS = [(8201, 64), (8195, 1000), (2051, 1025), (2049, 2047), (1027, 2500), (1031, 5000), (517, 9001), (521, 16383)]
+
+
+@pytest.mark.parametrize("M,K", ROUNDS)
+@pytest.mark.parametrize("centred", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bwd_in_several_rounds(M, K, centred, dtype):
+    """Rows whose statistics leave binary32's range in both halves of a workgroup, in the first round, in later ones
+    and as the last row, beside ordinary rows, whose gradients keep their bits."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x, dy, dres = rows(M, K, 5220, dtype), rows(M, K, 5221, dtype), rows(M, K, 5222, dtype)
+    g, _ = weights(K, 5223)
+    want = F.fp8q_norm_bwd(dy, x, g, 1e-6, centred=centred, dres=dres)
+    check_bwd(dy, x, g, 1e-6, centred, dres, want)
+    far = sorted({0, 3, 6, 7, M // 2, M // 2 + 1, M - 2, M - 1})
+    z = x.clone()
+    z[far] *= 2.0 ** 80
+    z[far[2]] *= 2.0 ** -160
+    got = F.fp8q_norm_bwd(dy, z, g, 1e-6, centred=centred, dres=dres)
+    check_bwd(dy, z, g, 1e-6, centred, dres, got)
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[far] = False
+    assert torch.equal(got[0][keep], want[0][keep])
+    z[far[1], K // 2], z[M // 2, 0], z[M - 1, K - 1] = float("nan"), float("inf"), float("nan")
+    got = F.fp8q_norm_bwd(dy, z, g, 1e-6, centred=centred, dres=dres)
+    assert torch.equal(got[0][keep], want[0][keep])
+    assert torch.isnan(got[0][[far[1], M // 2, M - 1]]).any(1).all() and torch.isnan(got[1]).any()

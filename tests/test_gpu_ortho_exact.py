@@ -183,3 +183,24 @@ def test_single_in_a_captured_graph_and_on_a_stream():
         assert torch.equal(got, F.fp8q_orthogonalize(g, single=True)) and torch.all(space[need:] == 0xFF)
     with pytest.raises(ValueError):
         F.fp8q_orthogonalize(g, out_dtype="f32", single=True)
+
+
+# a matrix in a workgroup, the joint kernel, a gram in runs of K, blocks of 16 and 32, tiles, tall ones
+PATHS = [(30, 40), (128, 700), (16, 8192), (200, 333), (333, 500), (700, 333), (600, 640), (900, 800), (1400, 1400), (1500, 2000),
+         (2100, 1900)]
+
+
+@pytest.mark.parametrize("M,N", PATHS)
+@pytest.mark.parametrize("out,single", [("f32", False), ("bf16", False), ("bf16", True)])
+def test_what_is_not_finite_fills_its_matrix(M, N, out, single):
+    """An infinity or NaN reaches every value of its own matrix (A A has it everywhere), whatever the way, and no other's."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    g = torch.randn(3, M, N, device="cuda", generator=torch.Generator("cuda").manual_seed(M))
+    want = F.fp8q_orthogonalize(g, out_dtype=out, single=single)[1]
+    g[0, M - 1, N // 2], g[2, M // 3, N - 1] = float("nan"), -float("inf")
+    got = F.fp8q_orthogonalize(g, out_dtype=out, single=single)
+    assert torch.isnan(got[0]).all() and torch.isnan(got[2]).all() and torch.equal(got[1], want)
+    # and alone, which may go another way
+    assert torch.isnan(F.fp8q_orthogonalize(g[0], out_dtype=out, single=single)).all()
+    assert torch.isnan(F.fp8q_orthogonalize(g[2], out_dtype=out, single=single)).all()
