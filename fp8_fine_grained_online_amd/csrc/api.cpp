@@ -189,7 +189,7 @@ int check_norm(float eps, int centred, int64_t M, int64_t K) {
   if (!(eps >= 0.0f) || eps > 3.0e38f) return FP8Q_ERR_SHAPE;  // NaN, negative or infinite
   // at most 512 threads per row, or 1024 for the longest (rows of up to 1024 values take 64, but one limit
   // for all of the shorter ones is easier to know)
-  if (K > kNormMaxK || !launchable(M, K > 12288 ? 1024 : 512)) return FP8Q_ERR_TOO_LARGE;
+  if (M > kMaxDim || K > kNormMaxK || !launchable(M, K > 12288 ? 1024 : 512)) return FP8Q_ERR_TOO_LARGE;
   return FP8Q_OK;
 }
 

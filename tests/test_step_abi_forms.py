@@ -59,3 +59,6 @@ def test_rows_of_the_normalization():
         assert (size(M, K, 1) > 0) == ok, (M, K)
         # (the missing x is looked at after the sizes)
         assert f(None, BF16, K, None, 0, X, None, F32, 1e-6, 1, M, K, Y, F32, None, None) == (NULL if ok else LARGE), (M, K)
+    # (nor do sizes pass whose threads, counted in 64 bits, wrap)
+    for M in (1 << 31, 1 << 55, 1 << 56, (1 << 63) - 1):
+        assert size(M, 64, 1) == -1 and f(None, BF16, 64, None, 0, X, None, F32, 1e-6, 1, M, 64, Y, F32, None, None) == LARGE, M
