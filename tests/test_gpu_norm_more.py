@@ -93,3 +93,21 @@ def test_bwd_in_several_rounds(M, K, centred, dtype):
     got = F.fp8q_norm_bwd(dy, z, g, 1e-6, centred=centred, dres=dres)
     assert torch.equal(got[0][keep], want[0][keep])
     assert torch.isnan(got[0][[far[1], M // 2, M - 1]]).any(1).all() and torch.isnan(got[1]).any()
+
+
+@pytest.mark.parametrize("M,K", [(262147, 8200), (2200000, 1000)])
+@pytest.mark.parametrize("centred", [False, True])
+def test_more_values_than_32_bits_count(M, K, centred):
+    """Rows at either side of 2^31 values, and the last, are the smaller call's, bit for bit."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    x = torch.empty(M, K, device="cuda", dtype=torch.bfloat16).normal_(generator=torch.Generator("cuda").manual_seed(M))
+    g, _ = weights(K, 5230)
+    y, h = F.fp8q_norm(x, g, 1e-6, centred=centred, residual=x)
+    dx, dgamma, _ = F.fp8q_norm_bwd(y, x, g, 1e-6, centred=centred, dres=x)
+    middle = (1 << 31) // K
+    for part in (slice(0, 3), slice(middle - 2, middle + 3), slice(M - 3, M)):
+        y1, h1 = F.fp8q_norm(x[part], g, 1e-6, centred=centred, residual=x[part])
+        assert torch.equal(y[part], y1) and torch.equal(h[part], h1)
+        assert torch.equal(dx[part], F.fp8q_norm_bwd(y1, x[part], g, 1e-6, centred=centred, dres=x[part])[0])
+    assert torch.isfinite(dgamma).all()

@@ -204,3 +204,39 @@ def test_what_is_not_finite_fills_its_matrix(M, N, out, single):
     # and alone, which may go another way
     assert torch.isnan(F.fp8q_orthogonalize(g[0], out_dtype=out, single=single)).all()
     assert torch.isnan(F.fp8q_orthogonalize(g[2], out_dtype=out, single=single)).all()
+
+
+@pytest.mark.parametrize("M,N", [(1, 65536), (65536, 1), (65536, 3), (60, 65536), (65536, 64), (129, 65535)])
+@pytest.mark.parametrize("out,single", [("f32", False), ("bf16", True)])
+def test_the_longest_sides(M, N, out, single):
+    """Matrices of one direction, +-1 / sqrt(M N): the result is the polynomial of 1, with that direction."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    gen = torch.Generator("cuda").manual_seed(M + N)
+    u, v = (torch.randint(0, 2, (k,), device="cuda", generator=gen).float() * 2 - 1 for k in (M, N))
+    got = F.fp8q_orthogonalize(u[:, None] * v[None], out_dtype=out, single=single).float()
+    s = 1.0
+    a, b, c = F32_COEFFS
+    for _ in range(5):
+        s = a * s + b * s ** 3 + c * s ** 5
+    want = s / np.sqrt(M * N)
+    # (of two numbers: 2^-14 as at the top, and binary32 sums of 65536 products, 4 sqrt(65536) 2^-24 in each of three
+    # products of five steps; of one number 1.2e-2 and the rounding)
+    tol = 2.0 ** -14 + 15 * 4 * 256 * 2.0 ** -24 if out == "f32" else 1.2e-2 + 2.0 ** -8
+    assert float((got * (u[:, None] * v[None]) - want).abs().max()) <= tol * want
+
+
+@pytest.mark.parametrize("L,M,N", [(65535, 3, 5), (500, 130, 140), (1200, 70, 300), (3000, 700, 1050)])
+@pytest.mark.parametrize("single", [False, True])
+def test_many_matrices(L, M, N, single):
+    """As many as the call takes; and more values than 32 bits count. Matrices from here and there against the same alone."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    gen = torch.Generator("cuda").manual_seed(L)
+    g = torch.randn(L, M, N, device="cuda", generator=gen, dtype=torch.bfloat16)
+    got = F.fp8q_orthogonalize(g, single=single)
+    for i in (0, 1, L // 2, L - 2, L - 1):
+        want = F.fp8q_orthogonalize(g[i], out_dtype="f32")
+        # the exact form, alone, may sum in another order (4e-5 at most, as documented); one FP16 number 2e-3
+        tol = (2e-3 if single and min(M, N) > 128 else 8e-5) + 2.0 ** -8
+        assert torch.linalg.norm(got[i].float() - want) <= tol * torch.linalg.norm(want), i

@@ -136,3 +136,23 @@ def test_gradients_whose_factors_overflow():
     assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
     # what does overflow is an infinity
     assert F.fp8q_swiglu_bwd(tensor([[1e20]]), tensor([[2.0, 1e20]]))[0, 0] == float("inf")
+
+
+def test_more_values_than_32_bits_count():
+    """Rows at either side of 2^31 values of gu and of y, and the last, are the smaller call's, bit for bit."""
+    import torch
+    import fp8_fine_grained_online_amd as F
+    M, I = 1050000, 2176
+    gu = torch.empty(M, 2 * I, device="cuda", dtype=torch.bfloat16).normal_(generator=torch.Generator("cuda").manual_seed(41))
+    parts = [slice(0, 3)] + [slice((1 << 31) // w - 2, (1 << 31) // w + 3) for w in (2 * I, I)] + [slice(M - 3, M)]
+    y = F.fp8q_swiglu(gu)
+    for p in parts:
+        assert torch.equal(y[p], F.fp8q_swiglu(gu[p]))
+    q, sa = F.fp8q_swiglu_quant_act_1x128(gu)
+    for p in parts:
+        q1, s1 = F.fp8q_swiglu_quant_act_1x128(gu[p])
+        assert torch.equal(q[p], q1) and torch.equal(sa[p], s1)
+    del q, sa
+    dgu = F.fp8q_swiglu_bwd(y, gu)
+    for p in parts:
+        assert torch.equal(dgu[p], F.fp8q_swiglu_bwd(y[p], gu[p]))
