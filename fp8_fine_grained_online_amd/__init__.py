@@ -40,7 +40,7 @@ A training step around the products, with gradients:
   fp8q_swiglu(gu, out_dtype)                             -> y   gated activation
   fp8q_swiglu_quant_act_1x128(gu)                        -> (q, sa)   the same, straight to FP8 tiles
   fp8q_swiglu_bwd(dy, gu)                                -> dgu
-  fp8q_orthogonalize(g, steps, coeffs, scale, out_dtype) -> out   a weight's update by Newton-Schulz products
+  fp8q_orthogonalize(g, steps, coeffs, scale, out_dtype, single) -> out   a weight's update by Newton-Schulz products
 """
 
 from ._lib import (  # noqa: F401

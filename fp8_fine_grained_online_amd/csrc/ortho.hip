@@ -219,9 +219,10 @@ __device__ __forceinline__ Turned turn_pairs(bool odd, uint32_t p0, uint32_t p1)
 // multiplies; A's slabs rotate through D + 1 buffers, B's through D. Lane l
 // supplies row l % 16 of a 16-row block and 8 values of K at 8 (l / 16); B is the
 // first operand, so a lane holds C[l % 16][4 (l / 16) + r].
-// The MFMAs bound it, at the clock that their power leaves: of 4096 x 4096 they are busy 64% of the
-// gram's time (72 us), 60% of the square's (75) and 56% of the update's (128), the rest being its
-// first copies and the epilogue's bursts (X, its low part and X^T, 101 MB).
+// Its own chain bounds it: of 4096 x 4096 the MFMAs are busy 54% of the gram's time (273 us) and the
+// square's (277) and 61% of the update's (381), in 128 x 128 tiles that copy six slabs per 64 values of K where
+// four hold both parts of both operands; with one number a value 64% (70), 60% (74) and 56% (133), the rest being
+// a tile's first copies and the epilogue's bursts (X, its low part and X^T, 101 MB), which nothing hides.
 // ---------------------------------------------------------------------------
 template <Product kWhat, Result kOut, bool kSplit, int BM, int BN, int D>
 __global__ __launch_bounds__(256, 1) void ortho_product_kernel(OrthoArgs p) {
@@ -1087,7 +1088,7 @@ struct OrthoPlan {
 // and, per 64 values of K, what the chip needs to feed the round: the same for few
 // workgroups, then growing with the share p of the round that is filled. Fitted to
 // kernels of 1024 to 4096 rows; the tile it picks is the fastest of the four, or within 3% of it, in 28 products of 1000 to
-// 4500 rows. us on MI355X
+// 4500 rows. us on MI355X, one FP16 number a value,
 // for 64 / 128 / 192 / 256 tiles:
 //   gram    2048 x 2048 23.0 / 19.4 / 32.3 / 50.2    2048 x 7168 75.6 / 55.9 / 84.0 / 141
 //           2900 x 2900 58.2 / 40.4 / 44.5 / 68.8    4096 x 4096 154 / 90.2 / 67.6 / 99.5
@@ -1137,7 +1138,8 @@ static OrthoPlan ortho_plan(int64_t L, int64_t M, int64_t N, bool single) {
   auto side = [&](int64_t v, int64_t t) { return (v + t - 1) / t; };
   auto sym = [&](int64_t t) { return side(o.m, t) * (side(o.m, t) + 1) / 2; };
   auto all = [&](int64_t t) { return side(o.m, t) * side(o.n, t); };
-  // Small products, for few blocks of 16 x 16 or 32 x 32; else tiles. us for five steps, MI355X, with
+  // Small products, for few blocks of 16 x 16 or 32 x 32; else tiles. us for five steps, MI355X (here and
+  // below with one FP16 number a value above 128 rows, unless float32 is named, which stands for two), with
   // the symmetric products in 16 x 16 blocks / 32 x 32 blocks / 64 x 64 tiles:
   //   256 x 1024 float32 68 / 78 / 133    333 x 1000 70 / 72 / 90    512 x 512 68 / 69 / 84    600 x 600 92 / 89 / 104
   //   800 x 800 118 / 109 / 122    1000 x 1000 135 / 120 / 132    1400 x 1400 242 / 186 / 170    1024 x 4096 - / 253 / 225
@@ -1205,7 +1207,7 @@ static void launch_columns(const OrthoArgs& a, int64_t L, hipStream_t stream) {
     hipLaunchKernelGGL((ortho_columns_kernel<kOut, kSplit, P>), dim3((unsigned)(L * a.count)), dim3(128 * P), 0, stream, a);
   };
   using std::integral_constant;
-  if constexpr (kSplit) {  // (for a bfloat16 result, m is more than 128)
+  if constexpr (kSplit) {  // (of one number a value, m is more than 128)
     if (a.m == 64) return go(integral_constant<int, 2>{});
     if (a.m == 128) return go(integral_constant<int, 4>{});
   }

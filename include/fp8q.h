@@ -694,7 +694,7 @@ FP8Q_API int fp8q_norm_bwd(const void* dy, int dy_dtype, int64_t ldy, const void
 /*
  * Gated activation: of a row gu = [gate | up] of 2 I values
  *   y = gate / (1 + exp(-gate)) * up
- * in binary32 (exp to about two units in the last place; a y below 2^-240 of up is
+ * in binary32 (exp to about two units in the last place; a y below 2^-243 of up may be
  * 0), rounded once to y's type.
  *
  *   gu : in,  M x 2I of gu_dtype, rows ld apart
@@ -740,7 +740,7 @@ FP8Q_API int fp8q_swiglu_bwd(const void* dy, int dy_dtype, int64_t ldy, const vo
  * NaN; the other matrices do not notice.
  *
  * The products run on the FP16 matrix cores with binary32 sums. Every operand is two
- * FP16 numbers, 22 bits: out is as near the definition as if formed in binary32, and
+ * FP16 numbers, 22 bits: out is about as near the definition as if formed in binary32, and
  * rounded once to its type. (More than a dozen steps amplify the rounding errors of a
  * matrix of low rank past use, here as in binary32.) Values of X_0 are kept to 2^-38 at
  * least: singular values below about 1e-6 lose bits that more than ten steps show.
